@@ -418,6 +418,111 @@ si_status si_moe_stack_graph_create_batched(const si_moe_layer *layers, int n_la
                                             int32_t *ids_out, void *workspace, size_t workspace_bytes,
                                             void *stream, si_graph **graph_out);
 
+/*
+ * MXFP4 - microscaled 4-bit matrices (OCP microscaling formats: E2M1 elements,
+ * one E8M0 scale per 32 consecutive values of a row).
+ *
+ * Format. s = max(exponent field of max |x| - 2, 0) per block, every value
+ * x * 2^(127 - s) rounded to the nearest of 0, .5, 1, 1.5, 2, 3, 4, 6 (ties to
+ * even, larger ones to 6); it stands for code * 2^(s - 127). A block that
+ * holds an infinity or a NaN gets s = 255 and codes 0, and stands for NaN.
+ *   codes   [n_mats][rows][cols / 2] bytes, the even column in the low nibble
+ *   scales  [n_mats] x si_mxfp4_scale_bytes(rows, cols) bytes: tiles of 128 rows
+ *           x 4 blocks, [ceil(rows / 128)][ceil(cols / 128)][512], byte
+ *           (row % 32) * 16 + (row % 128) / 32 * 4 + block % 4 of a tile. Bytes of
+ *           rows and blocks outside the matrix are written as 0; scales from
+ *           elsewhere must not hold 255 there.
+ *   cols    a multiple of 32; codes and scales 16-byte aligned
+ * The float matrix is fp32, fp16 or bf16 with contiguous columns, row_stride
+ * values between rows and mat_stride between matrices (ignored for one row, one
+ * matrix); rows and matrices may not overlap. n_mats = 0 or rows = 0 returns
+ * SI_OK and enqueues nothing. si_dequantize_mxfp4 rounds to nearest even where
+ * its type cannot hold a value (fp16; bf16 and fp32 hold every one).
+ */
+size_t si_mxfp4_scale_bytes(int64_t rows, int64_t cols);
+si_status si_quantize_mxfp4(const void *x, si_dtype x_type, int64_t n_mats, int64_t rows, int64_t cols,
+                            int64_t row_stride, int64_t mat_stride, void *codes, void *scales, void *stream);
+si_status si_dequantize_mxfp4(const void *codes, const void *scales, int64_t n_mats, int64_t rows,
+                              int64_t cols, void *y, si_dtype y_type, int64_t row_stride, int64_t mat_stride,
+                              void *stream);
+
+/*
+ * si_mxfp4_matmul - out[i][j] = sum_c a[i][c] * w[j][c] of two MXFP4 matrices on
+ * the tensor cores (exact products, fp32 accumulation), rounded once to out_type.
+ *   a     [m][k], w [n][k]; m, n >= 1, k a multiple of 32, <= 2^20
+ *   out   device [m] rows of n values (SI_BF16, SI_F16 or SI_F32), ld_out >= n
+ *         values apart; the values between them are left as they are
+ *   workspace  si_mxfp4_matmul_workspace_bytes(m, n, k) bytes, zeroed once
+ */
+size_t si_mxfp4_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k);
+si_status si_mxfp4_matmul(const void *a_codes, const void *a_scales, int64_t m, const void *w_codes,
+                          const void *w_scales, int64_t n, int64_t k, void *out, si_dtype out_type,
+                          int64_t ld_out, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Tokens sorted by expert and back. A pair is (token, rank); pairs whose id lies
+ * outside [0, n_experts) are dropped (experts of another partition).
+ *
+ * si_moe_sort: position[t][r] = place of the pair among the kept ones, ordered
+ * by expert and then by t * top_k + r, or -1 if it is dropped; order = the
+ * inverse (place -> t * top_k + r), -1 behind the kept pairs; offsets[e] = first
+ * place of expert e, offsets[n_experts] = number of kept pairs.
+ *   n_tokens >= 1, top_k 1..8, n_experts 1..1024
+ *   order int32 [n_tokens * top_k], position int32 [n_tokens][top_k],
+ *   offsets int32 [n_experts + 1]
+ *
+ * si_moe_gather:           xs[position[t][r]] = x[t]
+ * si_moe_gather_backward:  gx[t] = sum_r gxs[position[t][r]]
+ * si_moe_combine:          y[t] = sum_r topk_w[t][r] * ys[position[t][r]]
+ * si_moe_combine_backward: gys[position[t][r]] = topk_w[t][r] * gy[t],
+ *                          gw[t][r] = sum_c gy[t][c] * ys[position[t][r]][c]
+ * over rows of `hidden` values of `type` (SI_BF16, SI_F16 or SI_F32), x, y and
+ * their gradients [n_tokens] rows, the sorted side n_tokens * top_k rows, all
+ * contiguous; topk_w and gw fp32. Sums are fp32, in rank order in the rows,
+ * rounded once. A dropped pair adds nothing and has gw 0; a token without kept
+ * pairs gets a zero row; sorted rows at and behind *n_kept (device int32:
+ * offsets + n_experts) are written as zeros. Places must be distinct; those
+ * outside the sorted rows count as dropped. hidden 1..2^24; rows of whole 16-byte
+ * words at 16-byte aligned addresses move in such words, others value by value.
+ * Outputs may not alias inputs.
+ */
+si_status si_moe_sort(const int32_t *topk_ids, int n_tokens, int top_k, int n_experts, int32_t *order,
+                      int32_t *position, int32_t *offsets, void *stream);
+si_status si_moe_gather(const void *x, si_dtype type, int n_tokens, int top_k, int64_t hidden,
+                        const int32_t *position, const int32_t *n_kept, void *xs, void *stream);
+si_status si_moe_gather_backward(const void *gxs, si_dtype type, int n_tokens, int top_k, int64_t hidden,
+                                 const int32_t *position, void *gx, void *stream);
+si_status si_moe_combine(const void *ys, si_dtype type, int n_tokens, int top_k, int64_t hidden,
+                         const int32_t *position, const float *topk_w, void *y, void *stream);
+si_status si_moe_combine_backward(const void *gy, const void *ys, si_dtype type, int n_tokens, int top_k,
+                                  int64_t hidden, const int32_t *position, const int32_t *n_kept,
+                                  const float *topk_w, void *gys, float *gw, void *stream);
+
+/* The routed experts of one layer as MXFP4 matrices. */
+typedef struct si_mxfp4_experts {
+  int hidden, inter;          /* H, I: multiples of 32, <= 65536 */
+  int n_experts;              /* 1..1024 */
+  const void *gate_codes, *gate_scales;   /* n_experts matrices [I][H] */
+  const void *up_codes, *up_scales;       /* n_experts matrices [I][H] */
+  const void *down_codes, *down_scales;   /* n_experts matrices [H][I] */
+} si_mxfp4_experts;
+
+/*
+ * si_moe_ffn_mxfp4 - the routed experts of n_tokens tokens, each routed on its
+ * own, on the tensor cores: the pairs sorted by expert, x quantised to MXFP4,
+ * h = silu(G_e x) * (U_e x) in fp32 quantised to MXFP4, y = D_e h rounded to
+ * bf16, routed[t] = sum_r topk_w[t][r] * y_{t,r} in fp32 and rank order.
+ *   x          device bf16 [n_tokens][H]
+ *   topk_ids   device int32 [n_tokens][top_k]; ids outside [0, n_experts) are dropped
+ *   topk_w     device fp32 [n_tokens][top_k]; routed_out device bf16 [n_tokens][H]
+ *   workspace  si_moe_ffn_mxfp4_workspace_bytes(L, n_tokens, top_k) bytes, zeroed once
+ * n_tokens >= 1, top_k 1..8, n_tokens * top_k <= 2^24.
+ */
+size_t si_moe_ffn_mxfp4_workspace_bytes(const si_mxfp4_experts *L, int n_tokens, int top_k);
+si_status si_moe_ffn_mxfp4(const si_mxfp4_experts *L, int n_tokens, int top_k, const void *x,
+                           const int32_t *topk_ids, const float *topk_w, void *routed_out,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
 /* Synchronises `stream`, then reads the device status word of a workspace
  * used by any call above (SI_OK if no device-side error was recorded) and
  * clears it. */

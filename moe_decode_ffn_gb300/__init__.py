@@ -9,6 +9,7 @@ Names follow the C ABI in ``include/si_moe.h``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -41,6 +42,15 @@ class SiMoeLayer(ctypes.Structure):
         ("ws_gate", _vp), ("ws_up", _vp), ("ws_down", _vp), ("w_shared_sigmoid", _vp),
         ("w_router", _vp), ("router_type", _i32), ("w_norm", _vp), ("eps", _f32),
         ("down_type", _i32),
+    ]
+
+
+class SiMxfp4Experts(ctypes.Structure):
+    """Mirror of ``si_mxfp4_experts``."""
+    _fields_ = [
+        ("hidden", _i32), ("inter", _i32), ("n_experts", _i32),
+        ("gate_codes", _vp), ("gate_scales", _vp), ("up_codes", _vp), ("up_scales", _vp),
+        ("down_codes", _vp), ("down_scales", _vp),
     ]
 
 
@@ -83,6 +93,20 @@ SIGNATURES = {
     "si_moe_stack_graph_create_batched": (_i32, [ctypes.POINTER(SiMoeLayer), _i32, _i32, _i32, _vp,
                                                  _vp, _vp, _vp, _vp, _sz, _vp, ctypes.POINTER(_vp)]),
     "si_requant_q4_k": (_i32, [_vp, _i32, _i64, _i64, _vp, _vp]),
+    "si_mxfp4_scale_bytes": (_sz, [_i64, _i64]),
+    "si_quantize_mxfp4": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "si_dequantize_mxfp4": (_i32, [_vp, _vp, _i64, _i64, _i64, _vp, _i32, _i64, _i64, _vp]),
+    "si_mxfp4_matmul_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "si_mxfp4_matmul": (_i32, [_vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _i32, _i64, _vp, _sz, _vp]),
+    "si_moe_sort": (_i32, [_vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp]),
+    "si_moe_gather": (_i32, [_vp, _i32, _i32, _i32, _i64, _vp, _vp, _vp, _vp]),
+    "si_moe_gather_backward": (_i32, [_vp, _i32, _i32, _i32, _i64, _vp, _vp, _vp]),
+    "si_moe_combine": (_i32, [_vp, _i32, _i32, _i32, _i64, _vp, _vp, _vp, _vp]),
+    "si_moe_combine_backward": (_i32, [_vp, _vp, _i32, _i32, _i32, _i64, _vp, _vp, _vp, _vp, _vp,
+                                       _vp]),
+    "si_moe_ffn_mxfp4_workspace_bytes": (_sz, [ctypes.POINTER(SiMxfp4Experts), _i32, _i32]),
+    "si_moe_ffn_mxfp4": (_i32, [ctypes.POINTER(SiMxfp4Experts), _i32, _i32, _vp, _vp, _vp, _vp, _vp,
+                                _sz, _vp]),
     "si_graph_launch": (_i32, [_vp, _vp]),
     "si_graph_destroy": (None, [_vp]),
     "si_workspace_status": (_i32, [_vp, _vp, ctypes.POINTER(_i32)]),
@@ -519,6 +543,271 @@ def si_requant_q4_k(src: torch.Tensor, src_type: str, rows: int, cols: int,
                                      rows, cols, _shaped(out, "out", rows * (cols // 256 * 144), _U8),
                                      _stream(stream)), "si_requant_q4_k")
     return out
+
+
+# ----------------------------------------------------------------------------
+# MXFP4 matrices and their products, tokens sorted by expert
+# ----------------------------------------------------------------------------
+
+_TYPES = {torch.float32: SI_F32, torch.float16: SI_F16, torch.bfloat16: SI_BF16}
+
+
+def _type(t: torch.Tensor, name: str) -> int:
+    if t.dtype not in _TYPES:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected float32, float16 or bfloat16")
+    return _TYPES[t.dtype]
+
+
+def _scope(stream, *tensors):
+    """(context, stream handle) of a call on ``tensors``: inside the context
+    their device is current and allocations belong to the call's stream, so an
+    output or a temporary workspace is not handed out again while the kernels
+    run. Inputs are marked as used by a stream given by the caller."""
+    dev = tensors[0].device
+    if dev.type != "cuda":
+        raise ValueError("expected CUDA tensors")
+    for t in tensors[1:]:
+        if t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+    if stream is None:
+        handle = torch.cuda.current_stream(dev).cuda_stream
+        if dev.index == torch.cuda.current_device():
+            return contextlib.nullcontext(), handle
+        return torch.cuda.device(dev), handle
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    for t in tensors:
+        t.record_stream(stream)
+    return torch.cuda.stream(stream), stream.cuda_stream
+
+
+def _scratch(nbytes: int, device) -> torch.Tensor:
+    """A workspace for one call: only its status header has to be zero."""
+    if nbytes <= 0:
+        raise ValueError("workspace size query returned 0 (invalid shapes)")
+    ws = torch.empty(int(nbytes), dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def mxfp4_scale_shape(rows: int, cols: int) -> tuple:
+    """Shape of the scale tiles of a [rows, cols] matrix: 128 rows x 4 blocks of 32 each."""
+    return (-(-rows // 128), -(-cols // 128), 512)
+
+
+def _mxfp4(codes, scales, name: str, dims=None):
+    """(matrices, rows, cols) of an MXFP4 pair after checking that they belong together."""
+    if not isinstance(codes, torch.Tensor) or codes.dim() not in ((2, 3) if dims is None else (dims,)):
+        raise ValueError(f"{name} codes must be uint8 [{'n, ' if dims == 3 else ''}rows, cols / 2]")
+    n = 1 if codes.dim() == 2 else codes.shape[0]
+    rows, cols = codes.shape[-2], codes.shape[-1] * 2
+    _shaped(codes, f"{name} codes", n * rows * cols // 2, _U8)
+    per = int(library().si_mxfp4_scale_bytes(rows, cols))
+    if cols == 0 or (per == 0 and rows > 0):
+        raise ValueError(f"{name} has {cols} columns, expected a multiple of 32")
+    _shaped(scales, f"{name} scales", n * per, _U8)
+    return n, rows, cols
+
+
+def _strides(t: torch.Tensor, name: str):
+    """(matrices, rows, cols, row stride, matrix stride) of a 2-D or 3-D tensor with contiguous columns."""
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be [rows, cols] or [n, rows, cols]")
+    n, rows, cols = (1,) * (3 - t.dim()) + tuple(t.shape)
+    if cols > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have contiguous columns")
+    # a size of one has no stride to speak of
+    row = t.stride(-2) if rows > 1 else cols
+    return n, rows, cols, row, t.stride(0) if n > 1 else max(rows - 1, 0) * row + cols
+
+
+def si_quantize_mxfp4(x: torch.Tensor, codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                      stream=None):
+    """x [rows, cols] or [n, rows, cols] (fp32, fp16, bf16; rows and matrices at
+    any stride) -> (codes uint8 [.., rows, cols / 2], scale tiles uint8
+    [.., ceil(rows / 128), ceil(cols / 128), 512])."""
+    n, rows, cols, row, mat = _strides(x, "x")
+    if cols == 0 or cols % 32:
+        raise ValueError(f"x has {cols} columns, expected a multiple of 32")
+    tiles = mxfp4_scale_shape(rows, cols)
+    ctx, handle = _scope(stream, x, *(t for t in (codes, scales) if t is not None))
+    with ctx:
+        if codes is None:
+            codes = torch.empty(*x.shape[:-1], cols // 2, dtype=torch.uint8, device=x.device)
+        if scales is None:
+            scales = torch.empty(*x.shape[:-2], *tiles, dtype=torch.uint8, device=x.device)
+        _check(library().si_quantize_mxfp4(
+            x.data_ptr(), _type(x, "x"), n, rows, cols, row, mat,
+            _shaped(codes, "codes", n * rows * cols // 2, _U8),
+            _shaped(scales, "scales", n * tiles[0] * tiles[1] * 512, _U8), handle), "si_quantize_mxfp4")
+    return codes, scales
+
+
+def si_dequantize_mxfp4(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.bfloat16,
+                        out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The values of an MXFP4 matrix (or n of them) as ``dtype`` or into ``out``."""
+    n, rows, cols = _mxfp4(codes, scales, "x")
+    ctx, handle = _scope(stream, codes, scales, *(() if out is None else (out,)))
+    with ctx:
+        if out is None:
+            out = torch.empty(*codes.shape[:-1], cols, dtype=dtype, device=codes.device)
+        if tuple(out.shape) != (*codes.shape[:-1], cols):
+            raise ValueError(f"out has shape {tuple(out.shape)}, expected {(*codes.shape[:-1], cols)}")
+        _, _, _, row, mat = _strides(out, "out")
+        _check(library().si_dequantize_mxfp4(codes.data_ptr(), scales.data_ptr(), n, rows, cols, out.data_ptr(),
+                                             _type(out, "out"), row, mat, handle), "si_dequantize_mxfp4")
+    return out
+
+
+def mxfp4_matmul_workspace_bytes(m: int, n: int, k: int) -> int:
+    return int(library().si_mxfp4_matmul_workspace_bytes(m, n, k))
+
+
+def si_mxfp4_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+                    dtype=torch.bfloat16, out: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """a [m, k] and w [n, k] in MXFP4 -> a w^T [m, n] in ``dtype`` or into ``out`` (any row stride)."""
+    _, m, k = _mxfp4(a_codes, a_scales, "a", 2)
+    _, n, k2 = _mxfp4(w_codes, w_scales, "w", 2)
+    if k != k2:
+        raise ValueError(f"a has {k} columns, w has {k2}")
+    given = tuple(t for t in (out, ws) if t is not None)
+    ctx, handle = _scope(stream, a_codes, a_scales, w_codes, w_scales, *given)
+    with ctx:
+        if out is None:
+            out = torch.empty(m, n, dtype=dtype, device=a_codes.device)
+        if tuple(out.shape) != (m, n):
+            raise ValueError(f"out has shape {tuple(out.shape)}, expected {(m, n)}")
+        _, _, _, ld, _ = _strides(out, "out")
+        if ws is None:
+            ws = _scratch(mxfp4_matmul_workspace_bytes(m, n, k), a_codes.device)
+        _check(library().si_mxfp4_matmul(
+            a_codes.data_ptr(), a_scales.data_ptr(), m, w_codes.data_ptr(), w_scales.data_ptr(), n, k,
+            out.data_ptr(), _type(out, "out"), ld, _cuda(ws, "ws"), ws.numel(), handle), "si_mxfp4_matmul")
+    return out
+
+
+def si_moe_sort(ids: torch.Tensor, n_experts: int, stream=None):
+    """ids int32 [T, k] -> (order int32 [T * k], position int32 [T, k], offsets
+    int32 [n_experts + 1]); pairs whose id is outside [0, n_experts) are dropped
+    (position -1)."""
+    T, k = ids.shape
+    ctx, handle = _scope(stream, ids)
+    with ctx:
+        order = torch.empty(T * k, dtype=torch.int32, device=ids.device)
+        position = torch.empty(T, k, dtype=torch.int32, device=ids.device)
+        offsets = torch.empty(max(n_experts, 0) + 1, dtype=torch.int32, device=ids.device)
+        _check(library().si_moe_sort(_shaped(ids, "ids", T * k, _I32), T, k, n_experts, order.data_ptr(),
+                                     position.data_ptr(), offsets.data_ptr(), handle), "si_moe_sort")
+    return order, position, offsets
+
+
+def _kept(offsets: torch.Tensor) -> int:
+    """Address of the number of kept pairs, the last of the offsets."""
+    if offsets.dim() != 1 or offsets.numel() < 1 or offsets.dtype != torch.int32:
+        raise ValueError("offsets must be int32 [n_experts + 1]")
+    return _cuda(offsets, "offsets") + 4 * (offsets.numel() - 1)
+
+
+def si_moe_gather(x: torch.Tensor, position: torch.Tensor, offsets: torch.Tensor, stream=None) -> torch.Tensor:
+    """xs[position[t, r]] = x[t]: x [T, H] -> [T * k, H], zero rows behind the kept pairs."""
+    (T, H), k = x.shape, position.shape[-1]
+    ctx, handle = _scope(stream, x, position, offsets)
+    with ctx:
+        xs = torch.empty(T * k, H, dtype=x.dtype, device=x.device)
+        _check(library().si_moe_gather(_cuda(x, "x"), _type(x, "x"), T, k, H,
+                                       _shaped(position, "position", T * k, _I32), _kept(offsets), xs.data_ptr(),
+                                       handle), "si_moe_gather")
+    return xs
+
+
+def si_moe_gather_backward(gxs: torch.Tensor, position: torch.Tensor, stream=None) -> torch.Tensor:
+    """gx[t] = sum_r gxs[position[t, r]]: gxs [T * k, H] -> [T, H]."""
+    (T, k), H = position.shape, gxs.shape[-1]
+    ctx, handle = _scope(stream, gxs, position)
+    with ctx:
+        gx = torch.empty(T, H, dtype=gxs.dtype, device=gxs.device)
+        _check(library().si_moe_gather_backward(_shaped(gxs, "gxs", T * k * H, (gxs.dtype,)), _type(gxs, "gxs"),
+                                                T, k, H, _shaped(position, "position", T * k, _I32),
+                                                gx.data_ptr(), handle), "si_moe_gather_backward")
+    return gx
+
+
+def si_moe_combine(ys: torch.Tensor, position: torch.Tensor, w: torch.Tensor, stream=None) -> torch.Tensor:
+    """y[t] = sum_r w[t, r] ys[position[t, r]]: ys [T * k, H], w fp32 [T, k] -> [T, H]."""
+    (T, k), H = position.shape, ys.shape[-1]
+    ctx, handle = _scope(stream, ys, position, w)
+    with ctx:
+        y = torch.empty(T, H, dtype=ys.dtype, device=ys.device)
+        _check(library().si_moe_combine(_shaped(ys, "ys", T * k * H, (ys.dtype,)), _type(ys, "ys"), T, k, H,
+                                        _shaped(position, "position", T * k, _I32), _shaped(w, "w", T * k, _F32),
+                                        y.data_ptr(), handle), "si_moe_combine")
+    return y
+
+
+def si_moe_combine_backward(gy: torch.Tensor, ys: torch.Tensor, position: torch.Tensor, offsets: torch.Tensor,
+                            w: torch.Tensor, stream=None):
+    """gy [T, H], ys [T * k, H] -> (gys [T * k, H], gw fp32 [T, k])."""
+    (T, k), H = position.shape, gy.shape[-1]
+    ctx, handle = _scope(stream, gy, ys, position, offsets, w)
+    with ctx:
+        gys = torch.empty(T * k, H, dtype=gy.dtype, device=gy.device)
+        gw = torch.empty(T, k, dtype=torch.float32, device=gy.device)
+        _check(library().si_moe_combine_backward(
+            _shaped(gy, "gy", T * H, (gy.dtype,)), _shaped(ys, "ys", T * k * H, (gy.dtype,)), _type(gy, "gy"), T, k, H,
+            _shaped(position, "position", T * k, _I32), _kept(offsets), _shaped(w, "w", T * k, _F32),
+            gys.data_ptr(), gw.data_ptr(), handle), "si_moe_combine_backward")
+    return gys, gw
+
+
+class Mxfp4Experts:
+    """The routed experts of one layer in MXFP4 plus the ``si_mxfp4_experts``
+    descriptor. ``gate``, ``up`` [E, I, H] and ``down`` [E, H, I] are (codes,
+    scales) as ``si_quantize_mxfp4`` returns them."""
+
+    def __init__(self, gate, up, down):
+        self.gate, self.up, self.down = gate, up, down
+        E, I, H = _mxfp4(*gate, "gate", 3)
+        if _mxfp4(*up, "up", 3) != (E, I, H):
+            raise ValueError(f"up must be {E} matrices [{I}, {H}], as gate")
+        if _mxfp4(*down, "down", 3) != (E, H, I):
+            raise ValueError(f"down must be {E} matrices [{H}, {I}]")
+        self.device = gate[0].device
+        if any(t.device != self.device for t in (*gate, *up, *down)):
+            raise ValueError("gate, up and down on different devices")
+        self.hidden, self.inter, self.n_experts = H, I, E
+        self.c = SiMxfp4Experts(H, I, E, *(t.data_ptr() for t in (*gate, *up, *down)))
+
+    @classmethod
+    def quantize(cls, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, stream=None):
+        """From weights gate, up [E, I, H] and down [E, H, I] in fp32, fp16 or bf16."""
+        return cls(*(si_quantize_mxfp4(t, stream=stream) for t in (gate, up, down)))
+
+    @property
+    def ref(self):
+        return ctypes.byref(self.c)
+
+
+def ffn_mxfp4_workspace_bytes(experts: Mxfp4Experts, n_tokens: int, top_k: int) -> int:
+    return int(library().si_moe_ffn_mxfp4_workspace_bytes(experts.ref, n_tokens, top_k))
+
+
+def si_moe_ffn_mxfp4(experts: Mxfp4Experts, x: torch.Tensor, ids: torch.Tensor, w: torch.Tensor,
+                     ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """T tokens with per-token routing: x bf16 [T, H], ids int32 [T, k], w fp32
+    [T, k] -> routed bf16 [T, H]."""
+    T, k = ids.shape
+    H = experts.hidden
+    ctx, handle = _scope(stream, x, ids, w, experts.gate[0], *(() if ws is None else (ws,)))
+    with ctx:
+        if ws is None:
+            ws = _scratch(ffn_mxfp4_workspace_bytes(experts, T, k), x.device)
+        routed = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
+        _check(library().si_moe_ffn_mxfp4(
+            experts.ref, T, k, _shaped(x, "x", T * H, _BF16), _shaped(ids, "ids", T * k, _I32),
+            _shaped(w, "w", T * k, _F32), routed.data_ptr(), _cuda(ws, "ws"), ws.numel(), handle),
+            "si_moe_ffn_mxfp4")
+    return routed
 
 
 def si_workspace_status(ws: torch.Tensor, stream=None) -> int:

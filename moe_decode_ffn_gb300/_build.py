@@ -16,9 +16,11 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsi_moe.so")
-SOURCES = ["quant_norm.cu", "router.cu", "ffn.cu", "batched.cu", "stack.cu", "requant.cu", "api.cu"]
+SOURCES = ["quant_norm.cu", "router.cu", "ffn.cu", "batched.cu", "stack.cu", "requant.cu", "mxfp4.cu",
+           "mxfp4_gemm.cu", "sort.cu", "api.cu"]
 HEADERS = [os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "host.hpp"),
            os.path.join(CSRC, "topk.cuh"), os.path.join(CSRC, "tc.cuh"), os.path.join(CSRC, "norm.cuh"),
+           os.path.join(CSRC, "mxfp4.cuh"), os.path.join(CSRC, "sort.cuh"),
            os.path.join(ROOT, "include", "si_moe.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",

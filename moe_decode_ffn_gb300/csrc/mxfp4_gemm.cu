@@ -1,0 +1,649 @@
+// Products of MXFP4 matrices on the tensor cores: the plain product and the
+// expert FFN of a routed batch.
+//
+//   out[m][n] = sum_k a[m][k] w[n][k]            (si_mxfp4_matmul)
+//   h = silu(G x) * (U x), y = D h per pair      (si_moe_ffn_mxfp4)
+//
+// Both are one kernel: tcgen05.mma kind::mxf4 with block scales, the WEIGHT
+// rows as the 128-row operand and a tile of NT tokens as the N operand, so a
+// batch of few tokens wastes no tensor rows and every lane of tensor memory
+// holds one output feature. Products of two E2M1 values are exact and the
+// accumulators fp32.
+//
+// A block of 192 threads: warp 0 keeps a ring of stages full (256 columns of
+// the codes by tensor TMA in the 128-byte swizzle, their scale tiles by plain
+// bulk copies), one thread of warp 1 moves the scales into tensor memory
+// (tcgen05.cp) and issues the MMAs, warps 2..5 read the accumulators and write
+// the outputs. Blocks are persistent: tile i of block b is b + i * gridDim.
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "host.hpp"
+#include "mxfp4.cuh"
+#include "sort.cuh"
+#include "tc.cuh"
+
+namespace si {
+
+constexpr int kMmThreads = 192;
+constexpr int kMmStageK = 256;         // columns of a stage: 128 bytes of codes per row
+constexpr int kMmABytes = 128 * 128;   // 128 weight rows of a stage
+
+enum MmMode { kMmPlain = 0, kMmGateUp = 1 };
+
+// MA: 128-row weight tiles of a block's tile (gate and up, or two neighbours).
+template <int MA, int NT> struct MmCfg {
+  static constexpr int kBBytes = NT * 128;
+  static constexpr int kSfBytes = 2 * kMxTileBytes;               // per operand tile and stage
+  static constexpr int kStage = MA * kMmABytes + kBBytes + (MA + 1) * kSfBytes;
+  static constexpr int kMaxSmem = 227 * 1024 - 2048;              // less alignment and barriers
+  static constexpr int kStages = kMaxSmem / kStage < 8 ? kMaxSmem / kStage : 8;
+  // tensor memory: accumulators, then the scales of every stage (a column
+  // holds 4 blocks of 32 rows, so 128 rows x 8 blocks take 8 columns)
+  static constexpr int kAcc = MA * NT;
+  static constexpr int kSfCols = 8 * (MA + 1);
+  static constexpr int kBufs = 2 * kAcc + kStages * kSfCols <= 512 ? 2 : 1;
+  static constexpr int kUsed = kBufs * kAcc + kStages * kSfCols;
+  static constexpr int kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+  static_assert(kUsed <= 512, "tensor memory has 512 columns");
+  static constexpr int kSmem = kStages * kStage + 1024 + 512;
+};
+
+struct MmParams {
+  CUtensorMap a0, a1, b;               // weight rows [mats][rows][K / 2], token rows [..][K / 2]
+  const uint8_t *sa0, *sa1, *sb;       // their scale tiles
+  int rows, row_tiles;                 // weight rows of a matrix; its 128-row scale tiles
+  int n_rt;                            // tiles along the weight rows
+  int K, kt;                           // columns; scale tiles along them
+  // tokens: a dense batch of `tokens`, or the tiles of a sorted one
+  int64_t tokens;
+  const int32_t *tile_expert, *tile_count, *n_tiles;
+  // plain: out[token][feature]
+  void *out;
+  int64_t ld;
+  int out_type;
+  // gate/up: the MXFP4 rows of h
+  uint8_t *h_codes, *h_scales;
+  int h_kt;
+  uint32_t *status;
+};
+
+struct MmTile {
+  int rt, tt, mat, count;
+};
+
+SI_DEV int mm_total(const MmParams &p, int nt) {
+  const int n_tt = p.n_tiles ? __ldcg(p.n_tiles) : static_cast<int>((p.tokens + nt - 1) / nt);
+  return n_tt * p.n_rt;
+}
+SI_DEV MmTile mm_tile(const MmParams &p, int w, int nt) {
+  MmTile t;
+  t.rt = w % p.n_rt;
+  t.tt = w / p.n_rt;
+  if (p.n_tiles) {
+    t.mat = __ldcg(p.tile_expert + t.tt);
+    t.count = __ldcg(p.tile_count + t.tt);
+  } else {
+    const int64_t left = p.tokens - static_cast<int64_t>(t.tt) * nt;
+    t.mat = 0;
+    t.count = left < nt ? static_cast<int>(left) : nt;
+  }
+  return t;
+}
+
+SI_DEV void tma_load3(void *dst, const CUtensorMap *map, int c0, int c1, int c2, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(smem_addr(dst)),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar))
+      : "memory");
+}
+SI_DEV void mbar_arrive(uint64_t *bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// Shared-memory matrix descriptor, K-major, 128-byte swizzle: rows of 128
+// bytes, 8-row groups 1024 bytes apart. Bits as in umma_desc_kmajor, layout 2.
+SI_DEV uint64_t mm_desc_sw128(uint32_t addr) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+         (static_cast<uint64_t>(2) << 61);
+}
+// A scale tile: 32 rows of 16 bytes, 8-row groups 128 bytes apart.
+SI_DEV uint64_t mm_desc_sf(uint32_t addr) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 32) |
+         (static_cast<uint64_t>(1) << 46);
+}
+// 512 bytes of scales to 4 columns of tensor memory, on all four 32-lane quarters.
+SI_DEV void mm_copy_sf(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// Instruction descriptor, kind::mxf4: E2M1 operands (bits [7,10), [10,12)),
+// K-major, N >> 3 in [17,23), E8M0 scales (bit 23), M >> 4 in [24,29); the scale
+// pair of a 4-byte column (blocks 0-1 or 2-3) in [29,31) for A and [4,6) for B.
+SI_DEV uint32_t mm_idesc(int n) {
+  return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) | ((128u >> 4) << 24);
+}
+// D[tmem] (+)= A B^T over 64 columns, one thread.
+SI_DEV void mm_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+      : "memory");
+}
+// 16 consecutive fp32 columns of this warp's 32 lanes; the wait is separate so
+// that two loads can be in flight.
+SI_DEV void tmem_ld16(uint32_t taddr, uint32_t r[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+SI_DEV void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// ---- epilogues ---------------------------------------------------------------
+
+SI_DEV void mm_store(const MmParams &p, int64_t at, float v) {
+  if (p.out_type == SI_BF16) static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(v);
+  else if (p.out_type == SI_F32) static_cast<float *>(p.out)[at] = v;
+  else static_cast<__half *>(p.out)[at] = __float2half_rn(v);
+}
+
+// Lane = feature; for one token the 32 lanes write consecutive values.
+template <int MA, int NT>
+SI_DEV void mm_write_plain(const MmParams &p, const MmTile &t, uint32_t acc, int q, int lane) {
+  const int64_t row0 = static_cast<int64_t>(t.tt) * NT;
+#pragma unroll 1
+  for (int a = 0; a < MA; ++a) {
+    const int f = (t.rt * MA + a) * 128 + q * 32 + lane;
+    if ((t.rt * MA + a) * 128 >= p.rows) break;
+#pragma unroll 1
+    for (int j0 = 0; j0 < t.count; j0 += 16) {
+      uint32_t r[16];
+      tmem_ld16(acc + a * NT + j0, r);
+      tmem_wait_ld();
+      if (f < p.rows) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (j0 + j < t.count) mm_store(p, (row0 + j0 + j) * p.ld + f, __uint_as_float(r[j]));
+      }
+    }
+  }
+}
+
+// 8 x 8 nibbles over 8 consecutive lanes: nibble c of lane r to nibble r of lane c.
+SI_DEV uint32_t transpose_nibbles(uint32_t w, int lane) {
+  uint32_t o = __shfl_xor_sync(0xffffffffu, w, 4);
+  w = lane & 4 ? (w & 0xFFFF0000u) | (o >> 16) : (w & 0x0000FFFFu) | (o << 16);
+  o = __shfl_xor_sync(0xffffffffu, w, 2);
+  w = lane & 2 ? (w & 0xFF00FF00u) | ((o >> 8) & 0x00FF00FFu) : (w & 0x00FF00FFu) | ((o & 0x00FF00FFu) << 8);
+  o = __shfl_xor_sync(0xffffffffu, w, 1);
+  return lane & 1 ? (w & 0xF0F0F0F0u) | ((o >> 4) & 0x0F0F0F0Fu) : (w & 0x0F0F0F0Fu) | ((o & 0x0F0F0F0Fu) << 4);
+}
+
+// h = silu(g) u of a lane's feature for 16 tokens, then MXFP4: the 32 lanes of
+// the warp are one block of every token, so its scale is a warp maximum.
+template <int NT>
+SI_DEV void mm_write_h(const MmParams &p, const MmTile &t, uint32_t acc, int q, int lane) {
+  const int64_t row0 = static_cast<int64_t>(t.tt) * NT;
+  const int blk = t.rt * 4 + q;                 // this warp's block of 32 features
+  const bool live = blk * 32 < p.rows;          // rows % 32 == 0: the whole warp or none of it
+  const size_t row_bytes = static_cast<size_t>(p.rows) / 2;
+  uint8_t *sf = p.h_scales + (static_cast<size_t>(t.tt) * p.h_kt + t.rt) * kMxTileBytes;
+#pragma unroll 1
+  for (int j0 = 0; j0 < t.count; j0 += 16) {
+    uint32_t g[16], u[16];
+    tmem_ld16(acc + j0, g);
+    tmem_ld16(acc + NT + j0, u);
+    tmem_wait_ld();
+#pragma unroll
+    for (int h8 = 0; h8 < 16; h8 += 8) {
+      float v[8];
+      uint32_t mine = 0;                        // scale of token j0 + h8 + lane
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float gv = __uint_as_float(g[h8 + j]), uv = __uint_as_float(u[h8 + j]);
+        const float h = live ? __fdividef(gv, 1.f + __expf(-gv)) * uv : 0.f;
+        const uint32_t s = mx_scale_of(__reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7FFFFFFFu));
+        v[j] = h * mx_inv_scale(s);
+        if (s == 255u) v[j] = 0.f;
+        if ((lane & 7) == j) mine = s;
+      }
+      const uint32_t w = transpose_nibbles(mx_codes8(v), lane);
+      const int j = j0 + h8 + (lane & 7);
+      if (j < t.count) {
+        if (live)
+          *reinterpret_cast<uint32_t *>(p.h_codes + (row0 + j) * row_bytes + blk * 16 + (lane >> 3) * 4) = w;
+        // blocks behind the last feature too: their scales multiply zeros
+        if (lane < 8) sf[mx_scale_byte(j, blk)] = static_cast<uint8_t>(mine);
+      }
+    }
+  }
+}
+
+// ---- the kernel ----------------------------------------------------------------
+
+template <int MODE, int MA, int NT>
+__global__ void __launch_bounds__(kMmThreads, 1) mxfp4_mm_kernel(const __grid_constant__ MmParams p) {
+  using C = MmCfg<MA, NT>;
+  constexpr int S = C::kStages, BUFS = C::kBufs;
+  extern __shared__ uint8_t mm_smem[];
+  uint8_t *base = mm_smem + ((1024u - (smem_addr(mm_smem) & 1023u)) & 1023u);
+  uint64_t *full = reinterpret_cast<uint64_t *>(base + S * C::kStage);
+  uint64_t *empty = full + S, *acc_full = empty + S, *acc_empty = acc_full + BUFS, *drain = acc_empty + BUFS;
+  uint32_t *s_taddr = reinterpret_cast<uint32_t *>(drain + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    for (int i = 0; i < BUFS; ++i) {
+      mbar_init(acc_full + i, 1);
+      mbar_init(acc_empty + i, 4);
+    }
+    mbar_init(drain, 1);
+    fence_mbar_init();
+  }
+  grid_dep_wait();
+  if (warp == 1) {
+    // before the next kernel may start: its blocks take tensor memory too
+    tmem_alloc(s_taddr, C::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_dep_launch();
+  const uint32_t tmem = *s_taddr;
+  const int total = mm_total(p, NT);
+  const int n_ks = (p.K + kMmStageK - 1) / kMmStageK;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
+        const MmTile t = mm_tile(p, w, NT);
+        const int row0 = MODE == kMmGateUp ? t.rt * 128 : t.rt * MA * 128;
+        const int na = MODE == kMmGateUp || MA == 1 || row0 + 128 < p.rows ? MA : 1;
+        const int sr0 = t.mat * p.row_tiles + row0 / 128;
+        for (int ks = 0; ks < n_ks; ++ks, ++it) {
+          const int s = it % S;
+          if (!mbar_wait_bounded(empty + s, ((it / S) & 1) ^ 1, p.status)) {
+            ok = false;
+            break;
+          }
+          const int nkt = min(2, p.kt - 2 * ks);
+          uint8_t *st = base + s * C::kStage;
+          uint8_t *sb = st + MA * kMmABytes, *sf = sb + C::kBBytes;
+          const uint32_t sfb = nkt * kMxTileBytes;
+          mbar_arrive_expect_tx(full + s, na * kMmABytes + C::kBBytes + (na + 1) * sfb);
+#pragma unroll
+          for (int a = 0; a < MA; ++a) {
+            if (a >= na) break;
+            const bool up = MODE == kMmGateUp && a == 1;
+            tma_load3(st + a * kMmABytes, up ? &p.a1 : &p.a0, ks * 128, MODE == kMmGateUp ? row0 : row0 + a * 128,
+                      t.mat, full + s);
+            bulk_g2s(sf + a * C::kSfBytes,
+                     (up ? p.sa1 : p.sa0) +
+                         (static_cast<size_t>(sr0 + (MODE == kMmGateUp ? 0 : a)) * p.kt + 2 * ks) * kMxTileBytes,
+                     sfb, full + s);
+          }
+          tma_load3(sb, &p.b, ks * 128, t.tt * NT, 0, full + s);
+          bulk_g2s(sf + MA * C::kSfBytes, p.sb + (static_cast<size_t>(t.tt) * p.kt + 2 * ks) * kMxTileBytes, sfb,
+                   full + s);
+        }
+      }
+      if (!ok) {   // copies in flight land before the block's memory goes
+        const uint32_t n = it < static_cast<uint32_t>(S) ? it : S;
+        for (uint32_t i = it - n; i < it; ++i) mbar_wait_bounded(full + i % S, (i / S) & 1, p.status);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      uint32_t it = 0, n = 0;
+      bool ok = true;
+      for (int w = blockIdx.x; ok && w < total; w += gridDim.x, ++n) {
+        const MmTile t = mm_tile(p, w, NT);
+        const int row0 = t.rt * MA * 128;
+        const int na = MODE == kMmGateUp || MA == 1 || row0 + 128 < p.rows ? MA : 1;
+        const uint32_t buf = n % BUFS;
+        if (!mbar_wait_bounded(acc_empty + buf, ((n / BUFS) & 1) ^ 1, p.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + buf * C::kAcc;
+        const uint32_t idesc = mm_idesc((t.count + 15) & ~15);
+        for (int ks = 0; ks < n_ks; ++ks, ++it) {
+          const int s = it % S;
+          if (!mbar_wait_bounded(full + s, (it / S) & 1, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const int n64 = min(4, (p.K - ks * kMmStageK + 63) / 64), nkt = (n64 + 1) / 2;
+          const uint32_t st = smem_addr(base + s * C::kStage);
+          const uint32_t sb = st + MA * kMmABytes, sf = sb + C::kBBytes;
+          const uint32_t tsf = tmem + BUFS * C::kAcc + s * C::kSfCols;
+          for (int kt = 0; kt < nkt; ++kt) {
+#pragma unroll
+            for (int a = 0; a < MA; ++a)
+              if (a < na) mm_copy_sf(tsf + a * 8 + kt * 4, mm_desc_sf(sf + a * C::kSfBytes + kt * kMxTileBytes));
+            mm_copy_sf(tsf + MA * 8 + kt * 4, mm_desc_sf(sf + MA * C::kSfBytes + kt * kMxTileBytes));
+          }
+          for (int i = 0; i < n64; ++i) {
+            const uint32_t id = idesc | (static_cast<uint32_t>(i & 1) * 2u << 29) | (static_cast<uint32_t>(i & 1) * 2u << 4);
+#pragma unroll
+            for (int a = 0; a < MA; ++a)
+              if (a < na)
+                mm_mma(d + a * NT, mm_desc_sw128(st + a * kMmABytes + i * 32), mm_desc_sw128(sb + i * 32), id,
+                       tsf + a * 8 + (i >> 1) * 4, tsf + MA * 8 + (i >> 1) * 4, ks > 0 || i > 0);
+          }
+          umma_commit(empty + s);
+        }
+        if (ok) umma_commit(acc_full + buf);
+      }
+      if (!ok) {   // MMAs in flight end before the tensor memory goes
+        umma_commit(drain);
+        mbar_wait_bounded(drain, 0, p.status);
+      }
+    }
+  } else {
+    const int q = warp & 3;                     // the 32 lanes of tensor memory this warp may read
+    uint32_t n = 0;
+    for (int w = blockIdx.x; w < total; w += gridDim.x, ++n) {
+      const MmTile t = mm_tile(p, w, NT);
+      const uint32_t buf = n % BUFS;
+      const bool ok = mbar_wait_bounded(acc_full + buf, (n / BUFS) & 1, p.status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + buf * C::kAcc + (static_cast<uint32_t>(q * 32) << 16);
+      if constexpr (MODE == kMmGateUp) mm_write_h<NT>(p, t, acc, q, lane);
+      else mm_write_plain<MA, NT>(p, t, acc, q, lane);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty + buf);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc(tmem, C::kCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// x to MXFP4 rows at the sorted places: one block per token quantises its row
+// once and writes it to its k places. Scale tiles belong to one token tile each
+// (NT <= 128 rows of their 128).
+// ---------------------------------------------------------------------------
+struct ScatterArgs {
+  const __nv_bfloat16 *x;
+  int k, H, kt, nt;
+  const int32_t *position;
+  uint8_t *codes, *scales;
+};
+__global__ void __launch_bounds__(256) quantize_scatter_kernel(ScatterArgs a) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int64_t t = blockIdx.x;
+  int p[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) p[r] = r < a.k ? __ldcg(a.position + t * a.k + r) : -1;
+  const int lane = threadIdx.x & 31;
+  // whole scale tiles (128 columns, 16 lanes): the blocks behind H get scale 0
+  for (int c0 = (threadIdx.x & ~31) * 8; c0 < a.kt * 128; c0 += blockDim.x * 8) {
+    const int c = c0 + lane * 8;
+    float v[8];
+    if (c < a.H) {
+      Load8<__nv_bfloat16>::run(a.x + t * a.H + c, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    }
+    uint32_t s;
+    const uint32_t w = mx_encode_4lanes(v, s);
+    uint32_t s4 = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) s4 |= __shfl_sync(0xffffffffu, s, (lane & 16) + 4 * b) << (8 * b);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      if (p[r] < 0) continue;
+      if (c < a.H) *reinterpret_cast<uint32_t *>(a.codes + (static_cast<size_t>(p[r]) * a.H + c) / 2) = w;
+      if ((lane & 15) == 0 && c < a.kt * 128)
+        *reinterpret_cast<uint32_t *>(a.scales + (static_cast<size_t>(p[r] / a.nt) * a.kt + c / 128) * kMxTileBytes +
+                                      mx_scale_byte(p[r] % a.nt, 0)) = s4;
+    }
+  }
+}
+
+// ---- host ------------------------------------------------------------------
+
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+static EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  return fn;
+}
+
+// Codes [mats][rows][cols / 2], boxes of box_rows rows x 128 bytes; what lies
+// outside reads as zero.
+static bool codes_map(CUtensorMap *m, const void *codes, int64_t mats, int64_t rows, int64_t cols, int box_rows) {
+  const EncodeTiled fn = encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols / 2), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(mats)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols / 2), static_cast<cuuint64_t>(cols / 2 * rows)};
+  const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(box_rows), 1}, one[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(codes), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE, int MA, int NT>
+static cudaError_t mm_launch_as(const MmParams &p, int64_t max_tiles, cudaStream_t s) {
+  using C = MmCfg<MA, NT>;
+  const cudaError_t e = allow_smem(mxfp4_mm_kernel<MODE, MA, NT>, C::kSmem);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(max_tiles, sm_count()));
+  return launch_pdl(mxfp4_mm_kernel<MODE, MA, NT>, dim3(grid), dim3(kMmThreads), C::kSmem, s, p);
+}
+static cudaError_t mm_launch(int mode, int ma, int nt, const MmParams &p, int64_t max_tiles, cudaStream_t s) {
+  if (mode == kMmGateUp)
+    return nt == 16   ? mm_launch_as<kMmGateUp, 2, 16>(p, max_tiles, s)
+           : nt == 32 ? mm_launch_as<kMmGateUp, 2, 32>(p, max_tiles, s)
+           : nt == 64 ? mm_launch_as<kMmGateUp, 2, 64>(p, max_tiles, s)
+                      : mm_launch_as<kMmGateUp, 2, 128>(p, max_tiles, s);
+  if (ma == 2) return mm_launch_as<kMmPlain, 2, 128>(p, max_tiles, s);
+  return nt == 16   ? mm_launch_as<kMmPlain, 1, 16>(p, max_tiles, s)
+         : nt == 32 ? mm_launch_as<kMmPlain, 1, 32>(p, max_tiles, s)
+         : nt == 64 ? mm_launch_as<kMmPlain, 1, 64>(p, max_tiles, s)
+                    : mm_launch_as<kMmPlain, 1, 128>(p, max_tiles, s);
+}
+
+// ---- expert FFN: workspace ---------------------------------------------------
+struct FfnMxGeom {
+  int nt;                   // tokens of a tile
+  int64_t pairs, max_tiles, rows;
+  int kt_x, kt_h;
+  size_t off_position, off_expert, off_count, off_n, off_xc, off_xs, off_hc, off_hs, off_y, bytes;
+};
+static FfnMxGeom ffn_mx_geom(const si_mxfp4_experts &L, int n_tokens, int top_k) {
+  FfnMxGeom g{};
+  g.pairs = static_cast<int64_t>(n_tokens) * top_k;
+  // the smallest tile that holds an expert's average tokens
+  const int64_t avg = (g.pairs + L.n_experts - 1) / L.n_experts;
+  g.nt = avg <= 16 ? 16 : avg <= 32 ? 32 : avg <= 64 ? 64 : 128;
+  const int64_t with = std::min<int64_t>(L.n_experts, g.pairs);   // experts that can hold pairs
+  g.max_tiles = (g.pairs + with * (g.nt - 1)) / g.nt;
+  g.rows = g.max_tiles * g.nt;
+  g.kt_x = (L.hidden + 127) / 128;
+  g.kt_h = (L.inter + 127) / 128;
+  size_t off = sizeof(WsHeader);
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = round_up(off + bytes, 256);
+    return at;
+  };
+  g.off_position = take(g.pairs * 4);
+  g.off_expert = take(g.max_tiles * 4);
+  g.off_count = take(g.max_tiles * 4);
+  g.off_n = take(4);
+  g.off_xc = take(static_cast<size_t>(g.rows) * L.hidden / 2);
+  g.off_xs = take(static_cast<size_t>(g.max_tiles) * g.kt_x * kMxTileBytes);
+  g.off_hc = take(static_cast<size_t>(g.rows) * L.inter / 2);
+  g.off_hs = take(static_cast<size_t>(g.max_tiles) * g.kt_h * kMxTileBytes);
+  g.off_y = take(static_cast<size_t>(g.rows) * L.hidden * 2);
+  g.bytes = off;
+  return g;
+}
+static bool ffn_mx_shape_ok(const si_mxfp4_experts *L, int n_tokens, int top_k) {
+  return L && L->hidden > 0 && L->hidden % 32 == 0 && L->hidden <= 65536 && L->inter > 0 && L->inter % 32 == 0 &&
+         L->inter <= 65536 && L->n_experts >= 1 && L->n_experts <= kSortMaxExperts && top_k >= 1 && top_k <= 8 &&
+         n_tokens >= 1 && static_cast<int64_t>(n_tokens) * top_k <= (int64_t(1) << 24);
+}
+
+}  // namespace si
+
+using namespace si;
+
+extern "C" size_t si_mxfp4_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  if (m < 1 || n < 1 || k < 32 || k % 32 || m >= (int64_t(1) << 31) || n >= (int64_t(1) << 31) ||
+      k > (int64_t(1) << 20))
+    return 0;
+  return sizeof(WsHeader);
+}
+
+extern "C" si_status si_mxfp4_matmul(const void *a_codes, const void *a_scales, int64_t m, const void *w_codes,
+                                     const void *w_scales, int64_t n, int64_t k, void *out, si_dtype out_type,
+                                     int64_t ld_out, void *workspace, size_t workspace_bytes, void *stream) {
+  const size_t need = si_mxfp4_matmul_workspace_bytes(m, n, k);
+  if (!need || !a_codes || !a_scales || !w_codes || !w_scales || !out || ld_out < n || ld_out > (int64_t(1) << 40))
+    return SI_ERR_INVALID_ARG;
+  if (out_type != SI_F32 && out_type != SI_F16 && out_type != SI_BF16) return SI_ERR_UNSUPPORTED;
+  if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(w_codes) || !aligned16(w_scales) ||
+      reinterpret_cast<uintptr_t>(out) % (out_type == SI_F32 ? 4 : 2))
+    return SI_ERR_INVALID_ARG;
+  if (!workspace || !aligned256(workspace) || workspace_bytes < need) return SI_ERR_WORKSPACE;
+  MmParams p{};
+  const int nt = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
+  const int64_t n_tt = (m + nt - 1) / nt, row_tiles = (n + 127) / 128;
+  // two weight tiles share the tokens of a stage as soon as such tiles fill the SMs
+  const int ma = nt == 128 && n_tt * ((row_tiles + 1) / 2) >= sm_count() ? 2 : 1;
+  const int64_t n_rt = (row_tiles + ma - 1) / ma;
+  if (n_tt * n_rt > 0x7FFFFFFF || n_tt * nt > 0x7FFFFFFF) return SI_ERR_UNSUPPORTED;
+  if (!codes_map(&p.a0, w_codes, 1, n, k, 128) || !codes_map(&p.b, a_codes, 1, m, k, nt)) return SI_ERR_CUDA;
+  p.a1 = p.a0;
+  p.sa0 = p.sa1 = static_cast<const uint8_t *>(w_scales);
+  p.sb = static_cast<const uint8_t *>(a_scales);
+  p.rows = static_cast<int>(n);
+  p.row_tiles = static_cast<int>(row_tiles);
+  p.n_rt = static_cast<int>(n_rt);
+  p.K = static_cast<int>(k);
+  p.kt = static_cast<int>((k + 127) / 128);
+  p.tokens = m;
+  p.out = out;
+  p.ld = ld_out;
+  p.out_type = out_type;
+  p.status = static_cast<uint32_t *>(workspace);
+  return cuda_status(mm_launch(kMmPlain, ma, nt, p, n_tt * n_rt, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" size_t si_moe_ffn_mxfp4_workspace_bytes(const si_mxfp4_experts *L, int n_tokens, int top_k) {
+  return ffn_mx_shape_ok(L, n_tokens, top_k) ? ffn_mx_geom(*L, n_tokens, top_k).bytes : 0;
+}
+
+extern "C" si_status si_moe_ffn_mxfp4(const si_mxfp4_experts *L, int n_tokens, int top_k, const void *x,
+                                      const int32_t *topk_ids, const float *topk_w, void *routed_out,
+                                      void *workspace, size_t workspace_bytes, void *stream) {
+  if (!ffn_mx_shape_ok(L, n_tokens, top_k) || !x || !topk_ids || !topk_w || !routed_out) return SI_ERR_INVALID_ARG;
+  const void *ws[6] = {L->gate_codes, L->gate_scales, L->up_codes, L->up_scales, L->down_codes, L->down_scales};
+  for (const void *w : ws)
+    if (!w || !aligned16(w)) return SI_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(routed_out) || (reinterpret_cast<uintptr_t>(topk_ids) & 3u) ||
+      (reinterpret_cast<uintptr_t>(topk_w) & 3u))
+    return SI_ERR_INVALID_ARG;
+  const FfnMxGeom g = ffn_mx_geom(*L, n_tokens, top_k);
+  if (!workspace || !aligned256(workspace) || workspace_bytes < g.bytes) return SI_ERR_WORKSPACE;
+  if (g.rows > 0x7FFFFFFF) return SI_ERR_UNSUPPORTED;
+  uint8_t *base = static_cast<uint8_t *>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int H = L->hidden, I = L->inter, E = L->n_experts;
+
+  MmParams gu{}, dn{};
+  if (!codes_map(&gu.a0, L->gate_codes, E, I, H, 128) || !codes_map(&gu.a1, L->up_codes, E, I, H, 128) ||
+      !codes_map(&gu.b, base + g.off_xc, 1, g.rows, H, g.nt) || !codes_map(&dn.a0, L->down_codes, E, H, I, 128) ||
+      !codes_map(&dn.b, base + g.off_hc, 1, g.rows, I, g.nt))
+    return SI_ERR_CUDA;
+
+  SortArgs so{};
+  so.ids = topk_ids;
+  so.pairs = g.pairs;
+  so.n_experts = E;
+  so.position = reinterpret_cast<int32_t *>(base + g.off_position);
+  so.tile_rows = g.nt;
+  so.tile_expert = reinterpret_cast<int32_t *>(base + g.off_expert);
+  so.tile_count = reinterpret_cast<int32_t *>(base + g.off_count);
+  so.n_tiles = reinterpret_cast<int32_t *>(base + g.off_n);
+  cudaError_t e = sort_launch(so, s);
+  if (e != cudaSuccess) return SI_ERR_CUDA;
+
+  ScatterArgs sc{static_cast<const __nv_bfloat16 *>(x), top_k, H, g.kt_x, g.nt, so.position, base + g.off_xc,
+                 base + g.off_xs};
+  e = launch_pdl(quantize_scatter_kernel, dim3(n_tokens), dim3(256), 0, s, sc);
+  if (e != cudaSuccess) return SI_ERR_CUDA;
+
+  gu.sa0 = static_cast<const uint8_t *>(L->gate_scales);
+  gu.sa1 = static_cast<const uint8_t *>(L->up_scales);
+  gu.sb = base + g.off_xs;
+  gu.rows = I;
+  gu.row_tiles = gu.n_rt = (I + 127) / 128;
+  gu.K = H;
+  gu.kt = g.kt_x;
+  gu.tile_expert = so.tile_expert;
+  gu.tile_count = so.tile_count;
+  gu.n_tiles = so.n_tiles;
+  gu.h_codes = base + g.off_hc;
+  gu.h_scales = base + g.off_hs;
+  gu.h_kt = g.kt_h;
+  gu.status = reinterpret_cast<uint32_t *>(base);
+  e = mm_launch(kMmGateUp, 2, g.nt, gu, g.max_tiles * gu.n_rt, s);
+  if (e != cudaSuccess) return SI_ERR_CUDA;
+
+  const int ma = g.nt == 128 ? 2 : 1;
+  dn.a1 = dn.a0;
+  dn.sa0 = dn.sa1 = static_cast<const uint8_t *>(L->down_scales);
+  dn.sb = base + g.off_hs;
+  dn.rows = H;
+  dn.row_tiles = (H + 127) / 128;
+  dn.n_rt = (dn.row_tiles + ma - 1) / ma;
+  dn.K = I;
+  dn.kt = g.kt_h;
+  dn.tile_expert = so.tile_expert;
+  dn.tile_count = so.tile_count;
+  dn.n_tiles = so.n_tiles;
+  dn.out = base + g.off_y;
+  dn.ld = H;
+  dn.out_type = SI_BF16;
+  dn.status = reinterpret_cast<uint32_t *>(base);
+  e = mm_launch(kMmPlain, ma, g.nt, dn, g.max_tiles * dn.n_rt, s);
+  if (e != cudaSuccess) return SI_ERR_CUDA;
+  return cuda_status(combine_launch(base + g.off_y, g.rows, n_tokens, top_k, H, so.position, topk_w, routed_out, s));
+}
