@@ -452,7 +452,9 @@ si_status si_dequantize_mxfp4(const void *codes, const void *scales, int64_t n_m
  *   a     [m][k], w [n][k]; m, n >= 1, k a multiple of 32, <= 2^20
  *   out   device [m] rows of n values (SI_BF16, SI_F16 or SI_F32), ld_out >= n
  *         values apart; the values between them are left as they are
- *   workspace  si_mxfp4_matmul_workspace_bytes(m, n, k) bytes, zeroed once
+ *   workspace  si_mxfp4_matmul_workspace_bytes(m, n, k) bytes, zeroed once, or NULL:
+ *         it holds the status word alone, and without it a wait that ran out on
+ *         the device is not reported
  */
 size_t si_mxfp4_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k);
 si_status si_mxfp4_matmul(const void *a_codes, const void *a_scales, int64_t m, const void *w_codes,

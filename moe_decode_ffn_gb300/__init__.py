@@ -9,8 +9,9 @@ Names follow the C ABI in ``include/si_moe.h``.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
+import inspect
 import os
 
 import torch
@@ -550,42 +551,67 @@ def si_requant_q4_k(src: torch.Tensor, src_type: str, rows: int, cols: int,
 # ----------------------------------------------------------------------------
 
 _TYPES = {torch.float32: SI_F32, torch.float16: SI_F16, torch.bfloat16: SI_BF16}
+_Tensor, _empty = torch.Tensor, torch.empty
 
 
 def _type(t: torch.Tensor, name: str) -> int:
-    if t.dtype not in _TYPES:
+    ty = _TYPES.get(t.dtype)
+    if ty is None:
         raise ValueError(f"{name} has dtype {t.dtype}, expected float32, float16 or bfloat16")
-    return _TYPES[t.dtype]
+    return ty
 
 
-def _scope(stream, *tensors):
-    """(context, stream handle) of a call on ``tensors``: inside the context
-    their device is current and allocations belong to the call's stream, so an
-    output or a temporary workspace is not handed out again while the kernels
-    run. Inputs are marked as used by a stream given by the caller."""
-    dev = tensors[0].device
-    if dev.type != "cuda":
-        raise ValueError("expected CUDA tensors")
-    for t in tensors[1:]:
-        if t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
-    if stream is None:
-        handle = torch.cuda.current_stream(dev).cuda_stream
-        if dev.index == torch.cuda.current_device():
-            return contextlib.nullcontext(), handle
-        return torch.cuda.device(dev), handle
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
-    for t in tensors:
-        t.record_stream(stream)
-    return torch.cuda.stream(stream), stream.cuda_stream
+def _on_stream(call):
+    """Wraps ``call(handle, *tensors and sizes)`` into a function with a
+    ``stream`` argument: all tensors have to be on one CUDA device, which is
+    current while the call runs, and what it allocates belongs to the call's
+    stream, so an output or a temporary workspace is not handed out again while
+    the kernels run. Inputs are marked as used by a stream given by the caller.
+
+    A decode step makes these calls back to back, and the host time of one is
+    longer than its kernels: the usual case (the current stream of the current
+    device) takes no context manager and builds no stream object."""
+    @functools.wraps(call)
+    def run(*args, stream=None, **kw):
+        dev = -1
+        for t in (*args, *kw.values()) if kw else args:
+            if isinstance(t, _Tensor):
+                d = t.get_device()
+                if d < 0:
+                    raise ValueError("expected CUDA tensors")
+                if d != dev:
+                    if dev >= 0:
+                        raise ValueError(f"tensors on cuda:{dev} and cuda:{d}")
+                    dev = d
+        if dev < 0:
+            raise ValueError("expected CUDA tensors")
+        if stream is None:
+            if dev == torch._C._cuda_getDevice():
+                return call(torch._C._cuda_getCurrentRawStream(dev), *args, **kw)
+            with torch.cuda.device(dev):
+                return call(torch._C._cuda_getCurrentRawStream(dev), *args, **kw)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        if stream.device.index != dev:
+            raise ValueError(f"tensors on cuda:{dev}, stream on {stream.device}")
+        for t in (*args, *kw.values()):
+            if isinstance(t, _Tensor):
+                t.record_stream(stream)
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream, *args, **kw)
+
+    doc = inspect.signature(call)
+    keep = [p for n, p in doc.parameters.items() if n != "handle"]
+    run.__signature__ = doc.replace(parameters=keep + [inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY,
+                                                                         default=None)])
+    return run
 
 
 def _scratch(nbytes: int, device) -> torch.Tensor:
     """A workspace for one call: only its status header has to be zero."""
     if nbytes <= 0:
         raise ValueError("workspace size query returned 0 (invalid shapes)")
-    ws = torch.empty(int(nbytes), dtype=torch.uint8, device=device)
+    ws = _empty((int(nbytes),), dtype=torch.uint8, device=device)
     ws[:256].zero_()
     return ws
 
@@ -595,67 +621,71 @@ def mxfp4_scale_shape(rows: int, cols: int) -> tuple:
     return (-(-rows // 128), -(-cols // 128), 512)
 
 
-def _mxfp4(codes, scales, name: str, dims=None):
+def _mxfp4(codes, scales, name: str, dims: int):
     """(matrices, rows, cols) of an MXFP4 pair after checking that they belong together."""
-    if not isinstance(codes, torch.Tensor) or codes.dim() not in ((2, 3) if dims is None else (dims,)):
+    if not isinstance(codes, _Tensor) or codes.dim() != dims:
         raise ValueError(f"{name} codes must be uint8 [{'n, ' if dims == 3 else ''}rows, cols / 2]")
-    n = 1 if codes.dim() == 2 else codes.shape[0]
-    rows, cols = codes.shape[-2], codes.shape[-1] * 2
-    _shaped(codes, f"{name} codes", n * rows * cols // 2, _U8)
-    per = int(library().si_mxfp4_scale_bytes(rows, cols))
-    if cols == 0 or (per == 0 and rows > 0):
+    if dims == 2:
+        n, (rows, cols) = 1, codes.shape
+    else:
+        n, rows, cols = codes.shape
+    cols *= 2
+    if cols == 0 or cols % 32:
         raise ValueError(f"{name} has {cols} columns, expected a multiple of 32")
-    _shaped(scales, f"{name} scales", n * per, _U8)
+    _shaped(codes, f"{name} codes", n * rows * cols // 2, _U8)
+    _shaped(scales, f"{name} scales", n * -(-rows // 128) * -(-cols // 128) * 512, _U8)
     return n, rows, cols
 
 
 def _strides(t: torch.Tensor, name: str):
     """(matrices, rows, cols, row stride, matrix stride) of a 2-D or 3-D tensor with contiguous columns."""
-    if t.dim() not in (2, 3):
+    if t.dim() == 2:
+        n, (rows, cols), mat, (row, col) = 1, t.shape, 0, t.stride()
+    elif t.dim() == 3:
+        (n, rows, cols), (mat, row, col) = t.shape, t.stride()
+    else:
         raise ValueError(f"{name} must be [rows, cols] or [n, rows, cols]")
-    n, rows, cols = (1,) * (3 - t.dim()) + tuple(t.shape)
-    if cols > 1 and t.stride(-1) != 1:
+    if col != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous columns")
-    # a size of one has no stride to speak of
-    row = t.stride(-2) if rows > 1 else cols
-    return n, rows, cols, row, t.stride(0) if n > 1 else max(rows - 1, 0) * row + cols
+    return n, rows, cols, row if rows > 1 else cols, mat if n > 1 else 0
 
 
-def si_quantize_mxfp4(x: torch.Tensor, codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
-                      stream=None):
+@_on_stream
+def si_quantize_mxfp4(handle, x: torch.Tensor, codes: torch.Tensor | None = None,
+                      scales: torch.Tensor | None = None):
     """x [rows, cols] or [n, rows, cols] (fp32, fp16, bf16; rows and matrices at
     any stride) -> (codes uint8 [.., rows, cols / 2], scale tiles uint8
     [.., ceil(rows / 128), ceil(cols / 128), 512])."""
     n, rows, cols, row, mat = _strides(x, "x")
     if cols == 0 or cols % 32:
         raise ValueError(f"x has {cols} columns, expected a multiple of 32")
-    tiles = mxfp4_scale_shape(rows, cols)
-    ctx, handle = _scope(stream, x, *(t for t in (codes, scales) if t is not None))
-    with ctx:
-        if codes is None:
-            codes = torch.empty(*x.shape[:-1], cols // 2, dtype=torch.uint8, device=x.device)
-        if scales is None:
-            scales = torch.empty(*x.shape[:-2], *tiles, dtype=torch.uint8, device=x.device)
-        _check(library().si_quantize_mxfp4(
-            x.data_ptr(), _type(x, "x"), n, rows, cols, row, mat,
-            _shaped(codes, "codes", n * rows * cols // 2, _U8),
-            _shaped(scales, "scales", n * tiles[0] * tiles[1] * 512, _U8), handle), "si_quantize_mxfp4")
+    tiles, many = mxfp4_scale_shape(rows, cols), x.dim() == 3
+    if codes is None:
+        codes = _empty((n, rows, cols // 2) if many else (rows, cols // 2), dtype=torch.uint8, device=x.device)
+    else:
+        _shaped(codes, "codes", n * rows * cols // 2, _U8)
+    if scales is None:
+        scales = _empty((n, *tiles) if many else tiles, dtype=torch.uint8, device=x.device)
+    else:
+        _shaped(scales, "scales", n * tiles[0] * tiles[1] * 512, _U8)
+    _check(library().si_quantize_mxfp4(x.data_ptr(), _type(x, "x"), n, rows, cols, row, mat, codes.data_ptr(),
+                                       scales.data_ptr(), handle), "si_quantize_mxfp4")
     return codes, scales
 
 
-def si_dequantize_mxfp4(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.bfloat16,
-                        out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+@_on_stream
+def si_dequantize_mxfp4(handle, codes: torch.Tensor, scales: torch.Tensor, dtype=torch.bfloat16,
+                        out: torch.Tensor | None = None) -> torch.Tensor:
     """The values of an MXFP4 matrix (or n of them) as ``dtype`` or into ``out``."""
-    n, rows, cols = _mxfp4(codes, scales, "x")
-    ctx, handle = _scope(stream, codes, scales, *(() if out is None else (out,)))
-    with ctx:
-        if out is None:
-            out = torch.empty(*codes.shape[:-1], cols, dtype=dtype, device=codes.device)
-        if tuple(out.shape) != (*codes.shape[:-1], cols):
-            raise ValueError(f"out has shape {tuple(out.shape)}, expected {(*codes.shape[:-1], cols)}")
-        _, _, _, row, mat = _strides(out, "out")
-        _check(library().si_dequantize_mxfp4(codes.data_ptr(), scales.data_ptr(), n, rows, cols, out.data_ptr(),
-                                             _type(out, "out"), row, mat, handle), "si_dequantize_mxfp4")
+    n, rows, cols = _mxfp4(codes, scales, "x", 3 if codes.dim() == 3 else 2)
+    shape = (n, rows, cols) if codes.dim() == 3 else (rows, cols)
+    if out is None:
+        out = _empty(shape, dtype=dtype, device=codes.device)
+    elif out.shape != shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {shape}")
+    _, _, _, row, mat = _strides(out, "out")
+    _check(library().si_dequantize_mxfp4(codes.data_ptr(), scales.data_ptr(), n, rows, cols, out.data_ptr(),
+                                         _type(out, "out"), row, mat, handle), "si_dequantize_mxfp4")
     return out
 
 
@@ -663,42 +693,42 @@ def mxfp4_matmul_workspace_bytes(m: int, n: int, k: int) -> int:
     return int(library().si_mxfp4_matmul_workspace_bytes(m, n, k))
 
 
-def si_mxfp4_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
-                    dtype=torch.bfloat16, out: torch.Tensor | None = None, ws: torch.Tensor | None = None,
-                    stream=None) -> torch.Tensor:
-    """a [m, k] and w [n, k] in MXFP4 -> a w^T [m, n] in ``dtype`` or into ``out`` (any row stride)."""
+@_on_stream
+def si_mxfp4_matmul(handle, a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tensor,
+                    w_scales: torch.Tensor, dtype=torch.bfloat16, out: torch.Tensor | None = None,
+                    ws: torch.Tensor | None = None) -> torch.Tensor:
+    """a [m, k] and w [n, k] in MXFP4 -> a w^T [m, n] in ``dtype`` or into ``out``
+    (any row stride). ``ws`` receives the device status; without it an error on
+    the device is not reported."""
     _, m, k = _mxfp4(a_codes, a_scales, "a", 2)
     _, n, k2 = _mxfp4(w_codes, w_scales, "w", 2)
     if k != k2:
         raise ValueError(f"a has {k} columns, w has {k2}")
-    given = tuple(t for t in (out, ws) if t is not None)
-    ctx, handle = _scope(stream, a_codes, a_scales, w_codes, w_scales, *given)
-    with ctx:
-        if out is None:
-            out = torch.empty(m, n, dtype=dtype, device=a_codes.device)
-        if tuple(out.shape) != (m, n):
-            raise ValueError(f"out has shape {tuple(out.shape)}, expected {(m, n)}")
-        _, _, _, ld, _ = _strides(out, "out")
-        if ws is None:
-            ws = _scratch(mxfp4_matmul_workspace_bytes(m, n, k), a_codes.device)
-        _check(library().si_mxfp4_matmul(
-            a_codes.data_ptr(), a_scales.data_ptr(), m, w_codes.data_ptr(), w_scales.data_ptr(), n, k,
-            out.data_ptr(), _type(out, "out"), ld, _cuda(ws, "ws"), ws.numel(), handle), "si_mxfp4_matmul")
+    if out is None:
+        out, ld = _empty((m, n), dtype=dtype, device=a_codes.device), n
+    elif out.shape != (m, n):
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {(m, n)}")
+    else:
+        ld = _strides(out, "out")[3]
+    _check(library().si_mxfp4_matmul(
+        a_codes.data_ptr(), a_scales.data_ptr(), m, w_codes.data_ptr(), w_scales.data_ptr(), n, k,
+        out.data_ptr(), _type(out, "out"), ld, None if ws is None else _cuda(ws, "ws"),
+        0 if ws is None else ws.numel(), handle), "si_mxfp4_matmul")
     return out
 
 
-def si_moe_sort(ids: torch.Tensor, n_experts: int, stream=None):
+@_on_stream
+def si_moe_sort(handle, ids: torch.Tensor, n_experts: int):
     """ids int32 [T, k] -> (order int32 [T * k], position int32 [T, k], offsets
     int32 [n_experts + 1]); pairs whose id is outside [0, n_experts) are dropped
     (position -1)."""
     T, k = ids.shape
-    ctx, handle = _scope(stream, ids)
-    with ctx:
-        order = torch.empty(T * k, dtype=torch.int32, device=ids.device)
-        position = torch.empty(T, k, dtype=torch.int32, device=ids.device)
-        offsets = torch.empty(max(n_experts, 0) + 1, dtype=torch.int32, device=ids.device)
-        _check(library().si_moe_sort(_shaped(ids, "ids", T * k, _I32), T, k, n_experts, order.data_ptr(),
-                                     position.data_ptr(), offsets.data_ptr(), handle), "si_moe_sort")
+    dev = ids.device
+    order = _empty((T * k,), dtype=torch.int32, device=dev)
+    position = _empty((T, k), dtype=torch.int32, device=dev)
+    offsets = _empty((max(n_experts, 0) + 1,), dtype=torch.int32, device=dev)
+    _check(library().si_moe_sort(_shaped(ids, "ids", T * k, _I32), T, k, n_experts, order.data_ptr(),
+                                 position.data_ptr(), offsets.data_ptr(), handle), "si_moe_sort")
     return order, position, offsets
 
 
@@ -709,54 +739,50 @@ def _kept(offsets: torch.Tensor) -> int:
     return _cuda(offsets, "offsets") + 4 * (offsets.numel() - 1)
 
 
-def si_moe_gather(x: torch.Tensor, position: torch.Tensor, offsets: torch.Tensor, stream=None) -> torch.Tensor:
+@_on_stream
+def si_moe_gather(handle, x: torch.Tensor, position: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
     """xs[position[t, r]] = x[t]: x [T, H] -> [T * k, H], zero rows behind the kept pairs."""
     (T, H), k = x.shape, position.shape[-1]
-    ctx, handle = _scope(stream, x, position, offsets)
-    with ctx:
-        xs = torch.empty(T * k, H, dtype=x.dtype, device=x.device)
-        _check(library().si_moe_gather(_cuda(x, "x"), _type(x, "x"), T, k, H,
-                                       _shaped(position, "position", T * k, _I32), _kept(offsets), xs.data_ptr(),
-                                       handle), "si_moe_gather")
+    xs = _empty((T * k, H), dtype=x.dtype, device=x.device)
+    _check(library().si_moe_gather(_cuda(x, "x"), _type(x, "x"), T, k, H,
+                                   _shaped(position, "position", T * k, _I32), _kept(offsets), xs.data_ptr(),
+                                   handle), "si_moe_gather")
     return xs
 
 
-def si_moe_gather_backward(gxs: torch.Tensor, position: torch.Tensor, stream=None) -> torch.Tensor:
+@_on_stream
+def si_moe_gather_backward(handle, gxs: torch.Tensor, position: torch.Tensor) -> torch.Tensor:
     """gx[t] = sum_r gxs[position[t, r]]: gxs [T * k, H] -> [T, H]."""
     (T, k), H = position.shape, gxs.shape[-1]
-    ctx, handle = _scope(stream, gxs, position)
-    with ctx:
-        gx = torch.empty(T, H, dtype=gxs.dtype, device=gxs.device)
-        _check(library().si_moe_gather_backward(_shaped(gxs, "gxs", T * k * H, (gxs.dtype,)), _type(gxs, "gxs"),
-                                                T, k, H, _shaped(position, "position", T * k, _I32),
-                                                gx.data_ptr(), handle), "si_moe_gather_backward")
+    gx = _empty((T, H), dtype=gxs.dtype, device=gxs.device)
+    _check(library().si_moe_gather_backward(_shaped(gxs, "gxs", T * k * H, (gxs.dtype,)), _type(gxs, "gxs"),
+                                            T, k, H, _shaped(position, "position", T * k, _I32),
+                                            gx.data_ptr(), handle), "si_moe_gather_backward")
     return gx
 
 
-def si_moe_combine(ys: torch.Tensor, position: torch.Tensor, w: torch.Tensor, stream=None) -> torch.Tensor:
+@_on_stream
+def si_moe_combine(handle, ys: torch.Tensor, position: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
     """y[t] = sum_r w[t, r] ys[position[t, r]]: ys [T * k, H], w fp32 [T, k] -> [T, H]."""
     (T, k), H = position.shape, ys.shape[-1]
-    ctx, handle = _scope(stream, ys, position, w)
-    with ctx:
-        y = torch.empty(T, H, dtype=ys.dtype, device=ys.device)
-        _check(library().si_moe_combine(_shaped(ys, "ys", T * k * H, (ys.dtype,)), _type(ys, "ys"), T, k, H,
-                                        _shaped(position, "position", T * k, _I32), _shaped(w, "w", T * k, _F32),
-                                        y.data_ptr(), handle), "si_moe_combine")
+    y = _empty((T, H), dtype=ys.dtype, device=ys.device)
+    _check(library().si_moe_combine(_shaped(ys, "ys", T * k * H, (ys.dtype,)), _type(ys, "ys"), T, k, H,
+                                    _shaped(position, "position", T * k, _I32), _shaped(w, "w", T * k, _F32),
+                                    y.data_ptr(), handle), "si_moe_combine")
     return y
 
 
-def si_moe_combine_backward(gy: torch.Tensor, ys: torch.Tensor, position: torch.Tensor, offsets: torch.Tensor,
-                            w: torch.Tensor, stream=None):
+@_on_stream
+def si_moe_combine_backward(handle, gy: torch.Tensor, ys: torch.Tensor, position: torch.Tensor,
+                            offsets: torch.Tensor, w: torch.Tensor):
     """gy [T, H], ys [T * k, H] -> (gys [T * k, H], gw fp32 [T, k])."""
     (T, k), H = position.shape, gy.shape[-1]
-    ctx, handle = _scope(stream, gy, ys, position, offsets, w)
-    with ctx:
-        gys = torch.empty(T * k, H, dtype=gy.dtype, device=gy.device)
-        gw = torch.empty(T, k, dtype=torch.float32, device=gy.device)
-        _check(library().si_moe_combine_backward(
-            _shaped(gy, "gy", T * H, (gy.dtype,)), _shaped(ys, "ys", T * k * H, (gy.dtype,)), _type(gy, "gy"), T, k, H,
-            _shaped(position, "position", T * k, _I32), _kept(offsets), _shaped(w, "w", T * k, _F32),
-            gys.data_ptr(), gw.data_ptr(), handle), "si_moe_combine_backward")
+    gys = _empty((T * k, H), dtype=gy.dtype, device=gy.device)
+    gw = _empty((T, k), dtype=torch.float32, device=gy.device)
+    _check(library().si_moe_combine_backward(
+        _shaped(gy, "gy", T * H, (gy.dtype,)), _shaped(ys, "ys", T * k * H, (gy.dtype,)), _type(gy, "gy"), T, k, H,
+        _shaped(position, "position", T * k, _I32), _kept(offsets), _shaped(w, "w", T * k, _F32),
+        gys.data_ptr(), gw.data_ptr(), handle), "si_moe_combine_backward")
     return gys, gw
 
 
@@ -777,36 +803,34 @@ class Mxfp4Experts:
             raise ValueError("gate, up and down on different devices")
         self.hidden, self.inter, self.n_experts = H, I, E
         self.c = SiMxfp4Experts(H, I, E, *(t.data_ptr() for t in (*gate, *up, *down)))
+        self.ref = ctypes.byref(self.c)
 
     @classmethod
     def quantize(cls, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, stream=None):
         """From weights gate, up [E, I, H] and down [E, H, I] in fp32, fp16 or bf16."""
         return cls(*(si_quantize_mxfp4(t, stream=stream) for t in (gate, up, down)))
 
-    @property
-    def ref(self):
-        return ctypes.byref(self.c)
-
 
 def ffn_mxfp4_workspace_bytes(experts: Mxfp4Experts, n_tokens: int, top_k: int) -> int:
     return int(library().si_moe_ffn_mxfp4_workspace_bytes(experts.ref, n_tokens, top_k))
 
 
-def si_moe_ffn_mxfp4(experts: Mxfp4Experts, x: torch.Tensor, ids: torch.Tensor, w: torch.Tensor,
-                     ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+@_on_stream
+def si_moe_ffn_mxfp4(handle, experts: Mxfp4Experts, x: torch.Tensor, ids: torch.Tensor, w: torch.Tensor,
+                     ws: torch.Tensor | None = None) -> torch.Tensor:
     """T tokens with per-token routing: x bf16 [T, H], ids int32 [T, k], w fp32
     [T, k] -> routed bf16 [T, H]."""
     T, k = ids.shape
-    H = experts.hidden
-    ctx, handle = _scope(stream, x, ids, w, experts.gate[0], *(() if ws is None else (ws,)))
-    with ctx:
-        if ws is None:
-            ws = _scratch(ffn_mxfp4_workspace_bytes(experts, T, k), x.device)
-        routed = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
-        _check(library().si_moe_ffn_mxfp4(
-            experts.ref, T, k, _shaped(x, "x", T * H, _BF16), _shaped(ids, "ids", T * k, _I32),
-            _shaped(w, "w", T * k, _F32), routed.data_ptr(), _cuda(ws, "ws"), ws.numel(), handle),
-            "si_moe_ffn_mxfp4")
+    H, dev = experts.hidden, x.device
+    if experts.device != dev:
+        raise ValueError(f"tensors on {dev}, experts on {experts.device}")
+    if ws is None:
+        ws = _scratch(ffn_mxfp4_workspace_bytes(experts, T, k), dev)
+    routed = _empty((T, H), dtype=torch.bfloat16, device=dev)
+    _check(library().si_moe_ffn_mxfp4(
+        experts.ref, T, k, _shaped(x, "x", T * H, _BF16), _shaped(ids, "ids", T * k, _I32),
+        _shaped(w, "w", T * k, _F32), routed.data_ptr(), _cuda(ws, "ws"), ws.numel(), handle),
+        "si_moe_ffn_mxfp4")
     return routed
 
 

@@ -10,11 +10,14 @@
 // holds one output feature. Products of two E2M1 values are exact and the
 // accumulators fp32.
 //
-// A block of 192 threads: warp 0 keeps a ring of stages full (256 columns of
+// A block of 320 threads: warp 0 keeps a ring of stages full (256 columns of
 // the codes by tensor TMA in the 128-byte swizzle, their scale tiles by plain
 // bulk copies), one thread of warp 1 moves the scales into tensor memory
-// (tcgen05.cp) and issues the MMAs, warps 2..5 read the accumulators and write
-// the outputs. Blocks are persistent: tile i of block b is b + i * gridDim.
+// (tcgen05.cp) and issues the MMAs, warps 2..9 read the accumulators and write
+// the outputs (two warps per 32 lanes of tensor memory, each half of the
+// tokens). Blocks are persistent: tile i of block b is b + i * gridDim. The
+// accumulators are a ring too, so that the MMAs of a tile run beside the
+// epilogue of the one before.
 #include <cuda.h>
 
 #include <algorithm>
@@ -26,7 +29,9 @@
 
 namespace si {
 
-constexpr int kMmThreads = 192;
+constexpr int kMmEpiWarps = 8;
+constexpr int kMmThreads = 64 + 32 * kMmEpiWarps;
+constexpr int kMmEpiBytes = 512;       // staging of an epilogue warp: 8 tokens x 32 features of 2 bytes
 constexpr int kMmStageK = 256;         // columns of a stage: 128 bytes of codes per row
 constexpr int kMmABytes = 128 * 128;   // 128 weight rows of a stage
 
@@ -37,17 +42,21 @@ template <int MA, int NT> struct MmCfg {
   static constexpr int kBBytes = NT * 128;
   static constexpr int kSfBytes = 2 * kMxTileBytes;               // per operand tile and stage
   static constexpr int kStage = MA * kMmABytes + kBBytes + (MA + 1) * kSfBytes;
-  static constexpr int kMaxSmem = 227 * 1024 - 2048;              // less alignment and barriers
+  static constexpr int kMaxSmem = 227 * 1024 - kMmEpiWarps * kMmEpiBytes - 1536;   // less alignment and barriers
   static constexpr int kStages = kMaxSmem / kStage < 8 ? kMaxSmem / kStage : 8;
-  // tensor memory: accumulators, then the scales of every stage (a column
-  // holds 4 blocks of 32 rows, so 128 rows x 8 blocks take 8 columns)
-  static constexpr int kAcc = MA * NT;
+  // tensor memory: a ring of accumulators of NT columns (a tile takes MA of
+  // them; a third one of 128 columns lets the next tile start when the first
+  // half of this one is written), then the scales of every stage (a column
+  // holds 4 blocks of 32 rows: 128 rows x 8 blocks take 8 columns)
   static constexpr int kSfCols = 8 * (MA + 1);
-  static constexpr int kBufs = 2 * kAcc + kStages * kSfCols <= 512 ? 2 : 1;
-  static constexpr int kUsed = kBufs * kAcc + kStages * kSfCols;
+  static constexpr int kFit = (512 - kStages * kSfCols) / NT;
+  static constexpr int kAccs = kFit < 2 * MA ? kFit : 2 * MA;
+  static constexpr int kUsed = kAccs * NT + kStages * kSfCols;
   static constexpr int kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
-  static_assert(kUsed <= 512, "tensor memory has 512 columns");
-  static constexpr int kSmem = kStages * kStage + 1024 + 512;
+  static_assert(kAccs >= MA && kUsed <= 512, "tensor memory has 512 columns");
+  static constexpr int kBars = 2 * kStages + 2 * kAccs + 1;
+  static constexpr int kSmem = kStages * kStage + kMmEpiWarps * kMmEpiBytes + 1024 + 512;
+  static_assert(8 * kBars + 4 <= 512, "barriers");
 };
 
 struct MmParams {
@@ -62,11 +71,11 @@ struct MmParams {
   // plain: out[token][feature]
   void *out;
   int64_t ld;
-  int out_type;
   // gate/up: the MXFP4 rows of h
   uint8_t *h_codes, *h_scales;
   int h_kt;
   uint32_t *status;
+  int early;                           // the tile list and the weights are complete before the wait
 };
 
 struct MmTile {
@@ -148,29 +157,73 @@ SI_DEV void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "
 
 // ---- epilogues ---------------------------------------------------------------
 
-SI_DEV void mm_store(const MmParams &p, int64_t at, float v) {
-  if (p.out_type == SI_BF16) static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(v);
-  else if (p.out_type == SI_F32) static_cast<float *>(p.out)[at] = v;
-  else static_cast<__half *>(p.out)[at] = __float2half_rn(v);
+// Outputs whose rows start on 16-byte boundaries leave in 16-byte words (2-byte
+// types: VEC); other rows value by value, lane = feature.
+enum MmOut { kMmBf16, kMmF16, kMmF32, kMmBf16Vec, kMmF16Vec };
+
+template <int OUT> SI_DEV void mm_store(void *out, int64_t at, float v) {
+  if constexpr (OUT == kMmBf16) static_cast<__nv_bfloat16 *>(out)[at] = __float2bfloat16_rn(v);
+  else if constexpr (OUT == kMmF32) static_cast<float *>(out)[at] = v;
+  else static_cast<__half *>(out)[at] = __float2half_rn(v);
+}
+template <int OUT> SI_DEV uint32_t mm_pack(uint32_t lo, uint32_t hi) {
+  uint32_t w;
+  if constexpr (OUT == kMmBf16Vec)
+    asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(w) : "f"(__uint_as_float(lo)), "f"(__uint_as_float(hi)));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(w) : "f"(__uint_as_float(lo)), "f"(__uint_as_float(hi)));
+  return w;
+}
+// 16 lanes x 16 columns of tensor memory in the fragment order of an 8 x 8
+// matrix store: register 4c + 2h + i of lane l is row 8h + l / 4, column
+// 8c + 2 (l % 4) + i.
+SI_DEV void tmem_ld_frag(uint32_t taddr, uint32_t r[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
 }
 
-// Lane = feature; for one token the 32 lanes write consecutive values.
-template <int MA, int NT>
-SI_DEV void mm_write_plain(const MmParams &p, const MmTile &t, uint32_t acc, int q, int lane) {
-  const int64_t row0 = static_cast<int64_t>(t.tt) * NT;
+// One accumulator (128 features x count tokens) of this warp's 32 features, the
+// warp's half of the 16-token groups.
+template <int OUT>
+SI_DEV void mm_write_plain(const MmParams &p, int f0, int64_t row0, int count, uint32_t acc, int half, int lane,
+                           uint8_t *stage) {
+  if (f0 >= p.rows) return;
 #pragma unroll 1
-  for (int a = 0; a < MA; ++a) {
-    const int f = (t.rt * MA + a) * 128 + q * 32 + lane;
-    if ((t.rt * MA + a) * 128 >= p.rows) break;
-#pragma unroll 1
-    for (int j0 = 0; j0 < t.count; j0 += 16) {
-      uint32_t r[16];
-      tmem_ld16(acc + a * NT + j0, r);
+  for (int j0 = 16 * half; j0 < count; j0 += 32) {
+    if constexpr (OUT == kMmBf16Vec || OUT == kMmF16Vec) {
+      // 8 x 8 blocks transposed through shared memory: a token's 32 features
+      // are 64 bytes, its four 16-byte words permuted by the token so that
+      // neither side of the staging meets a bank twice
+      uint32_t lo[8], hi[8];
+      tmem_ld_frag(acc + j0, lo);
+      tmem_ld_frag(acc + (16u << 16) + j0, hi);
       tmem_wait_ld();
-      if (f < p.rows) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const uint32_t m0 = mm_pack<OUT>(lo[4 * c], lo[4 * c + 1]), m1 = mm_pack<OUT>(lo[4 * c + 2], lo[4 * c + 3]);
+        const uint32_t m2 = mm_pack<OUT>(hi[4 * c], hi[4 * c + 1]), m3 = mm_pack<OUT>(hi[4 * c + 2], hi[4 * c + 3]);
+        const int wj = lane & 7, wc = lane >> 3;      // this lane's row address: token wj, word wc
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                         smem_addr(stage + wj * 64 + ((wc ^ ((wj >> 1) & 3)) * 16))),
+                     "r"(m0), "r"(m1), "r"(m2), "r"(m3)
+                     : "memory");
+        __syncwarp();
+        const int rj = lane >> 2, rc = lane & 3, j = j0 + 8 * c + rj, f = f0 + 8 * rc;
+        const uint4 v = *reinterpret_cast<const uint4 *>(stage + rj * 64 + ((rc ^ ((rj >> 1) & 3)) * 16));
+        __syncwarp();
+        if (j < count && f < p.rows)                  // rows % 8 == 0: a word is whole or absent
+          *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + (row0 + j) * p.ld + f) = v;
+      }
+    } else {
+      uint32_t r[16];
+      tmem_ld16(acc + j0, r);
+      tmem_wait_ld();
+      if (f0 + lane < p.rows) {
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-          if (j0 + j < t.count) mm_store(p, (row0 + j0 + j) * p.ld + f, __uint_as_float(r[j]));
+          if (j0 + j < count) mm_store<OUT>(p.out, (row0 + j0 + j) * p.ld + f0 + lane, __uint_as_float(r[j]));
       }
     }
   }
@@ -189,17 +242,18 @@ SI_DEV uint32_t transpose_nibbles(uint32_t w, int lane) {
 // h = silu(g) u of a lane's feature for 16 tokens, then MXFP4: the 32 lanes of
 // the warp are one block of every token, so its scale is a warp maximum.
 template <int NT>
-SI_DEV void mm_write_h(const MmParams &p, const MmTile &t, uint32_t acc, int q, int lane) {
+SI_DEV void mm_write_h(const MmParams &p, const MmTile &t, uint32_t acc_g, uint32_t acc_u, int q, int half,
+                       int lane) {
   const int64_t row0 = static_cast<int64_t>(t.tt) * NT;
   const int blk = t.rt * 4 + q;                 // this warp's block of 32 features
   const bool live = blk * 32 < p.rows;          // rows % 32 == 0: the whole warp or none of it
   const size_t row_bytes = static_cast<size_t>(p.rows) / 2;
   uint8_t *sf = p.h_scales + (static_cast<size_t>(t.tt) * p.h_kt + t.rt) * kMxTileBytes;
 #pragma unroll 1
-  for (int j0 = 0; j0 < t.count; j0 += 16) {
+  for (int j0 = 16 * half; j0 < t.count; j0 += 32) {
     uint32_t g[16], u[16];
-    tmem_ld16(acc + j0, g);
-    tmem_ld16(acc + NT + j0, u);
+    tmem_ld16(acc_g + j0, g);
+    tmem_ld16(acc_u + j0, u);
     tmem_wait_ld();
 #pragma unroll
     for (int h8 = 0; h8 < 16; h8 += 8) {
@@ -228,27 +282,67 @@ SI_DEV void mm_write_h(const MmParams &p, const MmTile &t, uint32_t acc, int q, 
 
 // ---- the kernel ----------------------------------------------------------------
 
-template <int MODE, int MA, int NT>
+// The tiles of weight rows that tile t of the list reads, and of them the ones
+// inside the matrix.
+template <int MODE, int MA> SI_DEV int mm_operands(const MmParams &p, const MmTile &t) {
+  return MODE == kMmGateUp || MA == 1 || t.rt * MA * 128 + 128 < p.rows ? MA : 1;
+}
+
+template <int MODE, int MA, int NT, int OUT>
 __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_mm_kernel(const __grid_constant__ MmParams p) {
   using C = MmCfg<MA, NT>;
-  constexpr int S = C::kStages, BUFS = C::kBufs;
+  constexpr int S = C::kStages, U = C::kAccs;
   extern __shared__ uint8_t mm_smem[];
   uint8_t *base = mm_smem + ((1024u - (smem_addr(mm_smem) & 1023u)) & 1023u);
-  uint64_t *full = reinterpret_cast<uint64_t *>(base + S * C::kStage);
-  uint64_t *empty = full + S, *acc_full = empty + S, *acc_empty = acc_full + BUFS, *drain = acc_empty + BUFS;
+  uint8_t *staging = base + S * C::kStage;
+  uint64_t *full = reinterpret_cast<uint64_t *>(staging + kMmEpiWarps * kMmEpiBytes);
+  uint64_t *empty = full + S, *acc_full = empty + S, *acc_empty = acc_full + U, *drain = acc_empty + U;
   uint32_t *s_taddr = reinterpret_cast<uint32_t *>(drain + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n_ks = (p.K + kMmStageK - 1) / kMmStageK;
+
+  // the copies of stage ks of a tile: the weights and the tokens
+  auto load_weights = [&](const MmTile &t, int na, int ks, int s) {
+    uint8_t *st = base + s * C::kStage, *sf = st + MA * kMmABytes + C::kBBytes;
+    const uint32_t sfb = min(2, p.kt - 2 * ks) * kMxTileBytes;
+    mbar_arrive_expect_tx(full + s, na * kMmABytes + C::kBBytes + (na + 1) * sfb);
+    const int row0 = MODE == kMmGateUp ? t.rt * 128 : t.rt * MA * 128;
+#pragma unroll
+    for (int a = 0; a < MA; ++a) {
+      if (a >= na) break;
+      const bool up = MODE == kMmGateUp && a == 1;
+      const int r = MODE == kMmGateUp ? row0 : row0 + a * 128;
+      tma_load3(st + a * kMmABytes, up ? &p.a1 : &p.a0, ks * 128, r, t.mat, full + s);
+      bulk_g2s(sf + a * C::kSfBytes,
+               (up ? p.sa1 : p.sa0) +
+                   (static_cast<size_t>(t.mat * p.row_tiles + r / 128) * p.kt + 2 * ks) * kMxTileBytes,
+               sfb, full + s);
+    }
+  };
+  auto load_tokens = [&](const MmTile &t, int ks, int s) {
+    uint8_t *sb = base + s * C::kStage + MA * kMmABytes;
+    tma_load3(sb, &p.b, ks * 128, t.tt * NT, 0, full + s);
+    bulk_g2s(sb + C::kBBytes + MA * C::kSfBytes, p.sb + (static_cast<size_t>(t.tt) * p.kt + 2 * ks) * kMxTileBytes,
+             min(2, p.kt - 2 * ks) * kMxTileBytes, full + s);
+  };
+
+  int ahead = 0;                     // stages whose weights were requested before the wait
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(full + i, 1);
       mbar_init(empty + i, 1);
     }
-    for (int i = 0; i < BUFS; ++i) {
+    for (int i = 0; i < U; ++i) {
       mbar_init(acc_full + i, 1);
-      mbar_init(acc_empty + i, 4);
+      mbar_init(acc_empty + i, kMmEpiWarps);
     }
     mbar_init(drain, 1);
     fence_mbar_init();
+    if (p.early && static_cast<int>(blockIdx.x) < mm_total(p, NT)) {
+      const MmTile t = mm_tile(p, blockIdx.x, NT);
+      const int na = mm_operands<MODE, MA>(p, t);
+      for (; ahead < S && ahead < n_ks; ++ahead) load_weights(t, na, ahead, ahead);
+    }
   }
   grid_dep_wait();
   if (warp == 1) {
@@ -262,7 +356,6 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_mm_kernel(const __grid_co
   grid_dep_launch();
   const uint32_t tmem = *s_taddr;
   const int total = mm_total(p, NT);
-  const int n_ks = (p.K + kMmStageK - 1) / kMmStageK;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -270,34 +363,17 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_mm_kernel(const __grid_co
       bool ok = true;
       for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
         const MmTile t = mm_tile(p, w, NT);
-        const int row0 = MODE == kMmGateUp ? t.rt * 128 : t.rt * MA * 128;
-        const int na = MODE == kMmGateUp || MA == 1 || row0 + 128 < p.rows ? MA : 1;
-        const int sr0 = t.mat * p.row_tiles + row0 / 128;
+        const int na = mm_operands<MODE, MA>(p, t);
         for (int ks = 0; ks < n_ks; ++ks, ++it) {
           const int s = it % S;
-          if (!mbar_wait_bounded(empty + s, ((it / S) & 1) ^ 1, p.status)) {
-            ok = false;
-            break;
+          if (static_cast<int>(it) >= ahead) {
+            if (!mbar_wait_bounded(empty + s, ((it / S) & 1) ^ 1, p.status)) {
+              ok = false;
+              break;
+            }
+            load_weights(t, na, ks, s);
           }
-          const int nkt = min(2, p.kt - 2 * ks);
-          uint8_t *st = base + s * C::kStage;
-          uint8_t *sb = st + MA * kMmABytes, *sf = sb + C::kBBytes;
-          const uint32_t sfb = nkt * kMxTileBytes;
-          mbar_arrive_expect_tx(full + s, na * kMmABytes + C::kBBytes + (na + 1) * sfb);
-#pragma unroll
-          for (int a = 0; a < MA; ++a) {
-            if (a >= na) break;
-            const bool up = MODE == kMmGateUp && a == 1;
-            tma_load3(st + a * kMmABytes, up ? &p.a1 : &p.a0, ks * 128, MODE == kMmGateUp ? row0 : row0 + a * 128,
-                      t.mat, full + s);
-            bulk_g2s(sf + a * C::kSfBytes,
-                     (up ? p.sa1 : p.sa0) +
-                         (static_cast<size_t>(sr0 + (MODE == kMmGateUp ? 0 : a)) * p.kt + 2 * ks) * kMxTileBytes,
-                     sfb, full + s);
-          }
-          tma_load3(sb, &p.b, ks * 128, t.tt * NT, 0, full + s);
-          bulk_g2s(sf + MA * C::kSfBytes, p.sb + (static_cast<size_t>(t.tt) * p.kt + 2 * ks) * kMxTileBytes, sfb,
-                   full + s);
+          load_tokens(t, ks, s);
         }
       }
       if (!ok) {   // copies in flight land before the block's memory goes
@@ -307,19 +383,20 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_mm_kernel(const __grid_co
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      uint32_t it = 0, n = 0;
+      uint32_t it = 0, n = 0;        // n: accumulators taken so far
       bool ok = true;
-      for (int w = blockIdx.x; ok && w < total; w += gridDim.x, ++n) {
+      for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
         const MmTile t = mm_tile(p, w, NT);
-        const int row0 = t.rt * MA * 128;
-        const int na = MODE == kMmGateUp || MA == 1 || row0 + 128 < p.rows ? MA : 1;
-        const uint32_t buf = n % BUFS;
-        if (!mbar_wait_bounded(acc_empty + buf, ((n / BUFS) & 1) ^ 1, p.status)) {
-          ok = false;
-          break;
+        const int na = mm_operands<MODE, MA>(p, t);
+        uint32_t d[MA];
+#pragma unroll
+        for (int a = 0; a < MA; ++a) {
+          const uint32_t u = (n + a) % U;
+          d[a] = tmem + u * NT;
+          if (a < na && ok) ok = mbar_wait_bounded(acc_empty + u, (((n + a) / U) & 1) ^ 1, p.status);
         }
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem + buf * C::kAcc;
         const uint32_t idesc = mm_idesc((t.count + 15) & ~15);
         for (int ks = 0; ks < n_ks; ++ks, ++it) {
           const int s = it % S;
@@ -331,7 +408,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_mm_kernel(const __grid_co
           const int n64 = min(4, (p.K - ks * kMmStageK + 63) / 64), nkt = (n64 + 1) / 2;
           const uint32_t st = smem_addr(base + s * C::kStage);
           const uint32_t sb = st + MA * kMmABytes, sf = sb + C::kBBytes;
-          const uint32_t tsf = tmem + BUFS * C::kAcc + s * C::kSfCols;
+          const uint32_t tsf = tmem + U * NT + s * C::kSfCols;
           for (int kt = 0; kt < nkt; ++kt) {
 #pragma unroll
             for (int a = 0; a < MA; ++a)
@@ -339,16 +416,19 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_mm_kernel(const __grid_co
             mm_copy_sf(tsf + MA * 8 + kt * 4, mm_desc_sf(sf + MA * C::kSfBytes + kt * kMxTileBytes));
           }
           for (int i = 0; i < n64; ++i) {
-            const uint32_t id = idesc | (static_cast<uint32_t>(i & 1) * 2u << 29) | (static_cast<uint32_t>(i & 1) * 2u << 4);
+            const uint32_t id =
+                idesc | (static_cast<uint32_t>(i & 1) * 2u << 29) | (static_cast<uint32_t>(i & 1) * 2u << 4);
 #pragma unroll
             for (int a = 0; a < MA; ++a)
               if (a < na)
-                mm_mma(d + a * NT, mm_desc_sw128(st + a * kMmABytes + i * 32), mm_desc_sw128(sb + i * 32), id,
+                mm_mma(d[a], mm_desc_sw128(st + a * kMmABytes + i * 32), mm_desc_sw128(sb + i * 32), id,
                        tsf + a * 8 + (i >> 1) * 4, tsf + MA * 8 + (i >> 1) * 4, ks > 0 || i > 0);
           }
           umma_commit(empty + s);
         }
-        if (ok) umma_commit(acc_full + buf);
+        if (ok)
+          for (int a = 0; a < na; ++a) umma_commit(acc_full + (n + a) % U);
+        n += na;
       }
       if (!ok) {   // MMAs in flight end before the tensor memory goes
         umma_commit(drain);
@@ -356,20 +436,42 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_mm_kernel(const __grid_co
       }
     }
   } else {
-    const int q = warp & 3;                     // the 32 lanes of tensor memory this warp may read
+    const int q = warp & 3, half = (warp - 2) >> 2;   // the 32 lanes of tensor memory this warp may read
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    uint8_t *stage = staging + (warp - 2) * kMmEpiBytes;
     uint32_t n = 0;
-    for (int w = blockIdx.x; w < total; w += gridDim.x, ++n) {
-      const MmTile t = mm_tile(p, w, NT);
-      const uint32_t buf = n % BUFS;
-      const bool ok = mbar_wait_bounded(acc_full + buf, (n / BUFS) & 1, p.status);
-      if (!__all_sync(0xffffffffu, ok)) break;
+    bool ok = true;
+    auto wait_acc = [&](uint32_t i) {
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_full + i % U, (i / U) & 1, p.status));
       tc_fence_after();
-      const uint32_t acc = tmem + buf * C::kAcc + (static_cast<uint32_t>(q * 32) << 16);
-      if constexpr (MODE == kMmGateUp) mm_write_h<NT>(p, t, acc, q, lane);
-      else mm_write_plain<MA, NT>(p, t, acc, q, lane);
+      return lanes + (i % U) * NT;
+    };
+    auto free_acc = [&](uint32_t i) {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(acc_empty + buf);
+      if (lane == 0) mbar_arrive(acc_empty + i % U);
+    };
+    for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
+      const MmTile t = mm_tile(p, w, NT);
+      if constexpr (MODE == kMmGateUp) {
+        const uint32_t g = wait_acc(n);
+        if (!ok) break;
+        const uint32_t u = wait_acc(n + 1);
+        if (!ok) break;
+        mm_write_h<NT>(p, t, g, u, q, half, lane);
+        free_acc(n);
+        free_acc(n + 1);
+        n += 2;
+      } else {
+        const int na = mm_operands<MODE, MA>(p, t);
+        for (int a = 0; a < na; ++a, ++n) {
+          const uint32_t acc = wait_acc(n);
+          if (!ok) break;
+          mm_write_plain<OUT>(p, (t.rt * MA + a) * 128 + q * 32, static_cast<int64_t>(t.tt) * NT, t.count, acc, half,
+                              lane, stage);
+          free_acc(n);
+        }
+      }
     }
   }
   tc_fence_before();
@@ -384,7 +486,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_mm_kernel(const __grid_co
 // ---------------------------------------------------------------------------
 // x to MXFP4 rows at the sorted places: one block per token quantises its row
 // once and writes it to its k places. Scale tiles belong to one token tile each
-// (NT <= 128 rows of their 128).
+// (NT of their 128 rows).
 // ---------------------------------------------------------------------------
 struct ScatterArgs {
   const __nv_bfloat16 *x;
@@ -457,25 +559,33 @@ static bool codes_map(CUtensorMap *m, const void *codes, int64_t mats, int64_t r
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE, int MA, int NT>
+template <int MODE, int MA, int NT, int OUT>
 static cudaError_t mm_launch_as(const MmParams &p, int64_t max_tiles, cudaStream_t s) {
   using C = MmCfg<MA, NT>;
-  const cudaError_t e = allow_smem(mxfp4_mm_kernel<MODE, MA, NT>, C::kSmem);
+  const cudaError_t e = allow_smem(mxfp4_mm_kernel<MODE, MA, NT, OUT>, C::kSmem);
   if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(max_tiles, sm_count()));
-  return launch_pdl(mxfp4_mm_kernel<MODE, MA, NT>, dim3(grid), dim3(kMmThreads), C::kSmem, s, p);
+  return launch_pdl(mxfp4_mm_kernel<MODE, MA, NT, OUT>, dim3(grid), dim3(kMmThreads), C::kSmem, s, p);
 }
-static cudaError_t mm_launch(int mode, int ma, int nt, const MmParams &p, int64_t max_tiles, cudaStream_t s) {
-  if (mode == kMmGateUp)
-    return nt == 16   ? mm_launch_as<kMmGateUp, 2, 16>(p, max_tiles, s)
-           : nt == 32 ? mm_launch_as<kMmGateUp, 2, 32>(p, max_tiles, s)
-           : nt == 64 ? mm_launch_as<kMmGateUp, 2, 64>(p, max_tiles, s)
-                      : mm_launch_as<kMmGateUp, 2, 128>(p, max_tiles, s);
-  if (ma == 2) return mm_launch_as<kMmPlain, 2, 128>(p, max_tiles, s);
-  return nt == 16   ? mm_launch_as<kMmPlain, 1, 16>(p, max_tiles, s)
-         : nt == 32 ? mm_launch_as<kMmPlain, 1, 32>(p, max_tiles, s)
-         : nt == 64 ? mm_launch_as<kMmPlain, 1, 64>(p, max_tiles, s)
-                    : mm_launch_as<kMmPlain, 1, 128>(p, max_tiles, s);
+template <int OUT>
+static cudaError_t mm_launch_dense(int ma, int nt, const MmParams &p, int64_t max_tiles, cudaStream_t s) {
+  if (ma == 2) return mm_launch_as<kMmPlain, 2, 128, OUT>(p, max_tiles, s);
+  return nt == 16   ? mm_launch_as<kMmPlain, 1, 16, OUT>(p, max_tiles, s)
+         : nt == 32 ? mm_launch_as<kMmPlain, 1, 32, OUT>(p, max_tiles, s)
+         : nt == 64 ? mm_launch_as<kMmPlain, 1, 64, OUT>(p, max_tiles, s)
+                    : mm_launch_as<kMmPlain, 1, 128, OUT>(p, max_tiles, s);
+}
+static cudaError_t mm_launch_gateup(int nt, const MmParams &p, int64_t max_tiles, cudaStream_t s) {
+  return nt == 16   ? mm_launch_as<kMmGateUp, 2, 16, 0>(p, max_tiles, s)
+         : nt == 32 ? mm_launch_as<kMmGateUp, 2, 32, 0>(p, max_tiles, s)
+         : nt == 64 ? mm_launch_as<kMmGateUp, 2, 64, 0>(p, max_tiles, s)
+                    : mm_launch_as<kMmGateUp, 2, 96, 0>(p, max_tiles, s);
+}
+static cudaError_t mm_launch_down(int nt, const MmParams &p, int64_t max_tiles, cudaStream_t s) {
+  return nt == 16   ? mm_launch_as<kMmPlain, 1, 16, kMmBf16Vec>(p, max_tiles, s)
+         : nt == 32 ? mm_launch_as<kMmPlain, 1, 32, kMmBf16Vec>(p, max_tiles, s)
+         : nt == 64 ? mm_launch_as<kMmPlain, 1, 64, kMmBf16Vec>(p, max_tiles, s)
+                    : mm_launch_as<kMmPlain, 2, 96, kMmBf16Vec>(p, max_tiles, s);
 }
 
 // ---- expert FFN: workspace ---------------------------------------------------
@@ -488,9 +598,10 @@ struct FfnMxGeom {
 static FfnMxGeom ffn_mx_geom(const si_mxfp4_experts &L, int n_tokens, int top_k) {
   FfnMxGeom g{};
   g.pairs = static_cast<int64_t>(n_tokens) * top_k;
-  // the smallest tile that holds an expert's average tokens
+  // the smallest tile that holds an expert's average tokens; 96 is the largest
+  // with two accumulators for gate and up each
   const int64_t avg = (g.pairs + L.n_experts - 1) / L.n_experts;
-  g.nt = avg <= 16 ? 16 : avg <= 32 ? 32 : avg <= 64 ? 64 : 128;
+  g.nt = avg <= 16 ? 16 : avg <= 32 ? 32 : avg <= 64 ? 64 : 96;
   const int64_t with = std::min<int64_t>(L.n_experts, g.pairs);   // experts that can hold pairs
   g.max_tiles = (g.pairs + with * (g.nt - 1)) / g.nt;
   g.rows = g.max_tiles * g.nt;
@@ -541,7 +652,7 @@ extern "C" si_status si_mxfp4_matmul(const void *a_codes, const void *a_scales, 
   if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(w_codes) || !aligned16(w_scales) ||
       reinterpret_cast<uintptr_t>(out) % (out_type == SI_F32 ? 4 : 2))
     return SI_ERR_INVALID_ARG;
-  if (!workspace || !aligned256(workspace) || workspace_bytes < need) return SI_ERR_WORKSPACE;
+  if (workspace && (!aligned256(workspace) || workspace_bytes < need)) return SI_ERR_WORKSPACE;
   MmParams p{};
   const int nt = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
   const int64_t n_tt = (m + nt - 1) / nt, row_tiles = (n + 127) / 128;
@@ -561,9 +672,15 @@ extern "C" si_status si_mxfp4_matmul(const void *a_codes, const void *a_scales, 
   p.tokens = m;
   p.out = out;
   p.ld = ld_out;
-  p.out_type = out_type;
   p.status = static_cast<uint32_t *>(workspace);
-  return cuda_status(mm_launch(kMmPlain, ma, nt, p, n_tt * n_rt, static_cast<cudaStream_t>(stream)));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool vec = out_type != SI_F32 && n % 8 == 0 && ld_out % 8 == 0 && aligned16(out);
+  return cuda_status(out_type == SI_F32 ? mm_launch_dense<kMmF32>(ma, nt, p, n_tt * n_rt, s)
+                     : out_type == SI_BF16
+                         ? (vec ? mm_launch_dense<kMmBf16Vec>(ma, nt, p, n_tt * n_rt, s)
+                                : mm_launch_dense<kMmBf16>(ma, nt, p, n_tt * n_rt, s))
+                         : (vec ? mm_launch_dense<kMmF16Vec>(ma, nt, p, n_tt * n_rt, s)
+                                : mm_launch_dense<kMmF16>(ma, nt, p, n_tt * n_rt, s)));
 }
 
 extern "C" size_t si_moe_ffn_mxfp4_workspace_bytes(const si_mxfp4_experts *L, int n_tokens, int top_k) {
@@ -624,10 +741,11 @@ extern "C" si_status si_moe_ffn_mxfp4(const si_mxfp4_experts *L, int n_tokens, i
   gu.h_scales = base + g.off_hs;
   gu.h_kt = g.kt_h;
   gu.status = reinterpret_cast<uint32_t *>(base);
-  e = mm_launch(kMmGateUp, 2, g.nt, gu, g.max_tiles * gu.n_rt, s);
+  gu.early = 1;   // the sort is two launches back, complete when its successor's blocks have passed their wait
+  e = mm_launch_gateup(g.nt, gu, g.max_tiles * gu.n_rt, s);
   if (e != cudaSuccess) return SI_ERR_CUDA;
 
-  const int ma = g.nt == 128 ? 2 : 1;
+  const int ma = g.nt == 96 ? 2 : 1;
   dn.a1 = dn.a0;
   dn.sa0 = dn.sa1 = static_cast<const uint8_t *>(L->down_scales);
   dn.sb = base + g.off_hs;
@@ -641,9 +759,9 @@ extern "C" si_status si_moe_ffn_mxfp4(const si_mxfp4_experts *L, int n_tokens, i
   dn.n_tiles = so.n_tiles;
   dn.out = base + g.off_y;
   dn.ld = H;
-  dn.out_type = SI_BF16;
   dn.status = reinterpret_cast<uint32_t *>(base);
-  e = mm_launch(kMmPlain, ma, g.nt, dn, g.max_tiles * dn.n_rt, s);
+  dn.early = 1;
+  e = mm_launch_down(g.nt, dn, g.max_tiles * dn.n_rt, s);
   if (e != cudaSuccess) return SI_ERR_CUDA;
   return cuda_status(combine_launch(base + g.off_y, g.rows, n_tokens, top_k, H, so.position, topk_w, routed_out, s));
 }

@@ -19,16 +19,42 @@ namespace si {
 // ---------------------------------------------------------------------------
 // Sort: one block per expert (and one for the dropped pairs), one launch.
 // Every block counts all ids into shared memory, so it knows where its expert
-// starts without waiting for another block; then each of its warps takes a
-// contiguous range of ids, counts its own matches, and after a scan over the
-// warps writes them in order (a ballot per 32 ids gives the rank).
+// starts without waiting for another block, and keeps one bit per id for its
+// own matches; a scan over the words of 32 ids then gives every match its
+// place. More ids than kSortChunk go through the bits in chunks, read again.
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortWords = 2048;                    // bit words in shared memory
+constexpr int64_t kSortChunk = kSortWords * 32;     // ids they hold
+
+// The ids of one chunk: match bits of expert `me`, and all ids counted if COUNT.
+template <bool COUNT>
+SI_DEV void sort_scan(const SortArgs &a, int64_t c0, int me, int *s_hist, uint32_t *s_bits) {
+  constexpr int U = 8;                              // loads in flight per thread
+  const int E = a.n_experts, lane = threadIdx.x & 31;
+  const int64_t c1 = c0 + kSortChunk < a.pairs ? c0 + kSortChunk : a.pairs;
+  for (int64_t b = c0 + (threadIdx.x & ~31) * U; b < c1; b += kSortThreads * U) {
+    int id[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = b + u * 32 + lane;
+      id[u] = i < c1 ? __ldcg(a.ids + i) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = b + u * 32 + lane;
+      const int e = id[u] >= 0 && id[u] < E ? id[u] : E;
+      if (COUNT && i < c1) atomicAdd(&s_hist[e], 1);
+      const uint32_t m = __ballot_sync(0xffffffffu, i < c1 && e == me);
+      if (lane == 0 && b + u * 32 < c1) s_bits[(b - c0) / 32 + u] = m;
+    }
+  }
+}
 
 __global__ void __launch_bounds__(kSortThreads) sort_pairs_kernel(SortArgs a) {
   __shared__ int s_hist[kSortMaxExperts + 1];
-  __shared__ int s_warp[kSortWarps];
+  __shared__ uint32_t s_bits[kSortWords];
   __shared__ int s_red[2][kSortWarps];
   grid_dep_wait();
   grid_dep_launch();
@@ -36,18 +62,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_pairs_kernel(SortArgs a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int i = tid; i <= E; i += kSortThreads) s_hist[i] = 0;
   __syncthreads();
-  // the ids of warp w: [w * span, (w + 1) * span)
-  const int64_t span = (a.pairs + kSortThreads - 1) / kSortThreads * 32;
-  const int64_t i0 = span * warp, i1 = i0 + span < a.pairs ? i0 + span : a.pairs;
-  int mine = 0;
-  for (int64_t i = i0 + lane; i < i1; i += 32) {
-    const int id = __ldcg(a.ids + i);
-    const int e = id >= 0 && id < E ? id : E;
-    atomicAdd(&s_hist[e], 1);
-    mine += e == me;
-  }
-  mine = __reduce_add_sync(0xffffffffu, mine);
-  if (lane == 0) s_warp[warp] = mine;
+  for (int64_t c0 = 0; c0 < a.pairs; c0 += kSortChunk) sort_scan<true>(a, c0, me, s_hist, s_bits);
   __syncthreads();
   // places and tiles before this expert
   int before = 0, tiles = 0;
@@ -63,17 +78,15 @@ __global__ void __launch_bounds__(kSortThreads) sort_pairs_kernel(SortArgs a) {
   }
   __syncthreads();
   before = tiles = 0;
-  int at = 0;
 #pragma unroll
   for (int w = 0; w < kSortWarps; ++w) {
     before += s_red[0][w];
     tiles += s_red[1][w];
-    if (w < warp) at += s_warp[w];
   }
-  const int base = a.tile_rows > 0 ? tiles * a.tile_rows : before;
+  int place = a.tile_rows > 0 ? tiles * a.tile_rows : before;
   const int count = s_hist[me];
   if (tid == 0) {
-    if (a.offsets) a.offsets[me] = base;
+    if (a.offsets) a.offsets[me] = place;
     if (me == E && a.n_tiles) *a.n_tiles = tiles;
   }
   if (me < E && a.tile_rows > 0) {
@@ -84,20 +97,42 @@ __global__ void __launch_bounds__(kSortThreads) sort_pairs_kernel(SortArgs a) {
     }
   }
   if (count == 0) return;
-  for (int64_t b = i0; b < i1; b += 32) {
-    const int64_t i = b + lane;
-    bool hit = false;
-    if (i < i1) {
-      const int id = __ldcg(a.ids + i);
-      hit = (id >= 0 && id < E ? id : E) == me;
+  for (int64_t c0 = 0; c0 < a.pairs; c0 += kSortChunk) {
+    if (a.pairs > kSortChunk) {
+      __syncthreads();                              // the chunk before is written out
+      sort_scan<false>(a, c0, me, s_hist, s_bits);
     }
-    const uint32_t m = __ballot_sync(0xffffffffu, hit);
-    if (hit) {
-      const int p = base + at + __popc(m & ((1u << lane) - 1u));
-      if (a.position) a.position[i] = me < E ? p : -1;
-      if (a.order) a.order[p] = me < E ? static_cast<int32_t>(i) : -1;
+    const int64_t ids = a.pairs - c0 < kSortChunk ? a.pairs - c0 : kSortChunk;
+    const int words = static_cast<int>((ids + 31) / 32);
+    // each thread owns `per` consecutive words
+    const int per = (words + kSortThreads - 1) / kSortThreads;
+    const int w0 = min(tid * per, words), w1 = min(w0 + per, words);
+    __syncthreads();
+    int mine = 0;
+    for (int w = w0; w < w1; ++w) mine += __popc(s_bits[w]);
+    int at = mine;                                  // inclusive scan over the warp, then the warps
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, at, m);
+      if (lane >= m) at += o;
     }
-    at += __popc(m);
+    if (lane == 31) s_red[0][warp] = at;
+    __syncthreads();
+    int sum = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) {
+      if (w < warp) at += s_red[0][w];
+      sum += s_red[0][w];
+    }
+    int p = place + at - mine;
+    for (int w = w0; w < w1; ++w) {
+      for (uint32_t m = s_bits[w]; m; m &= m - 1, ++p) {
+        const int64_t i = c0 + static_cast<int64_t>(w) * 32 + __ffs(m) - 1;
+        if (a.position) a.position[i] = me < E ? p : -1;
+        if (a.order) a.order[p] = me < E ? static_cast<int32_t>(i) : -1;
+      }
+    }
+    place += sum;
   }
 }
 

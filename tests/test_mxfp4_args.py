@@ -51,7 +51,7 @@ def test_matmul_refusals(lib):
                {"ac": 8}, {"wc": 24}, {"out": 17}, {"k": (1 << 20) + 32}, {"mm": -1}):
         assert call(**kw) == BAD, kw
     assert call(ty=m.SI_Q8_0) == UNS
-    for kw in ({"ws": None}, {"ws": 16}, {"nb": 255}):
+    for kw in ({"ws": 16}, {"nb": 255}):
         assert call(**kw) == WS, kw
 
 
