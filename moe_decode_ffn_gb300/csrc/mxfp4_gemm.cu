@@ -10,10 +10,11 @@
 // holds one output feature. Products of two E2M1 values are exact and the
 // accumulators fp32.
 //
-// A block of 320 threads: warp 0 keeps a ring of stages full (256 columns of
-// the codes by tensor TMA in the 128-byte swizzle, their scale tiles by plain
-// bulk copies), one thread of warp 1 moves the scales into tensor memory
-// (tcgen05.cp) and issues the MMAs, warps 2..9 read the accumulators and write
+// A block of 352 threads: a thread of warp 0 keeps the codes of a ring of stages
+// coming (256 columns by tensor TMA in the 128-byte swizzle), lanes of warp 10
+// their scale tiles (plain bulk copies, one operand each: a thread is held up
+// by every copy it issues), one thread of warp 1 moves the scales into tensor
+// memory (tcgen05.cp) and issues the MMAs, warps 2..9 read the accumulators and write
 // the outputs (two warps per 32 lanes of tensor memory, each half of the
 // tokens). Blocks are persistent: tile i of block b is b + i * gridDim. The
 // accumulators are a ring too, so that the MMAs of a tile run beside the
@@ -30,7 +31,8 @@
 namespace si {
 
 constexpr int kMmEpiWarps = 8;
-constexpr int kMmThreads = 64 + 32 * kMmEpiWarps;
+constexpr int kMmThreads = 96 + 32 * kMmEpiWarps;
+constexpr int kMmScaleWarp = 2 + kMmEpiWarps;
 constexpr int kMmEpiBytes = 512;       // staging of an epilogue warp: 8 tokens x 32 features of 2 bytes
 constexpr int kMmStageK = 256;         // columns of a stage: 128 bytes of codes per row
 constexpr int kMmABytes = 128 * 128;   // 128 weight rows of a stage
@@ -112,21 +114,30 @@ SI_DEV void mbar_arrive(uint64_t *bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// Shared-memory matrix descriptor, K-major, 128-byte swizzle: rows of 128
-// bytes, 8-row groups 1024 bytes apart. Bits as in umma_desc_kmajor, layout 2.
-SI_DEV uint64_t mm_desc_sw128(uint32_t addr) {
-  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
-         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
-         (static_cast<uint64_t>(2) << 61);
-}
-// A scale tile: 32 rows of 16 bytes, 8-row groups 128 bytes apart.
-SI_DEV uint64_t mm_desc_sf(uint32_t addr) {
-  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 32) |
-         (static_cast<uint64_t>(1) << 46);
+// Shared-memory matrix descriptors (bits as in umma_desc_kmajor): low words,
+// with the address, and the high words, which are constants.
+//  - codes: K-major, 128-byte swizzle (layout 2), rows of 128 bytes, 8-row
+//    groups 1024 bytes apart;
+//  - a scale tile: no swizzle, 32 rows of 16 bytes, 8-row groups 128 bytes apart.
+constexpr uint32_t kMmCodesHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kMmScaleHi = (128u >> 4) | (1u << 14);
+SI_DEV uint32_t mm_codes_lo(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+SI_DEV uint32_t mm_scale_lo(uint32_t addr) { return addr >> 4; }
+// One lane of a converged warp. The MMA warp runs its loops together and only
+// this lane issues: the operands then are uniform values, which the tensor
+// instructions take as they are (a single-lane loop converts each of them for
+// each instruction and cannot feed the tensor core).
+SI_DEV bool elect_lane() {
+  uint32_t is;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(is));
+  return is != 0;
 }
 // 512 bytes of scales to 4 columns of tensor memory, on all four 32-lane quarters.
-SI_DEV void mm_copy_sf(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+SI_DEV void mm_copy_sf(uint32_t taddr, uint32_t lo) {
+  asm volatile("{\n .reg .b64 d;\n mov.b64 d, {%1, %2};\n"
+               " tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n}\n" ::"r"(taddr),
+               "r"(lo), "n"(kMmScaleHi)
+               : "memory");
 }
 // Instruction descriptor, kind::mxf4: E2M1 operands (bits [7,10), [10,12)),
 // K-major, N >> 3 in [17,23), E8M0 scales (bit 23), M >> 4 in [24,29); the scale
@@ -135,11 +146,12 @@ SI_DEV uint32_t mm_idesc(int n) {
   return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) | ((128u >> 4) << 24);
 }
 // D[tmem] (+)= A B^T over 64 columns, one thread.
-SI_DEV void mm_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t acc) {
+SI_DEV void mm_mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+      "{\n .reg .pred p;\n .reg .b64 da, db;\n mov.b64 da, {%1, %7};\n mov.b64 db, {%2, %7};\n"
+      " setp.ne.b32 p, %6, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc), "n"(kMmCodesHi)
       : "memory");
 }
 // 16 consecutive fp32 columns of this warp's 32 lanes; the wait is separate so
@@ -239,8 +251,18 @@ SI_DEV uint32_t transpose_nibbles(uint32_t w, int lane) {
   return lane & 1 ? (w & 0xF0F0F0F0u) | ((o >> 4) & 0x0F0F0F0Fu) : (w & 0x0F0F0F0Fu) | ((o & 0x0F0F0F0Fu) << 4);
 }
 
+// silu(g) u: ex2 and rcp of the hardware, each within 2 units in the last place.
+// g far below zero: the exponential overflows, the reciprocal is 0.
+SI_DEV float mm_silu_mul(float g, float u) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return g * r * u;
+}
+
 // h = silu(g) u of a lane's feature for 16 tokens, then MXFP4: the 32 lanes of
-// the warp are one block of every token, so its scale is a warp maximum.
+// the warp are one block of every token, so its scale is a warp maximum. Lane j
+// keeps the scale of token j and its multiplier, which the others fetch.
 template <int NT>
 SI_DEV void mm_write_h(const MmParams &p, const MmTile &t, uint32_t acc_g, uint32_t acc_u, int q, int half,
                        int lane) {
@@ -251,31 +273,40 @@ SI_DEV void mm_write_h(const MmParams &p, const MmTile &t, uint32_t acc_g, uint3
   uint8_t *sf = p.h_scales + (static_cast<size_t>(t.tt) * p.h_kt + t.rt) * kMxTileBytes;
 #pragma unroll 1
   for (int j0 = 16 * half; j0 < t.count; j0 += 32) {
+    const int js = j0 + (lane & 15);            // the token whose scale this lane keeps
+    if (!live) {                                // behind the last feature: scales that multiply zeros
+      if (lane < 16 && js < t.count) sf[mx_scale_byte(js, blk)] = 0;
+      continue;
+    }
     uint32_t g[16], u[16];
     tmem_ld16(acc_g + j0, g);
     tmem_ld16(acc_u + j0, u);
     tmem_wait_ld();
+    float h[16];
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      h[j] = mm_silu_mul(__uint_as_float(g[j]), __uint_as_float(u[j]));
+      const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h[j]) & 0x7FFFFFFFu);
+      if ((lane & 15) == j) top = m;
+    }
+    const uint32_t s = mx_scale_of(top);
+    const float up = mx_inv_scale(s);
+    const uint32_t bad = __ballot_sync(0xffffffffu, s == 255u);   // tokens with an infinity or a NaN
+    if (lane < 16 && js < t.count) sf[mx_scale_byte(js, blk)] = static_cast<uint8_t>(s);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) h[j] *= __shfl_sync(0xffffffffu, up, j);
 #pragma unroll
     for (int h8 = 0; h8 < 16; h8 += 8) {
-      float v[8];
-      uint32_t mine = 0;                        // scale of token j0 + h8 + lane
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float gv = __uint_as_float(g[h8 + j]), uv = __uint_as_float(u[h8 + j]);
-        const float h = live ? __fdividef(gv, 1.f + __expf(-gv)) * uv : 0.f;
-        const uint32_t s = mx_scale_of(__reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7FFFFFFFu));
-        v[j] = h * mx_inv_scale(s);
-        if (s == 255u) v[j] = 0.f;
-        if ((lane & 7) == j) mine = s;
+      uint32_t w = mx_codes8(h + h8);
+      if (bad) {                                // their codes are 0
+        for (int j = 0; j < 8; ++j)
+          if (bad >> (h8 + j) & 1u) w &= ~(15u << (4 * j));
       }
-      const uint32_t w = transpose_nibbles(mx_codes8(v), lane);
+      w = transpose_nibbles(w, lane);
       const int j = j0 + h8 + (lane & 7);
-      if (j < t.count) {
-        if (live)
-          *reinterpret_cast<uint32_t *>(p.h_codes + (row0 + j) * row_bytes + blk * 16 + (lane >> 3) * 4) = w;
-        // blocks behind the last feature too: their scales multiply zeros
-        if (lane < 8) sf[mx_scale_byte(j, blk)] = static_cast<uint8_t>(mine);
-      }
+      if (j < t.count)
+        *reinterpret_cast<uint32_t *>(p.h_codes + (row0 + j) * row_bytes + blk * 16 + (lane >> 3) * 4) = w;
     }
   }
 }
@@ -301,35 +332,36 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_mm_kernel(const __grid_co
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_ks = (p.K + kMmStageK - 1) / kMmStageK;
 
-  // the copies of stage ks of a tile: the weights and the tokens
+  // the copies of stage ks of a tile, codes and scales, weights and tokens; the
+  // full barrier of a stage takes the codes' and the scales' arrival
   auto load_weights = [&](const MmTile &t, int na, int ks, int s) {
-    uint8_t *st = base + s * C::kStage, *sf = st + MA * kMmABytes + C::kBBytes;
-    const uint32_t sfb = min(2, p.kt - 2 * ks) * kMxTileBytes;
-    mbar_arrive_expect_tx(full + s, na * kMmABytes + C::kBBytes + (na + 1) * sfb);
-    const int row0 = MODE == kMmGateUp ? t.rt * 128 : t.rt * MA * 128;
+    uint8_t *st = base + s * C::kStage;
+    mbar_arrive_expect_tx(full + s, na * kMmABytes + C::kBBytes);
 #pragma unroll
     for (int a = 0; a < MA; ++a) {
       if (a >= na) break;
-      const bool up = MODE == kMmGateUp && a == 1;
-      const int r = MODE == kMmGateUp ? row0 : row0 + a * 128;
-      tma_load3(st + a * kMmABytes, up ? &p.a1 : &p.a0, ks * 128, r, t.mat, full + s);
-      bulk_g2s(sf + a * C::kSfBytes,
-               (up ? p.sa1 : p.sa0) +
-                   (static_cast<size_t>(t.mat * p.row_tiles + r / 128) * p.kt + 2 * ks) * kMxTileBytes,
-               sfb, full + s);
+      const int r = MODE == kMmGateUp ? t.rt * 128 : (t.rt * MA + a) * 128;
+      tma_load3(st + a * kMmABytes, MODE == kMmGateUp && a == 1 ? &p.a1 : &p.a0, ks * 128, r, t.mat, full + s);
     }
   };
   auto load_tokens = [&](const MmTile &t, int ks, int s) {
-    uint8_t *sb = base + s * C::kStage + MA * kMmABytes;
-    tma_load3(sb, &p.b, ks * 128, t.tt * NT, 0, full + s);
-    bulk_g2s(sb + C::kBBytes + MA * C::kSfBytes, p.sb + (static_cast<size_t>(t.tt) * p.kt + 2 * ks) * kMxTileBytes,
-             min(2, p.kt - 2 * ks) * kMxTileBytes, full + s);
+    tma_load3(base + s * C::kStage + MA * kMmABytes, &p.b, ks * 128, t.tt * NT, 0, full + s);
+  };
+  auto load_scales = [&](const MmTile &t, int a, int ks, int s) {   // operand a; a == MA: the tokens
+    const int rt = MODE == kMmGateUp ? t.rt : t.rt * MA + a;
+    const uint8_t *src = a == MA ? p.sb : MODE == kMmGateUp && a == 1 ? p.sa1 : p.sa0;
+    const size_t tile = a == MA ? t.tt : t.mat * p.row_tiles + rt;
+    bulk_g2s(base + s * C::kStage + MA * kMmABytes + C::kBBytes + a * C::kSfBytes,
+             src + (tile * p.kt + 2 * ks) * kMxTileBytes, min(2, p.kt - 2 * ks) * kMxTileBytes, full + s);
+  };
+  auto expect_scales = [&](int na, int ks, int s) {
+    mbar_arrive_expect_tx(full + s, (na + 1) * min(2, p.kt - 2 * ks) * kMxTileBytes);
   };
 
   int ahead = 0;                     // stages whose weights were requested before the wait
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(full + i, 1);
+      mbar_init(full + i, 2);
       mbar_init(empty + i, 1);
     }
     for (int i = 0; i < U; ++i) {
@@ -338,10 +370,21 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_mm_kernel(const __grid_co
     }
     mbar_init(drain, 1);
     fence_mbar_init();
-    if (p.early && static_cast<int>(blockIdx.x) < mm_total(p, NT)) {
+  }
+  if (p.early) {                     // uniform over the grid
+    __syncthreads();
+    if ((threadIdx.x == 0 || warp == kMmScaleWarp) && static_cast<int>(blockIdx.x) < mm_total(p, NT)) {
       const MmTile t = mm_tile(p, blockIdx.x, NT);
       const int na = mm_operands<MODE, MA>(p, t);
-      for (; ahead < S && ahead < n_ks; ++ahead) load_weights(t, na, ahead, ahead);
+      for (; ahead < S && ahead < n_ks; ++ahead) {
+        if (warp == 0) {
+          load_weights(t, na, ahead, ahead);
+        } else {
+          if (lane == 0) expect_scales(na, ahead, ahead);
+          __syncwarp();
+          if (lane < na) load_scales(t, lane, ahead, ahead);
+        }
+      }
     }
   }
   grid_dep_wait();
@@ -354,26 +397,41 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_mm_kernel(const __grid_co
   __syncthreads();
   tc_fence_after();
   grid_dep_launch();
-  const uint32_t tmem = *s_taddr;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *s_taddr, 0);
   const int total = mm_total(p, NT);
 
-  if (warp == 0) {
-    if (lane == 0) {
+  // every role reads a tile's entry of the list one tile ahead
+  const int step = gridDim.x;
+  const MmTile none = {0, 0, 0, 0};
+  MmTile nx = static_cast<int>(blockIdx.x) < total ? mm_tile(p, blockIdx.x, NT) : none;
+  auto next_tile = [&](int w) {
+    const MmTile t = nx;
+    if (w + step < total) nx = mm_tile(p, w + step, NT);
+    return t;
+  };
+
+  if (warp == 0 || warp == kMmScaleWarp) {
+    if (warp != 0 || lane == 0) {    // one thread of warp 0; warp 10 together
       uint32_t it = 0;
       bool ok = true;
-      for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
-        const MmTile t = mm_tile(p, w, NT);
+      for (int w = blockIdx.x; ok && w < total; w += step) {
+        const MmTile t = next_tile(w);
         const int na = mm_operands<MODE, MA>(p, t);
         for (int ks = 0; ks < n_ks; ++ks, ++it) {
           const int s = it % S;
-          if (static_cast<int>(it) >= ahead) {
-            if (!mbar_wait_bounded(empty + s, ((it / S) & 1) ^ 1, p.status)) {
-              ok = false;
-              break;
-            }
-            load_weights(t, na, ks, s);
+          const bool fresh = static_cast<int>(it) >= ahead;
+          if (fresh) ok = mbar_wait_bounded(empty + s, ((it / S) & 1) ^ 1, p.status);
+          if (warp == 0) {
+            if (!ok) break;
+            if (fresh) load_weights(t, na, ks, s);
+            load_tokens(t, ks, s);
+          } else {
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (fresh && lane == 0) expect_scales(na, ks, s);
+            __syncwarp();
+            if (lane < na ? fresh : lane == MA) load_scales(t, lane, ks, s);
           }
-          load_tokens(t, ks, s);
         }
       }
       if (!ok) {   // copies in flight land before the block's memory goes
@@ -382,58 +440,72 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_mm_kernel(const __grid_co
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      uint32_t it = 0, n = 0;        // n: accumulators taken so far
-      bool ok = true;
-      for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
-        const MmTile t = mm_tile(p, w, NT);
-        const int na = mm_operands<MODE, MA>(p, t);
-        uint32_t d[MA];
+    const bool leader = elect_lane();
+    const uint32_t smem0 = smem_addr(base);
+    uint32_t n = 0;                  // accumulators taken so far
+    int s = 0;                       // stage and its parity
+    uint32_t parity = 0;
+    bool ok = true;
+    auto wait_all = [&](uint64_t *bar, uint32_t ph) {
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, ph, p.status));
+    };
+    for (int w = blockIdx.x; ok && w < total; w += step) {
+      const MmTile t = next_tile(w);
+      const int na = mm_operands<MODE, MA>(p, t);
+      uint32_t d[MA];
 #pragma unroll
-        for (int a = 0; a < MA; ++a) {
-          const uint32_t u = (n + a) % U;
-          d[a] = tmem + u * NT;
-          if (a < na && ok) ok = mbar_wait_bounded(acc_empty + u, (((n + a) / U) & 1) ^ 1, p.status);
-        }
+      for (int a = 0; a < MA; ++a) {
+        const uint32_t u = (n + a) % U;
+        d[a] = tmem + u * NT;
+        if (a < na && ok) wait_all(acc_empty + u, (((n + a) / U) & 1) ^ 1);
+      }
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t idesc = mm_idesc((t.count + 15) & ~15);
+      for (int ks = 0; ks < n_ks; ++ks) {
+        wait_all(full + s, parity);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t idesc = mm_idesc((t.count + 15) & ~15);
-        for (int ks = 0; ks < n_ks; ++ks, ++it) {
-          const int s = it % S;
-          if (!mbar_wait_bounded(full + s, (it / S) & 1, p.status)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const int n64 = min(4, (p.K - ks * kMmStageK + 63) / 64), nkt = (n64 + 1) / 2;
-          const uint32_t st = smem_addr(base + s * C::kStage);
-          const uint32_t sb = st + MA * kMmABytes, sf = sb + C::kBBytes;
-          const uint32_t tsf = tmem + U * NT + s * C::kSfCols;
-          for (int kt = 0; kt < nkt; ++kt) {
+        const int n64 = min(4, (p.K - ks * kMmStageK + 63) / 64);
+        const uint32_t st = smem0 + s * C::kStage;
+        const uint32_t sf = mm_scale_lo(st + MA * kMmABytes + C::kBBytes);
+        const uint32_t ca = mm_codes_lo(st), cb = mm_codes_lo(st + MA * kMmABytes);
+        const uint32_t tsf = tmem + U * NT + s * C::kSfCols;
+        if (leader) {
 #pragma unroll
-            for (int a = 0; a < MA; ++a)
-              if (a < na) mm_copy_sf(tsf + a * 8 + kt * 4, mm_desc_sf(sf + a * C::kSfBytes + kt * kMxTileBytes));
-            mm_copy_sf(tsf + MA * 8 + kt * 4, mm_desc_sf(sf + MA * C::kSfBytes + kt * kMxTileBytes));
+          for (int kt = 0; kt < 2; ++kt) {
+            if (2 * kt >= n64) break;
+#pragma unroll
+            for (int a = 0; a <= MA; ++a)
+              if (a < na || a == MA)
+                mm_copy_sf(tsf + a * 8 + kt * 4, sf + (a * C::kSfBytes + kt * kMxTileBytes) / 16);
           }
-          for (int i = 0; i < n64; ++i) {
-            const uint32_t id =
-                idesc | (static_cast<uint32_t>(i & 1) * 2u << 29) | (static_cast<uint32_t>(i & 1) * 2u << 4);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (i >= n64) break;
+            const uint32_t id = idesc | (static_cast<uint32_t>(i & 1) * 2u << 29) | (static_cast<uint32_t>(i & 1) * 2u << 4);
 #pragma unroll
             for (int a = 0; a < MA; ++a)
               if (a < na)
-                mm_mma(d[a], mm_desc_sw128(st + a * kMmABytes + i * 32), mm_desc_sw128(sb + i * 32), id,
-                       tsf + a * 8 + (i >> 1) * 4, tsf + MA * 8 + (i >> 1) * 4, ks > 0 || i > 0);
+                mm_mma(d[a], ca + (a * kMmABytes + i * 32) / 16, cb + i * 32 / 16, id, tsf + a * 8 + (i >> 1) * 4,
+                       tsf + MA * 8 + (i >> 1) * 4, ks > 0 || i > 0);
           }
           umma_commit(empty + s);
         }
-        if (ok)
-          for (int a = 0; a < na; ++a) umma_commit(acc_full + (n + a) % U);
-        n += na;
+        __syncwarp();
+        if (++s == S) {
+          s = 0;
+          parity ^= 1;
+        }
       }
-      if (!ok) {   // MMAs in flight end before the tensor memory goes
-        umma_commit(drain);
-        mbar_wait_bounded(drain, 0, p.status);
-      }
+      if (ok && leader)
+        for (int a = 0; a < na; ++a) umma_commit(acc_full + (n + a) % U);
+      __syncwarp();
+      n += na;
+    }
+    if (!ok) {   // MMAs in flight end before the tensor memory goes
+      if (leader) umma_commit(drain);
+      mbar_wait_bounded(drain, 0, p.status);
     }
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;   // the 32 lanes of tensor memory this warp may read
@@ -451,8 +523,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_mm_kernel(const __grid_co
       __syncwarp();
       if (lane == 0) mbar_arrive(acc_empty + i % U);
     };
-    for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
-      const MmTile t = mm_tile(p, w, NT);
+    for (int w = blockIdx.x; ok && w < total; w += step) {
+      const MmTile t = next_tile(w);
       if constexpr (MODE == kMmGateUp) {
         const uint32_t g = wait_acc(n);
         if (!ok) break;
@@ -498,9 +570,14 @@ __global__ void __launch_bounds__(256) quantize_scatter_kernel(ScatterArgs a) {
   grid_dep_wait();
   grid_dep_launch();
   const int64_t t = blockIdx.x;
-  int p[8];
+  uint8_t *code[8], *scale[8];       // of this token's pairs; NULL for a dropped one
 #pragma unroll
-  for (int r = 0; r < 8; ++r) p[r] = r < a.k ? __ldcg(a.position + t * a.k + r) : -1;
+  for (int r = 0; r < 8; ++r) {
+    const int p = r < a.k ? __ldcg(a.position + t * a.k + r) : -1;
+    code[r] = p < 0 ? nullptr : a.codes + static_cast<size_t>(p) * a.H / 2;
+    scale[r] = p < 0 ? nullptr
+                     : a.scales + static_cast<size_t>(p / a.nt) * a.kt * kMxTileBytes + mx_scale_byte(p % a.nt, 0);
+  }
   const int lane = threadIdx.x & 31;
   // whole scale tiles (128 columns, 16 lanes): the blocks behind H get scale 0
   for (int c0 = (threadIdx.x & ~31) * 8; c0 < a.kt * 128; c0 += blockDim.x * 8) {
@@ -519,11 +596,9 @@ __global__ void __launch_bounds__(256) quantize_scatter_kernel(ScatterArgs a) {
     for (int b = 0; b < 4; ++b) s4 |= __shfl_sync(0xffffffffu, s, (lane & 16) + 4 * b) << (8 * b);
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
-      if (p[r] < 0) continue;
-      if (c < a.H) *reinterpret_cast<uint32_t *>(a.codes + (static_cast<size_t>(p[r]) * a.H + c) / 2) = w;
-      if ((lane & 15) == 0 && c < a.kt * 128)
-        *reinterpret_cast<uint32_t *>(a.scales + (static_cast<size_t>(p[r] / a.nt) * a.kt + c / 128) * kMxTileBytes +
-                                      mx_scale_byte(p[r] % a.nt, 0)) = s4;
+      if (!code[r]) continue;
+      if (c < a.H) *reinterpret_cast<uint32_t *>(code[r] + c / 2) = w;
+      if ((lane & 15) == 0 && c < a.kt * 128) *reinterpret_cast<uint32_t *>(scale[r] + c / 128 * kMxTileBytes) = s4;
     }
   }
 }
