@@ -30,7 +30,7 @@
 
 namespace si {
 
-constexpr int kMmEpiWarps = 8;
+constexpr int kMmEpiWarps = 8, kMmEpiParts = kMmEpiWarps / 4;
 constexpr int kMmThreads = 96 + 32 * kMmEpiWarps;
 constexpr int kMmScaleWarp = 2 + kMmEpiWarps;
 constexpr int kMmEpiBytes = 512;       // staging of an epilogue warp: 8 tokens x 32 features of 2 bytes
@@ -197,13 +197,13 @@ SI_DEV void tmem_ld_frag(uint32_t taddr, uint32_t r[8]) {
 }
 
 // One accumulator (128 features x count tokens) of this warp's 32 features, the
-// warp's half of the 16-token groups.
+// warp's part of the 16-token groups.
 template <int OUT>
-SI_DEV void mm_write_plain(const MmParams &p, int f0, int64_t row0, int count, uint32_t acc, int half, int lane,
+SI_DEV void mm_write_plain(const MmParams &p, int f0, int64_t row0, int count, uint32_t acc, int part, int lane,
                            uint8_t *stage) {
   if (f0 >= p.rows) return;
 #pragma unroll 1
-  for (int j0 = 16 * half; j0 < count; j0 += 32) {
+  for (int j0 = 16 * part; j0 < count; j0 += 16 * kMmEpiParts) {
     if constexpr (OUT == kMmBf16Vec || OUT == kMmF16Vec) {
       // 8 x 8 blocks transposed through shared memory: a token's 32 features
       // are 64 bytes, its four 16-byte words permuted by the token so that
@@ -264,7 +264,7 @@ SI_DEV float mm_silu_mul(float g, float u) {
 // the warp are one block of every token, so its scale is a warp maximum. Lane j
 // keeps the scale of token j and its multiplier, which the others fetch.
 template <int NT>
-SI_DEV void mm_write_h(const MmParams &p, const MmTile &t, uint32_t acc_g, uint32_t acc_u, int q, int half,
+SI_DEV void mm_write_h(const MmParams &p, const MmTile &t, uint32_t acc_g, uint32_t acc_u, int q, int part,
                        int lane) {
   const int64_t row0 = static_cast<int64_t>(t.tt) * NT;
   const int blk = t.rt * 4 + q;                 // this warp's block of 32 features
@@ -272,7 +272,7 @@ SI_DEV void mm_write_h(const MmParams &p, const MmTile &t, uint32_t acc_g, uint3
   const size_t row_bytes = static_cast<size_t>(p.rows) / 2;
   uint8_t *sf = p.h_scales + (static_cast<size_t>(t.tt) * p.h_kt + t.rt) * kMxTileBytes;
 #pragma unroll 1
-  for (int j0 = 16 * half; j0 < t.count; j0 += 32) {
+  for (int j0 = 16 * part; j0 < t.count; j0 += 16 * kMmEpiParts) {
     const int js = j0 + (lane & 15);            // the token whose scale this lane keeps
     if (!live) {                                // behind the last feature: scales that multiply zeros
       if (lane < 16 && js < t.count) sf[mx_scale_byte(js, blk)] = 0;
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_mm_kernel(const __grid_co
       mbar_wait_bounded(drain, 0, p.status);
     }
   } else {
-    const int q = warp & 3, half = (warp - 2) >> 2;   // the 32 lanes of tensor memory this warp may read
+    const int q = warp & 3, part = (warp - 2) >> 2;   // the 32 lanes of tensor memory this warp may read
     const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
     uint8_t *stage = staging + (warp - 2) * kMmEpiBytes;
     uint32_t n = 0;
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_mm_kernel(const __grid_co
         if (!ok) break;
         const uint32_t u = wait_acc(n + 1);
         if (!ok) break;
-        mm_write_h<NT>(p, t, g, u, q, half, lane);
+        mm_write_h<NT>(p, t, g, u, q, part, lane);
         free_acc(n);
         free_acc(n + 1);
         n += 2;
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_mm_kernel(const __grid_co
         for (int a = 0; a < na; ++a, ++n) {
           const uint32_t acc = wait_acc(n);
           if (!ok) break;
-          mm_write_plain<OUT>(p, (t.rt * MA + a) * 128 + q * 32, static_cast<int64_t>(t.tt) * NT, t.count, acc, half,
+          mm_write_plain<OUT>(p, (t.rt * MA + a) * 128 + q * 32, static_cast<int64_t>(t.tt) * NT, t.count, acc, part,
                               lane, stage);
           free_acc(n);
         }
@@ -567,18 +567,24 @@ struct ScatterArgs {
   uint8_t *codes, *scales;
 };
 __global__ void __launch_bounds__(256) quantize_scatter_kernel(ScatterArgs a) {
+  __shared__ uint8_t *s_code[8], *s_scale[8];   // of this token's kept pairs
+  __shared__ int s_n;
   grid_dep_wait();
   grid_dep_launch();
   const int64_t t = blockIdx.x;
-  uint8_t *code[8], *scale[8];       // of this token's pairs; NULL for a dropped one
-#pragma unroll
-  for (int r = 0; r < 8; ++r) {
-    const int p = r < a.k ? __ldcg(a.position + t * a.k + r) : -1;
-    code[r] = p < 0 ? nullptr : a.codes + static_cast<size_t>(p) * a.H / 2;
-    scale[r] = p < 0 ? nullptr
-                     : a.scales + static_cast<size_t>(p / a.nt) * a.kt * kMxTileBytes + mx_scale_byte(p % a.nt, 0);
-  }
   const int lane = threadIdx.x & 31;
+  if (threadIdx.x < 32) {
+    const int p = lane < a.k ? __ldcg(a.position + t * a.k + lane) : -1;
+    const uint32_t kept = __ballot_sync(0xffffffffu, p >= 0);
+    const int at = __popc(kept & ((1u << lane) - 1u));
+    if (p >= 0) {
+      s_code[at] = a.codes + static_cast<size_t>(p) * a.H / 2;
+      s_scale[at] = a.scales + static_cast<size_t>(p / a.nt) * a.kt * kMxTileBytes + mx_scale_byte(p % a.nt, 0);
+    }
+    if (lane == 0) s_n = __popc(kept);
+  }
+  __syncthreads();
+  const int n = s_n;
   // whole scale tiles (128 columns, 16 lanes): the blocks behind H get scale 0
   for (int c0 = (threadIdx.x & ~31) * 8; c0 < a.kt * 128; c0 += blockDim.x * 8) {
     const int c = c0 + lane * 8;
@@ -594,11 +600,9 @@ __global__ void __launch_bounds__(256) quantize_scatter_kernel(ScatterArgs a) {
     uint32_t s4 = 0;
 #pragma unroll
     for (int b = 0; b < 4; ++b) s4 |= __shfl_sync(0xffffffffu, s, (lane & 16) + 4 * b) << (8 * b);
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      if (!code[r]) continue;
-      if (c < a.H) *reinterpret_cast<uint32_t *>(code[r] + c / 2) = w;
-      if ((lane & 15) == 0 && c < a.kt * 128) *reinterpret_cast<uint32_t *>(scale[r] + c / 128 * kMxTileBytes) = s4;
+    for (int r = 0; r < n; ++r) {
+      if (c < a.H) *reinterpret_cast<uint32_t *>(s_code[r] + c / 2) = w;
+      if ((lane & 15) == 0 && c < a.kt * 128) *reinterpret_cast<uint32_t *>(s_scale[r] + c / 128 * kMxTileBytes) = s4;
     }
   }
 }

@@ -8,6 +8,7 @@
 namespace si {
 
 constexpr int kSortMaxExperts = 1024;
+constexpr int64_t kSortSharePairs = 4096;   // pairs from which clusters share the count
 
 // For pairs = n_tokens * top_k ids: position[i] = place of pair i (by expert,
 // then by i) or -1 for ids outside [0, E); offsets[e] = first place of expert
@@ -23,8 +24,9 @@ struct SortArgs {
   int32_t *order, *position, *offsets;
   int tile_rows;
   int32_t *tile_expert, *tile_count, *n_tiles;
+  int vec;   // ids 16-byte aligned (set by sort_launch)
 };
-cudaError_t sort_launch(const SortArgs &a, cudaStream_t s);
+cudaError_t sort_launch(SortArgs a, cudaStream_t s);
 
 // y[t] = sum_r w[t][r] rows[position[t][r]] over bf16 rows of `hidden` values
 // (a multiple of 8, 16-byte aligned), fp32 sums in rank order.
