@@ -470,6 +470,8 @@ si_status si_mxfp4_matmul(const void *a_codes, const void *a_scales, int64_t m, 
  * inverse (place -> t * top_k + r), -1 behind the kept pairs; offsets[e] = first
  * place of expert e, offsets[n_experts] = number of kept pairs.
  *   n_tokens >= 1, top_k 1..8, n_experts 1..1024
+ *   workspace  si_moe_sort_workspace_bytes(n_tokens, top_k, n_experts) bytes (0 up to
+ *              2048 pairs: NULL then), any contents, no status word
  *   order int32 [n_tokens * top_k], position int32 [n_tokens][top_k],
  *   offsets int32 [n_experts + 1]
  *
@@ -488,8 +490,10 @@ si_status si_mxfp4_matmul(const void *a_codes, const void *a_scales, int64_t m, 
  * words at 16-byte aligned addresses move in such words, others value by value.
  * Outputs may not alias inputs.
  */
+size_t si_moe_sort_workspace_bytes(int n_tokens, int top_k, int n_experts);
 si_status si_moe_sort(const int32_t *topk_ids, int n_tokens, int top_k, int n_experts, int32_t *order,
-                      int32_t *position, int32_t *offsets, void *stream);
+                      int32_t *position, int32_t *offsets, void *workspace, size_t workspace_bytes,
+                      void *stream);
 si_status si_moe_gather(const void *x, si_dtype type, int n_tokens, int top_k, int64_t hidden,
                         const int32_t *position, const int32_t *n_kept, void *xs, void *stream);
 si_status si_moe_gather_backward(const void *gxs, si_dtype type, int n_tokens, int top_k, int64_t hidden,

@@ -99,7 +99,8 @@ SIGNATURES = {
     "si_dequantize_mxfp4": (_i32, [_vp, _vp, _i64, _i64, _i64, _vp, _i32, _i64, _i64, _vp]),
     "si_mxfp4_matmul_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "si_mxfp4_matmul": (_i32, [_vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _i32, _i64, _vp, _sz, _vp]),
-    "si_moe_sort": (_i32, [_vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp]),
+    "si_moe_sort_workspace_bytes": (_sz, [_i32, _i32, _i32]),
+    "si_moe_sort": (_i32, [_vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _sz, _vp]),
     "si_moe_gather": (_i32, [_vp, _i32, _i32, _i32, _i64, _vp, _vp, _vp, _vp]),
     "si_moe_gather_backward": (_i32, [_vp, _i32, _i32, _i32, _i64, _vp, _vp, _vp]),
     "si_moe_combine": (_i32, [_vp, _i32, _i32, _i32, _i64, _vp, _vp, _vp, _vp]),
@@ -149,7 +150,7 @@ def _check(status: int, where: str):
 
 
 def _cuda(t: torch.Tensor, name: str) -> int:
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -632,8 +633,8 @@ def _mxfp4(codes, scales, name: str, dims: int):
     cols *= 2
     if cols == 0 or cols % 32:
         raise ValueError(f"{name} has {cols} columns, expected a multiple of 32")
-    _shaped(codes, f"{name} codes", n * rows * cols // 2, _U8)
-    _shaped(scales, f"{name} scales", n * -(-rows // 128) * -(-cols // 128) * 512, _U8)
+    _shaped(codes, name, codes.numel(), _U8)
+    _shaped(scales, name, n * -(-rows // 128) * -(-cols // 128) * 512, _U8)
     return n, rows, cols
 
 
@@ -727,8 +728,11 @@ def si_moe_sort(handle, ids: torch.Tensor, n_experts: int):
     order = _empty((T * k,), dtype=torch.int32, device=dev)
     position = _empty((T, k), dtype=torch.int32, device=dev)
     offsets = _empty((max(n_experts, 0) + 1,), dtype=torch.int32, device=dev)
+    need = library().si_moe_sort_workspace_bytes(T, k, n_experts)
+    ws = _empty((need,), dtype=torch.uint8, device=dev) if need else None
     _check(library().si_moe_sort(_shaped(ids, "ids", T * k, _I32), T, k, n_experts, order.data_ptr(),
-                                 position.data_ptr(), offsets.data_ptr(), handle), "si_moe_sort")
+                                 position.data_ptr(), offsets.data_ptr(), ws.data_ptr() if need else None, need,
+                                 handle), "si_moe_sort")
     return order, position, offsets
 
 

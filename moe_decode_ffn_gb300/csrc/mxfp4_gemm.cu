@@ -672,7 +672,7 @@ struct FfnMxGeom {
   int nt;                   // tokens of a tile
   int64_t pairs, max_tiles, rows;
   int kt_x, kt_h;
-  size_t off_position, off_expert, off_count, off_n, off_xc, off_xs, off_hc, off_hs, off_y, bytes;
+  size_t off_position, off_counts, off_expert, off_count, off_n, off_xc, off_xs, off_hc, off_hs, off_y, bytes;
 };
 static FfnMxGeom ffn_mx_geom(const si_mxfp4_experts &L, int n_tokens, int top_k) {
   FfnMxGeom g{};
@@ -693,6 +693,7 @@ static FfnMxGeom ffn_mx_geom(const si_mxfp4_experts &L, int n_tokens, int top_k)
     return at;
   };
   g.off_position = take(g.pairs * 4);
+  g.off_counts = take(sort_workspace_bytes(g.pairs, L.n_experts));
   g.off_expert = take(g.max_tiles * 4);
   g.off_count = take(g.max_tiles * 4);
   g.off_n = take(4);
@@ -794,6 +795,7 @@ extern "C" si_status si_moe_ffn_mxfp4(const si_mxfp4_experts *L, int n_tokens, i
   so.pairs = g.pairs;
   so.n_experts = E;
   so.position = reinterpret_cast<int32_t *>(base + g.off_position);
+  so.counts = reinterpret_cast<int32_t *>(base + g.off_counts);
   so.tile_rows = g.nt;
   so.tile_expert = reinterpret_cast<int32_t *>(base + g.off_expert);
   so.tile_count = reinterpret_cast<int32_t *>(base + g.off_count);

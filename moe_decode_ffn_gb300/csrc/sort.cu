@@ -17,109 +17,54 @@
 namespace si {
 
 // ---------------------------------------------------------------------------
-// Sort: one block per expert (and one for the dropped pairs), one launch. Every
-// block compares all ids with its expert and keeps one bit per id; a scan over
-// the words of 32 bits then gives every match its place. Where its expert
-// starts follows from a count of all ids, which it takes itself or, for long
-// batches, shares with the blocks of its cluster (each counts a part into its
-// shared memory and reads the other parts): no block waits for more than that.
-// More ids than kSortChunk go through the bits in chunks, read again.
+// Sort of few pairs: one block per expert (and one for the dropped pairs), one
+// launch. Every block counts all ids into shared memory, so it knows where its
+// expert starts without waiting for another block, and keeps one bit per id for
+// its own matches; a scan over the words of 32 bits gives every match its place.
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortWords = 2048;                    // bit words in shared memory
-constexpr int64_t kSortChunk = kSortWords * 32;     // ids they hold
-constexpr int kSortCluster = 8;
 
-SI_DEV void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
+// Expert of a pair, E for a dropped one (negative ids are large unsigned ones).
+SI_DEV int sort_expert(const SortArgs &a, int64_t i) {
+  return static_cast<int>(min(static_cast<uint32_t>(__ldcg(a.ids + i)), static_cast<uint32_t>(a.n_experts)));
 }
-// 32 bits of shared memory of block `rank` of this cluster, at our own address p.
-SI_DEV int ld_cluster(const int *p, uint32_t rank) {
-  uint32_t at;
-  int v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-  return v;
+SI_DEV void sort_place(const SortArgs &a, int64_t i, int e, int p) {
+  if (a.position) a.position[i] = e < a.n_experts ? p : -1;
+  if (a.order) a.order[p] = e < a.n_experts ? static_cast<int32_t>(i) : -1;
 }
-
-// The ids of one chunk: match bits of expert `me`; COUNT: the ids of every
-// `of`-th round of the block counted, from round `part` on. A thread takes 8
-// consecutive ids, a byte of the bits.
-template <bool COUNT>
-SI_DEV void sort_scan(const SortArgs &a, int64_t c0, uint32_t me, int part, int of, int *s_hist, uint8_t *s_bits) {
-  constexpr int U = 2;                              // bytes per thread in flight
-  const uint32_t E = a.n_experts;
-  const int64_t c1 = c0 + kSortChunk < a.pairs ? c0 + kSortChunk : a.pairs;
-  int round = 0;
-  for (int64_t b0 = c0; b0 < c1; b0 += kSortThreads * 8 * U) {
-    uint32_t id[U][8];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t b = b0 + (u * kSortThreads + threadIdx.x) * 8;
-      if (a.vec && b + 8 <= c1) {
-        const uint4 lo = __ldcg(reinterpret_cast<const uint4 *>(a.ids + b));
-        const uint4 hi = __ldcg(reinterpret_cast<const uint4 *>(a.ids + b) + 1);
-        id[u][0] = lo.x; id[u][1] = lo.y; id[u][2] = lo.z; id[u][3] = lo.w;
-        id[u][4] = hi.x; id[u][5] = hi.y; id[u][6] = hi.z; id[u][7] = hi.w;
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) id[u][i] = b + i < c1 ? static_cast<uint32_t>(__ldcg(a.ids + b + i)) : 0u;
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u, ++round) {
-      const int64_t b = b0 + (u * kSortThreads + threadIdx.x) * 8;
-      if (b >= c1) break;
-      uint32_t bits = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t e = min(id[u][i], E);        // negative ids are large unsigned ones
-        bits |= (e == me ? 1u : 0u) << i;
-        if (COUNT && round % of == part && b + i < c1) atomicAdd(&s_hist[e], 1);
-      }
-      if (c1 - b < 8) bits &= (1u << (c1 - b)) - 1u;
-      s_bits[(b - c0) / 8] = static_cast<uint8_t>(bits);
-    }
+SI_DEV int sort_tiles(const SortArgs &a, int n) { return a.tile_rows > 0 ? (n + a.tile_rows - 1) / a.tile_rows : 0; }
+// The list entries of expert e: its pairs, first tile `t`.
+SI_DEV void sort_list(const SortArgs &a, int e, int count, int t, int from, int step) {
+  for (int i = from; i * a.tile_rows < count; i += step) {
+    a.tile_expert[t + i] = e;
+    a.tile_count[t + i] = min(a.tile_rows, count - i * a.tile_rows);
   }
 }
 
-template <bool SHARED>
 __global__ void __launch_bounds__(kSortThreads) sort_pairs_kernel(SortArgs a) {
   __shared__ int s_hist[kSortMaxExperts + 1];
-  __shared__ uint32_t s_bits[kSortWords];
+  __shared__ uint32_t s_bits[kSortFewPairs / 32];
   __shared__ int s_red[2][kSortWarps];
-  __shared__ int s_count;
   grid_dep_wait();
   grid_dep_launch();
-  const int E = a.n_experts, me = blockIdx.x;     // me == E: the dropped pairs; beyond: only counting
-  const int part = SHARED ? static_cast<int>(blockIdx.x) % kSortCluster : 0;
-  constexpr int of = SHARED ? kSortCluster : 1;
+  const int E = a.n_experts, me = blockIdx.x, n = static_cast<int>(a.pairs);   // me == E: the dropped pairs
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int i = tid; i <= E; i += kSortThreads) s_hist[i] = 0;
-  // whole words for the scan: bytes behind the last id are 0
-  if (tid < 4) reinterpret_cast<uint8_t *>(s_bits)[min((a.pairs - 1) % kSortChunk / 8 + 1 + tid, kSortChunk / 8 - 1)] = 0;
   __syncthreads();
-  for (int64_t c0 = 0; c0 < a.pairs; c0 += kSortChunk)
-    sort_scan<true>(a, c0, me, part, of, s_hist, reinterpret_cast<uint8_t *>(s_bits));
-  if constexpr (SHARED) cluster_sync();
-  else __syncthreads();
-  // pairs and tiles before this expert, and its own pairs
+  for (int b = tid & ~31; b < n; b += kSortThreads) {
+    const int i = b + lane;
+    const int e = i < n ? sort_expert(a, i) : -1;
+    if (e >= 0) atomicAdd(&s_hist[e], 1);
+    const uint32_t m = __ballot_sync(0xffffffffu, e == me);
+    if (lane == 0) s_bits[b >> 5] = m;
+  }
+  __syncthreads();
+  // pairs and tiles before this expert
   int before = 0, tiles = 0;
-  for (int e = tid; e <= min(me, E); e += kSortThreads) {
-    int n = 0;
-    if constexpr (SHARED) {
-#pragma unroll
-      for (int r = 0; r < kSortCluster; ++r) n += ld_cluster(s_hist + e, r);
-    } else {
-      n = s_hist[e];
-    }
-    if (e < me) {
-      before += n;
-      if (a.tile_rows > 0) tiles += (n + a.tile_rows - 1) / a.tile_rows;
-    } else {
-      s_count = n;
-    }
+  for (int e = tid; e < me; e += kSortThreads) {
+    before += s_hist[e];
+    tiles += sort_tiles(a, s_hist[e]);
   }
   before = __reduce_add_sync(0xffffffffu, before);
   tiles = __reduce_add_sync(0xffffffffu, tiles);
@@ -127,88 +72,164 @@ __global__ void __launch_bounds__(kSortThreads) sort_pairs_kernel(SortArgs a) {
     s_red[0][warp] = before;
     s_red[1][warp] = tiles;
   }
-  if constexpr (SHARED) cluster_sync();             // every part has been read
-  else __syncthreads();
-  if (me > E) return;
+  __syncthreads();
   before = tiles = 0;
 #pragma unroll
   for (int w = 0; w < kSortWarps; ++w) {
     before += s_red[0][w];
     tiles += s_red[1][w];
   }
-  const int count = s_count;
-  int place = a.tile_rows > 0 ? tiles * a.tile_rows : before;
+  const int place = a.tile_rows > 0 ? tiles * a.tile_rows : before;
   if (tid == 0) {
     if (a.offsets) a.offsets[me] = place;
     if (me == E && a.n_tiles) *a.n_tiles = tiles;
   }
-  if (me < E && a.tile_rows > 0) {
-    const int n = (count + a.tile_rows - 1) / a.tile_rows;
-    for (int i = tid; i < n; i += kSortThreads) {
-      a.tile_expert[tiles + i] = me;
-      a.tile_count[tiles + i] = min(a.tile_rows, count - i * a.tile_rows);
-    }
-  }
-  if (count == 0) return;
-  for (int64_t c0 = 0; c0 < a.pairs; c0 += kSortChunk) {
-    if (a.pairs > kSortChunk) {
-      __syncthreads();                              // the chunk before is written out
-      if (tid < 4 && c0 + kSortChunk >= a.pairs)
-        reinterpret_cast<uint8_t *>(s_bits)[min((a.pairs - 1) % kSortChunk / 8 + 1 + tid, kSortChunk / 8 - 1)] = 0;
-      __syncthreads();
-      sort_scan<false>(a, c0, me, 0, 1, s_hist, reinterpret_cast<uint8_t *>(s_bits));
-    }
-    const int64_t ids = a.pairs - c0 < kSortChunk ? a.pairs - c0 : kSortChunk;
-    const int words = static_cast<int>((ids + 31) / 32);
-    // each thread owns `per` consecutive words
-    const int per = (words + kSortThreads - 1) / kSortThreads;
-    const int w0 = min(tid * per, words), w1 = min(w0 + per, words);
-    __syncthreads();
-    int mine = 0;
-    for (int w = w0; w < w1; ++w) mine += __popc(s_bits[w]);
-    int at = mine;                                  // inclusive scan over the warp, then the warps
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, at, m);
-      if (lane >= m) at += o;
-    }
-    if (lane == 31) s_red[0][warp] = at;
-    __syncthreads();
-    int sum = 0;
-#pragma unroll
-    for (int w = 0; w < kSortWarps; ++w) {
-      if (w < warp) at += s_red[0][w];
-      sum += s_red[0][w];
-    }
-    int p = place + at - mine;
-    for (int w = w0; w < w1; ++w) {
-      for (uint32_t m = s_bits[w]; m; m &= m - 1, ++p) {
-        const int64_t i = c0 + static_cast<int64_t>(w) * 32 + __ffs(m) - 1;
-        if (a.position) a.position[i] = me < E ? p : -1;
-        if (a.order) a.order[p] = me < E ? static_cast<int32_t>(i) : -1;
-      }
-    }
-    place += sum;
+  if (me < E && a.tile_rows > 0) sort_list(a, me, s_hist[me], tiles, tid, kSortThreads);
+  // a thread's word: the matches before it are those of the words before
+  for (int w = warp; w * 32 < n; w += kSortWarps) {
+    const uint32_t m = s_bits[w];
+    if (m == 0) continue;
+    int at = 0;
+    for (int j = lane; j < w; j += 32) at += __popc(s_bits[j]);
+    at = __reduce_add_sync(0xffffffffu, at);
+    if (m >> lane & 1u) sort_place(a, w * 32 + lane, me, place + at + __popc(m & ((1u << lane) - 1u)));
   }
 }
 
+// ---------------------------------------------------------------------------
+// Sort of many pairs, two launches over at most kSortChunks chunks of ids: the
+// first counts every chunk's ids by expert; a block of the second sums the
+// counts of the chunks before its own and of the experts before each expert, and
+// places its ids in rounds of kSortRound: a warp ranks its ids with match.any,
+// a scan over the warps' counts does the rest.
+// ---------------------------------------------------------------------------
+constexpr int kSortIds = 4;                                // ids per thread and round
+constexpr int kSortRound = kSortThreads * kSortIds;
+
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a) {
+  __shared__ int s_hist[kSortMaxExperts + 1];
+  grid_dep_wait();
+  grid_dep_launch();
+  for (int i = threadIdx.x; i <= a.n_experts; i += kSortThreads) s_hist[i] = 0;
+  __syncthreads();
+  const int64_t c0 = a.chunk * blockIdx.x, c1 = min(c0 + a.chunk, a.pairs);
+  for (int64_t i = c0 + threadIdx.x; i < c1; i += kSortRound) {
+#pragma unroll
+    for (int u = 0; u < kSortIds; ++u)
+      if (i + u * kSortThreads < c1) atomicAdd(&s_hist[sort_expert(a, i + u * kSortThreads)], 1);
+  }
+  __syncthreads();
+  int32_t *row = a.counts + static_cast<size_t>(blockIdx.x) * (a.n_experts + 1);
+  for (int i = threadIdx.x; i <= a.n_experts; i += kSortThreads) row[i] = s_hist[i];
+}
+
+// Exclusive sums of v over the threads of the block (s_red: one word a warp).
+SI_DEV int block_scan(int v, int *s_red) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int at = v;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, at, m);
+    if (lane >= m) at += o;
+  }
+  __syncthreads();                                         // s_red may still be read
+  if (lane == 31) s_red[warp] = at;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kSortWarps; ++w)
+    if (w < warp) at += s_red[w];
+  return at - v;
+}
+
+__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a) {
+  extern __shared__ int s_warp[];                          // [kSortWarps][E + 1]
+  __shared__ int s_next[kSortMaxExperts + 1];              // next place of an expert in this chunk
+  __shared__ int s_red[kSortWarps];
+  const int E = a.n_experts, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int64_t c0 = a.chunk * blockIdx.x, c1 = min(c0 + a.chunk, a.pairs);
+  // experts in runs of `per` consecutive ones a thread
+  const int per = (E + kSortThreads) / kSortThreads;
+  const int e0 = min(tid * per, E + 1), e1 = min(e0 + per, E + 1);
+  int mine = 0, my_tiles = 0;
+  for (int e = e0; e < e1; ++e) {
+    int total = 0, before = 0;
+    for (int c = 0; c < static_cast<int>(gridDim.x); ++c) {
+      const int n = __ldcg(a.counts + static_cast<size_t>(c) * (E + 1) + e);
+      if (c < static_cast<int>(blockIdx.x)) before += n;
+      total += n;
+    }
+    s_next[e] = before;
+    s_warp[e] = total;
+    mine += total;
+    if (e < E) my_tiles += sort_tiles(a, total);
+  }
+  int at = block_scan(mine, s_red), tile = a.tile_rows > 0 ? block_scan(my_tiles, s_red) : 0;
+  for (int e = e0; e < e1; ++e) {
+    const int total = s_warp[e], place = a.tile_rows > 0 ? tile * a.tile_rows : at;
+    s_next[e] += place;
+    if (blockIdx.x == 0) {
+      if (a.offsets) a.offsets[e] = place;
+      if (e == E && a.n_tiles) *a.n_tiles = tile;
+    }
+    // every block lists the tiles of some experts
+    if (e < E && a.tile_rows > 0 && e % gridDim.x == blockIdx.x) sort_list(a, e, total, tile, 0, 1);
+    at += total;
+    if (e < E) tile += sort_tiles(a, total);
+  }
+  int *counts = s_warp + warp * (E + 1);
+  for (int64_t b = c0; b < c1; b += kSortRound) {
+    __syncthreads();
+    for (int i = lane; i <= E; i += 32) counts[i] = 0;
+    __syncwarp();
+    int e[kSortIds], rank[kSortIds];
+    const int64_t i0 = b + warp * (32 * kSortIds) + lane;
+#pragma unroll
+    for (int u = 0; u < kSortIds; ++u) e[u] = i0 + u * 32 < c1 ? sort_expert(a, i0 + u * 32) : -1;
+#pragma unroll
+    for (int u = 0; u < kSortIds; ++u) {
+      const uint32_t same = __match_any_sync(0xffffffffu, e[u]);
+      rank[u] = __popc(same & ((1u << lane) - 1u));
+      if (e[u] >= 0) rank[u] += counts[e[u]];
+      __syncwarp();
+      if (e[u] >= 0 && lane == 31 - __clz(same)) counts[e[u]] = rank[u] + 1;
+      __syncwarp();
+    }
+    __syncthreads();
+    for (int x = tid; x <= E; x += kSortThreads) {
+      int next = s_next[x];
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) {
+        const int n = s_warp[w * (E + 1) + x];
+        s_warp[w * (E + 1) + x] = next;
+        next += n;
+      }
+      s_next[x] = next;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kSortIds; ++u)
+      if (e[u] >= 0) sort_place(a, i0 + u * 32, e[u], counts[e[u]] + rank[u]);
+  }
+}
+
+size_t sort_workspace_bytes(int64_t pairs, int n_experts) {
+  return pairs <= kSortFewPairs ? 0 : static_cast<size_t>(kSortChunks) * (n_experts + 1) * sizeof(int32_t);
+}
+
 cudaError_t sort_launch(SortArgs a, cudaStream_t s) {
-  a.vec = (reinterpret_cast<uintptr_t>(a.ids) & 15u) == 0;
-  // the shared count pays from a few thousand pairs on
-  if (a.pairs < kSortSharePairs) return launch_pdl(sort_pairs_kernel<false>, dim3(a.n_experts + 1), dim3(kSortThreads), 0, s, a);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((a.n_experts + kSortCluster) / kSortCluster * kSortCluster);
-  cfg.blockDim = dim3(kSortThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kSortCluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, sort_pairs_kernel<true>, a);
+  if (a.pairs <= kSortFewPairs)
+    return launch_pdl(sort_pairs_kernel, dim3(a.n_experts + 1), dim3(kSortThreads), 0, s, a);
+  // whole rounds, at most kSortChunks chunks
+  a.chunk = (a.pairs + kSortChunks * int64_t(kSortRound) - 1) / (kSortChunks * int64_t(kSortRound)) * kSortRound;
+  const dim3 grid(static_cast<unsigned>((a.pairs + a.chunk - 1) / a.chunk));
+  cudaError_t e = launch_pdl(sort_count_kernel, grid, dim3(kSortThreads), 0, s, a);
+  if (e != cudaSuccess) return e;
+  const size_t smem = static_cast<size_t>(kSortWarps) * (a.n_experts + 1) * sizeof(int);
+  e = allow_smem(sort_place_kernel, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(sort_place_kernel, grid, dim3(kSortThreads), smem, s, a);
 }
 
 // ---------------------------------------------------------------------------
@@ -466,12 +487,24 @@ cudaError_t combine_launch(const void *rows, int64_t n_rows, int n_tokens, int t
 
 using namespace si;
 
+static bool sort_shape_ok(int n_tokens, int top_k, int n_experts) {
+  return n_tokens >= 1 && top_k >= 1 && top_k <= kRowMaxK && n_experts >= 1 && n_experts <= kSortMaxExperts &&
+         static_cast<int64_t>(n_tokens) * top_k <= 0x7FFFFFFF;
+}
+
+extern "C" size_t si_moe_sort_workspace_bytes(int n_tokens, int top_k, int n_experts) {
+  if (!sort_shape_ok(n_tokens, top_k, n_experts)) return 0;
+  const size_t need = sort_workspace_bytes(static_cast<int64_t>(n_tokens) * top_k, n_experts);
+  return need ? round_up(need, 256) : 0;
+}
+
 extern "C" si_status si_moe_sort(const int32_t *topk_ids, int n_tokens, int top_k, int n_experts, int32_t *order,
-                                 int32_t *position, int32_t *offsets, void *stream) {
+                                 int32_t *position, int32_t *offsets, void *workspace, size_t workspace_bytes,
+                                 void *stream) {
   if (!whole(topk_ids, 4) || !whole(order, 4) || !whole(position, 4) || !whole(offsets, 4)) return SI_ERR_INVALID_ARG;
-  if (n_tokens < 1 || top_k < 1 || top_k > kRowMaxK || n_experts < 1 || n_experts > kSortMaxExperts ||
-      static_cast<int64_t>(n_tokens) * top_k > 0x7FFFFFFF)
-    return SI_ERR_INVALID_ARG;
+  if (!sort_shape_ok(n_tokens, top_k, n_experts)) return SI_ERR_INVALID_ARG;
+  const size_t need = si_moe_sort_workspace_bytes(n_tokens, top_k, n_experts);
+  if (need && (!workspace || !aligned256(workspace) || workspace_bytes < need)) return SI_ERR_WORKSPACE;
   SortArgs a{};
   a.ids = topk_ids;
   a.pairs = static_cast<int64_t>(n_tokens) * top_k;
@@ -479,6 +512,7 @@ extern "C" si_status si_moe_sort(const int32_t *topk_ids, int n_tokens, int top_
   a.order = order;
   a.position = position;
   a.offsets = offsets;
+  a.counts = static_cast<int32_t *>(workspace);
   return cuda_status(sort_launch(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -8,7 +8,8 @@
 namespace si {
 
 constexpr int kSortMaxExperts = 1024;
-constexpr int64_t kSortSharePairs = 4096;   // pairs from which clusters share the count
+constexpr int kSortFewPairs = 2048;    // pairs that one launch sorts
+constexpr int kSortChunks = 64;        // chunks of a longer batch
 
 // For pairs = n_tokens * top_k ids: position[i] = place of pair i (by expert,
 // then by i) or -1 for ids outside [0, E); offsets[e] = first place of expert
@@ -24,8 +25,10 @@ struct SortArgs {
   int32_t *order, *position, *offsets;
   int tile_rows;
   int32_t *tile_expert, *tile_count, *n_tiles;
-  int vec;   // ids 16-byte aligned (set by sort_launch)
+  int32_t *counts;   // sort_workspace_bytes, for more than kSortFewPairs pairs
+  int64_t chunk;     // set by sort_launch
 };
+size_t sort_workspace_bytes(int64_t pairs, int n_experts);
 cudaError_t sort_launch(SortArgs a, cudaStream_t s);
 
 // y[t] = sum_r w[t][r] rows[position[t][r]] over bf16 rows of `hidden` values

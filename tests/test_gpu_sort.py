@@ -56,6 +56,24 @@ def test_sort_skewed_and_large():
     assert torch.equal(position.reshape(-1)[order.long()].cpu(), torch.arange(65536, dtype=torch.int32))
 
 
+@pytest.mark.parametrize("pairs", [2047, 2048, 2049, 4095, 4097, 64 * 2048 - 1, 64 * 2048 + 1, 300001])
+@pytest.mark.parametrize("E", [1, 100, 1024])
+def test_sort_at_the_borders_of_its_rounds(pairs, E):
+    """One launch or two, chunks of one round or of several, the last one ragged."""
+    ids, _ = routing(pairs + E, pairs, 1, E, 0.05)
+    order, position, offsets = m.si_moe_sort(ids.cuda(), E)
+    flat = ids.reshape(-1).long()
+    keep = (flat >= 0) & (flat < E)
+    key = torch.where(keep, flat, torch.full_like(flat, E))
+    perm = torch.sort(key, stable=True).indices
+    kept = int(keep.sum())
+    assert torch.equal(order.cpu()[:kept].long(), perm[:kept]) and bool((order.cpu()[kept:] == -1).all())
+    want = torch.full_like(flat, -1)
+    want[perm[:kept]] = torch.arange(kept)
+    assert torch.equal(position.cpu().reshape(-1).long(), want)
+    assert torch.equal(offsets.cpu().long(), torch.searchsorted(key[perm], torch.arange(E + 1)))
+
+
 def _inputs(T, k, E, H, outside, kind):
     ids, w = routing(T * 3 + H, T, k, E, outside)
     g = torch.Generator().manual_seed(T + H)

@@ -56,7 +56,7 @@ def test_matmul_refusals(lib):
 
 
 def test_sort_and_row_refusals(lib):
-    ok = [16, 4, 2, 8, 16, 16, 16, None]
+    ok = [16, 4, 2, 8, 16, 16, 16, None, 0, None]
     for i, v in ((0, None), (0, 18), (1, 0), (1, -1), (2, 0), (2, 9), (3, 0), (3, 1025), (4, None), (5, None), (6, 17),
                  (1, 1 << 30)):
         a = list(ok)
@@ -64,6 +64,12 @@ def test_sort_and_row_refusals(lib):
         if i == 1 and v == 1 << 30:
             a[2] = 8                                          # 2^33 pairs
         assert lib.si_moe_sort(*a) == BAD, (i, v)
+    size = lib.si_moe_sort_workspace_bytes
+    assert size(4, 2, 8) == 0 and size(0, 2, 8) == 0 and size(1000, 9, 8) == 0
+    need = size(1000, 8, 8)
+    assert need > 0 and need % 256 == 0
+    for ws, n in ((None, need), (128, need), (256, need - 1)):
+        assert lib.si_moe_sort(16, 1000, 8, 8, 16, 16, 16, ws, n, None) == WS
     g = [16, m.SI_BF16, 4, 2, 64, 16, 16, 16, None]
     for i, v in ((0, None), (0, 17), (2, 0), (3, 0), (3, 9), (4, 0), (4, (1 << 24) + 1), (5, None), (6, None), (7, None)):
         a = list(g)
