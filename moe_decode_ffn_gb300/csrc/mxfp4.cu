@@ -36,17 +36,6 @@ SI_DEV MxTile mx_tile(const MxShape &s) {
 
 // VEC: the 8 values of a lane are loaded or stored as 16-byte words (every row
 // starts on a 16-byte boundary); otherwise one by one.
-template <typename T, bool VEC> SI_DEV void mx_load8(const T *p, float v[8]) {
-  if constexpr (VEC) {
-#pragma unroll
-    for (int i = 0; i < 8 / kVecOf<T>; ++i)
-      unpack16<T>(__ldg(reinterpret_cast<const uint4 *>(p) + i), v + i * kVecOf<T>);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_f32<T>(p[i]);
-  }
-}
-
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kMxThreads)
     quantize_mxfp4_kernel(const T *__restrict__ x, MxShape sh, uint8_t *__restrict__ codes,
@@ -63,16 +52,13 @@ __global__ void __launch_bounds__(kMxThreads)
   const bool in_col = c < sh.cols;                // cols % 32 == 0: 8 values are in or out together
 #pragma unroll
   for (int p0 = 0; p0 < kMxPasses; p0 += kMxInFlight) {
-    float v[kMxInFlight][8];
+    Raw8<T> v[kMxInFlight];
 #pragma unroll
     for (int u = 0; u < kMxInFlight; ++u) {
       const int64_t r = r0 + (p0 + u) * kMxRowsPerPass;
-      if (in_col && r < sh.rows) {
-        mx_load8<T, VEC>(src + r * sh.row_stride, v[u]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
-      }
+      if (!in_col || r >= sh.rows) v[u].zero();
+      else if constexpr (VEC) v[u].load16(src + r * sh.row_stride);
+      else v[u].load(src + r * sh.row_stride);
     }
 #pragma unroll
     for (int u = 0; u < kMxInFlight; ++u) {
@@ -90,8 +76,10 @@ __global__ void __launch_bounds__(kMxThreads)
         reinterpret_cast<const uint4 *>(s_tile)[threadIdx.x];
 }
 
+// 6 blocks an SM: 77.0 us for 98304 x 2048 bf16 values, against 86.2 with the 5
+// that the registers otherwise leave.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kMxThreads)
+__global__ void __launch_bounds__(kMxThreads, 6)
     dequantize_mxfp4_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
                             MxShape sh, T *__restrict__ y) {
   __shared__ __align__(16) uint8_t s_tile[kMxTileBytes];

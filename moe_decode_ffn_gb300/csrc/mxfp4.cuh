@@ -67,24 +67,6 @@ SI_DEV void mx_values8(uint32_t w, float v[8]) {
     v[2 * i + 1] = half_bits_to_float(static_cast<uint16_t>(h[i] >> 16));
   }
 }
-// Quantise 8 values of a 32-value block held by 4 consecutive lanes (8 each):
-// the codes of this lane's values; s is the same on the four lanes. Every lane
-// of the warp takes part.
-SI_DEV uint32_t mx_encode_4lanes(const float v[8], uint32_t &s) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  s = mx_scale_of(top);
-  const float up = mx_inv_scale(s);
-  float q[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = v[i] * up;
-  const uint32_t w = mx_codes8(q);
-  return s == 255u ? 0u : w;
-}
-
 // ---- rows of bf16, fp16 or fp32 ------------------------------------------------
 template <typename T> SI_DEV float to_f32(T v);
 template <> SI_DEV float to_f32<float>(float v) { return v; }
@@ -125,6 +107,69 @@ template <typename T> SI_DEV uint4 pack16(const float *v) {
     }
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Eight consecutive values of a row as they lie in memory.
+template <typename T> struct Raw8 {
+  static constexpr int kWords = 2 * static_cast<int>(sizeof(T));
+  uint32_t w[kWords];
+  SI_DEV void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+  }
+  SI_DEV void load16(const T *p) {               // p on a 16-byte boundary
+#pragma unroll
+    for (int i = 0; i < kWords / 4; ++i) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+      w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
+    }
+  }
+  SI_DEV void load(const T *p) {                 // value by value
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(p[i]);
+    } else {
+      const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = q[2 * i] | (static_cast<uint32_t>(q[2 * i + 1]) << 16);
+    }
+  }
+  SI_DEV void unpack(float v[8]) const {
+#pragma unroll
+    for (int i = 0; i < kWords / 4; ++i)
+      unpack16<T>(make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]), v + i * kVecOf<T>);
+  }
+};
+
+// Quantise 8 values of a 32-value block held by 4 consecutive lanes (8 each):
+// the codes of this lane's values; s is the same on the four lanes. Every lane
+// of the warp takes part. Magnitudes order like their bits, so the largest of a
+// 16-bit type is found two values at a time.
+template <typename T> SI_DEV uint32_t mx_encode_4lanes(const Raw8<T> &x, uint32_t &s) {
+  uint32_t top;
+  if constexpr (sizeof(T) == 4) {
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, x.w[i] & 0x7FFFFFFFu);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  } else {
+    constexpr uint32_t kAbs = 0x7FFF7FFFu;
+    uint32_t m = __vimax3_u16x2(x.w[0] & kAbs, x.w[1] & kAbs, x.w[2] & kAbs);
+    m = __vimax3_u16x2(m, x.w[3] & kAbs, __shfl_xor_sync(0xffffffffu, __vmaxu2(m, x.w[3] & kAbs), 1));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    m = max(m >> 16, m & 0xFFFFu);
+    if constexpr (std::is_same_v<T, __nv_bfloat16>) top = m << 16;
+    else top = __float_as_uint(half_bits_to_float(static_cast<uint16_t>(m)));
+  }
+  s = mx_scale_of(top);
+  const float up = mx_inv_scale(s);
+  float q[8];
+  x.unpack(q);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] *= up;
+  const uint32_t w = mx_codes8(q);
+  return s == 255u ? 0u : w;
 }
 
 }  // namespace si

@@ -588,13 +588,9 @@ __global__ void __launch_bounds__(256) quantize_scatter_kernel(ScatterArgs a) {
   // whole scale tiles (128 columns, 16 lanes): the blocks behind H get scale 0
   for (int c0 = (threadIdx.x & ~31) * 8; c0 < a.kt * 128; c0 += blockDim.x * 8) {
     const int c = c0 + lane * 8;
-    float v[8];
-    if (c < a.H) {
-      Load8<__nv_bfloat16>::run(a.x + t * a.H + c, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    }
+    Raw8<__nv_bfloat16> v;
+    if (c < a.H) v.load16(a.x + t * a.H + c);
+    else v.zero();
     uint32_t s;
     const uint32_t w = mx_encode_4lanes(v, s);
     uint32_t s4 = 0;
