@@ -4,21 +4,31 @@
 //   out[m][n] = sum_k a[m][k] w[n][k]            (si_mxfp4_matmul)
 //   h = silu(G x) * (U x), y = D h per pair      (si_moe_ffn_mxfp4)
 //
-// Both are one kernel: tcgen05.mma kind::mxf4 with block scales, the WEIGHT
-// rows as the 128-row operand and a tile of NT tokens as the N operand, so a
-// batch of few tokens wastes no tensor rows and every lane of tensor memory
-// holds one output feature. Products of two E2M1 values are exact and the
-// accumulators fp32.
+// Both are one kernel: tcgen05.mma kind::mxf4 with block scales. Products of two
+// E2M1 values are exact and the accumulators fp32. It has two orientations:
+//  - few tokens: 128 (or gate 128 and up 128) weight rows on the lanes of tensor
+//    memory, a tile of NT tokens as the N operand, so that a small batch wastes
+//    no tensor rows;
+//  - many tokens (TOK): 128 tokens on the lanes and 256 weight rows (gate 128 and
+//    up 128, or 256 neighbours) as the N operand. An MMA of N <= 128 takes about
+//    90 cycles whatever its N, one of N = 256 about 128, so this orientation does
+//    the same products in 4 MMAs a stage instead of 8; and a lane holds whole
+//    32-value blocks of its token, which quantises h without any exchange.
 //
-// A block of 352 threads: a thread of warp 0 keeps the codes of a ring of stages
-// coming (256 columns by tensor TMA in the 128-byte swizzle), lanes of warp 10
-// their scale tiles (plain bulk copies, one operand each: a thread is held up
-// by every copy it issues), one thread of warp 1 moves the scales into tensor
-// memory (tcgen05.cp) and issues the MMAs, warps 2..9 read the accumulators and write
-// the outputs (two warps per 32 lanes of tensor memory, each half of the
-// tokens). Blocks are persistent: tile i of block b is b + i * gridDim. The
-// accumulators are a ring too, so that the MMAs of a tile run beside the
-// epilogue of the one before.
+// A block: a thread of warp 0 keeps the codes of a ring of stages coming (256
+// columns by tensor TMA in the 128-byte swizzle), one thread of warp 1 moves the
+// scales into tensor memory (tcgen05.cp) and issues the MMAs, warps 2.. read the
+// accumulators and write the outputs (4 of them cover the 128 lanes of tensor
+// memory; each group of 4 takes a part of the tokens), and a thread of each of
+// the last warps keeps one operand's scale tiles coming. Blocks are persistent:
+// tile i of block b is b + i * gridDim. The accumulators are a ring too, so that
+// the MMAs of a tile run beside the epilogue of the one before.
+//
+// What bounds a long product is the one thread that issues: a stage is 6 scale
+// copies, 4 or 8 MMAs and a commit, and each of them takes 20 to 30 cycles to
+// issue, so everything else is kept out of that thread's way. A plain bulk copy of scales holds its thread up for
+// about 270 cycles, which is why every operand's scales have a thread of their
+// own.
 #include <cuda.h>
 
 #include <algorithm>
@@ -30,34 +40,44 @@
 
 namespace si {
 
-constexpr int kMmEpiWarps = 8, kMmEpiParts = kMmEpiWarps / 4;
-constexpr int kMmThreads = 96 + 32 * kMmEpiWarps;
-constexpr int kMmScaleWarp = 2 + kMmEpiWarps;
-constexpr int kMmEpiBytes = 512;       // staging of an epilogue warp: 8 tokens x 32 features of 2 bytes
 constexpr int kMmStageK = 256;         // columns of a stage: 128 bytes of codes per row
 constexpr int kMmABytes = 128 * 128;   // 128 weight rows of a stage
 
 enum MmMode { kMmPlain = 0, kMmGateUp = 1 };
 
 // MA: 128-row weight tiles of a block's tile (gate and up, or two neighbours).
-template <int MA, int NT> struct MmCfg {
+// NT: tokens of a tile. TOK: the tokens on the lanes (NT = 128).
+template <int MODE, int MA, int NT, bool TOK> struct MmCfg {
+  static_assert(!TOK || (MA == 2 && NT == 128), "128 tokens by 256 weight rows");
+  // epilogue warps: 4 for the lanes, times the parts of the columns. TOK: a part
+  // is 64 columns, which fit into registers, so that the accumulator is free
+  // before it is written; otherwise parts of the tokens.
+  static constexpr int kParts = TOK ? 4 : 2;
+  static constexpr int kEpiWarps = 4 * kParts;
+  static constexpr int kScaleWarp = 2 + kEpiWarps;
+  static constexpr int kThreads = 32 * (kScaleWarp + MA + 1);
   static constexpr int kBBytes = NT * 128;
   static constexpr int kSfBytes = 2 * kMxTileBytes;               // per operand tile and stage
   static constexpr int kStage = MA * kMmABytes + kBBytes + (MA + 1) * kSfBytes;
-  static constexpr int kMaxSmem = 227 * 1024 - kMmEpiWarps * kMmEpiBytes - 1536;   // less alignment and barriers
+  // 16-token groups of an epilogue warp's part, all read at once; staging for
+  // two of them at a time (16 tokens x 32 features of 2 bytes each)
+  static constexpr int kGroups = NT < 16 * kParts ? 1 : NT / 16 / kParts;
+  static constexpr int kEpiBytes = MODE == kMmGateUp || TOK ? 0 : kGroups == 1 ? 1024 : 2048;
+  static constexpr int kMaxSmem = 227 * 1024 - kEpiWarps * kEpiBytes - 1536;   // less alignment and barriers
   static constexpr int kStages = kMaxSmem / kStage < 8 ? kMaxSmem / kStage : 8;
-  // tensor memory: a ring of accumulators of NT columns (a tile takes MA of
-  // them; a third one of 128 columns lets the next tile start when the first
-  // half of this one is written), then the scales of every stage (a column
-  // holds 4 blocks of 32 rows: 128 rows x 8 blocks take 8 columns)
+  // tensor memory: a ring of accumulators (a tile takes one of 256 columns, or MA
+  // of NT columns), then the scales of every stage (a column holds 4 blocks of 32
+  // rows: 128 rows x 8 blocks take 8 columns)
+  static constexpr int kAccCols = TOK ? 256 : NT;
+  static constexpr int kTileAccs = TOK ? 1 : MA;
   static constexpr int kSfCols = 8 * (MA + 1);
-  static constexpr int kFit = (512 - kStages * kSfCols) / NT;
-  static constexpr int kAccs = kFit < 2 * MA ? kFit : 2 * MA;
-  static constexpr int kUsed = kAccs * NT + kStages * kSfCols;
+  static constexpr int kFit = (512 - kStages * kSfCols) / kAccCols;
+  static constexpr int kAccs = kFit < 2 * kTileAccs ? kFit : 2 * kTileAccs;
+  static constexpr int kUsed = kAccs * kAccCols + kStages * kSfCols;
   static constexpr int kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
-  static_assert(kAccs >= MA && kUsed <= 512, "tensor memory has 512 columns");
+  static_assert(kAccs >= kTileAccs && kUsed <= 512, "tensor memory has 512 columns");
   static constexpr int kBars = 2 * kStages + 2 * kAccs + 1;
-  static constexpr int kSmem = kStages * kStage + kMmEpiWarps * kMmEpiBytes + 1024 + 512;
+  static constexpr int kSmem = kStages * kStage + kEpiWarps * kEpiBytes + 1024 + 512;
   static_assert(8 * kBars + 4 <= 512, "barriers");
 };
 
@@ -73,6 +93,7 @@ struct MmParams {
   // plain: out[token][feature]
   void *out;
   int64_t ld;
+  int wide;                            // rows of whole 32-byte words
   // gate/up: the MXFP4 rows of h
   uint8_t *h_codes, *h_scales;
   int h_kt;
@@ -171,7 +192,7 @@ SI_DEV void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "
 
 // Outputs whose rows start on 16-byte boundaries leave in 16-byte words (2-byte
 // types: VEC); other rows value by value, lane = feature.
-enum MmOut { kMmBf16, kMmF16, kMmF32, kMmBf16Vec, kMmF16Vec };
+enum MmOut { kMmBf16, kMmF16, kMmF32, kMmBf16Vec, kMmF16Vec, kMmF32Vec };
 
 template <int OUT> SI_DEV void mm_store(void *out, int64_t at, float v) {
   if constexpr (OUT == kMmBf16) static_cast<__nv_bfloat16 *>(out)[at] = __float2bfloat16_rn(v);
@@ -197,46 +218,69 @@ SI_DEV void tmem_ld_frag(uint32_t taddr, uint32_t r[8]) {
 }
 
 // One accumulator (128 features x count tokens) of this warp's 32 features, the
-// warp's part of the 16-token groups.
-template <int OUT>
+// warp's part of the tokens. release() once everything is in registers.
+template <int OUT, typename C, typename Release>
 SI_DEV void mm_write_plain(const MmParams &p, int f0, int64_t row0, int count, uint32_t acc, int part, int lane,
-                           uint8_t *stage) {
-  if (f0 >= p.rows) return;
-#pragma unroll 1
-  for (int j0 = 16 * part; j0 < count; j0 += 16 * kMmEpiParts) {
-    if constexpr (OUT == kMmBf16Vec || OUT == kMmF16Vec) {
-      // 8 x 8 blocks transposed through shared memory: a token's 32 features
-      // are 64 bytes, its four 16-byte words permuted by the token so that
-      // neither side of the staging meets a bank twice
-      uint32_t lo[8], hi[8];
-      tmem_ld_frag(acc + j0, lo);
-      tmem_ld_frag(acc + (16u << 16) + j0, hi);
-      tmem_wait_ld();
+                           uint8_t *stage, Release release) {
+  constexpr int G = C::kGroups;
+  const int j0 = 16 * G * part;
+  const int left = f0 < p.rows ? count - j0 : 0;        // of this warp's tokens
+  if constexpr (OUT == kMmBf16Vec || OUT == kMmF16Vec) {
+    // 8 x 8 blocks transposed through shared memory: a token's 32 features are
+    // 64 bytes, its four 16-byte words permuted by the token so that neither
+    // side of the staging meets a bank twice
+    uint32_t lo[G][8], hi[G][8];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const uint32_t m0 = mm_pack<OUT>(lo[4 * c], lo[4 * c + 1]), m1 = mm_pack<OUT>(lo[4 * c + 2], lo[4 * c + 3]);
-        const uint32_t m2 = mm_pack<OUT>(hi[4 * c], hi[4 * c + 1]), m3 = mm_pack<OUT>(hi[4 * c + 2], hi[4 * c + 3]);
-        const int wj = lane & 7, wc = lane >> 3;      // this lane's row address: token wj, word wc
-        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
-                         smem_addr(stage + wj * 64 + ((wc ^ ((wj >> 1) & 3)) * 16))),
-                     "r"(m0), "r"(m1), "r"(m2), "r"(m3)
+    for (int i = 0; i < G; ++i) {
+      if (16 * i >= left) break;
+      tmem_ld_frag(acc + j0 + 16 * i, lo[i]);
+      tmem_ld_frag(acc + (16u << 16) + j0 + 16 * i, hi[i]);
+    }
+    tmem_wait_ld();
+    release();
+    const int wj = lane & 7, wc = lane >> 3;            // this lane's row address: token wj, word wc
+    const int rj = lane >> 2, rc = lane & 3;            // the word that it writes out
+    const uint32_t put = smem_addr(stage + wj * 64 + ((wc ^ ((wj >> 1) & 3)) * 16));
+    const uint8_t *get = stage + rj * 64 + ((rc ^ ((rj >> 1) & 3)) * 16);
+    uint16_t *out = static_cast<uint16_t *>(p.out) + (row0 + j0 + rj) * p.ld + f0 + 8 * rc;
+    const bool in = f0 + 8 * rc < p.rows;               // rows % 8 == 0: a word is whole or absent
+#pragma unroll
+    for (int i0 = 0; i0 < G; i0 += 2) {
+      if (16 * i0 >= left) break;
+      constexpr int kN = G == 1 ? 2 : 4;                // 8-token blocks of a round
+      __syncwarp();                                     // the staging has been read
+#pragma unroll
+      for (int c = 0; c < kN; ++c) {
+        const int i = i0 + c / 2;
+        if (i >= G) break;
+        const uint32_t *l = lo[i] + 4 * (c & 1), *h = hi[i] + 4 * (c & 1);
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(put + c * 512),
+                     "r"(mm_pack<OUT>(l[0], l[1])), "r"(mm_pack<OUT>(l[2], l[3])), "r"(mm_pack<OUT>(h[0], h[1])),
+                     "r"(mm_pack<OUT>(h[2], h[3]))
                      : "memory");
-        __syncwarp();
-        const int rj = lane >> 2, rc = lane & 3, j = j0 + 8 * c + rj, f = f0 + 8 * rc;
-        const uint4 v = *reinterpret_cast<const uint4 *>(stage + rj * 64 + ((rc ^ ((rj >> 1) & 3)) * 16));
-        __syncwarp();
-        if (j < count && f < p.rows)                  // rows % 8 == 0: a word is whole or absent
-          *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + (row0 + j) * p.ld + f) = v;
       }
-    } else {
-      uint32_t r[16];
-      tmem_ld16(acc + j0, r);
-      tmem_wait_ld();
-      if (f0 + lane < p.rows) {
+      __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (j0 + j < count) mm_store<OUT>(p.out, (row0 + j0 + j) * p.ld + f0 + lane, __uint_as_float(r[j]));
+      for (int c = 0; c < kN; ++c) {
+        if (i0 + c / 2 >= G) break;
+        const int j = 16 * i0 + 8 * c;
+        const uint4 v = *reinterpret_cast<const uint4 *>(get + c * 512);
+        if (in && j + rj < left) *reinterpret_cast<uint4 *>(out + j * p.ld) = v;
       }
+    }
+  } else {
+    uint32_t r[G][16];
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      if (16 * i >= left) break;
+      tmem_ld16(acc + j0 + 16 * i, r[i]);
+    }
+    tmem_wait_ld();
+    release();
+    if (f0 + lane < p.rows) {
+#pragma unroll
+      for (int j = 0; j < 16 * G; ++j)
+        if (j < left) mm_store<OUT>(p.out, (row0 + j0 + j) * p.ld + f0 + lane, __uint_as_float(r[j / 16][j % 16]));
     }
   }
 }
@@ -263,7 +307,7 @@ SI_DEV float mm_silu_mul(float g, float u) {
 // h = silu(g) u of a lane's feature for 16 tokens, then MXFP4: the 32 lanes of
 // the warp are one block of every token, so its scale is a warp maximum. Lane j
 // keeps the scale of token j and its multiplier, which the others fetch.
-template <int NT>
+template <int NT, int PARTS>
 SI_DEV void mm_write_h(const MmParams &p, const MmTile &t, uint32_t acc_g, uint32_t acc_u, int q, int part,
                        int lane) {
   const int64_t row0 = static_cast<int64_t>(t.tt) * NT;
@@ -271,22 +315,30 @@ SI_DEV void mm_write_h(const MmParams &p, const MmTile &t, uint32_t acc_g, uint3
   const bool live = blk * 32 < p.rows;          // rows % 32 == 0: the whole warp or none of it
   const size_t row_bytes = static_cast<size_t>(p.rows) / 2;
   uint8_t *sf = p.h_scales + (static_cast<size_t>(t.tt) * p.h_kt + t.rt) * kMxTileBytes;
+  if (!live) {                                  // behind the last feature: scales that multiply zeros
+    for (int j = 16 * part + lane; j < t.count; j += 16 * PARTS)
+      if (lane < 16) sf[mx_scale_byte(j, blk)] = 0;
+    return;
+  }
+  uint32_t g[16], u[16];
+  if (16 * part < t.count) {
+    tmem_ld16(acc_g + 16 * part, g);
+    tmem_ld16(acc_u + 16 * part, u);
+  }
 #pragma unroll 1
-  for (int j0 = 16 * part; j0 < t.count; j0 += 16 * kMmEpiParts) {
+  for (int j0 = 16 * part; j0 < t.count; j0 += 16 * PARTS) {
     const int js = j0 + (lane & 15);            // the token whose scale this lane keeps
-    if (!live) {                                // behind the last feature: scales that multiply zeros
-      if (lane < 16 && js < t.count) sf[mx_scale_byte(js, blk)] = 0;
-      continue;
-    }
-    uint32_t g[16], u[16];
-    tmem_ld16(acc_g + j0, g);
-    tmem_ld16(acc_u + j0, u);
     tmem_wait_ld();
     float h[16];
     uint32_t top = 0;
 #pragma unroll
+    for (int j = 0; j < 16; ++j) h[j] = mm_silu_mul(__uint_as_float(g[j]), __uint_as_float(u[j]));
+    if (j0 + 16 * PARTS < t.count) {      // the next group's accumulators meanwhile
+      tmem_ld16(acc_g + j0 + 16 * PARTS, g);
+      tmem_ld16(acc_u + j0 + 16 * PARTS, u);
+    }
+#pragma unroll
     for (int j = 0; j < 16; ++j) {
-      h[j] = mm_silu_mul(__uint_as_float(g[j]), __uint_as_float(u[j]));
       const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h[j]) & 0x7FFFFFFFu);
       if ((lane & 15) == j) top = m;
     }
@@ -311,6 +363,112 @@ SI_DEV void mm_write_h(const MmParams &p, const MmTile &t, uint32_t acc_g, uint3
   }
 }
 
+// ---- epilogues, tokens on the lanes ---------------------------------------------
+
+SI_DEV void tmem_ld32(uint32_t taddr, uint32_t r[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+// 32 bytes of a row: one sector, one store.
+SI_DEV void st_global32(void *p, const uint32_t w[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// 64 features (from f0) of this lane's token `j`, 32 at a time (a block's warps
+// leave 80 registers a thread); 2-byte outputs wait, packed, until all are read.
+template <int OUT, typename Release>
+SI_DEV void mm_write_tokens(const MmParams &p, int f0, int64_t row0, int j, bool valid, uint32_t acc, Release release) {
+  constexpr int kSize = OUT == kMmF32Vec ? 4 : 2;
+  constexpr int kPer = 32 / kSize;               // values of a 32-byte word
+  constexpr int kWords = 8 * kSize;              // words of 32 features
+  const bool any = f0 < p.rows;
+  uint8_t *out = static_cast<uint8_t *>(p.out) + ((row0 + j) * p.ld + f0) * kSize;
+  auto write = [&](int c0, const uint32_t *w) {  // features f0 + c0 .. + 31
+#pragma unroll
+    for (int c = 0; c < 32; c += kPer, w += 8) {
+      if (f0 + c0 + c >= p.rows) break;
+      uint8_t *o = out + (c0 + c) * kSize;
+      const bool whole = f0 + c0 + c + kPer <= p.rows;
+      if (p.wide && whole) {
+        st_global32(o, w);
+      } else {                                   // rows of 16-byte words
+        *reinterpret_cast<uint4 *>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (whole) *reinterpret_cast<uint4 *>(o + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+    }
+  };
+  uint32_t w[2][kWords];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (any) {
+      uint32_t r[32];
+      tmem_ld32(acc + 32 * h, r);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        if constexpr (OUT == kMmF32Vec) w[h][i] = r[i];
+        else w[h][i] = mm_pack<OUT>(r[2 * i], r[2 * i + 1]);
+      }
+    }
+    if (h == 1) release();
+    if (OUT == kMmF32Vec && any && valid) write(32 * h, w[h]);
+  }
+  if (OUT != kMmF32Vec && any && valid) {
+    write(0, w[0]);
+    write(32, w[1]);
+  }
+}
+
+// h = silu(g) u of one block of 32 features of this lane's token, as MXFP4: the
+// block lies in this lane's registers.
+template <typename Release>
+SI_DEV void mm_write_h_tokens(const MmParams &p, const MmTile &t, int blk, int j, bool valid, uint32_t acc_g,
+                              uint32_t acc_u, Release release) {
+  const bool live = blk * 32 < p.rows;           // rows % 32 == 0
+  float h[32];
+  uint32_t top = 0;
+  if (live) {
+#pragma unroll
+    for (int i0 = 0; i0 < 32; i0 += 16) {
+      uint32_t g[16], u[16];
+      tmem_ld16(acc_g + i0, g);
+      tmem_ld16(acc_u + i0, u);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        h[i0 + i] = mm_silu_mul(__uint_as_float(g[i]), __uint_as_float(u[i]));
+        top = max(top, __float_as_uint(h[i0 + i]) & 0x7FFFFFFFu);
+      }
+    }
+  }
+  release();
+  if (!valid) return;
+  uint8_t *sf = p.h_scales + (static_cast<size_t>(t.tt) * p.h_kt + t.rt) * kMxTileBytes + mx_scale_byte(j, blk);
+  if (!live) {                                   // behind the last feature: a scale that multiplies zeros
+    *sf = 0;
+    return;
+  }
+  const uint32_t s = mx_scale_of(top);
+  const float up = mx_inv_scale(s);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) h[i] *= up;
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = s == 255u ? 0u : mx_codes8(h + 8 * i);
+  *reinterpret_cast<uint4 *>(p.h_codes + (static_cast<size_t>(t.tt) * 128 + j) * (static_cast<size_t>(p.rows) / 2) +
+                             blk * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+  *sf = static_cast<uint8_t>(s);
+}
+
 // ---- the kernel ----------------------------------------------------------------
 
 // The tiles of weight rows that tile t of the list reads, and of them the ones
@@ -319,21 +477,24 @@ template <int MODE, int MA> SI_DEV int mm_operands(const MmParams &p, const MmTi
   return MODE == kMmGateUp || MA == 1 || t.rt * MA * 128 + 128 < p.rows ? MA : 1;
 }
 
-template <int MODE, int MA, int NT, int OUT>
-__global__ void __launch_bounds__(kMmThreads, 1) mxfp4_mm_kernel(const __grid_constant__ MmParams p) {
-  using C = MmCfg<MA, NT>;
+template <int MODE, int MA, int NT, bool TOK, int OUT>
+__global__ void __launch_bounds__(MmCfg<MODE, MA, NT, TOK>::kThreads, 1)
+    mxfp4_mm_kernel(const __grid_constant__ MmParams p) {
+  using C = MmCfg<MODE, MA, NT, TOK>;
   constexpr int S = C::kStages, U = C::kAccs;
   extern __shared__ uint8_t mm_smem[];
   uint8_t *base = mm_smem + ((1024u - (smem_addr(mm_smem) & 1023u)) & 1023u);
   uint8_t *staging = base + S * C::kStage;
-  uint64_t *full = reinterpret_cast<uint64_t *>(staging + kMmEpiWarps * kMmEpiBytes);
+  uint64_t *full = reinterpret_cast<uint64_t *>(staging + C::kEpiWarps * C::kEpiBytes);
   uint64_t *empty = full + S, *acc_full = empty + S, *acc_empty = acc_full + U, *drain = acc_empty + U;
   uint32_t *s_taddr = reinterpret_cast<uint32_t *>(drain + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_ks = (p.K + kMmStageK - 1) / kMmStageK;
+  // the operand whose scales this warp brings: weights 0 .. MA - 1, tokens MA
+  const int operand = warp - C::kScaleWarp;
 
-  // the copies of stage ks of a tile, codes and scales, weights and tokens; the
-  // full barrier of a stage takes the codes' and the scales' arrival
+  // the copies of stage ks of a tile; the full barrier of a stage takes the
+  // arrival of the codes and of every operand's scales
   auto load_weights = [&](const MmTile &t, int na, int ks, int s) {
     uint8_t *st = base + s * C::kStage;
     mbar_arrive_expect_tx(full + s, na * kMmABytes + C::kBBytes);
@@ -347,43 +508,41 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_mm_kernel(const __grid_co
   auto load_tokens = [&](const MmTile &t, int ks, int s) {
     tma_load3(base + s * C::kStage + MA * kMmABytes, &p.b, ks * 128, t.tt * NT, 0, full + s);
   };
-  auto load_scales = [&](const MmTile &t, int a, int ks, int s) {   // operand a; a == MA: the tokens
-    const int rt = MODE == kMmGateUp ? t.rt : t.rt * MA + a;
-    const uint8_t *src = a == MA ? p.sb : MODE == kMmGateUp && a == 1 ? p.sa1 : p.sa0;
-    const size_t tile = a == MA ? t.tt : t.mat * p.row_tiles + rt;
-    bulk_g2s(base + s * C::kStage + MA * kMmABytes + C::kBBytes + a * C::kSfBytes,
-             src + (tile * p.kt + 2 * ks) * kMxTileBytes, min(2, p.kt - 2 * ks) * kMxTileBytes, full + s);
-  };
-  auto expect_scales = [&](int na, int ks, int s) {
-    mbar_arrive_expect_tx(full + s, (na + 1) * min(2, p.kt - 2 * ks) * kMxTileBytes);
+  auto load_scales = [&](const MmTile &t, int na, int ks, int s) {   // of this warp's operand
+    if (operand >= na && operand < MA) {
+      mbar_arrive(full + s);         // no such weights in this tile
+      return;
+    }
+    const int rt = MODE == kMmGateUp ? t.rt : t.rt * MA + operand;
+    const uint8_t *src = operand == MA ? p.sb : MODE == kMmGateUp && operand == 1 ? p.sa1 : p.sa0;
+    const size_t tile = operand == MA ? t.tt : t.mat * p.row_tiles + rt;
+    const uint32_t bytes = min(2, p.kt - 2 * ks) * kMxTileBytes;
+    mbar_arrive_expect_tx(full + s, bytes);
+    bulk_g2s(base + s * C::kStage + MA * kMmABytes + C::kBBytes + operand * C::kSfBytes,
+             src + (tile * p.kt + 2 * ks) * kMxTileBytes, bytes, full + s);
   };
 
   int ahead = 0;                     // stages whose weights were requested before the wait
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(full + i, 2);
+      mbar_init(full + i, 2 + MA);
       mbar_init(empty + i, 1);
     }
     for (int i = 0; i < U; ++i) {
       mbar_init(acc_full + i, 1);
-      mbar_init(acc_empty + i, kMmEpiWarps);
+      mbar_init(acc_empty + i, C::kEpiWarps);
     }
     mbar_init(drain, 1);
     fence_mbar_init();
   }
   if (p.early) {                     // uniform over the grid
     __syncthreads();
-    if ((threadIdx.x == 0 || warp == kMmScaleWarp) && static_cast<int>(blockIdx.x) < mm_total(p, NT)) {
+    if (lane == 0 && (warp == 0 || (operand >= 0 && operand < MA)) && static_cast<int>(blockIdx.x) < mm_total(p, NT)) {
       const MmTile t = mm_tile(p, blockIdx.x, NT);
       const int na = mm_operands<MODE, MA>(p, t);
       for (; ahead < S && ahead < n_ks; ++ahead) {
-        if (warp == 0) {
-          load_weights(t, na, ahead, ahead);
-        } else {
-          if (lane == 0) expect_scales(na, ahead, ahead);
-          __syncwarp();
-          if (lane < na) load_scales(t, lane, ahead, ahead);
-        }
+        if (warp == 0) load_weights(t, na, ahead, ahead);
+        else load_scales(t, na, ahead, ahead);
       }
     }
   }
@@ -410,8 +569,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_mm_kernel(const __grid_co
     return t;
   };
 
-  if (warp == 0 || warp == kMmScaleWarp) {
-    if (warp != 0 || lane == 0) {    // one thread of warp 0; warp 10 together
+  if (warp == 0 || operand >= 0) {
+    if (lane == 0) {
       uint32_t it = 0;
       bool ok = true;
       for (int w = blockIdx.x; ok && w < total; w += step) {
@@ -420,17 +579,15 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_mm_kernel(const __grid_co
         for (int ks = 0; ks < n_ks; ++ks, ++it) {
           const int s = it % S;
           const bool fresh = static_cast<int>(it) >= ahead;
-          if (fresh) ok = mbar_wait_bounded(empty + s, ((it / S) & 1) ^ 1, p.status);
+          if (fresh && !mbar_wait_bounded(empty + s, ((it / S) & 1) ^ 1, p.status)) {
+            ok = false;
+            break;
+          }
           if (warp == 0) {
-            if (!ok) break;
             if (fresh) load_weights(t, na, ks, s);
             load_tokens(t, ks, s);
-          } else {
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            if (fresh && lane == 0) expect_scales(na, ks, s);
-            __syncwarp();
-            if (lane < na ? fresh : lane == MA) load_scales(t, lane, ks, s);
+          } else if (fresh) {
+            load_scales(t, na, ks, s);
           }
         }
       }
@@ -440,83 +597,97 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_mm_kernel(const __grid_co
       }
     }
   } else if (warp == 1) {
+    // the warp walks over the stages together, the leader alone waits and issues
     const bool leader = elect_lane();
     const uint32_t smem0 = smem_addr(base);
     uint32_t n = 0;                  // accumulators taken so far
     int s = 0;                       // stage and its parity
     uint32_t parity = 0;
     bool ok = true;
-    auto wait_all = [&](uint64_t *bar, uint32_t ph) {
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, ph, p.status));
-    };
-    for (int w = blockIdx.x; ok && w < total; w += step) {
+    for (int w = blockIdx.x; w < total; w += step) {
       const MmTile t = next_tile(w);
       const int na = mm_operands<MODE, MA>(p, t);
-      uint32_t d[MA];
+      const int nu = TOK ? 1 : na;   // accumulators of this tile
+      uint32_t d[C::kTileAccs];
 #pragma unroll
-      for (int a = 0; a < MA; ++a) {
+      for (int a = 0; a < C::kTileAccs; ++a) {
         const uint32_t u = (n + a) % U;
-        d[a] = tmem + u * NT;
-        if (a < na && ok) wait_all(acc_empty + u, (((n + a) / U) & 1) ^ 1);
+        d[a] = tmem + u * C::kAccCols;
+        if (leader && a < nu && ok) ok = mbar_wait_bounded(acc_empty + u, (((n + a) / U) & 1) ^ 1, p.status);
       }
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t idesc = mm_idesc((t.count + 15) & ~15);
+      const uint32_t idesc = mm_idesc(TOK ? 128 * na : (t.count + 15) & ~15);
       for (int ks = 0; ks < n_ks; ++ks) {
-        wait_all(full + s, parity);
-        if (!ok) break;
-        tc_fence_after();
         const int n64 = min(4, (p.K - ks * kMmStageK + 63) / 64);
         const uint32_t st = smem0 + s * C::kStage;
         const uint32_t sf = mm_scale_lo(st + MA * kMmABytes + C::kBBytes);
         const uint32_t ca = mm_codes_lo(st), cb = mm_codes_lo(st + MA * kMmABytes);
-        const uint32_t tsf = tmem + U * NT + s * C::kSfCols;
-        if (leader) {
+        const uint32_t tsf = tmem + U * C::kAccCols + s * C::kSfCols;
+        const uint32_t more = ks > 0;
+        // columns of operand a's scales: TOK keeps the two weight tiles of a 128-column
+        // piece side by side, the 256 rows of one operand
+        auto sf_cols = [&](int kt, int a) { return TOK && a < MA ? tsf + kt * 8 + a * 4 : tsf + a * 8 + kt * 4; };
+        auto copy_sf = [&](int kt, int a) {
+          mm_copy_sf(sf_cols(kt, a), sf + (a * C::kSfBytes + kt * kMxTileBytes) / 16);
+        };
+        auto mma = [&](int i, int a) {
+          const uint32_t id = idesc | (static_cast<uint32_t>(i & 1) * 2u << 29) | (static_cast<uint32_t>(i & 1) * 2u << 4);
+          const uint32_t acc = i > 0 ? 1u : more;
+          if constexpr (TOK)
+            mm_mma(d[0], cb + i * 32 / 16, ca + i * 32 / 16, id, sf_cols(i >> 1, MA), sf_cols(i >> 1, 0), acc);
+          else
+            mm_mma(d[a], ca + (a * kMmABytes + i * 32) / 16, cb + i * 32 / 16, id, sf_cols(i >> 1, a),
+                   sf_cols(i >> 1, MA), acc);
+        };
+        if (leader && ok) ok = mbar_wait_bounded(full + s, parity, p.status);
+        if (leader && ok) {
+          tc_fence_after();
+          if (n64 == 4 && na == MA) {
 #pragma unroll
-          for (int kt = 0; kt < 2; ++kt) {
-            if (2 * kt >= n64) break;
+            for (int i = 0; i < 2 * (MA + 1); ++i) copy_sf(i / (MA + 1), i % (MA + 1));
 #pragma unroll
-            for (int a = 0; a <= MA; ++a)
-              if (a < na || a == MA)
-                mm_copy_sf(tsf + a * 8 + kt * 4, sf + (a * C::kSfBytes + kt * kMxTileBytes) / 16);
-          }
+            for (int i = 0; i < 4 * C::kTileAccs; ++i) mma(i / C::kTileAccs, i % C::kTileAccs);
+          } else {                   // the last columns, or the last rows of an odd number of tiles
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (i >= n64) break;
-            const uint32_t id = idesc | (static_cast<uint32_t>(i & 1) * 2u << 29) | (static_cast<uint32_t>(i & 1) * 2u << 4);
+            for (int kt = 0; kt < 2; ++kt) {
+              if (2 * kt >= n64) break;
 #pragma unroll
-            for (int a = 0; a < MA; ++a)
-              if (a < na)
-                mm_mma(d[a], ca + (a * kMmABytes + i * 32) / 16, cb + i * 32 / 16, id, tsf + a * 8 + (i >> 1) * 4,
-                       tsf + MA * 8 + (i >> 1) * 4, ks > 0 || i > 0);
+              for (int a = 0; a <= MA; ++a)
+                if (a < na || a == MA) copy_sf(kt, a);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (i >= n64) break;
+#pragma unroll
+              for (int a = 0; a < C::kTileAccs; ++a)
+                if (a < nu) mma(i, a);
+            }
           }
           umma_commit(empty + s);
         }
-        __syncwarp();
         if (++s == S) {
           s = 0;
           parity ^= 1;
         }
       }
-      if (ok && leader)
-        for (int a = 0; a < na; ++a) umma_commit(acc_full + (n + a) % U);
-      __syncwarp();
-      n += na;
+      if (leader && ok)
+        for (int a = 0; a < nu; ++a) umma_commit(acc_full + (n + a) % U);
+      n += nu;
     }
-    if (!ok) {   // MMAs in flight end before the tensor memory goes
-      if (leader) umma_commit(drain);
+    if (leader && !ok) {   // MMAs in flight end before the tensor memory goes
+      umma_commit(drain);
       mbar_wait_bounded(drain, 0, p.status);
     }
+    __syncwarp();
   } else {
     const int q = warp & 3, part = (warp - 2) >> 2;   // the 32 lanes of tensor memory this warp may read
     const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    uint8_t *stage = staging + (warp - 2) * kMmEpiBytes;
+    uint8_t *stage = staging + (warp - 2) * C::kEpiBytes;
     uint32_t n = 0;
     bool ok = true;
     auto wait_acc = [&](uint32_t i) {
       ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_full + i % U, (i / U) & 1, p.status));
       tc_fence_after();
-      return lanes + (i % U) * NT;
+      return lanes + (i % U) * C::kAccCols;
     };
     auto free_acc = [&](uint32_t i) {
       tc_fence_before();
@@ -525,12 +696,23 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_mm_kernel(const __grid_co
     };
     for (int w = blockIdx.x; ok && w < total; w += step) {
       const MmTile t = next_tile(w);
-      if constexpr (MODE == kMmGateUp) {
+      if constexpr (TOK) {
+        const uint32_t acc = wait_acc(n);
+        if (!ok) break;
+        const int j = q * 32 + lane;
+        auto release = [&] { free_acc(n); };
+        if constexpr (MODE == kMmGateUp)
+          mm_write_h_tokens(p, t, t.rt * 4 + part, j, j < t.count, acc + part * 32, acc + 128 + part * 32, release);
+        else
+          mm_write_tokens<OUT>(p, t.rt * 256 + part * 64, static_cast<int64_t>(t.tt) * NT, j, j < t.count,
+                               acc + part * 64, release);
+        ++n;
+      } else if constexpr (MODE == kMmGateUp) {
         const uint32_t g = wait_acc(n);
         if (!ok) break;
         const uint32_t u = wait_acc(n + 1);
         if (!ok) break;
-        mm_write_h<NT>(p, t, g, u, q, part, lane);
+        mm_write_h<NT, C::kParts>(p, t, g, u, q, part, lane);
         free_acc(n);
         free_acc(n + 1);
         n += 2;
@@ -539,9 +721,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_mm_kernel(const __grid_co
         for (int a = 0; a < na; ++a, ++n) {
           const uint32_t acc = wait_acc(n);
           if (!ok) break;
-          mm_write_plain<OUT>(p, (t.rt * MA + a) * 128 + q * 32, static_cast<int64_t>(t.tt) * NT, t.count, acc, part,
-                              lane, stage);
-          free_acc(n);
+          mm_write_plain<OUT, C>(p, (t.rt * MA + a) * 128 + q * 32, static_cast<int64_t>(t.tt) * NT, t.count, acc, part,
+                                 lane, stage, [&] { free_acc(n); });
         }
       }
     }
@@ -634,33 +815,30 @@ static bool codes_map(CUtensorMap *m, const void *codes, int64_t mats, int64_t r
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE, int MA, int NT, int OUT>
+template <int MODE, int MA, int NT, bool TOK, int OUT>
 static cudaError_t mm_launch_as(const MmParams &p, int64_t max_tiles, cudaStream_t s) {
-  using C = MmCfg<MA, NT>;
-  const cudaError_t e = allow_smem(mxfp4_mm_kernel<MODE, MA, NT, OUT>, C::kSmem);
+  using C = MmCfg<MODE, MA, NT, TOK>;
+  const cudaError_t e = allow_smem(mxfp4_mm_kernel<MODE, MA, NT, TOK, OUT>, C::kSmem);
   if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(max_tiles, sm_count()));
-  return launch_pdl(mxfp4_mm_kernel<MODE, MA, NT, OUT>, dim3(grid), dim3(kMmThreads), C::kSmem, s, p);
+  return launch_pdl(mxfp4_mm_kernel<MODE, MA, NT, TOK, OUT>, dim3(grid), dim3(C::kThreads), C::kSmem, s, p);
 }
 template <int OUT>
-static cudaError_t mm_launch_dense(int ma, int nt, const MmParams &p, int64_t max_tiles, cudaStream_t s) {
-  if (ma == 2) return mm_launch_as<kMmPlain, 2, 128, OUT>(p, max_tiles, s);
-  return nt == 16   ? mm_launch_as<kMmPlain, 1, 16, OUT>(p, max_tiles, s)
-         : nt == 32 ? mm_launch_as<kMmPlain, 1, 32, OUT>(p, max_tiles, s)
-         : nt == 64 ? mm_launch_as<kMmPlain, 1, 64, OUT>(p, max_tiles, s)
-                    : mm_launch_as<kMmPlain, 1, 128, OUT>(p, max_tiles, s);
+static cudaError_t mm_launch_dense(int nt, const MmParams &p, int64_t max_tiles, cudaStream_t s) {
+  return nt == 16   ? mm_launch_as<kMmPlain, 1, 16, false, OUT>(p, max_tiles, s)
+         : nt == 32 ? mm_launch_as<kMmPlain, 1, 32, false, OUT>(p, max_tiles, s)
+         : nt == 64 ? mm_launch_as<kMmPlain, 1, 64, false, OUT>(p, max_tiles, s)
+                    : mm_launch_as<kMmPlain, 1, 128, false, OUT>(p, max_tiles, s);
 }
 static cudaError_t mm_launch_gateup(int nt, const MmParams &p, int64_t max_tiles, cudaStream_t s) {
-  return nt == 16   ? mm_launch_as<kMmGateUp, 2, 16, 0>(p, max_tiles, s)
-         : nt == 32 ? mm_launch_as<kMmGateUp, 2, 32, 0>(p, max_tiles, s)
-         : nt == 64 ? mm_launch_as<kMmGateUp, 2, 64, 0>(p, max_tiles, s)
-                    : mm_launch_as<kMmGateUp, 2, 96, 0>(p, max_tiles, s);
+  return nt == 16   ? mm_launch_as<kMmGateUp, 2, 16, false, 0>(p, max_tiles, s)
+         : nt == 32 ? mm_launch_as<kMmGateUp, 2, 32, false, 0>(p, max_tiles, s)
+                    : mm_launch_as<kMmGateUp, 2, 128, true, 0>(p, max_tiles, s);
 }
 static cudaError_t mm_launch_down(int nt, const MmParams &p, int64_t max_tiles, cudaStream_t s) {
-  return nt == 16   ? mm_launch_as<kMmPlain, 1, 16, kMmBf16Vec>(p, max_tiles, s)
-         : nt == 32 ? mm_launch_as<kMmPlain, 1, 32, kMmBf16Vec>(p, max_tiles, s)
-         : nt == 64 ? mm_launch_as<kMmPlain, 1, 64, kMmBf16Vec>(p, max_tiles, s)
-                    : mm_launch_as<kMmPlain, 2, 96, kMmBf16Vec>(p, max_tiles, s);
+  return nt == 16   ? mm_launch_as<kMmPlain, 1, 16, false, kMmBf16Vec>(p, max_tiles, s)
+         : nt == 32 ? mm_launch_as<kMmPlain, 1, 32, false, kMmBf16Vec>(p, max_tiles, s)
+                    : mm_launch_as<kMmPlain, 2, 128, true, kMmBf16Vec>(p, max_tiles, s);
 }
 
 // ---- expert FFN: workspace ---------------------------------------------------
@@ -673,10 +851,10 @@ struct FfnMxGeom {
 static FfnMxGeom ffn_mx_geom(const si_mxfp4_experts &L, int n_tokens, int top_k) {
   FfnMxGeom g{};
   g.pairs = static_cast<int64_t>(n_tokens) * top_k;
-  // the smallest tile that holds an expert's average tokens; 96 is the largest
-  // with two accumulators for gate and up each
+  // the smallest tile that holds an expert's average tokens, and from 33 on the
+  // tokens on the lanes
   const int64_t avg = (g.pairs + L.n_experts - 1) / L.n_experts;
-  g.nt = avg <= 16 ? 16 : avg <= 32 ? 32 : avg <= 64 ? 64 : 96;
+  g.nt = avg <= 16 ? 16 : avg <= 32 ? 32 : 128;
   const int64_t with = std::min<int64_t>(L.n_experts, g.pairs);   // experts that can hold pairs
   g.max_tiles = (g.pairs + with * (g.nt - 1)) / g.nt;
   g.rows = g.max_tiles * g.nt;
@@ -732,8 +910,12 @@ extern "C" si_status si_mxfp4_matmul(const void *a_codes, const void *a_scales, 
   MmParams p{};
   const int nt = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
   const int64_t n_tt = (m + nt - 1) / nt, row_tiles = (n + 127) / 128;
-  // two weight tiles share the tokens of a stage as soon as such tiles fill the SMs
-  const int ma = nt == 128 && n_tt * ((row_tiles + 1) / 2) >= sm_count() ? 2 : 1;
+  const int size = out_type == SI_F32 ? 4 : 2;
+  const bool vec = n * size % 16 == 0 && ld_out * size % 16 == 0 && aligned16(out);
+  // the tokens on the lanes as soon as such tiles fill the SMs and the rows can
+  // be written in whole words
+  const bool tok = nt == 128 && vec && n_tt * ((row_tiles + 1) / 2) >= sm_count();
+  const int ma = tok ? 2 : 1;
   const int64_t n_rt = (row_tiles + ma - 1) / ma;
   if (n_tt * n_rt > 0x7FFFFFFF || n_tt * nt > 0x7FFFFFFF) return SI_ERR_UNSUPPORTED;
   if (!codes_map(&p.a0, w_codes, 1, n, k, 128) || !codes_map(&p.b, a_codes, 1, m, k, nt)) return SI_ERR_CUDA;
@@ -750,13 +932,16 @@ extern "C" si_status si_mxfp4_matmul(const void *a_codes, const void *a_scales, 
   p.ld = ld_out;
   p.status = static_cast<uint32_t *>(workspace);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool vec = out_type != SI_F32 && n % 8 == 0 && ld_out % 8 == 0 && aligned16(out);
-  return cuda_status(out_type == SI_F32 ? mm_launch_dense<kMmF32>(ma, nt, p, n_tt * n_rt, s)
+  p.wide = ld_out * size % 32 == 0 && (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
+  const int64_t tiles = n_tt * n_rt;
+  if (tok)
+    return cuda_status(out_type == SI_F32    ? mm_launch_as<kMmPlain, 2, 128, true, kMmF32Vec>(p, tiles, s)
+                       : out_type == SI_BF16 ? mm_launch_as<kMmPlain, 2, 128, true, kMmBf16Vec>(p, tiles, s)
+                                             : mm_launch_as<kMmPlain, 2, 128, true, kMmF16Vec>(p, tiles, s));
+  return cuda_status(out_type == SI_F32 ? mm_launch_dense<kMmF32>(nt, p, tiles, s)
                      : out_type == SI_BF16
-                         ? (vec ? mm_launch_dense<kMmBf16Vec>(ma, nt, p, n_tt * n_rt, s)
-                                : mm_launch_dense<kMmBf16>(ma, nt, p, n_tt * n_rt, s))
-                         : (vec ? mm_launch_dense<kMmF16Vec>(ma, nt, p, n_tt * n_rt, s)
-                                : mm_launch_dense<kMmF16>(ma, nt, p, n_tt * n_rt, s)));
+                         ? (vec ? mm_launch_dense<kMmBf16Vec>(nt, p, tiles, s) : mm_launch_dense<kMmBf16>(nt, p, tiles, s))
+                         : (vec ? mm_launch_dense<kMmF16Vec>(nt, p, tiles, s) : mm_launch_dense<kMmF16>(nt, p, tiles, s)));
 }
 
 extern "C" size_t si_moe_ffn_mxfp4_workspace_bytes(const si_mxfp4_experts *L, int n_tokens, int top_k) {
@@ -822,7 +1007,7 @@ extern "C" si_status si_moe_ffn_mxfp4(const si_mxfp4_experts *L, int n_tokens, i
   e = mm_launch_gateup(g.nt, gu, g.max_tiles * gu.n_rt, s);
   if (e != cudaSuccess) return SI_ERR_CUDA;
 
-  const int ma = g.nt == 96 ? 2 : 1;
+  const int ma = g.nt == 128 ? 2 : 1;
   dn.a1 = dn.a0;
   dn.sa0 = dn.sa1 = static_cast<const uint8_t *>(L->down_scales);
   dn.sb = base + g.off_hs;
@@ -836,6 +1021,7 @@ extern "C" si_status si_moe_ffn_mxfp4(const si_mxfp4_experts *L, int n_tokens, i
   dn.n_tiles = so.n_tiles;
   dn.out = base + g.off_y;
   dn.ld = H;
+  dn.wide = H % 16 == 0;
   dn.status = reinterpret_cast<uint32_t *>(base);
   dn.early = 1;
   e = mm_launch_down(g.nt, dn, g.max_tiles * dn.n_rt, s);
