@@ -10,8 +10,6 @@ Names follow the C ABI in ``include/si_moe.h``.
 from __future__ import annotations
 
 import ctypes
-import functools
-import inspect
 import os
 
 import torch
@@ -553,66 +551,52 @@ def si_requant_q4_k(src: torch.Tensor, src_type: str, rows: int, cols: int,
 
 _TYPES = {torch.float32: SI_F32, torch.float16: SI_F16, torch.bfloat16: SI_BF16}
 _Tensor, _empty = torch.Tensor, torch.empty
+_u8, _i32_t, _f32_t, _bf16_t = torch.uint8, torch.int32, torch.float32, torch.bfloat16
+
+# A decode step makes these calls back to back, and the host time of one is longer
+# than its kernels. So the usual case (the current stream of the current device)
+# runs straight through; _elsewhere takes the others.
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
-def _type(t: torch.Tensor, name: str) -> int:
-    ty = _TYPES.get(t.dtype)
-    if ty is None:
-        raise ValueError(f"{name} has dtype {t.dtype}, expected float32, float16 or bfloat16")
-    return ty
+def _elsewhere(call, stream, first, *args, **kw):
+    """``call`` with the device of ``first`` current and, if ``stream`` is given,
+    on that stream: what the call allocates then belongs to the stream, so an
+    output or a temporary workspace is not handed out again while the kernels
+    run. Inputs are marked as used by it."""
+    if not isinstance(first, _Tensor) or not first.is_cuda:
+        raise ValueError("expected CUDA tensors")
+    if stream is None:
+        with torch.cuda.device(first.device):
+            return call(first, *args, **kw)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=first.device)
+    if stream.device != first.device:
+        raise ValueError(f"tensors on {first.device}, stream on {stream.device}")
+    for t in (first, *args, *kw.values()):
+        if isinstance(t, _Tensor) and t.is_cuda:
+            t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        return call(first, *args, **kw)
 
 
-def _on_stream(call):
-    """Wraps ``call(handle, *tensors and sizes)`` into a function with a
-    ``stream`` argument: all tensors have to be on one CUDA device, which is
-    current while the call runs, and what it allocates belongs to the call's
-    stream, so an output or a temporary workspace is not handed out again while
-    the kernels run. Inputs are marked as used by a stream given by the caller.
+def _ptr(t, dev: int, numel: int, dtype, name: str) -> int:
+    """Device pointer of ``t`` after checking its device, size, dtype and that it is contiguous."""
+    if t.get_device() == dev and t.dtype is dtype and t.numel() == numel and t.is_contiguous():
+        return t.data_ptr()
+    _shaped(t, name, numel, (dtype,))
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
 
-    A decode step makes these calls back to back, and the host time of one is
-    longer than its kernels: the usual case (the current stream of the current
-    device) takes no context manager and builds no stream object."""
-    @functools.wraps(call)
-    def run(*args, stream=None, **kw):
-        dev = -1
-        for t in (*args, *kw.values()) if kw else args:
-            if isinstance(t, _Tensor):
-                d = t.get_device()
-                if d < 0:
-                    raise ValueError("expected CUDA tensors")
-                if d != dev:
-                    if dev >= 0:
-                        raise ValueError(f"tensors on cuda:{dev} and cuda:{d}")
-                    dev = d
-        if dev < 0:
-            raise ValueError("expected CUDA tensors")
-        if stream is None:
-            if dev == torch._C._cuda_getDevice():
-                return call(torch._C._cuda_getCurrentRawStream(dev), *args, **kw)
-            with torch.cuda.device(dev):
-                return call(torch._C._cuda_getCurrentRawStream(dev), *args, **kw)
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=dev)
-        if stream.device.index != dev:
-            raise ValueError(f"tensors on cuda:{dev}, stream on {stream.device}")
-        for t in (*args, *kw.values()):
-            if isinstance(t, _Tensor):
-                t.record_stream(stream)
-        with torch.cuda.stream(stream):
-            return call(stream.cuda_stream, *args, **kw)
 
-    doc = inspect.signature(call)
-    keep = [p for n, p in doc.parameters.items() if n != "handle"]
-    run.__signature__ = doc.replace(parameters=keep + [inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY,
-                                                                         default=None)])
-    return run
+def _bad_type(t, name: str):
+    raise ValueError(f"{name} has dtype {t.dtype}, expected float32, float16 or bfloat16")
 
 
 def _scratch(nbytes: int, device) -> torch.Tensor:
     """A workspace for one call: only its status header has to be zero."""
     if nbytes <= 0:
         raise ValueError("workspace size query returned 0 (invalid shapes)")
-    ws = _empty((int(nbytes),), dtype=torch.uint8, device=device)
+    ws = _empty((int(nbytes),), dtype=_u8, device=device)
     ws[:256].zero_()
     return ws
 
@@ -622,8 +606,8 @@ def mxfp4_scale_shape(rows: int, cols: int) -> tuple:
     return (-(-rows // 128), -(-cols // 128), 512)
 
 
-def _mxfp4(codes, scales, name: str, dims: int):
-    """(matrices, rows, cols) of an MXFP4 pair after checking that they belong together."""
+def _mxfp4(codes, scales, dev: int, name: str, dims: int):
+    """(matrices, rows, cols, pointers) of an MXFP4 pair after checking that they belong together."""
     if not isinstance(codes, _Tensor) or codes.dim() != dims:
         raise ValueError(f"{name} codes must be uint8 [{'n, ' if dims == 3 else ''}rows, cols / 2]")
     if dims == 2:
@@ -633,9 +617,8 @@ def _mxfp4(codes, scales, name: str, dims: int):
     cols *= 2
     if cols == 0 or cols % 32:
         raise ValueError(f"{name} has {cols} columns, expected a multiple of 32")
-    _shaped(codes, name, codes.numel(), _U8)
-    _shaped(scales, name, n * -(-rows // 128) * -(-cols // 128) * 512, _U8)
-    return n, rows, cols
+    return (n, rows, cols, _ptr(codes, dev, n * rows * cols // 2, _u8, name),
+            _ptr(scales, dev, n * (-(-rows // 128)) * (-(-cols // 128)) * 512, _u8, name))
 
 
 def _strides(t: torch.Tensor, name: str):
@@ -651,42 +634,54 @@ def _strides(t: torch.Tensor, name: str):
     return n, rows, cols, row if rows > 1 else cols, mat if n > 1 else 0
 
 
-@_on_stream
-def si_quantize_mxfp4(handle, x: torch.Tensor, codes: torch.Tensor | None = None,
-                      scales: torch.Tensor | None = None):
+def si_quantize_mxfp4(x: torch.Tensor, codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                      stream=None):
     """x [rows, cols] or [n, rows, cols] (fp32, fp16, bf16; rows and matrices at
     any stride) -> (codes uint8 [.., rows, cols / 2], scale tiles uint8
     [.., ceil(rows / 128), ceil(cols / 128), 512])."""
+    dev = x.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(si_quantize_mxfp4, stream, x, codes, scales)
     n, rows, cols, row, mat = _strides(x, "x")
     if cols == 0 or cols % 32:
         raise ValueError(f"x has {cols} columns, expected a multiple of 32")
-    tiles, many = mxfp4_scale_shape(rows, cols), x.dim() == 3
+    tr, tc = (rows + 127) // 128, (cols + 127) // 128
     if codes is None:
-        codes = _empty((n, rows, cols // 2) if many else (rows, cols // 2), dtype=torch.uint8, device=x.device)
-    else:
-        _shaped(codes, "codes", n * rows * cols // 2, _U8)
+        codes = _empty((n, rows, cols // 2) if x.dim() == 3 else (rows, cols // 2), dtype=_u8, device=x.device)
     if scales is None:
-        scales = _empty((n, *tiles) if many else tiles, dtype=torch.uint8, device=x.device)
-    else:
-        _shaped(scales, "scales", n * tiles[0] * tiles[1] * 512, _U8)
-    _check(library().si_quantize_mxfp4(x.data_ptr(), _type(x, "x"), n, rows, cols, row, mat, codes.data_ptr(),
-                                       scales.data_ptr(), handle), "si_quantize_mxfp4")
+        scales = _empty((n, tr, tc, 512) if x.dim() == 3 else (tr, tc, 512), dtype=_u8, device=x.device)
+    if x.dtype not in _TYPES:
+        _bad_type(x, "x")
+    st = library().si_quantize_mxfp4(
+        x.data_ptr(), _TYPES[x.dtype], n, rows, cols, row, mat, _ptr(codes, dev, n * rows * cols // 2, _u8, "codes"),
+        _ptr(scales, dev, n * tr * tc * 512, _u8, "scales"), _raw_stream(dev))
+    if st:
+        _check(st, "si_quantize_mxfp4")
     return codes, scales
 
 
-@_on_stream
-def si_dequantize_mxfp4(handle, codes: torch.Tensor, scales: torch.Tensor, dtype=torch.bfloat16,
-                        out: torch.Tensor | None = None) -> torch.Tensor:
+def si_dequantize_mxfp4(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.bfloat16,
+                        out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The values of an MXFP4 matrix (or n of them) as ``dtype`` or into ``out``."""
-    n, rows, cols = _mxfp4(codes, scales, "x", 3 if codes.dim() == 3 else 2)
-    shape = (n, rows, cols) if codes.dim() == 3 else (rows, cols)
+    dev = codes.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(si_dequantize_mxfp4, stream, codes, scales, dtype, out)
+    dims = 3 if codes.dim() == 3 else 2
+    n, rows, cols, c, sc = _mxfp4(codes, scales, dev, "x", dims)
+    shape = (n, rows, cols) if dims == 3 else (rows, cols)
     if out is None:
         out = _empty(shape, dtype=dtype, device=codes.device)
-    elif out.shape != shape:
-        raise ValueError(f"out has shape {tuple(out.shape)}, expected {shape}")
-    _, _, _, row, mat = _strides(out, "out")
-    _check(library().si_dequantize_mxfp4(codes.data_ptr(), scales.data_ptr(), n, rows, cols, out.data_ptr(),
-                                         _type(out, "out"), row, mat, handle), "si_dequantize_mxfp4")
+        row, mat = cols, rows * cols
+    elif out.shape != shape or out.get_device() != dev:
+        raise ValueError(f"out has shape {tuple(out.shape)} on {out.device}, expected {shape} on cuda:{dev}")
+    else:
+        _, _, _, row, mat = _strides(out, "out")
+    if out.dtype not in _TYPES:
+        _bad_type(out, "out")
+    st = library().si_dequantize_mxfp4(c, sc, n, rows, cols, out.data_ptr(), _TYPES[out.dtype], row, mat,
+                                       _raw_stream(dev))
+    if st:
+        _check(st, "si_dequantize_mxfp4")
     return out
 
 
@@ -694,99 +689,132 @@ def mxfp4_matmul_workspace_bytes(m: int, n: int, k: int) -> int:
     return int(library().si_mxfp4_matmul_workspace_bytes(m, n, k))
 
 
-@_on_stream
-def si_mxfp4_matmul(handle, a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tensor,
-                    w_scales: torch.Tensor, dtype=torch.bfloat16, out: torch.Tensor | None = None,
-                    ws: torch.Tensor | None = None) -> torch.Tensor:
+def si_mxfp4_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+                    dtype=torch.bfloat16, out: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
     """a [m, k] and w [n, k] in MXFP4 -> a w^T [m, n] in ``dtype`` or into ``out``
     (any row stride). ``ws`` receives the device status; without it an error on
     the device is not reported."""
-    _, m, k = _mxfp4(a_codes, a_scales, "a", 2)
-    _, n, k2 = _mxfp4(w_codes, w_scales, "w", 2)
+    dev = a_codes.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(si_mxfp4_matmul, stream, a_codes, a_scales, w_codes, w_scales, dtype, out, ws)
+    _, m, k, ac, asc = _mxfp4(a_codes, a_scales, dev, "a", 2)
+    _, n, k2, wc, wsc = _mxfp4(w_codes, w_scales, dev, "w", 2)
     if k != k2:
         raise ValueError(f"a has {k} columns, w has {k2}")
     if out is None:
         out, ld = _empty((m, n), dtype=dtype, device=a_codes.device), n
-    elif out.shape != (m, n):
-        raise ValueError(f"out has shape {tuple(out.shape)}, expected {(m, n)}")
+    elif out.shape != (m, n) or out.get_device() != dev:
+        raise ValueError(f"out has shape {tuple(out.shape)} on {out.device}, expected {(m, n)} on cuda:{dev}")
     else:
         ld = _strides(out, "out")[3]
-    _check(library().si_mxfp4_matmul(
-        a_codes.data_ptr(), a_scales.data_ptr(), m, w_codes.data_ptr(), w_scales.data_ptr(), n, k,
-        out.data_ptr(), _type(out, "out"), ld, None if ws is None else _cuda(ws, "ws"),
-        0 if ws is None else ws.numel(), handle), "si_mxfp4_matmul")
+    if out.dtype not in _TYPES:
+        _bad_type(out, "out")
+    st = library().si_mxfp4_matmul(ac, asc, m, wc, wsc, n, k, out.data_ptr(), _TYPES[out.dtype], ld,
+                                   None if ws is None else _ptr(ws, dev, ws.numel(), _u8, "ws"),
+                                   0 if ws is None else ws.numel(), _raw_stream(dev))
+    if st:
+        _check(st, "si_mxfp4_matmul")
     return out
 
 
-@_on_stream
-def si_moe_sort(handle, ids: torch.Tensor, n_experts: int):
+def si_moe_sort(ids: torch.Tensor, n_experts: int, stream=None):
     """ids int32 [T, k] -> (order int32 [T * k], position int32 [T, k], offsets
     int32 [n_experts + 1]); pairs whose id is outside [0, n_experts) are dropped
     (position -1)."""
-    T, k = ids.shape
-    dev = ids.device
-    order = _empty((T * k,), dtype=torch.int32, device=dev)
-    position = _empty((T, k), dtype=torch.int32, device=dev)
-    offsets = _empty((max(n_experts, 0) + 1,), dtype=torch.int32, device=dev)
-    need = library().si_moe_sort_workspace_bytes(T, k, n_experts)
-    ws = _empty((need,), dtype=torch.uint8, device=dev) if need else None
-    _check(library().si_moe_sort(_shaped(ids, "ids", T * k, _I32), T, k, n_experts, order.data_ptr(),
-                                 position.data_ptr(), offsets.data_ptr(), ws.data_ptr() if need else None, need,
-                                 handle), "si_moe_sort")
+    dev = ids.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(si_moe_sort, stream, ids, n_experts)
+    (T, k), d, lib = ids.shape, ids.device, library()
+    order = _empty((T * k,), dtype=_i32_t, device=d)
+    position = _empty((T, k), dtype=_i32_t, device=d)
+    offsets = _empty((n_experts + 1 if n_experts > 0 else 1,), dtype=_i32_t, device=d)
+    need = lib.si_moe_sort_workspace_bytes(T, k, n_experts)
+    ws = _empty((need,), dtype=_u8, device=d) if need else None
+    st = lib.si_moe_sort(_ptr(ids, dev, T * k, _i32_t, "ids"), T, k, n_experts, order.data_ptr(),
+                         position.data_ptr(), offsets.data_ptr(), ws.data_ptr() if need else None, need,
+                         _raw_stream(dev))
+    if st:
+        _check(st, "si_moe_sort")
     return order, position, offsets
 
 
-def _kept(offsets: torch.Tensor) -> int:
+def _kept(offsets: torch.Tensor, dev: int) -> int:
     """Address of the number of kept pairs, the last of the offsets."""
-    if offsets.dim() != 1 or offsets.numel() < 1 or offsets.dtype != torch.int32:
+    n = offsets.numel()
+    if offsets.dim() != 1 or n < 1:
         raise ValueError("offsets must be int32 [n_experts + 1]")
-    return _cuda(offsets, "offsets") + 4 * (offsets.numel() - 1)
+    return _ptr(offsets, dev, n, _i32_t, "offsets") + 4 * (n - 1)
 
 
-@_on_stream
-def si_moe_gather(handle, x: torch.Tensor, position: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
+def si_moe_gather(x: torch.Tensor, position: torch.Tensor, offsets: torch.Tensor, stream=None) -> torch.Tensor:
     """xs[position[t, r]] = x[t]: x [T, H] -> [T * k, H], zero rows behind the kept pairs."""
-    (T, H), k = x.shape, position.shape[-1]
-    xs = _empty((T * k, H), dtype=x.dtype, device=x.device)
-    _check(library().si_moe_gather(_cuda(x, "x"), _type(x, "x"), T, k, H,
-                                   _shaped(position, "position", T * k, _I32), _kept(offsets), xs.data_ptr(),
-                                   handle), "si_moe_gather")
+    dev = x.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(si_moe_gather, stream, x, position, offsets)
+    (T, H), k, dtype = x.shape, position.shape[-1], x.dtype
+    if dtype not in _TYPES:
+        _bad_type(x, "x")
+    xs = _empty((T * k, H), dtype=dtype, device=x.device)
+    st = library().si_moe_gather(_ptr(x, dev, T * H, dtype, "x"), _TYPES[dtype], T, k, H,
+                                 _ptr(position, dev, T * k, _i32_t, "position"), _kept(offsets, dev),
+                                 xs.data_ptr(), _raw_stream(dev))
+    if st:
+        _check(st, "si_moe_gather")
     return xs
 
 
-@_on_stream
-def si_moe_gather_backward(handle, gxs: torch.Tensor, position: torch.Tensor) -> torch.Tensor:
+def si_moe_gather_backward(gxs: torch.Tensor, position: torch.Tensor, stream=None) -> torch.Tensor:
     """gx[t] = sum_r gxs[position[t, r]]: gxs [T * k, H] -> [T, H]."""
-    (T, k), H = position.shape, gxs.shape[-1]
-    gx = _empty((T, H), dtype=gxs.dtype, device=gxs.device)
-    _check(library().si_moe_gather_backward(_shaped(gxs, "gxs", T * k * H, (gxs.dtype,)), _type(gxs, "gxs"),
-                                            T, k, H, _shaped(position, "position", T * k, _I32),
-                                            gx.data_ptr(), handle), "si_moe_gather_backward")
+    dev = gxs.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(si_moe_gather_backward, stream, gxs, position)
+    (T, k), H, dtype = position.shape, gxs.shape[-1], gxs.dtype
+    if dtype not in _TYPES:
+        _bad_type(gxs, "gxs")
+    gx = _empty((T, H), dtype=dtype, device=gxs.device)
+    st = library().si_moe_gather_backward(_ptr(gxs, dev, T * k * H, dtype, "gxs"), _TYPES[dtype], T, k, H,
+                                          _ptr(position, dev, T * k, _i32_t, "position"), gx.data_ptr(),
+                                          _raw_stream(dev))
+    if st:
+        _check(st, "si_moe_gather_backward")
     return gx
 
 
-@_on_stream
-def si_moe_combine(handle, ys: torch.Tensor, position: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
+def si_moe_combine(ys: torch.Tensor, position: torch.Tensor, w: torch.Tensor, stream=None) -> torch.Tensor:
     """y[t] = sum_r w[t, r] ys[position[t, r]]: ys [T * k, H], w fp32 [T, k] -> [T, H]."""
-    (T, k), H = position.shape, ys.shape[-1]
-    y = _empty((T, H), dtype=ys.dtype, device=ys.device)
-    _check(library().si_moe_combine(_shaped(ys, "ys", T * k * H, (ys.dtype,)), _type(ys, "ys"), T, k, H,
-                                    _shaped(position, "position", T * k, _I32), _shaped(w, "w", T * k, _F32),
-                                    y.data_ptr(), handle), "si_moe_combine")
+    dev = ys.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(si_moe_combine, stream, ys, position, w)
+    (T, k), H, dtype = position.shape, ys.shape[-1], ys.dtype
+    if dtype not in _TYPES:
+        _bad_type(ys, "ys")
+    y = _empty((T, H), dtype=dtype, device=ys.device)
+    st = library().si_moe_combine(_ptr(ys, dev, T * k * H, dtype, "ys"), _TYPES[dtype], T, k, H,
+                                  _ptr(position, dev, T * k, _i32_t, "position"), _ptr(w, dev, T * k, _f32_t, "w"),
+                                  y.data_ptr(), _raw_stream(dev))
+    if st:
+        _check(st, "si_moe_combine")
     return y
 
 
-@_on_stream
-def si_moe_combine_backward(handle, gy: torch.Tensor, ys: torch.Tensor, position: torch.Tensor,
-                            offsets: torch.Tensor, w: torch.Tensor):
+def si_moe_combine_backward(gy: torch.Tensor, ys: torch.Tensor, position: torch.Tensor, offsets: torch.Tensor,
+                            w: torch.Tensor, stream=None):
     """gy [T, H], ys [T * k, H] -> (gys [T * k, H], gw fp32 [T, k])."""
-    (T, k), H = position.shape, gy.shape[-1]
-    gys = _empty((T * k, H), dtype=gy.dtype, device=gy.device)
-    gw = _empty((T, k), dtype=torch.float32, device=gy.device)
-    _check(library().si_moe_combine_backward(
-        _shaped(gy, "gy", T * H, (gy.dtype,)), _shaped(ys, "ys", T * k * H, (gy.dtype,)), _type(gy, "gy"), T, k, H,
-        _shaped(position, "position", T * k, _I32), _kept(offsets), _shaped(w, "w", T * k, _F32),
-        gys.data_ptr(), gw.data_ptr(), handle), "si_moe_combine_backward")
+    dev = gy.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(si_moe_combine_backward, stream, gy, ys, position, offsets, w)
+    (T, k), H, dtype, d = position.shape, gy.shape[-1], gy.dtype, gy.device
+    if dtype not in _TYPES:
+        _bad_type(gy, "gy")
+    gys = _empty((T * k, H), dtype=dtype, device=d)
+    gw = _empty((T, k), dtype=_f32_t, device=d)
+    st = library().si_moe_combine_backward(
+        _ptr(gy, dev, T * H, dtype, "gy"), _ptr(ys, dev, T * k * H, dtype, "ys"), _TYPES[dtype], T, k, H,
+        _ptr(position, dev, T * k, _i32_t, "position"), _kept(offsets, dev), _ptr(w, dev, T * k, _f32_t, "w"),
+        gys.data_ptr(), gw.data_ptr(), _raw_stream(dev))
+    if st:
+        _check(st, "si_moe_combine_backward")
     return gys, gw
 
 
@@ -797,16 +825,18 @@ class Mxfp4Experts:
 
     def __init__(self, gate, up, down):
         self.gate, self.up, self.down = gate, up, down
-        E, I, H = _mxfp4(*gate, "gate", 3)
-        if _mxfp4(*up, "up", 3) != (E, I, H):
+        if not isinstance(gate[0], _Tensor) or not gate[0].is_cuda:
+            raise ValueError("gate must be CUDA tensors")
+        self.dev = gate[0].get_device()
+        E, I, H, gc, gs = _mxfp4(*gate, self.dev, "gate", 3)
+        n, rows, cols, uc, us = _mxfp4(*up, self.dev, "up", 3)
+        if (n, rows, cols) != (E, I, H):
             raise ValueError(f"up must be {E} matrices [{I}, {H}], as gate")
-        if _mxfp4(*down, "down", 3) != (E, H, I):
+        n, rows, cols, dc, ds = _mxfp4(*down, self.dev, "down", 3)
+        if (n, rows, cols) != (E, H, I):
             raise ValueError(f"down must be {E} matrices [{H}, {I}]")
-        self.device = gate[0].device
-        if any(t.device != self.device for t in (*gate, *up, *down)):
-            raise ValueError("gate, up and down on different devices")
         self.hidden, self.inter, self.n_experts = H, I, E
-        self.c = SiMxfp4Experts(H, I, E, *(t.data_ptr() for t in (*gate, *up, *down)))
+        self.c = SiMxfp4Experts(H, I, E, gc, gs, uc, us, dc, ds)
         self.ref = ctypes.byref(self.c)
 
     @classmethod
@@ -819,22 +849,25 @@ def ffn_mxfp4_workspace_bytes(experts: Mxfp4Experts, n_tokens: int, top_k: int) 
     return int(library().si_moe_ffn_mxfp4_workspace_bytes(experts.ref, n_tokens, top_k))
 
 
-@_on_stream
-def si_moe_ffn_mxfp4(handle, experts: Mxfp4Experts, x: torch.Tensor, ids: torch.Tensor, w: torch.Tensor,
-                     ws: torch.Tensor | None = None) -> torch.Tensor:
+def si_moe_ffn_mxfp4(experts: Mxfp4Experts, x: torch.Tensor, ids: torch.Tensor, w: torch.Tensor,
+                     ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """T tokens with per-token routing: x bf16 [T, H], ids int32 [T, k], w fp32
     [T, k] -> routed bf16 [T, H]."""
-    T, k = ids.shape
-    H, dev = experts.hidden, x.device
-    if experts.device != dev:
-        raise ValueError(f"tensors on {dev}, experts on {experts.device}")
+    dev = x.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(lambda x, ids, w, ws: si_moe_ffn_mxfp4(experts, x, ids, w, ws), stream, x, ids, w, ws)
+    (T, k), H = ids.shape, experts.hidden
+    if experts.dev != dev:
+        raise ValueError(f"tensors on cuda:{dev}, experts on cuda:{experts.dev}")
     if ws is None:
-        ws = _scratch(ffn_mxfp4_workspace_bytes(experts, T, k), dev)
-    routed = _empty((T, H), dtype=torch.bfloat16, device=dev)
-    _check(library().si_moe_ffn_mxfp4(
-        experts.ref, T, k, _shaped(x, "x", T * H, _BF16), _shaped(ids, "ids", T * k, _I32),
-        _shaped(w, "w", T * k, _F32), routed.data_ptr(), _cuda(ws, "ws"), ws.numel(), handle),
-        "si_moe_ffn_mxfp4")
+        ws = _scratch(ffn_mxfp4_workspace_bytes(experts, T, k), x.device)
+    routed = _empty((T, H), dtype=_bf16_t, device=x.device)
+    n = ws.numel()
+    st = library().si_moe_ffn_mxfp4(
+        experts.ref, T, k, _ptr(x, dev, T * H, _bf16_t, "x"), _ptr(ids, dev, T * k, _i32_t, "ids"),
+        _ptr(w, dev, T * k, _f32_t, "w"), routed.data_ptr(), _ptr(ws, dev, n, _u8, "ws"), n, _raw_stream(dev))
+    if st:
+        _check(st, "si_moe_ffn_mxfp4")
     return routed
 
 

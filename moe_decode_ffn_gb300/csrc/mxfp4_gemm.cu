@@ -20,15 +20,15 @@
 // scales into tensor memory (tcgen05.cp) and issues the MMAs, warps 2.. read the
 // accumulators and write the outputs (4 of them cover the 128 lanes of tensor
 // memory; each group of 4 takes a part of the tokens), and a thread of each of
-// the last warps keeps one operand's scale tiles coming. Blocks are persistent:
+// the last warps keeps one weight operand's scale tiles coming. Blocks are persistent:
 // tile i of block b is b + i * gridDim. The accumulators are a ring too, so that
 // the MMAs of a tile run beside the epilogue of the one before.
 //
 // What bounds a long product is the one thread that issues: a stage is 6 scale
 // copies, 4 or 8 MMAs and a commit, and each of them takes 20 to 30 cycles to
 // issue, so everything else is kept out of that thread's way. A plain bulk copy of scales holds its thread up for
-// about 270 cycles, which is why every operand's scales have a thread of their
-// own.
+// about 270 cycles, which is why they are spread over threads: the weights' have one each,
+// the tokens' go with the codes.
 #include <cuda.h>
 
 #include <algorithm>
@@ -55,7 +55,7 @@ template <int MODE, int MA, int NT, bool TOK> struct MmCfg {
   static constexpr int kParts = TOK ? 4 : 2;
   static constexpr int kEpiWarps = 4 * kParts;
   static constexpr int kScaleWarp = 2 + kEpiWarps;
-  static constexpr int kThreads = 32 * (kScaleWarp + MA + 1);
+  static constexpr int kThreads = 32 * (kScaleWarp + MA);   // TOK: 20 warps, which leave 96 registers a thread
   static constexpr int kBBytes = NT * 128;
   static constexpr int kSfBytes = 2 * kMxTileBytes;               // per operand tile and stage
   static constexpr int kStage = MA * kMmABytes + kBBytes + (MA + 1) * kSfBytes;
@@ -376,15 +376,17 @@ SI_DEV void tmem_ld32(uint32_t taddr, uint32_t r[32]) {
       : "r"(taddr)
       : "memory");
 }
-// 32 bytes of a row: one sector, one store.
+// 32 bytes of a row: one sector, one store. (Rows exchanged over 8 lanes to
+// 128-byte pieces measured slower: 80.8 against 73.2 us for 8192 x 4096 x 4096
+// with its quantisation, for the registers that the exchange takes.)
 SI_DEV void st_global32(void *p, const uint32_t w[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
 }
 
-// 64 features (from f0) of this lane's token `j`, 32 at a time (a block's warps
-// leave 80 registers a thread); 2-byte outputs wait, packed, until all are read.
+// 64 features (from f0) of this lane's token `j`, 32 at a time; 2-byte
+// outputs wait, packed, until all are read.
 template <int OUT, typename Release>
 SI_DEV void mm_write_tokens(const MmParams &p, int f0, int64_t row0, int j, bool valid, uint32_t acc, Release release) {
   constexpr int kSize = OUT == kMmF32Vec ? 4 : 2;
@@ -490,14 +492,14 @@ __global__ void __launch_bounds__(MmCfg<MODE, MA, NT, TOK>::kThreads, 1)
   uint32_t *s_taddr = reinterpret_cast<uint32_t *>(drain + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_ks = (p.K + kMmStageK - 1) / kMmStageK;
-  // the operand whose scales this warp brings: weights 0 .. MA - 1, tokens MA
+  // the weight operand whose scales this warp brings
   const int operand = warp - C::kScaleWarp;
 
   // the copies of stage ks of a tile; the full barrier of a stage takes the
   // arrival of the codes and of every operand's scales
   auto load_weights = [&](const MmTile &t, int na, int ks, int s) {
     uint8_t *st = base + s * C::kStage;
-    mbar_arrive_expect_tx(full + s, na * kMmABytes + C::kBBytes);
+    mbar_arrive_expect_tx(full + s, na * kMmABytes + C::kBBytes + min(2, p.kt - 2 * ks) * kMxTileBytes);
 #pragma unroll
     for (int a = 0; a < MA; ++a) {
       if (a >= na) break;
@@ -506,26 +508,29 @@ __global__ void __launch_bounds__(MmCfg<MODE, MA, NT, TOK>::kThreads, 1)
     }
   };
   auto load_tokens = [&](const MmTile &t, int ks, int s) {
-    tma_load3(base + s * C::kStage + MA * kMmABytes, &p.b, ks * 128, t.tt * NT, 0, full + s);
+    uint8_t *sb = base + s * C::kStage + MA * kMmABytes;
+    tma_load3(sb, &p.b, ks * 128, t.tt * NT, 0, full + s);
+    bulk_g2s(sb + C::kBBytes + MA * C::kSfBytes, p.sb + (static_cast<size_t>(t.tt) * p.kt + 2 * ks) * kMxTileBytes,
+             min(2, p.kt - 2 * ks) * kMxTileBytes, full + s);
   };
   auto load_scales = [&](const MmTile &t, int na, int ks, int s) {   // of this warp's operand
-    if (operand >= na && operand < MA) {
+    if (operand >= na) {
       mbar_arrive(full + s);         // no such weights in this tile
       return;
     }
     const int rt = MODE == kMmGateUp ? t.rt : t.rt * MA + operand;
-    const uint8_t *src = operand == MA ? p.sb : MODE == kMmGateUp && operand == 1 ? p.sa1 : p.sa0;
-    const size_t tile = operand == MA ? t.tt : t.mat * p.row_tiles + rt;
     const uint32_t bytes = min(2, p.kt - 2 * ks) * kMxTileBytes;
     mbar_arrive_expect_tx(full + s, bytes);
     bulk_g2s(base + s * C::kStage + MA * kMmABytes + C::kBBytes + operand * C::kSfBytes,
-             src + (tile * p.kt + 2 * ks) * kMxTileBytes, bytes, full + s);
+             (MODE == kMmGateUp && operand == 1 ? p.sa1 : p.sa0) +
+                 (static_cast<size_t>(t.mat * p.row_tiles + rt) * p.kt + 2 * ks) * kMxTileBytes,
+             bytes, full + s);
   };
 
   int ahead = 0;                     // stages whose weights were requested before the wait
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(full + i, 2 + MA);
+      mbar_init(full + i, 1 + MA);
       mbar_init(empty + i, 1);
     }
     for (int i = 0; i < U; ++i) {
@@ -537,7 +542,7 @@ __global__ void __launch_bounds__(MmCfg<MODE, MA, NT, TOK>::kThreads, 1)
   }
   if (p.early) {                     // uniform over the grid
     __syncthreads();
-    if (lane == 0 && (warp == 0 || (operand >= 0 && operand < MA)) && static_cast<int>(blockIdx.x) < mm_total(p, NT)) {
+    if (lane == 0 && (warp == 0 || operand >= 0) && static_cast<int>(blockIdx.x) < mm_total(p, NT)) {
       const MmTile t = mm_tile(p, blockIdx.x, NT);
       const int na = mm_operands<MODE, MA>(p, t);
       for (; ahead < S && ahead < n_ks; ++ahead) {
@@ -738,8 +743,8 @@ __global__ void __launch_bounds__(MmCfg<MODE, MA, NT, TOK>::kThreads, 1)
 
 // ---------------------------------------------------------------------------
 // x to MXFP4 rows at the sorted places: one block per token quantises its row
-// once and writes it to its k places. Scale tiles belong to one token tile each
-// (NT of their 128 rows).
+// once and writes it to its kept places. Scale tiles belong to one token tile
+// each (NT of their 128 rows).
 // ---------------------------------------------------------------------------
 struct ScatterArgs {
   const __nv_bfloat16 *x;
@@ -747,25 +752,22 @@ struct ScatterArgs {
   const int32_t *position;
   uint8_t *codes, *scales;
 };
-__global__ void __launch_bounds__(256) quantize_scatter_kernel(ScatterArgs a) {
-  __shared__ uint8_t *s_code[8], *s_scale[8];   // of this token's kept pairs
-  __shared__ int s_n;
-  grid_dep_wait();
-  grid_dep_launch();
-  const int64_t t = blockIdx.x;
-  const int lane = threadIdx.x & 31;
-  if (threadIdx.x < 32) {
-    const int p = lane < a.k ? __ldcg(a.position + t * a.k + lane) : -1;
-    const uint32_t kept = __ballot_sync(0xffffffffu, p >= 0);
-    const int at = __popc(kept & ((1u << lane) - 1u));
-    if (p >= 0) {
-      s_code[at] = a.codes + static_cast<size_t>(p) * a.H / 2;
-      s_scale[at] = a.scales + static_cast<size_t>(p / a.nt) * a.kt * kMxTileBytes + mx_scale_byte(p % a.nt, 0);
-    }
-    if (lane == 0) s_n = __popc(kept);
+struct ScatterRows {
+  uint8_t *code[8], *scale[8];   // rows of the token's kept pairs
+  int n;
+};
+// Place p (-1: dropped) of pair `lane` of the token to the list; one whole warp.
+SI_DEV void scatter_list(const ScatterArgs &a, int p, int lane, ScatterRows &out) {
+  const uint32_t kept = __ballot_sync(0xffffffffu, p >= 0);
+  const int at = __popc(kept & ((1u << lane) - 1u));
+  if (p >= 0) {
+    out.code[at] = a.codes + static_cast<size_t>(p) * a.H / 2;
+    out.scale[at] = a.scales + static_cast<size_t>(p / a.nt) * a.kt * kMxTileBytes + mx_scale_byte(p % a.nt, 0);
   }
-  __syncthreads();
-  const int n = s_n;
+  if (lane == 0) out.n = __popc(kept);
+}
+SI_DEV void scatter_row(const ScatterArgs &a, int64_t t, const ScatterRows &to) {
+  const int lane = threadIdx.x & 31, n = to.n;
   // whole scale tiles (128 columns, 16 lanes): the blocks behind H get scale 0
   for (int c0 = (threadIdx.x & ~31) * 8; c0 < a.kt * 128; c0 += blockDim.x * 8) {
     const int c = c0 + lane * 8;
@@ -778,10 +780,57 @@ __global__ void __launch_bounds__(256) quantize_scatter_kernel(ScatterArgs a) {
 #pragma unroll
     for (int b = 0; b < 4; ++b) s4 |= __shfl_sync(0xffffffffu, s, (lane & 16) + 4 * b) << (8 * b);
     for (int r = 0; r < n; ++r) {
-      if (c < a.H) *reinterpret_cast<uint32_t *>(s_code[r] + c / 2) = w;
-      if ((lane & 15) == 0 && c < a.kt * 128) *reinterpret_cast<uint32_t *>(s_scale[r] + c / 128 * kMxTileBytes) = s4;
+      if (c < a.H) *reinterpret_cast<uint32_t *>(to.code[r] + c / 2) = w;
+      if ((lane & 15) == 0 && c < a.kt * 128) *reinterpret_cast<uint32_t *>(to.scale[r] + c / 128 * kMxTileBytes) = s4;
     }
   }
+}
+__global__ void __launch_bounds__(256) quantize_scatter_kernel(ScatterArgs a) {
+  __shared__ ScatterRows s_rows;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int64_t t = blockIdx.x;
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x < 32) scatter_list(a, lane < a.k ? __ldcg(a.position + t * a.k + lane) : -1, lane, s_rows);
+  __syncthreads();
+  scatter_row(a, t, s_rows);
+}
+
+// At most 32 pairs: the sort too, in the same launch, by one warp of every block
+// (a lane per pair); block 0 writes the tile list. The launch that this saves
+// counts more there than the weights that gate/up could request before its wait
+// with the sort two launches back (128 experts, H 2048, I 768, top-8: 1 token
+// 19.8 against 22.0 us, 4 tokens 26.6 against 26.8, 16 tokens 44.0 against 43.2).
+constexpr int kFewPairs = 32;
+__global__ void __launch_bounds__(256) sort_scatter_kernel(SortArgs so, ScatterArgs a) {
+  __shared__ ScatterRows s_rows;
+  grid_dep_wait();
+  grid_dep_launch();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x, first = blockIdx.x * a.k;   // this token's pairs: first .. first + k - 1
+    const int e = lane < static_cast<int>(so.pairs) ? sort_expert(so, lane) : 0x7FFFFFFF;
+    const bool kept = e < so.n_experts;
+    const uint32_t same = __match_any_sync(0xffffffffu, e);
+    const int rank = __popc(same & ((1u << lane) - 1u));
+    const int tiles = kept && rank == 0 ? sort_tiles(so, __popc(same)) : 0;
+    int tile = 0;                                             // tiles of the experts before e
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const int ej = __shfl_sync(0xffffffffu, e, j), n = __shfl_sync(0xffffffffu, tiles, j);
+      if (ej < e) tile += n;
+    }
+    const int total = __reduce_add_sync(0xffffffffu, tiles);
+    if (blockIdx.x == 0) {
+      if (tiles > 0) sort_list(so, e, __popc(same), tile, 0, 1);
+      if (lane == 0) *so.n_tiles = total;
+    }
+    int p = __shfl_sync(0xffffffffu, kept ? tile * so.tile_rows + rank : -1, (first + lane) & 31);
+    if (lane < a.k) so.position[first + lane] = p;
+    else p = -1;
+    scatter_list(a, p, lane, s_rows);
+  }
+  __syncthreads();
+  scatter_row(a, blockIdx.x, s_rows);
 }
 
 // ---- host ------------------------------------------------------------------
@@ -981,12 +1030,17 @@ extern "C" si_status si_moe_ffn_mxfp4(const si_mxfp4_experts *L, int n_tokens, i
   so.tile_expert = reinterpret_cast<int32_t *>(base + g.off_expert);
   so.tile_count = reinterpret_cast<int32_t *>(base + g.off_count);
   so.n_tiles = reinterpret_cast<int32_t *>(base + g.off_n);
-  cudaError_t e = sort_launch(so, s);
-  if (e != cudaSuccess) return SI_ERR_CUDA;
-
-  ScatterArgs sc{static_cast<const __nv_bfloat16 *>(x), top_k, H, g.kt_x, g.nt, so.position, base + g.off_xc,
-                 base + g.off_xs};
-  e = launch_pdl(quantize_scatter_kernel, dim3(n_tokens), dim3(256), 0, s, sc);
+  const ScatterArgs sc{static_cast<const __nv_bfloat16 *>(x), top_k, H, g.kt_x, g.nt, so.position, base + g.off_xc,
+                       base + g.off_xs};
+  const bool few = g.pairs <= kFewPairs;
+  cudaError_t e;
+  if (few) {
+    e = launch_pdl(sort_scatter_kernel, dim3(n_tokens), dim3(256), 0, s, so, sc);
+  } else {
+    e = sort_launch(so, s);
+    if (e != cudaSuccess) return SI_ERR_CUDA;
+    e = launch_pdl(quantize_scatter_kernel, dim3(n_tokens), dim3(256), 0, s, sc);
+  }
   if (e != cudaSuccess) return SI_ERR_CUDA;
 
   gu.sa0 = static_cast<const uint8_t *>(L->gate_scales);
@@ -1003,7 +1057,9 @@ extern "C" si_status si_moe_ffn_mxfp4(const si_mxfp4_experts *L, int n_tokens, i
   gu.h_scales = base + g.off_hs;
   gu.h_kt = g.kt_h;
   gu.status = reinterpret_cast<uint32_t *>(base);
-  gu.early = 1;   // the sort is two launches back, complete when its successor's blocks have passed their wait
+  // the sort is two launches back: complete when the blocks of its successor have
+  // passed their wait, before which this launch does not start
+  gu.early = few ? 0 : 1;
   e = mm_launch_gateup(g.nt, gu, g.max_tiles * gu.n_rt, s);
   if (e != cudaSuccess) return SI_ERR_CUDA;
 

@@ -25,21 +25,9 @@ namespace si {
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
 
-// Expert of a pair, E for a dropped one (negative ids are large unsigned ones).
-SI_DEV int sort_expert(const SortArgs &a, int64_t i) {
-  return static_cast<int>(min(static_cast<uint32_t>(__ldcg(a.ids + i)), static_cast<uint32_t>(a.n_experts)));
-}
 SI_DEV void sort_place(const SortArgs &a, int64_t i, int e, int p) {
   if (a.position) a.position[i] = e < a.n_experts ? p : -1;
   if (a.order) a.order[p] = e < a.n_experts ? static_cast<int32_t>(i) : -1;
-}
-SI_DEV int sort_tiles(const SortArgs &a, int n) { return a.tile_rows > 0 ? (n + a.tile_rows - 1) / a.tile_rows : 0; }
-// The list entries of expert e: its pairs, first tile `t`.
-SI_DEV void sort_list(const SortArgs &a, int e, int count, int t, int from, int step) {
-  for (int i = from; i * a.tile_rows < count; i += step) {
-    a.tile_expert[t + i] = e;
-    a.tile_count[t + i] = min(a.tile_rows, count - i * a.tile_rows);
-  }
 }
 
 __global__ void __launch_bounds__(kSortThreads) sort_pairs_kernel(SortArgs a) {

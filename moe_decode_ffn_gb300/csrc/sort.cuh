@@ -2,8 +2,7 @@
 // the sort call and the MXFP4 expert FFN share.
 #pragma once
 
-#include <cuda_runtime.h>
-#include <stdint.h>
+#include "common.cuh"
 
 namespace si {
 
@@ -35,5 +34,18 @@ cudaError_t sort_launch(SortArgs a, cudaStream_t s);
 // (a multiple of 8, 16-byte aligned), fp32 sums in rank order.
 cudaError_t combine_launch(const void *rows, int64_t n_rows, int n_tokens, int top_k, int64_t hidden,
                            const int32_t *position, const float *w, void *y, cudaStream_t s);
+
+// Expert of a pair, E for a dropped one (negative ids are large unsigned ones).
+SI_DEV int sort_expert(const SortArgs &a, int64_t i) {
+  return static_cast<int>(min(static_cast<uint32_t>(__ldcg(a.ids + i)), static_cast<uint32_t>(a.n_experts)));
+}
+SI_DEV int sort_tiles(const SortArgs &a, int n) { return a.tile_rows > 0 ? (n + a.tile_rows - 1) / a.tile_rows : 0; }
+// The list entries of expert e: its pairs, first tile `t`.
+SI_DEV void sort_list(const SortArgs &a, int e, int count, int t, int from, int step) {
+  for (int i = from; i * a.tile_rows < count; i += step) {
+    a.tile_expert[t + i] = e;
+    a.tile_count[t + i] = min(a.tile_rows, count - i * a.tile_rows);
+  }
+}
 
 }  // namespace si

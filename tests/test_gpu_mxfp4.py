@@ -150,6 +150,25 @@ def test_matmul_exact(mm, n, k):
         assert torch.equal(y, torch.from_numpy(want).to(TYPES[kind]))
 
 
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("mm,n,k,pad", [(2500, 2088, 96, 0), (1290, 4356, 320, 0), (2600, 2056, 64, 24), (2049, 2500, 544, 4)])
+def test_matmul_of_many_tokens(mm, n, k, pad, kind):
+    """Enough tiles for the tokens to lie on the lanes: ragged in tokens, in the
+    256 rows of a tile and (one tile of 128 left) in their halves, odd columns,
+    rows of whole 16-byte words and others."""
+    g = torch.Generator(device="cuda").manual_seed(mm + n)
+    draw = lambda r, hi: torch.randint(0, hi, r, generator=g, device="cuda", dtype=torch.int32)  # noqa: E731
+    ac, asc = draw((mm, k), 16).cpu().numpy().astype(np.uint8), (126 + draw((mm, k // 32), 3)).cpu().numpy().astype(np.uint8)
+    wc, wsc = draw((n, k), 16).cpu().numpy().astype(np.uint8), (126 + draw((n, k // 32), 3)).cpu().numpy().astype(np.uint8)
+    a, w = X.values(ac, asc), X.values(wc, wsc)
+    check_exact_sums(a, w)
+    want = torch.from_numpy(a @ w.T).to(TYPES[kind])
+    out = torch.full((mm, n + pad), 9.0, dtype=TYPES[kind], device="cuda")
+    m.si_mxfp4_matmul(*on_gpu(ac, asc), *on_gpu(wc, wsc), out=out[:, :n])
+    assert torch.equal(out[:, :n].cpu(), want)
+    assert bool((out[:, n:] == 9.0).all())
+
+
 def test_matmul_of_the_whole_code_range():
     """Scales far apart: the fp32 sum of k terms is off by at most
     k 2^-23 sum |a||w| (each addition rounds or truncates the running sum)."""
@@ -257,7 +276,9 @@ def ffn_oracle(weights, x, ids, w, E):
     return out, tol + half * (np.abs(out) + tol)
 
 
-FFN = [(1, 8, 2, 256, 128), (1, 4, 1, 32, 32), (5, 8, 8, 96, 160), (16, 3, 2, 288, 96), (70, 4, 3, 128, 256),
+# up to 32 pairs in one launch with the sort, then one or two launches of it; 16, 32
+# and 128 tokens a tile
+FFN = [(32, 1, 1, 64, 64), (33, 1, 1, 64, 64), (16, 2, 2, 96, 64), (4, 1024, 8, 64, 32), (1, 8, 2, 256, 128), (1, 4, 1, 32, 32), (5, 8, 8, 96, 160), (16, 3, 2, 288, 96), (70, 4, 3, 128, 256),
        (40, 1, 1, 64, 416), (150, 2, 2, 160, 64), (200, 1, 1, 544, 32), (9, 40, 8, 256, 128)]
 
 
