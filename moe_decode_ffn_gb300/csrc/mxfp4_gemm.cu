@@ -880,14 +880,12 @@ static cudaError_t mm_launch_dense(int nt, const MmParams &p, int64_t max_tiles,
                     : mm_launch_as<kMmPlain, 1, 128, false, OUT>(p, max_tiles, s);
 }
 static cudaError_t mm_launch_gateup(int nt, const MmParams &p, int64_t max_tiles, cudaStream_t s) {
-  return nt == 16   ? mm_launch_as<kMmGateUp, 2, 16, false, 0>(p, max_tiles, s)
-         : nt == 32 ? mm_launch_as<kMmGateUp, 2, 32, false, 0>(p, max_tiles, s)
-                    : mm_launch_as<kMmGateUp, 2, 128, true, 0>(p, max_tiles, s);
+  return nt == 16 ? mm_launch_as<kMmGateUp, 2, 16, false, 0>(p, max_tiles, s)
+                  : mm_launch_as<kMmGateUp, 2, 128, true, 0>(p, max_tiles, s);
 }
 static cudaError_t mm_launch_down(int nt, const MmParams &p, int64_t max_tiles, cudaStream_t s) {
-  return nt == 16   ? mm_launch_as<kMmPlain, 1, 16, false, kMmBf16Vec>(p, max_tiles, s)
-         : nt == 32 ? mm_launch_as<kMmPlain, 1, 32, false, kMmBf16Vec>(p, max_tiles, s)
-                    : mm_launch_as<kMmPlain, 2, 128, true, kMmBf16Vec>(p, max_tiles, s);
+  return nt == 16 ? mm_launch_as<kMmPlain, 1, 16, false, kMmBf16Vec>(p, max_tiles, s)
+                  : mm_launch_as<kMmPlain, 2, 128, true, kMmBf16Vec>(p, max_tiles, s);
 }
 
 // ---- expert FFN: workspace ---------------------------------------------------
@@ -900,10 +898,11 @@ struct FfnMxGeom {
 static FfnMxGeom ffn_mx_geom(const si_mxfp4_experts &L, int n_tokens, int top_k) {
   FfnMxGeom g{};
   g.pairs = static_cast<int64_t>(n_tokens) * top_k;
-  // the smallest tile that holds an expert's average tokens, and from 33 on the
-  // tokens on the lanes
+  // tiles of 16 tokens as long as they hold an expert's average (128 experts,
+  // H 2048, I 768, top-8: 128 tokens 66.7 us), else the tokens on the lanes (256
+  // tokens 72.1 us, in tiles of 16 79.4)
   const int64_t avg = (g.pairs + L.n_experts - 1) / L.n_experts;
-  g.nt = avg <= 16 ? 16 : avg <= 32 ? 32 : 128;
+  g.nt = avg <= 8 ? 16 : 128;
   const int64_t with = std::min<int64_t>(L.n_experts, g.pairs);   // experts that can hold pairs
   g.max_tiles = (g.pairs + with * (g.nt - 1)) / g.nt;
   g.rows = g.max_tiles * g.nt;
@@ -961,9 +960,10 @@ extern "C" si_status si_mxfp4_matmul(const void *a_codes, const void *a_scales, 
   const int64_t n_tt = (m + nt - 1) / nt, row_tiles = (n + 127) / 128;
   const int size = out_type == SI_F32 ? 4 : 2;
   const bool vec = n * size % 16 == 0 && ld_out * size % 16 == 0 && aligned16(out);
-  // the tokens on the lanes as soon as such tiles fill the SMs and the rows can
-  // be written in whole words
-  const bool tok = nt == 128 && vec && n_tt * ((row_tiles + 1) / 2) >= sm_count();
+  // the tokens on the lanes when tiles of 128 x 128 take more than one round of
+  // the SMs (k 4096, n 4096: m 1024 10.2 us against 12.9, but m 512 10.0 against
+  // 8.1) and the rows can be written in whole words
+  const bool tok = nt == 128 && vec && n_tt * row_tiles > sm_count();
   const int ma = tok ? 2 : 1;
   const int64_t n_rt = (row_tiles + ma - 1) / ma;
   if (n_tt * n_rt > 0x7FFFFFFF || n_tt * nt > 0x7FFFFFFF) return SI_ERR_UNSUPPORTED;

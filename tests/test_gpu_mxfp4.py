@@ -276,7 +276,7 @@ def ffn_oracle(weights, x, ids, w, E):
     return out, tol + half * (np.abs(out) + tol)
 
 
-# up to 32 pairs in one launch with the sort, then one or two launches of it; 16, 32
+# up to 32 pairs in one launch with the sort, then one or two launches of it; 16
 # and 128 tokens a tile
 FFN = [(32, 1, 1, 64, 64), (33, 1, 1, 64, 64), (16, 2, 2, 96, 64), (4, 1024, 8, 64, 32), (1, 8, 2, 256, 128), (1, 4, 1, 32, 32), (5, 8, 8, 96, 160), (16, 3, 2, 288, 96), (70, 4, 3, 128, 256),
        (40, 1, 1, 64, 416), (150, 2, 2, 160, 64), (200, 1, 1, 544, 32), (9, 40, 8, 256, 128)]
