@@ -435,7 +435,7 @@ si_status si_moe_stack_graph_create_batched(const si_moe_layer *layers, int n_la
  *   cols    a multiple of 32; codes and scales 16-byte aligned
  * The float matrix is fp32, fp16 or bf16 with contiguous columns, row_stride
  * values between rows and mat_stride between matrices (ignored for one row, one
- * matrix); rows and matrices may not overlap. n_mats = 0 or rows = 0 returns
+ * matrix): matrices one behind the other, or their rows in turn, without overlap. n_mats = 0 or rows = 0 returns
  * SI_OK and enqueues nothing. si_dequantize_mxfp4 rounds to nearest even where
  * its type cannot hold a value (fp16; bf16 and fp32 hold every one).
  */
@@ -449,9 +449,10 @@ si_status si_dequantize_mxfp4(const void *codes, const void *scales, int64_t n_m
 /*
  * si_mxfp4_matmul - out[i][j] = sum_c a[i][c] * w[j][c] of two MXFP4 matrices on
  * the tensor cores (exact products, fp32 accumulation), rounded once to out_type.
- *   a     [m][k], w [n][k]; m, n >= 1, k a multiple of 32, <= 2^20
+ *   a     [m][k], w [n][k]; m, n 1..2^30, k a multiple of 32, <= 2^20 (more than 2^30
+ *         output tiles of at least 16 x 128: SI_ERR_UNSUPPORTED)
  *   out   device [m] rows of n values (SI_BF16, SI_F16 or SI_F32), ld_out >= n
- *         values apart; the values between them are left as they are
+ *         values apart; the values between them are left as they are. May not alias a or w
  *   workspace  si_mxfp4_matmul_workspace_bytes(m, n, k) bytes, zeroed once, or NULL:
  *         it holds the status word alone, and without it a wait that ran out on
  *         the device is not reported

@@ -143,10 +143,14 @@ static si_status mx_check(const void *f, si_dtype type, const void *codes, const
   if (!f || !codes || !scales || !aligned16(codes) || !aligned16(scales) ||
       (reinterpret_cast<uintptr_t>(f) % size))
     return SI_ERR_INVALID_ARG;
-  // rows that overlap or run backwards are refused, for reading too
-  if ((rows > 1 && row_stride < cols) || row_stride < 0 || row_stride > (int64_t(1) << 40)) return SI_ERR_INVALID_ARG;
-  if ((n_mats > 1 && mat_stride < (rows - 1) * row_stride + cols) || mat_stride < 0 ||
-      mat_stride > (int64_t(1) << 50))
+  // rows that overlap or run backwards are refused, for reading too: matrices lie
+  // one behind the other, or row by row in turn
+  if (row_stride < 0 || row_stride > (int64_t(1) << 40) || mat_stride < 0 || mat_stride > (int64_t(1) << 50) ||
+      (rows > 1 && row_stride < cols) || (n_mats > 1 && mat_stride < cols))
+    return SI_ERR_INVALID_ARG;
+  const int64_t rows_end = rows > 1 ? (rows - 1) * row_stride + cols : cols;
+  const int64_t mats_end = n_mats > 1 && mat_stride <= (int64_t(1) << 40) / n_mats ? (n_mats - 1) * mat_stride + cols : 0;
+  if (n_mats > 1 && mat_stride < rows_end && (rows == 1 || mats_end == 0 || row_stride < mats_end))
     return SI_ERR_INVALID_ARG;
   sh.rows = rows;
   sh.cols = cols;

@@ -938,7 +938,7 @@ static bool ffn_mx_shape_ok(const si_mxfp4_experts *L, int n_tokens, int top_k) 
 using namespace si;
 
 extern "C" size_t si_mxfp4_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-  if (m < 1 || n < 1 || k < 32 || k % 32 || m >= (int64_t(1) << 31) || n >= (int64_t(1) << 31) ||
+  if (m < 1 || n < 1 || k < 32 || k % 32 || m > (int64_t(1) << 30) || n > (int64_t(1) << 30) ||
       k > (int64_t(1) << 20))
     return 0;
   return sizeof(WsHeader);
@@ -966,7 +966,7 @@ extern "C" si_status si_mxfp4_matmul(const void *a_codes, const void *a_scales, 
   const bool tok = nt == 128 && vec && n_tt * row_tiles > sm_count();
   const int ma = tok ? 2 : 1;
   const int64_t n_rt = (row_tiles + ma - 1) / ma;
-  if (n_tt * n_rt > 0x7FFFFFFF || n_tt * nt > 0x7FFFFFFF) return SI_ERR_UNSUPPORTED;
+  if (n_tt * n_rt > (int64_t(1) << 30)) return SI_ERR_UNSUPPORTED;
   if (!codes_map(&p.a0, w_codes, 1, n, k, 128) || !codes_map(&p.b, a_codes, 1, m, k, nt)) return SI_ERR_CUDA;
   p.a1 = p.a0;
   p.sa0 = p.sa1 = static_cast<const uint8_t *>(w_scales);

@@ -6,6 +6,10 @@ every partial sum of every dot is a multiple of one quantum below 2^24 of them
 only the rounding to the output type is allowed for, half a unit in the last
 place (finfo.eps / 2 relative).
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -111,6 +115,11 @@ def test_quantize_strides_and_alignment(kind):
     assert torch.equal(out[:, ::2, 3:99].cpu(), m.si_dequantize_mxfp4(codes, scales, dtype=TYPES[kind]).cpu())
     out[:, ::2, 3:99] = 7.0
     assert bool((out == 7.0).all())
+    # matrices whose rows lie in turn
+    turn = big.view(70, 3, 331)[..., :96].transpose(0, 1)
+    codes, scales = m.si_quantize_mxfp4(turn)
+    want = m.si_quantize_mxfp4(turn.contiguous())
+    assert torch.equal(codes, want[0]) and torch.equal(scales, want[1])
     with pytest.raises(m.SiError):      # rows that lie on one another
         m.si_quantize_mxfp4(big[:1, :96].expand(4, 96))
 
@@ -231,6 +240,38 @@ def test_matmul_graph_and_streams():
     got = [m.si_mxfp4_matmul(a, sa, w, sw, stream=streams[i % 2]) for i in range(16)]
     torch.cuda.synchronize()
     assert all(torch.equal(y.cpu(), -want) for y in got)
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first calls are captured: nothing that a capture forbids
+    happens in them."""
+    code = """
+import torch, moe_decode_ffn_gb300 as m
+x = torch.randn(40, 256, device="cuda").to(torch.bfloat16)
+ids = torch.randint(0, 4, (40, 2), device="cuda", dtype=torch.int32)
+w = torch.rand(40, 2, device="cuda")
+gate, up, down = (torch.randn(4, 128, 256, device="cuda"), torch.randn(4, 128, 256, device="cuda"), torch.randn(4, 256, 128, device="cuda"))
+def step():
+    e = m.Mxfp4Experts.quantize(gate, up, down)
+    y = m.si_moe_ffn_mxfp4(e, x, ids, w)
+    c, s = m.si_quantize_mxfp4(x)
+    z = m.si_mxfp4_matmul(c, s, *m.si_quantize_mxfp4(gate[0]))
+    o, p, f = m.si_moe_sort(ids, 4)
+    xs = m.si_moe_gather(x, p, f)
+    g = m.si_moe_combine_backward(x, xs, p, f, w)
+    return y, z, m.si_moe_combine(xs, p, w), m.si_moe_gather_backward(xs, p), *g, m.si_dequantize_mxfp4(c, s), e
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = step()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(out[:-1], step()[:-1]))
+print("same")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=root)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
 
 
 # ---- expert FFN --------------------------------------------------------------

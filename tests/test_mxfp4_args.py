@@ -28,6 +28,9 @@ def test_scale_bytes(lib):
     ((16, m.SI_BF16, 1, 4, 48, 48, 0, 16, 16), BAD),       # columns not a multiple of 32
     ((16, m.SI_BF16, 1, 4, 64, 32, 0, 16, 16), BAD),       # rows overlap
     ((16, m.SI_BF16, 2, 4, 64, 64, 128, 16, 16), BAD),     # matrices overlap
+    ((16, m.SI_BF16, 2, 4, 64, 100, 64, 16, 16), BAD),     # rows in turn that overlap
+    ((16, m.SI_BF16, 2, 4, 64, 128, 32, 16, 16), BAD),
+    ((16, m.SI_BF16, 1, 4, 64, -64, 0, 16, 16), BAD),
     ((16, m.SI_BF16, 1, -1, 64, 64, 0, 16, 16), BAD),
     ((16, m.SI_BF16, -1, 4, 64, 64, 0, 16, 16), BAD),
     ((16, m.SI_BF16, 1, 4, 64, 64, 0, 8, 16), BAD),        # misaligned codes
@@ -48,9 +51,10 @@ def test_matmul_refusals(lib):
     def call(ac=16, asc=16, mm=4, wc=16, wsc=16, n=8, k=64, out=16, ty=m.SI_BF16, ld=8, ws=256, nb=256):
         return lib.si_mxfp4_matmul(ac, asc, mm, wc, wsc, n, k, out, ty, ld, ws, nb, None)
     for kw in ({"ac": None}, {"wsc": None}, {"out": None}, {"mm": 0}, {"n": 0}, {"k": 0}, {"k": 48}, {"ld": 7},
-               {"ac": 8}, {"wc": 24}, {"out": 17}, {"k": (1 << 20) + 32}, {"mm": -1}):
+               {"ac": 8}, {"wc": 24}, {"out": 17}, {"k": (1 << 20) + 32}, {"mm": -1}, {"mm": (1 << 30) + 1}):
         assert call(**kw) == BAD, kw
     assert call(ty=m.SI_Q8_0) == UNS
+    assert call(mm=1 << 30, n=1 << 30, ld=1 << 30) == UNS      # more tiles than a launch counts
     for kw in ({"ws": 16}, {"nb": 255}):
         assert call(**kw) == WS, kw
 
