@@ -884,7 +884,8 @@ static cudaError_t mm_launch_gateup(int nt, const MmParams &p, int64_t max_tiles
                   : mm_launch_as<kMmGateUp, 2, 128, true, 0>(p, max_tiles, s);
 }
 static cudaError_t mm_launch_down(int nt, const MmParams &p, int64_t max_tiles, cudaStream_t s) {
-  return nt == 16 ? mm_launch_as<kMmPlain, 1, 16, false, kMmBf16Vec>(p, max_tiles, s)
+  // 256 rows a tile: fewer loads for the same bytes (128 tokens 66.2 -> 63.5 us)
+  return nt == 16 ? mm_launch_as<kMmPlain, 2, 16, false, kMmBf16Vec>(p, max_tiles, s)
                   : mm_launch_as<kMmPlain, 2, 128, true, kMmBf16Vec>(p, max_tiles, s);
 }
 
@@ -1063,13 +1064,12 @@ extern "C" si_status si_moe_ffn_mxfp4(const si_mxfp4_experts *L, int n_tokens, i
   e = mm_launch_gateup(g.nt, gu, g.max_tiles * gu.n_rt, s);
   if (e != cudaSuccess) return SI_ERR_CUDA;
 
-  const int ma = g.nt == 128 ? 2 : 1;
   dn.a1 = dn.a0;
   dn.sa0 = dn.sa1 = static_cast<const uint8_t *>(L->down_scales);
   dn.sb = base + g.off_hs;
   dn.rows = H;
   dn.row_tiles = (H + 127) / 128;
-  dn.n_rt = (dn.row_tiles + ma - 1) / ma;
+  dn.n_rt = (dn.row_tiles + 1) / 2;
   dn.K = I;
   dn.kt = g.kt_h;
   dn.tile_expert = so.tile_expert;
