@@ -472,7 +472,7 @@ si_status si_mxfp4_matmul(const void *a_codes, const void *a_scales, int64_t m, 
  * place of expert e, offsets[n_experts] = number of kept pairs.
  *   n_tokens >= 1, top_k 1..8, n_experts 1..1024
  *   workspace  si_moe_sort_workspace_bytes(n_tokens, top_k, n_experts) bytes (0 up to
- *              2048 pairs: NULL then), any contents, no status word
+ *              4096 pairs: NULL then), any contents, no status word
  *   order int32 [n_tokens * top_k], position int32 [n_tokens][top_k],
  *   offsets int32 [n_experts + 1]
  *

@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_pairs_kernel(SortArgs a) {
 // places its ids in rounds of kSortRound: a warp ranks its ids with match.any,
 // a scan over the warps' counts does the rest.
 // ---------------------------------------------------------------------------
-constexpr int kSortIds = 4;                                // ids per thread and round
+constexpr int kSortIds = 2;                                // ids per thread and round
 constexpr int kSortRound = kSortThreads * kSortIds;
 
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a) {
@@ -143,10 +143,16 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a) {
   int mine = 0, my_tiles = 0;
   for (int e = e0; e < e1; ++e) {
     int total = 0, before = 0;
-    for (int c = 0; c < static_cast<int>(gridDim.x); ++c) {
-      const int n = __ldcg(a.counts + static_cast<size_t>(c) * (E + 1) + e);
-      if (c < static_cast<int>(blockIdx.x)) before += n;
-      total += n;
+    for (int c0 = 0; c0 < static_cast<int>(gridDim.x); c0 += 16) {
+      int n[16];
+#pragma unroll
+      for (int u = 0; u < 16; ++u)
+        n[u] = c0 + u < static_cast<int>(gridDim.x) ? __ldcg(a.counts + static_cast<size_t>(c0 + u) * (E + 1) + e) : 0;
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        if (c0 + u < static_cast<int>(blockIdx.x)) before += n[u];
+        total += n[u];
+      }
     }
     s_next[e] = before;
     s_warp[e] = total;

@@ -7,7 +7,7 @@
 namespace si {
 
 constexpr int kSortMaxExperts = 1024;
-constexpr int kSortFewPairs = 2048;    // pairs that one launch sorts
+constexpr int kSortFewPairs = 4096;    // pairs that one launch sorts (5.5 us; two launches 5.6)
 constexpr int kSortChunks = 64;        // chunks of a longer batch
 
 // For pairs = n_tokens * top_k ids: position[i] = place of pair i (by expert,

@@ -56,7 +56,7 @@ def test_sort_skewed_and_large():
     assert torch.equal(position.reshape(-1)[order.long()].cpu(), torch.arange(65536, dtype=torch.int32))
 
 
-@pytest.mark.parametrize("pairs", [2047, 2048, 2049, 4095, 4097, 64 * 2048 - 1, 64 * 2048 + 1, 300001])
+@pytest.mark.parametrize("pairs", [2049, 4095, 4096, 4097, 64 * 1024 - 1, 64 * 1024 + 1, 64 * 2048 + 1, 300001])
 @pytest.mark.parametrize("E", [1, 100, 1024])
 def test_sort_at_the_borders_of_its_rounds(pairs, E):
     """One launch or two, chunks of one round or of several, the last one ragged."""
