@@ -3,7 +3,10 @@
 // Both kernels give a block of 256 threads one scale tile: 128 rows x 128
 // columns. 16 consecutive lanes take a row (8 values, 16 or 32 bytes each), so
 // every access of a warp covers whole 32-byte sectors, and the tile's 512
-// scale bytes are assembled in shared memory and move as one piece.
+// scale bytes are assembled in shared memory and move as one piece. Both are
+// bound by HBM: 98304 x 2048 bf16 values are quantised in 75.2 us and decoded in
+// 76.9 us (6.8 and 6.6 TB/s; a copy of them reaches 6.7); before the largest value
+// of a block was found two values at a time the quantiser issued for 89 us.
 #include "host.hpp"
 #include "mxfp4.cuh"
 

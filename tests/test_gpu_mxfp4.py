@@ -415,3 +415,57 @@ def test_ffn_graph_replay():
         got = out.clone()
         assert torch.equal(got, m.si_moe_ffn_mxfp4(experts, x, ids, w))
     assert m.si_workspace_status(ws) == m.SI_OK
+
+
+def test_layer_of_router_experts_and_norm():
+    """A layer as a user builds it: the router, the MXFP4 experts, the residual
+    norm; then the same rows through the sorted calls. Captured and replayed on
+    other tokens, equal to the calls one by one, and the expert outputs near the
+    same chain with fp32 products. There y and the result are rounded to bf16
+    (2^-8 each, y in k = 4 terms whose norms add up to about twice the sum's: 3 *
+    2^-8 = 0.012 of the norm) and a few h lie on a border between two codes."""
+    E, H, I, T, k = 16, 256, 128, 24, 4
+    g = torch.Generator(device="cuda").manual_seed(11)
+    draw = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    gate, up, down = draw(E, I, H) * 0.1, draw(E, I, H) * 0.1, draw(E, H, I) * 0.1
+    experts = m.Mxfp4Experts.quantize(gate, up, down)
+    wr, wn = draw(E, H).to(torch.bfloat16), torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    x = draw(T, H).to(torch.bfloat16)
+    ws = m.workspace(m.ffn_mxfp4_workspace_bytes(experts, T, k))
+    wsr = m.workspace(m.router_workspace_bytes(E, H, T))
+
+    def layer():
+        ids, w, _ = m.si_moe_router_topk(x, wr, k, ws=wsr)
+        routed = m.si_moe_ffn_mxfp4(experts, x, ids, w, ws=ws)
+        s, y, _ = m.si_add_rmsnorm3(routed, x, None, wn)
+        order, position, offsets = m.si_moe_sort(ids, E)
+        xs = m.si_moe_gather(x, position, offsets)
+        return ids, w, routed, s, y, order, xs, m.si_moe_combine(xs, position, w)
+
+    layer()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = layer()
+    for _ in range(2):
+        x.copy_(draw(T, H))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        assert all(torch.equal(a, b) for a, b in zip(got, layer()))
+    ids, w, routed, s, y, order, xs, comb = got
+    assert torch.equal(s, (routed + x))
+    # the combine of a token's own rows is the token times the sum of its weights (one)
+    assert torch.allclose(comb.float(), x.float(), rtol=2.0 ** -7, atol=2.0 ** -20)
+    G, U, D = (m.si_dequantize_mxfp4(*p, dtype=torch.float32) for p in (experts.gate, experts.up, experts.down))
+    xq = m.si_dequantize_mxfp4(*m.si_quantize_mxfp4(x), dtype=torch.float32)
+    want = torch.zeros(T, H, device="cuda")
+    for t in range(T):
+        for r in range(k):
+            e = int(ids[t, r])
+            z = G[e] @ xq[t]
+            h = m.si_dequantize_mxfp4(*m.si_quantize_mxfp4((z * torch.sigmoid(z) * (U[e] @ xq[t]))[None]), dtype=torch.float32)[0]
+            want[t] += w[t, r] * (D[e] @ h)
+    assert float((routed.float() - want).norm() / want.norm()) < 0.02
+    assert m.si_workspace_status(ws) == m.SI_OK and m.si_workspace_status(wsr) == m.SI_OK
