@@ -52,10 +52,11 @@ enum MmMode { kMmPlain = 0, kMmGateUp = 1 };
 // NT: tokens of a tile. TOK: the tokens on the lanes (NT = 128).
 template <int MODE, int MA, int NT, bool TOK> struct MmCfg {
   static_assert(!TOK || (MA == 2 && NT == 128), "128 tokens by 256 weight rows");
+  static_assert(MODE == kMmPlain || TOK || NT == 16, "the SwiGLU epilogue takes 16 tokens");
   // epilogue warps: 4 for the lanes, times the parts of the columns. TOK: a part
   // is 64 columns, which fit into registers, so that the accumulator is free
   // before it is written; otherwise parts of the tokens.
-  static constexpr int kParts = TOK ? 4 : 2;
+  static constexpr int kParts = TOK ? 4 : NT >= 32 ? 2 : 1;
   static constexpr int kEpiWarps = 4 * kParts;
   static constexpr int kScaleWarp = 2 + kEpiWarps;
   static constexpr int kThreads = 32 * (kScaleWarp + MA);   // TOK: 20 warps, which leave 96 registers a thread
@@ -307,62 +308,48 @@ SI_DEV float mm_silu_mul(float g, float u) {
   return g * r * u;
 }
 
-// h = silu(g) u of a lane's feature for 16 tokens, then MXFP4: the 32 lanes of
-// the warp are one block of every token, so its scale is a warp maximum. Lane j
+// h = silu(g) u of a lane's feature for up to 16 tokens, then MXFP4: the 32 lanes
+// of the warp are one block of every token, so its scale is a warp maximum. Lane j
 // keeps the scale of token j and its multiplier, which the others fetch.
-template <int NT, int PARTS>
-SI_DEV void mm_write_h(const MmParams &p, const MmTile &t, uint32_t acc_g, uint32_t acc_u, int q, int part,
-                       int lane) {
-  const int64_t row0 = static_cast<int64_t>(t.tt) * NT;
+SI_DEV void mm_write_h(const MmParams &p, const MmTile &t, uint32_t acc_g, uint32_t acc_u, int q, int lane) {
+  const int64_t row0 = static_cast<int64_t>(t.tt) * 16;
   const int blk = t.rt * 4 + q;                 // this warp's block of 32 features
-  const bool live = blk * 32 < p.rows;          // rows % 32 == 0: the whole warp or none of it
   const size_t row_bytes = static_cast<size_t>(p.rows) / 2;
   uint8_t *sf = p.h_scales + (static_cast<size_t>(t.tt) * p.h_kt + t.rt) * kMxTileBytes;
-  if (!live) {                                  // behind the last feature: scales that multiply zeros
-    for (int j = 16 * part + lane; j < t.count; j += 16 * PARTS)
-      if (lane < 16) sf[mx_scale_byte(j, blk)] = 0;
+  const bool mine = lane < 16 && lane < t.count;
+  if (blk * 32 >= p.rows) {                     // behind the last feature (rows % 32 == 0): scales that multiply zeros
+    if (mine) sf[mx_scale_byte(lane, blk)] = 0;
     return;
   }
   uint32_t g[16], u[16];
-  if (16 * part < t.count) {
-    tmem_ld16(acc_g + 16 * part, g);
-    tmem_ld16(acc_u + 16 * part, u);
+  tmem_ld16(acc_g, g);
+  tmem_ld16(acc_u, u);
+  tmem_wait_ld();
+  float h[16];
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    h[j] = mm_silu_mul(__uint_as_float(g[j]), __uint_as_float(u[j]));
+    const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h[j]) & 0x7FFFFFFFu);
+    if ((lane & 15) == j) top = m;
   }
-#pragma unroll 1
-  for (int j0 = 16 * part; j0 < t.count; j0 += 16 * PARTS) {
-    const int js = j0 + (lane & 15);            // the token whose scale this lane keeps
-    tmem_wait_ld();
-    float h[16];
-    uint32_t top = 0;
+  const uint32_t s = mx_scale_of(top);
+  const float up = mx_inv_scale(s);
+  const uint32_t bad = __ballot_sync(0xffffffffu, s == 255u);   // tokens with an infinity or a NaN
+  if (mine) sf[mx_scale_byte(lane, blk)] = static_cast<uint8_t>(s);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) h[j] = mm_silu_mul(__uint_as_float(g[j]), __uint_as_float(u[j]));
-    if (j0 + 16 * PARTS < t.count) {      // the next group's accumulators meanwhile
-      tmem_ld16(acc_g + j0 + 16 * PARTS, g);
-      tmem_ld16(acc_u + j0 + 16 * PARTS, u);
+  for (int j = 0; j < 16; ++j) h[j] *= __shfl_sync(0xffffffffu, up, j);
+#pragma unroll
+  for (int h8 = 0; h8 < 16; h8 += 8) {
+    uint32_t w = mx_codes8(h + h8);
+    if (bad) {                                  // their codes are 0
+      for (int j = 0; j < 8; ++j)
+        if (bad >> (h8 + j) & 1u) w &= ~(15u << (4 * j));
     }
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h[j]) & 0x7FFFFFFFu);
-      if ((lane & 15) == j) top = m;
-    }
-    const uint32_t s = mx_scale_of(top);
-    const float up = mx_inv_scale(s);
-    const uint32_t bad = __ballot_sync(0xffffffffu, s == 255u);   // tokens with an infinity or a NaN
-    if (lane < 16 && js < t.count) sf[mx_scale_byte(js, blk)] = static_cast<uint8_t>(s);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) h[j] *= __shfl_sync(0xffffffffu, up, j);
-#pragma unroll
-    for (int h8 = 0; h8 < 16; h8 += 8) {
-      uint32_t w = mx_codes8(h + h8);
-      if (bad) {                                // their codes are 0
-        for (int j = 0; j < 8; ++j)
-          if (bad >> (h8 + j) & 1u) w &= ~(15u << (4 * j));
-      }
-      w = transpose_nibbles(w, lane);
-      const int j = j0 + h8 + (lane & 7);
-      if (j < t.count)
-        *reinterpret_cast<uint32_t *>(p.h_codes + (row0 + j) * row_bytes + blk * 16 + (lane >> 3) * 4) = w;
-    }
+    w = transpose_nibbles(w, lane);
+    const int j = h8 + (lane & 7);
+    if (j < t.count)
+      *reinterpret_cast<uint32_t *>(p.h_codes + (row0 + j) * row_bytes + blk * 16 + (lane >> 3) * 4) = w;
   }
 }
 
@@ -720,7 +707,7 @@ __global__ void __launch_bounds__(MmCfg<MODE, MA, NT, TOK>::kThreads, 1)
         if (!ok) break;
         const uint32_t u = wait_acc(n + 1);
         if (!ok) break;
-        mm_write_h<NT, C::kParts>(p, t, g, u, q, part, lane);
+        mm_write_h(p, t, g, u, q, lane);
         free_acc(n);
         free_acc(n + 1);
         n += 2;
