@@ -637,7 +637,7 @@ def _strides(t: torch.Tensor, name: str):
 def si_quantize_mxfp4(x: torch.Tensor, codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
                       stream=None):
     """x [rows, cols] or [n, rows, cols] (fp32, fp16, bf16; rows and matrices at
-    any stride) -> (codes uint8 [.., rows, cols / 2], scale tiles uint8
+    any stride without overlap) -> (codes uint8 [.., rows, cols / 2], scale tiles uint8
     [.., ceil(rows / 128), ceil(cols / 128), 512])."""
     dev = x.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
@@ -645,16 +645,19 @@ def si_quantize_mxfp4(x: torch.Tensor, codes: torch.Tensor | None = None, scales
     n, rows, cols, row, mat = _strides(x, "x")
     if cols == 0 or cols % 32:
         raise ValueError(f"x has {cols} columns, expected a multiple of 32")
-    tr, tc = (rows + 127) // 128, (cols + 127) // 128
-    if codes is None:
-        codes = _empty((n, rows, cols // 2) if x.dim() == 3 else (rows, cols // 2), dtype=_u8, device=x.device)
-    if scales is None:
-        scales = _empty((n, tr, tc, 512) if x.dim() == 3 else (tr, tc, 512), dtype=_u8, device=x.device)
+    tr, tc, many, d = (rows + 127) // 128, (cols + 127) // 128, x.dim() == 3, x.device
     if x.dtype not in _TYPES:
         _bad_type(x, "x")
-    st = library().si_quantize_mxfp4(
-        x.data_ptr(), _TYPES[x.dtype], n, rows, cols, row, mat, _ptr(codes, dev, n * rows * cols // 2, _u8, "codes"),
-        _ptr(scales, dev, n * tr * tc * 512, _u8, "scales"), _raw_stream(dev))
+    if codes is None:
+        codes = _empty((n, rows, cols // 2) if many else (rows, cols // 2), dtype=_u8, device=d)
+    else:
+        _ptr(codes, dev, n * rows * cols // 2, _u8, "codes")
+    if scales is None:
+        scales = _empty((n, tr, tc, 512) if many else (tr, tc, 512), dtype=_u8, device=d)
+    else:
+        _ptr(scales, dev, n * tr * tc * 512, _u8, "scales")
+    st = library().si_quantize_mxfp4(x.data_ptr(), _TYPES[x.dtype], n, rows, cols, row, mat, codes.data_ptr(),
+                                     scales.data_ptr(), _raw_stream(dev))
     if st:
         _check(st, "si_quantize_mxfp4")
     return codes, scales
