@@ -858,7 +858,9 @@ def si_moe_ffn_mxfp4(experts: Mxfp4Experts, x: torch.Tensor, ids: torch.Tensor, 
     [T, k] -> routed bf16 [T, H]."""
     dev = x.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
-        return _elsewhere(lambda x, ids, w, ws: si_moe_ffn_mxfp4(experts, x, ids, w, ws), stream, x, ids, w, ws)
+        weights = (*experts.gate, *experts.up, *experts.down)
+        return _elsewhere(lambda x, ids, w, ws, *_: si_moe_ffn_mxfp4(experts, x, ids, w, ws), stream, x, ids, w, ws,
+                          *weights)
     (T, k), H = ids.shape, experts.hidden
     if experts.dev != dev:
         raise ValueError(f"tensors on cuda:{dev}, experts on cuda:{experts.dev}")

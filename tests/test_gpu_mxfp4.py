@@ -417,6 +417,33 @@ def test_ffn_graph_replay():
     assert m.si_workspace_status(ws) == m.SI_OK
 
 
+def test_ffn_marks_weights_as_used_by_the_given_stream():
+    """Experts that are let go right after a call on another stream: their memory
+    is not handed out again while that stream still has the call before it."""
+    E, H, I, k, T = 8, 256, 128, 2, 5
+    _, experts = make_experts(81, E, H, I)
+    x = torch.randn(T, H, device="cuda").to(torch.bfloat16)
+    ids = torch.randint(0, E, (T, k), dtype=torch.int32, device="cuda")
+    w = torch.rand(T, k, device="cuda")
+    want = m.si_moe_ffn_mxfp4(experts, x, ids, w)
+    ws = m.workspace(m.ffn_mxfp4_workspace_bytes(experts, T, k))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)      # about 0.1 s
+    got = m.si_moe_ffn_mxfp4(experts, x, ids, w, ws=ws, stream=side)
+    size = sum(t.numel() for t in (*experts.gate, *experts.up, *experts.down))
+    stat = lambda name: torch.cuda.memory_stats()[name + "_bytes.all.current"]  # noqa: E731
+    owned, busy = stat("allocated"), stat("active")
+    del experts
+    assert owned - stat("allocated") >= size        # let go ...
+    assert stat("active") == busy                   # ... but not free for others
+    assert not side.query()                         # the call still waits
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
 def test_layer_of_router_experts_and_norm():
     """A layer as a user builds it: the router, the MXFP4 experts, the residual
     norm; then the same rows through the sorted calls. Captured and replayed on
