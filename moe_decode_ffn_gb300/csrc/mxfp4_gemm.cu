@@ -46,13 +46,18 @@ namespace si {
 constexpr int kMmStageK = 256;         // columns of a stage: 128 bytes of codes per row
 constexpr int kMmABytes = 128 * 128;   // 128 weight rows of a stage
 
-enum MmMode { kMmPlain = 0, kMmGateUp = 1 };
+enum MmMode {
+  kMmPlain = 0,
+  kMmGateUp = 1,
+  kMmStaged = 2,   // TOK: plain, its stores through shared memory (mm_launch_tok)
+};
 
 // MA: 128-row weight tiles of a block's tile (gate and up, or two neighbours).
 // NT: tokens of a tile. TOK: the tokens on the lanes (NT = 128).
 template <int MODE, int MA, int NT, bool TOK> struct MmCfg {
   static_assert(!TOK || (MA == 2 && NT == 128), "128 tokens by 256 weight rows");
-  static_assert(MODE == kMmPlain || TOK || NT == 16, "the SwiGLU epilogue takes 16 tokens");
+  static_assert(MODE != kMmGateUp || TOK || NT == 16, "the SwiGLU epilogue takes 16 tokens");
+  static_assert(MODE != kMmStaged || TOK, "weights on the lanes: kMmPlain stages its 2-byte outputs itself");
   // epilogue warps: 4 for the lanes, times the parts of the columns. TOK: a part
   // is 64 columns, which fit into registers, so that the accumulator is free
   // before it is written; otherwise parts of the tokens.
@@ -66,7 +71,7 @@ template <int MODE, int MA, int NT, bool TOK> struct MmCfg {
   // 16-token groups of an epilogue warp's part, all read at once; staging for
   // two of them at a time (16 tokens x 32 features of 2 bytes each)
   static constexpr int kGroups = NT < 16 * kParts ? 1 : NT / 16 / kParts;
-  static constexpr int kEpiBytes = MODE == kMmGateUp || TOK ? 0 : kGroups == 1 ? 1024 : 2048;
+  static constexpr int kEpiBytes = MODE == kMmStaged ? 1024 : MODE == kMmGateUp || TOK ? 0 : kGroups == 1 ? 1024 : 2048;
   static constexpr int kMaxSmem = 227 * 1024 - kEpiWarps * kEpiBytes - 1536;   // less alignment and barriers
   static constexpr int kStages = kMaxSmem / kStage < 8 ? kMaxSmem / kStage : 8;
   // tensor memory: a ring of accumulators (a tile takes one of 256 columns, or MA
@@ -366,9 +371,7 @@ SI_DEV void tmem_ld32(uint32_t taddr, uint32_t r[32]) {
       : "r"(taddr)
       : "memory");
 }
-// 32 bytes of a row: one sector, one store. (Rows exchanged over 8 lanes to
-// 128-byte pieces measured slower: 80.8 against 73.2 us for 8192 x 4096 x 4096
-// with its quantisation, for the registers that the exchange takes.)
+// 32 bytes of a row: one sector, one store (mm_launch_tok says when).
 SI_DEV void st_global32(void *p, const uint32_t w[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
@@ -418,6 +421,58 @@ SI_DEV void mm_write_tokens(const MmParams &p, int f0, int64_t row0, int j, bool
     write(0, w[0]);
     write(32, w[1]);
   }
+}
+
+// 64 features (from f0) of the warp's 32 tokens (lane = token, from row0, `left`
+// of them in the batch), 32 at a time; 2-byte outputs wait, packed, until all are
+// read. 128 bytes of 8 tokens at a time go through the warp's staging (words
+// permuted by the token: no bank met twice), so that a store writes 4 whole
+// 128-byte pieces of rows.
+template <int OUT, typename Release>
+SI_DEV void mm_write_tokens_staged(const MmParams &p, int f0, int64_t row0, int left, uint32_t acc, int lane,
+                                   uint8_t *stage, Release release) {
+  constexpr int kSize = OUT == kMmF32Vec ? 4 : 2;
+  constexpr int kWords = 8 * kSize;              // words of 32 features
+  const bool any = f0 < p.rows && left > 0;
+  auto write = [&](int c0, const uint32_t *w) {  // features f0 + c0 .. + 128 / kSize - 1
+    const int r = lane >> 3, c = lane & 7;       // the word that this lane writes out, of tokens r and r + 4
+    const bool in = f0 + c0 + c * (16 / kSize) < p.rows;   // whole words (rows * kSize % 16 == 0)
+    uint8_t *out = static_cast<uint8_t *>(p.out) + ((row0 + r) * p.ld + f0 + c0) * kSize + c * 16;
+#pragma unroll
+    for (int t = 0; t < 32; t += 8) {
+      if (t >= left) break;
+      __syncwarp();                              // the staging has been read
+      if ((lane & 24) == t) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4 *>(stage + c * 128 + ((i ^ c) * 16)) =
+              make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 8; i += 4) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(stage + (r + i) * 128 + ((c ^ (r + i)) * 16));
+        if (in && t + i + r < left) *reinterpret_cast<uint4 *>(out + (t + i) * p.ld * kSize) = v;
+      }
+    }
+  };
+  uint32_t w[2 * kWords];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (any) {
+      uint32_t r[32];
+      tmem_ld32(acc + 32 * h, r);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        if constexpr (OUT == kMmF32Vec) w[h * kWords + i] = r[i];
+        else w[h * kWords + i] = mm_pack<OUT>(r[2 * i], r[2 * i + 1]);
+      }
+    }
+    if (h == 1) release();
+    if (OUT == kMmF32Vec && any) write(32 * h, w + h * kWords);
+  }
+  if (OUT != kMmF32Vec && any) write(0, w);
 }
 
 // h = silu(g) u of one block of 32 features of this lane's token, as MXFP4: the
@@ -698,6 +753,9 @@ __global__ void __launch_bounds__(MmCfg<MODE, MA, NT, TOK>::kThreads, 1)
         auto release = [&] { free_acc(n); };
         if constexpr (MODE == kMmGateUp)
           mm_write_h_tokens(p, t, t.rt * 4 + part, j, j < t.count, acc + part * 32, acc + 128 + part * 32, release);
+        else if constexpr (MODE == kMmStaged)
+          mm_write_tokens_staged<OUT>(p, t.rt * 256 + part * 64, static_cast<int64_t>(t.tt) * NT + q * 32,
+                                      t.count - q * 32, acc + part * 64, lane, stage, release);
         else
           mm_write_tokens<OUT>(p, t.rt * 256 + part * 64, static_cast<int64_t>(t.tt) * NT, j, j < t.count,
                                acc + part * 64, release);
@@ -862,6 +920,17 @@ static cudaError_t mm_launch_as(const MmParams &p, int64_t max_tiles, cudaStream
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(max_tiles, sm_count()));
   return launch_pdl(mxfp4_mm_kernel<MODE, MA, NT, TOK, OUT>, dim3(grid), dim3(C::kThreads), C::kSmem, s, p);
 }
+// The tokens on the lanes. While a tile's columns fit into the ring of stages, the
+// next tile's loads are all on their way when the stores come, and these bound
+// it: whole 128-byte pieces of rows (16384 x 4096 x 1024 bf16 39.3 against 42.3 us,
+// fp32 62.1 against 69.5; x 256: 31.2 against 33.8). With more columns the stores
+// stand in the way of the loads, and 32 bytes a lane, straight from the registers,
+// do so less (x 1152: 47.9 against 51.8, x 4096: 102.0 against 106.2).
+template <int OUT> static cudaError_t mm_launch_tok(const MmParams &p, int64_t max_tiles, cudaStream_t s) {
+  return p.K <= MmCfg<kMmStaged, 2, 128, true>::kStages * kMmStageK
+             ? mm_launch_as<kMmStaged, 2, 128, true, OUT>(p, max_tiles, s)
+             : mm_launch_as<kMmPlain, 2, 128, true, OUT>(p, max_tiles, s);
+}
 template <int OUT>
 static cudaError_t mm_launch_dense(int nt, const MmParams &p, int64_t max_tiles, cudaStream_t s) {
   return nt == 16   ? mm_launch_as<kMmPlain, 1, 16, false, OUT>(p, max_tiles, s)
@@ -876,7 +945,7 @@ static cudaError_t mm_launch_gateup(int nt, const MmParams &p, int64_t max_tiles
 static cudaError_t mm_launch_down(int nt, const MmParams &p, int64_t max_tiles, cudaStream_t s) {
   // 256 rows a tile: fewer loads for the same bytes (128 tokens 66.2 -> 63.5 us)
   return nt == 16 ? mm_launch_as<kMmPlain, 2, 16, false, kMmBf16Vec>(p, max_tiles, s)
-                  : mm_launch_as<kMmPlain, 2, 128, true, kMmBf16Vec>(p, max_tiles, s);
+                  : mm_launch_tok<kMmBf16Vec>(p, max_tiles, s);
 }
 
 // ---- expert FFN: workspace ---------------------------------------------------
@@ -975,9 +1044,9 @@ extern "C" si_status si_mxfp4_matmul(const void *a_codes, const void *a_scales, 
   p.wide = ld_out * size % 32 == 0 && (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   const int64_t tiles = n_tt * n_rt;
   if (tok)
-    return cuda_status(out_type == SI_F32    ? mm_launch_as<kMmPlain, 2, 128, true, kMmF32Vec>(p, tiles, s)
-                       : out_type == SI_BF16 ? mm_launch_as<kMmPlain, 2, 128, true, kMmBf16Vec>(p, tiles, s)
-                                             : mm_launch_as<kMmPlain, 2, 128, true, kMmF16Vec>(p, tiles, s));
+    return cuda_status(out_type == SI_F32    ? mm_launch_tok<kMmF32Vec>(p, tiles, s)
+                       : out_type == SI_BF16 ? mm_launch_tok<kMmBf16Vec>(p, tiles, s)
+                                             : mm_launch_tok<kMmF16Vec>(p, tiles, s));
   return cuda_status(out_type == SI_F32 ? mm_launch_dense<kMmF32>(nt, p, tiles, s)
                      : out_type == SI_BF16
                          ? (vec ? mm_launch_dense<kMmBf16Vec>(nt, p, tiles, s) : mm_launch_dense<kMmBf16>(nt, p, tiles, s))

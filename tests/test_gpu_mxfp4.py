@@ -160,11 +160,13 @@ def test_matmul_exact(mm, n, k):
 
 
 @pytest.mark.parametrize("kind", list(TYPES))
-@pytest.mark.parametrize("mm,n,k,pad", [(2500, 2088, 96, 0), (1290, 4356, 320, 0), (2600, 2056, 64, 24), (2049, 2500, 544, 4)])
+@pytest.mark.parametrize("mm,n,k,pad", [(2500, 2088, 96, 0), (1290, 4356, 320, 0), (2600, 2056, 64, 24), (2049, 2500, 544, 4),
+                                        (2500, 2088, 1024, 0), (2500, 2088, 1120, 0), (2600, 2056, 1056, 8), (2049, 2500, 1152, 4)])
 def test_matmul_of_many_tokens(mm, n, k, pad, kind):
     """Enough tiles for the tokens to lie on the lanes: ragged in tokens, in the
     256 rows of a tile and (one tile of 128 left) in their halves, odd columns,
-    rows of whole 16-byte words and others."""
+    rows of whole 16-byte words and others; up to 1024 columns, whose outputs go
+    through shared memory, and more."""
     g = torch.Generator(device="cuda").manual_seed(mm + n)
     draw = lambda r, hi: torch.randint(0, hi, r, generator=g, device="cuda", dtype=torch.int32)  # noqa: E731
     ac, asc = draw((mm, k), 16).cpu().numpy().astype(np.uint8), (126 + draw((mm, k // 32), 3)).cpu().numpy().astype(np.uint8)
