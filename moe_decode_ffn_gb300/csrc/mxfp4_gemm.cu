@@ -15,12 +15,12 @@
 //    the same products in 4 MMAs a stage instead of 8; and a lane holds whole
 //    32-value blocks of its token, which quantises h without any exchange.
 //
-// A block: a thread of warp 0 keeps the codes of a ring of stages coming (256
-// columns by tensor TMA in the 128-byte swizzle) with the tokens' scale tiles,
-// one thread of warp 1 moves the scales into tensor memory (tcgen05.cp) and issues
-// the MMAs, warps 2.. read the accumulators and write the outputs (4 of them cover
-// the 128 lanes of tensor memory; each group of 4 takes a part of the columns), and
-// a thread of each of the last warps brings the scale tiles of one weight operand.
+// A block: a thread of warp 0 keeps the tokens of a ring of stages coming (256
+// columns: codes by tensor TMA in the 128-byte swizzle, scale tiles by plain bulk
+// copies), a thread of each of the last warps the same of one weight operand; one
+// thread of warp 1 moves the scales into tensor memory (tcgen05.cp) and issues the
+// MMAs, warps 2.. read the accumulators and write the outputs (4 of them cover the
+// 128 lanes of tensor memory; each group of 4 takes a part of the columns).
 // Blocks are persistent: tile i of block b is b + i * gridDim. The accumulators are
 // a ring too, so that the MMAs of a tile run beside the epilogue of the one before.
 //
@@ -63,8 +63,8 @@ template <int MODE, int MA, int NT, bool TOK> struct MmCfg {
   // before it is written; otherwise parts of the tokens.
   static constexpr int kParts = TOK ? 4 : NT >= 32 ? 2 : 1;
   static constexpr int kEpiWarps = 4 * kParts;
-  static constexpr int kScaleWarp = 2 + kEpiWarps;
-  static constexpr int kThreads = 32 * (kScaleWarp + MA);   // TOK: 20 warps, which leave 96 registers a thread
+  static constexpr int kWeightWarp = 2 + kEpiWarps;
+  static constexpr int kThreads = 32 * (kWeightWarp + MA);   // TOK: 20 warps, which leave 96 registers a thread
   static constexpr int kBBytes = NT * 128;
   static constexpr int kSfBytes = 2 * kMxTileBytes;               // per operand tile and stage
   static constexpr int kStage = MA * kMmABytes + kBBytes + (MA + 1) * kSfBytes;
@@ -371,9 +371,11 @@ SI_DEV void tmem_ld32(uint32_t taddr, uint32_t r[32]) {
       : "r"(taddr)
       : "memory");
 }
-// 32 bytes of a row: one sector, one store (mm_launch_tok says when).
+// 32 bytes of a row: one sector, one store (mm_launch_tok says when). Not kept in
+// the L1, which the ring of stages shares: 8192 x 4096 x 4096 with its quantisation
+// 73.0 -> 72.1 us.
 SI_DEV void st_global32(void *p, const uint32_t w[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+  asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
 }
@@ -490,6 +492,7 @@ SI_DEV void mm_write_h_tokens(const MmParams &p, const MmTile &t, int blk, int j
       tmem_ld16(acc_g + i0, g);
       tmem_ld16(acc_u + i0, u);
       tmem_wait_ld();
+      if (i0 == 16) release();                   // the next tile's MMAs run beside the rest
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         h[i0 + i] = mm_silu_mul(__uint_as_float(g[i]), __uint_as_float(u[i]));
@@ -497,7 +500,7 @@ SI_DEV void mm_write_h_tokens(const MmParams &p, const MmTile &t, int blk, int j
       }
     }
   }
-  release();
+  if (!live) release();
   if (!valid) return;
   uint8_t *sf = p.h_scales + (static_cast<size_t>(t.tt) * p.h_kt + t.rt) * kMxTileBytes + mx_scale_byte(j, blk);
   if (!live) {                                   // behind the last feature: a scale that multiplies zeros
@@ -537,38 +540,32 @@ __global__ void __launch_bounds__(MmCfg<MODE, MA, NT, TOK>::kThreads, 1)
   uint32_t *s_taddr = reinterpret_cast<uint32_t *>(drain + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_ks = (p.K + kMmStageK - 1) / kMmStageK;
-  // the weight operand whose scales this warp brings
-  const int operand = warp - C::kScaleWarp;
+  // the weight operand that this warp brings
+  const int operand = warp - C::kWeightWarp;
 
-  // the copies of stage ks of a tile; the full barrier of a stage takes the
-  // arrival of the codes and of every operand's scales
-  auto load_weights = [&](const MmTile &t, int na, int ks, int s) {
-    uint8_t *st = base + s * C::kStage;
-    mbar_arrive_expect_tx(full + s, na * kMmABytes + C::kBBytes + min(2, p.kt - 2 * ks) * kMxTileBytes);
-#pragma unroll
-    for (int a = 0; a < MA; ++a) {
-      if (a >= na) break;
-      const int r = MODE == kMmGateUp ? t.rt * 128 : (t.rt * MA + a) * 128;
-      tma_load3(st + a * kMmABytes, MODE == kMmGateUp && a == 1 ? &p.a1 : &p.a0, ks * 128, r, t.mat, full + s);
-    }
-  };
+  // the copies of stage ks of a tile, codes and scales: a thread for the tokens and
+  // one for each weight operand, which all arrive at the full barrier of the stage
   auto load_tokens = [&](const MmTile &t, int ks, int s) {
     uint8_t *sb = base + s * C::kStage + MA * kMmABytes;
+    const uint32_t bytes = min(2, p.kt - 2 * ks) * kMxTileBytes;
+    mbar_arrive_expect_tx(full + s, C::kBBytes + bytes);
     tma_load3(sb, &p.b, ks * 128, t.tt * NT, 0, full + s);
     bulk_g2s(sb + C::kBBytes + MA * C::kSfBytes, p.sb + (static_cast<size_t>(t.tt) * p.kt + 2 * ks) * kMxTileBytes,
-             min(2, p.kt - 2 * ks) * kMxTileBytes, full + s);
+             bytes, full + s);
   };
-  auto load_scales = [&](const MmTile &t, int na, int ks, int s) {   // of this warp's operand
+  auto load_weights = [&](const MmTile &t, int na, int ks, int s) {   // of this warp's operand
     if (operand >= na) {
       mbar_arrive(full + s);         // no such weights in this tile
       return;
     }
+    const bool up = MODE == kMmGateUp && operand == 1;
     const int rt = MODE == kMmGateUp ? t.rt : t.rt * MA + operand;
     const uint32_t bytes = min(2, p.kt - 2 * ks) * kMxTileBytes;
-    mbar_arrive_expect_tx(full + s, bytes);
-    bulk_g2s(base + s * C::kStage + MA * kMmABytes + C::kBBytes + operand * C::kSfBytes,
-             (MODE == kMmGateUp && operand == 1 ? p.sa1 : p.sa0) +
-                 (static_cast<size_t>(t.mat * p.row_tiles + rt) * p.kt + 2 * ks) * kMxTileBytes,
+    uint8_t *st = base + s * C::kStage;
+    mbar_arrive_expect_tx(full + s, kMmABytes + bytes);
+    tma_load3(st + operand * kMmABytes, up ? &p.a1 : &p.a0, ks * 128, rt * 128, t.mat, full + s);
+    bulk_g2s(st + MA * kMmABytes + C::kBBytes + operand * C::kSfBytes,
+             (up ? p.sa1 : p.sa0) + (static_cast<size_t>(t.mat * p.row_tiles + rt) * p.kt + 2 * ks) * kMxTileBytes,
              bytes, full + s);
   };
 
@@ -587,13 +584,10 @@ __global__ void __launch_bounds__(MmCfg<MODE, MA, NT, TOK>::kThreads, 1)
   }
   if (p.early) {                     // uniform over the grid
     __syncthreads();
-    if (lane == 0 && (warp == 0 || operand >= 0) && static_cast<int>(blockIdx.x) < mm_total(p, NT)) {
+    if (lane == 0 && operand >= 0 && static_cast<int>(blockIdx.x) < mm_total(p, NT)) {
       const MmTile t = mm_tile(p, blockIdx.x, NT);
       const int na = mm_operands<MODE, MA>(p, t);
-      for (; ahead < S && ahead < n_ks; ++ahead) {
-        if (warp == 0) load_weights(t, na, ahead, ahead);
-        else load_scales(t, na, ahead, ahead);
-      }
+      for (; ahead < S && ahead < n_ks; ++ahead) load_weights(t, na, ahead, ahead);
     }
   }
   grid_dep_wait();
@@ -633,12 +627,8 @@ __global__ void __launch_bounds__(MmCfg<MODE, MA, NT, TOK>::kThreads, 1)
             ok = false;
             break;
           }
-          if (warp == 0) {
-            if (fresh) load_weights(t, na, ks, s);
-            load_tokens(t, ks, s);
-          } else if (fresh) {
-            load_scales(t, na, ks, s);
-          }
+          if (warp == 0) load_tokens(t, ks, s);
+          else if (fresh) load_weights(t, na, ks, s);
         }
       }
       if (!ok) {   // copies in flight land before the block's memory goes
