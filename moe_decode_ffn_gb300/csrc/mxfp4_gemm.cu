@@ -26,12 +26,13 @@
 //
 // What bounds it. Few tokens: the weights' way from HBM; 64 tokens over 128 experts
 // (H 2048, I 768) read 181.5 MB for gate and up in 34.5 us and 90.4 MB for down in
-// 20 us. Many tokens: the issue of a stage (6 scale copies, 4 MMAs and a commit, 20
-// to 30 cycles each, beside 512 tensor cycles; a plain bulk copy holds its thread
-// for about 270, so these are spread over threads), and at the change of tiles the
-// loads of the next, which come 3 times later than otherwise while every SM writes
-// its outputs: 8192 x 4096 x 4096 takes 54.5 us (5.0 PFLOP/s; tensor pipe active 58 %
-// of cycles), gate/up of 4096 x 8 pairs 67 us, down 46 us.
+// 20 us. Many tokens: shared memory, into which a stage brings 51 KB while its MMAs
+// read 48 KB (690 cycles, 512 of them the MMAs'; a third less to load or a quarter of
+// the MMAs takes only 4 or 5 us off 53, both 11), and the stores, which hold up the
+// loads of the next tile (11 us): 8192 x 4096 x 4096 takes 53 us (5.2 PFLOP/s; tensor
+// pipe active 62 % of cycles), gate/up of 4096 x 8 pairs 64 us, down 46 us. A plain
+// bulk copy holds its thread for about 270 cycles, so the copies of a stage are
+// spread over threads.
 #include <cuda.h>
 
 #include <algorithm>
