@@ -32,8 +32,10 @@ int sm_count() {
   return cache[dev];
 }
 
+// Without the attribute a block gets 48 KB of static and dynamic shared memory
+// together; the dynamic part alone does not tell, so it is set for every size.
 cudaError_t ensure_smem(const void *kernel, size_t bytes) {
-  if (bytes <= 48 * 1024) return cudaSuccess;
+  if (bytes == 0) return cudaSuccess;
   static std::mutex mu;
   static const void *keys[256];
   static size_t vals[256];
@@ -42,16 +44,17 @@ cudaError_t ensure_smem(const void *kernel, size_t bytes) {
   int dev = 0;
   cudaGetDevice(&dev);
   std::lock_guard<std::mutex> lock(mu);
-  for (int i = 0; i < n; ++i)
-    if (keys[i] == kernel && dev_of[i] == dev && vals[i] >= bytes) return cudaSuccess;
+  int i = 0;                       // a kernel's entry on this device; its limit only grows
+  while (i < n && !(keys[i] == kernel && dev_of[i] == dev)) ++i;
+  if (i < n && vals[i] >= bytes) return cudaSuccess;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(bytes));
   if (e != cudaSuccess) return e;
-  if (n < 256) {
-    keys[n] = kernel;
-    vals[n] = bytes;
-    dev_of[n] = dev;
-    ++n;
+  if (i < 256) {
+    keys[i] = kernel;
+    vals[i] = bytes;
+    dev_of[i] = dev;
+    if (i == n) ++n;
   }
   return cudaSuccess;
 }
