@@ -606,6 +606,18 @@ def mxfp4_scale_shape(rows: int, cols: int) -> tuple:
     return (-(-rows // 128), -(-cols // 128), 512)
 
 
+def _scales(t, dev: int, n: int, rows: int, cols: int, many: bool, name: str) -> int:
+    """Device pointer of the scale tiles of a matrix (or ``many``: n of them) after
+    checking their shape; flat bytes are taken as tiles too. Scales that lie row by
+    row can have the same number of bytes, so that alone does not do."""
+    r, c, b = mxfp4_scale_shape(rows, cols)
+    p = _ptr(t, dev, n * r * c * b, _u8, name)
+    shape = (n, r, c, b) if many else (r, c, b)
+    if t.shape != shape and t.dim() != 1:
+        raise ValueError(f"{name} have shape {tuple(t.shape)}, expected tiles {shape} or their bytes")
+    return p
+
+
 def _mxfp4(codes, scales, dev: int, name: str, dims: int):
     """(matrices, rows, cols, pointers) of an MXFP4 pair after checking that they belong together."""
     if not isinstance(codes, _Tensor) or codes.dim() != dims:
@@ -618,7 +630,7 @@ def _mxfp4(codes, scales, dev: int, name: str, dims: int):
     if cols == 0 or cols % 32:
         raise ValueError(f"{name} has {cols} columns, expected a multiple of 32")
     return (n, rows, cols, _ptr(codes, dev, n * rows * cols // 2, _u8, name),
-            _ptr(scales, dev, n * (-(-rows // 128)) * (-(-cols // 128)) * 512, _u8, name))
+            _scales(scales, dev, n, rows, cols, dims == 3, f"{name} scales"))
 
 
 def _strides(t: torch.Tensor, name: str):
@@ -655,7 +667,7 @@ def si_quantize_mxfp4(x: torch.Tensor, codes: torch.Tensor | None = None, scales
     if scales is None:
         scales = _empty((n, tr, tc, 512) if many else (tr, tc, 512), dtype=_u8, device=d)
     else:
-        _ptr(scales, dev, n * tr * tc * 512, _u8, "scales")
+        _scales(scales, dev, n, rows, cols, many, "scales")
     st = library().si_quantize_mxfp4(x.data_ptr(), _TYPES[x.dtype], n, rows, cols, row, mat, codes.data_ptr(),
                                      scales.data_ptr(), _raw_stream(dev))
     if st:
@@ -824,7 +836,8 @@ def si_moe_combine_backward(gy: torch.Tensor, ys: torch.Tensor, position: torch.
 class Mxfp4Experts:
     """The routed experts of one layer in MXFP4 plus the ``si_mxfp4_experts``
     descriptor. ``gate``, ``up`` [E, I, H] and ``down`` [E, H, I] are (codes,
-    scales) as ``si_quantize_mxfp4`` returns them."""
+    scales) as ``si_quantize_mxfp4`` returns them: the scales in tiles
+    (``mxfp4_scale_shape``), not row by row as checkpoints hold them."""
 
     def __init__(self, gate, up, down):
         self.gate, self.up, self.down = gate, up, down
