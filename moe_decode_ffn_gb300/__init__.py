@@ -588,6 +588,14 @@ def _ptr(t, dev: int, numel: int, dtype, name: str) -> int:
     raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
 
 
+def _pairs(T: int, k: int) -> int:
+    """T * k after checking that it is an int of the C ABI: ctypes would pass on
+    the low 32 bits of a larger one."""
+    if T * k >> 31 or T >> 31:
+        raise ValueError(f"{T} tokens x {k} ranks, expected fewer than 2^31 pairs")
+    return T * k
+
+
 def _bad_type(t, name: str):
     raise ValueError(f"{name} has dtype {t.dtype}, expected float32, float16 or bfloat16")
 
@@ -741,12 +749,15 @@ def si_moe_sort(ids: torch.Tensor, n_experts: int, stream=None):
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(si_moe_sort, stream, ids, n_experts)
     (T, k), d, lib = ids.shape, ids.device, library()
-    order = _empty((T * k,), dtype=_i32_t, device=d)
+    n = _pairs(T, k)
+    if n_experts >> 31:
+        raise ValueError(f"{n_experts} experts, expected 1..1024")
+    order = _empty((n,), dtype=_i32_t, device=d)
     position = _empty((T, k), dtype=_i32_t, device=d)
     offsets = _empty((n_experts + 1 if n_experts > 0 else 1,), dtype=_i32_t, device=d)
     need = lib.si_moe_sort_workspace_bytes(T, k, n_experts)
     ws = _empty((need,), dtype=_u8, device=d) if need else None
-    st = lib.si_moe_sort(_ptr(ids, dev, T * k, _i32_t, "ids"), T, k, n_experts, order.data_ptr(),
+    st = lib.si_moe_sort(_ptr(ids, dev, n, _i32_t, "ids"), T, k, n_experts, order.data_ptr(),
                          position.data_ptr(), offsets.data_ptr(), ws.data_ptr() if need else None, need,
                          _raw_stream(dev))
     if st:
@@ -768,11 +779,12 @@ def si_moe_gather(x: torch.Tensor, position: torch.Tensor, offsets: torch.Tensor
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(si_moe_gather, stream, x, position, offsets)
     (T, H), k, dtype = x.shape, position.shape[-1], x.dtype
+    n = _pairs(T, k)
     if dtype not in _TYPES:
         _bad_type(x, "x")
-    xs = _empty((T * k, H), dtype=dtype, device=x.device)
+    xs = _empty((n, H), dtype=dtype, device=x.device)
     st = library().si_moe_gather(_ptr(x, dev, T * H, dtype, "x"), _TYPES[dtype], T, k, H,
-                                 _ptr(position, dev, T * k, _i32_t, "position"), _kept(offsets, dev),
+                                 _ptr(position, dev, n, _i32_t, "position"), _kept(offsets, dev),
                                  xs.data_ptr(), _raw_stream(dev))
     if st:
         _check(st, "si_moe_gather")
@@ -785,11 +797,12 @@ def si_moe_gather_backward(gxs: torch.Tensor, position: torch.Tensor, stream=Non
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(si_moe_gather_backward, stream, gxs, position)
     (T, k), H, dtype = position.shape, gxs.shape[-1], gxs.dtype
+    n = _pairs(T, k)
     if dtype not in _TYPES:
         _bad_type(gxs, "gxs")
     gx = _empty((T, H), dtype=dtype, device=gxs.device)
-    st = library().si_moe_gather_backward(_ptr(gxs, dev, T * k * H, dtype, "gxs"), _TYPES[dtype], T, k, H,
-                                          _ptr(position, dev, T * k, _i32_t, "position"), gx.data_ptr(),
+    st = library().si_moe_gather_backward(_ptr(gxs, dev, n * H, dtype, "gxs"), _TYPES[dtype], T, k, H,
+                                          _ptr(position, dev, n, _i32_t, "position"), gx.data_ptr(),
                                           _raw_stream(dev))
     if st:
         _check(st, "si_moe_gather_backward")
@@ -802,11 +815,12 @@ def si_moe_combine(ys: torch.Tensor, position: torch.Tensor, w: torch.Tensor, st
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(si_moe_combine, stream, ys, position, w)
     (T, k), H, dtype = position.shape, ys.shape[-1], ys.dtype
+    n = _pairs(T, k)
     if dtype not in _TYPES:
         _bad_type(ys, "ys")
     y = _empty((T, H), dtype=dtype, device=ys.device)
-    st = library().si_moe_combine(_ptr(ys, dev, T * k * H, dtype, "ys"), _TYPES[dtype], T, k, H,
-                                  _ptr(position, dev, T * k, _i32_t, "position"), _ptr(w, dev, T * k, _f32_t, "w"),
+    st = library().si_moe_combine(_ptr(ys, dev, n * H, dtype, "ys"), _TYPES[dtype], T, k, H,
+                                  _ptr(position, dev, n, _i32_t, "position"), _ptr(w, dev, n, _f32_t, "w"),
                                   y.data_ptr(), _raw_stream(dev))
     if st:
         _check(st, "si_moe_combine")
@@ -820,13 +834,14 @@ def si_moe_combine_backward(gy: torch.Tensor, ys: torch.Tensor, position: torch.
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(si_moe_combine_backward, stream, gy, ys, position, offsets, w)
     (T, k), H, dtype, d = position.shape, gy.shape[-1], gy.dtype, gy.device
+    n = _pairs(T, k)
     if dtype not in _TYPES:
         _bad_type(gy, "gy")
-    gys = _empty((T * k, H), dtype=dtype, device=d)
+    gys = _empty((n, H), dtype=dtype, device=d)
     gw = _empty((T, k), dtype=_f32_t, device=d)
     st = library().si_moe_combine_backward(
-        _ptr(gy, dev, T * H, dtype, "gy"), _ptr(ys, dev, T * k * H, dtype, "ys"), _TYPES[dtype], T, k, H,
-        _ptr(position, dev, T * k, _i32_t, "position"), _kept(offsets, dev), _ptr(w, dev, T * k, _f32_t, "w"),
+        _ptr(gy, dev, T * H, dtype, "gy"), _ptr(ys, dev, n * H, dtype, "ys"), _TYPES[dtype], T, k, H,
+        _ptr(position, dev, n, _i32_t, "position"), _kept(offsets, dev), _ptr(w, dev, n, _f32_t, "w"),
         gys.data_ptr(), gw.data_ptr(), _raw_stream(dev))
     if st:
         _check(st, "si_moe_combine_backward")
@@ -851,6 +866,8 @@ class Mxfp4Experts:
         n, rows, cols, dc, ds = _mxfp4(*down, self.dev, "down", 3)
         if (n, rows, cols) != (E, H, I):
             raise ValueError(f"down must be {E} matrices [{H}, {I}]")
+        if (H | I | E) >> 31:
+            raise ValueError(f"{E} experts of width {H} x {I}, expected at most 1024 of 65536 x 65536")
         self.hidden, self.inter, self.n_experts = H, I, E
         self.c = SiMxfp4Experts(H, I, E, gc, gs, uc, us, dc, ds)
         self.ref = ctypes.byref(self.c)
@@ -862,6 +879,8 @@ class Mxfp4Experts:
 
 
 def ffn_mxfp4_workspace_bytes(experts: Mxfp4Experts, n_tokens: int, top_k: int) -> int:
+    if (n_tokens | top_k) >> 31:
+        return 0
     return int(library().si_moe_ffn_mxfp4_workspace_bytes(experts.ref, n_tokens, top_k))
 
 
@@ -875,6 +894,7 @@ def si_moe_ffn_mxfp4(experts: Mxfp4Experts, x: torch.Tensor, ids: torch.Tensor, 
         return _elsewhere(lambda x, ids, w, ws, *_: si_moe_ffn_mxfp4(experts, x, ids, w, ws), stream, x, ids, w, ws,
                           *weights)
     (T, k), H = ids.shape, experts.hidden
+    pairs = _pairs(T, k)
     if experts.dev != dev:
         raise ValueError(f"tensors on cuda:{dev}, experts on cuda:{experts.dev}")
     if ws is None:
@@ -882,8 +902,8 @@ def si_moe_ffn_mxfp4(experts: Mxfp4Experts, x: torch.Tensor, ids: torch.Tensor, 
     routed = _empty((T, H), dtype=_bf16_t, device=x.device)
     n = ws.numel()
     st = library().si_moe_ffn_mxfp4(
-        experts.ref, T, k, _ptr(x, dev, T * H, _bf16_t, "x"), _ptr(ids, dev, T * k, _i32_t, "ids"),
-        _ptr(w, dev, T * k, _f32_t, "w"), routed.data_ptr(), _ptr(ws, dev, n, _u8, "ws"), n, _raw_stream(dev))
+        experts.ref, T, k, _ptr(x, dev, T * H, _bf16_t, "x"), _ptr(ids, dev, pairs, _i32_t, "ids"),
+        _ptr(w, dev, pairs, _f32_t, "w"), routed.data_ptr(), _ptr(ws, dev, n, _u8, "ws"), n, _raw_stream(dev))
     if st:
         _check(st, "si_moe_ffn_mxfp4")
     return routed
