@@ -13,6 +13,7 @@ import ctypes
 import os
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from ._build import LIB, build  # noqa: F401
 
@@ -774,10 +775,13 @@ def _kept(offsets: torch.Tensor, dev: int) -> int:
 
 
 def si_moe_gather(x: torch.Tensor, position: torch.Tensor, offsets: torch.Tensor, stream=None) -> torch.Tensor:
-    """xs[position[t, r]] = x[t]: x [T, H] -> [T * k, H], zero rows behind the kept pairs."""
+    """xs[position[t, r]] = x[t]: x [T, H] -> [T * k, H], zero rows behind the kept pairs.
+    Differentiable in x (once)."""
     dev = x.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(si_moe_gather, stream, x, position, offsets)
+    if x.requires_grad and torch.is_grad_enabled():
+        return _Gather.apply(x, position, offsets)
     (T, H), k, dtype = x.shape, position.shape[-1], x.dtype
     n = _pairs(T, k)
     if dtype not in _TYPES:
@@ -810,10 +814,13 @@ def si_moe_gather_backward(gxs: torch.Tensor, position: torch.Tensor, stream=Non
 
 
 def si_moe_combine(ys: torch.Tensor, position: torch.Tensor, w: torch.Tensor, stream=None) -> torch.Tensor:
-    """y[t] = sum_r w[t, r] ys[position[t, r]]: ys [T * k, H], w fp32 [T, k] -> [T, H]."""
+    """y[t] = sum_r w[t, r] ys[position[t, r]]: ys [T * k, H], w fp32 [T, k] -> [T, H].
+    Differentiable in ys and w (once)."""
     dev = ys.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(si_moe_combine, stream, ys, position, w)
+    if (ys.requires_grad or w.requires_grad) and torch.is_grad_enabled():
+        return _Combine.apply(ys, position, w)
     (T, k), H, dtype = position.shape, ys.shape[-1], ys.dtype
     n = _pairs(T, k)
     if dtype not in _TYPES:
@@ -833,11 +840,16 @@ def si_moe_combine_backward(gy: torch.Tensor, ys: torch.Tensor, position: torch.
     dev = gy.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(si_moe_combine_backward, stream, gy, ys, position, offsets, w)
+    return _combine_backward(dev, gy, ys, position, offsets, w)
+
+
+def _combine_backward(dev: int, gy, ys, position, offsets, w, gys=None):
     (T, k), H, dtype, d = position.shape, gy.shape[-1], gy.dtype, gy.device
     n = _pairs(T, k)
     if dtype not in _TYPES:
         _bad_type(gy, "gy")
-    gys = _empty((n, H), dtype=dtype, device=d)
+    if gys is None:
+        gys = _empty((n, H), dtype=dtype, device=d)
     gw = _empty((T, k), dtype=_f32_t, device=d)
     st = library().si_moe_combine_backward(
         _ptr(gy, dev, T * H, dtype, "gy"), _ptr(ys, dev, n * H, dtype, "ys"), _TYPES[dtype], T, k, H,
@@ -846,6 +858,40 @@ def si_moe_combine_backward(gy: torch.Tensor, ys: torch.Tensor, position: torch.
     if st:
         _check(st, "si_moe_combine_backward")
     return gys, gw
+
+
+class _Gather(torch.autograd.Function):
+    """si_moe_gather of an x that requires a gradient."""
+
+    @staticmethod
+    def forward(ctx, x, position, offsets):
+        ctx.save_for_backward(position)
+        return si_moe_gather(x, position, offsets)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, gxs):
+        position, = ctx.saved_tensors
+        return si_moe_gather_backward(gxs.contiguous(), position), None, None
+
+
+class _Combine(torch.autograd.Function):
+    """si_moe_combine of rows or weights that require a gradient. Without the
+    sort's offsets the places may have gaps, so the rows' gradient starts as zeros
+    and the kernel, told that every row is kept, clears none."""
+
+    @staticmethod
+    def forward(ctx, ys, position, w):
+        ctx.save_for_backward(ys, position, w)
+        return si_moe_combine(ys, position, w)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, gy):
+        ys, position, w = ctx.saved_tensors
+        kept = torch.full((1,), position.numel(), dtype=_i32_t, device=ys.device)
+        gys, gw = _combine_backward(ys.get_device(), gy.contiguous(), ys, position, kept, w, torch.zeros_like(ys))
+        return gys if ctx.needs_input_grad[0] else None, None, gw.view(w.shape) if ctx.needs_input_grad[2] else None
 
 
 class Mxfp4Experts:
