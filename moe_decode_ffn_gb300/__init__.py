@@ -556,8 +556,10 @@ _u8, _i32_t, _f32_t, _bf16_t = torch.uint8, torch.int32, torch.float32, torch.bf
 
 # A decode step makes these calls back to back, and the host time of one is longer
 # than its kernels. So the usual case (the current stream of the current device)
-# runs straight through; _elsewhere takes the others.
-_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# runs straight through; _elsewhere takes the others. A torch without CUDA has
+# neither binding, and no tensor for which they are asked.
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _elsewhere(call, stream, first, *args, **kw):
