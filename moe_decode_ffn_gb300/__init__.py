@@ -719,7 +719,7 @@ def si_mxfp4_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torc
                     dtype=torch.bfloat16, out: torch.Tensor | None = None, ws: torch.Tensor | None = None,
                     stream=None) -> torch.Tensor:
     """a [m, k] and w [n, k] in MXFP4 -> a w^T [m, n] in ``dtype`` or into ``out``
-    (any row stride). ``ws`` receives the device status; without it an error on
+    (any row stride); without rows (m or n 0) nothing is launched. ``ws`` receives the device status; without it an error on
     the device is not reported."""
     dev = a_codes.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
@@ -736,6 +736,8 @@ def si_mxfp4_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torc
         ld = _strides(out, "out")[3]
     if out.dtype not in _TYPES:
         _bad_type(out, "out")
+    if m == 0 or n == 0:
+        return out
     st = library().si_mxfp4_matmul(ac, asc, m, wc, wsc, n, k, out.data_ptr(), _TYPES[out.dtype], ld,
                                    None if ws is None else _ptr(ws, dev, ws.numel(), _u8, "ws"),
                                    0 if ws is None else ws.numel(), _raw_stream(dev))
