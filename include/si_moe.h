@@ -517,8 +517,8 @@ typedef struct si_mxfp4_experts {
 /*
  * si_moe_ffn_mxfp4 - the routed experts of n_tokens tokens, each routed on its
  * own, on the tensor cores: the pairs sorted by expert, x quantised to MXFP4,
- * h = silu(G_e x) * (U_e x) in fp32 quantised to MXFP4, y = D_e h rounded to
- * bf16, routed[t] = sum_r topk_w[t][r] * y_{t,r} in fp32 and rank order.
+ * h = silu(G_e x) * (U_e x) in fp32 quantised to MXFP4, y = D_e h in fp32,
+ * routed[t] = sum_r topk_w[t][r] * y_{t,r} in fp32 and rank order, rounded to bf16.
  *   x          device bf16 [n_tokens][H]
  *   topk_ids   device int32 [n_tokens][top_k]; ids outside [0, n_experts) are dropped
  *   topk_w     device fp32 [n_tokens][top_k]; routed_out device bf16 [n_tokens][H]

@@ -317,9 +317,10 @@ __global__ void __launch_bounds__(kRowThreads) gather_rows_kernel(RowArgs a, con
 // y[t] = sum_r w[t][r] rows[position[t][r]]. Three blocks an SM: 53.6 us for 8192
 // x 8 rows of 4 KB (5.6 TB/s); four 58.2, two with the next token's rows in
 // flight as well 63.5, rows asked into the L2 a token ahead 64.2.
-template <typename T, int V>
+// TO: the sums' type; the MXFP4 experts' rows are fp32 and their sums bf16.
+template <typename T, int V, typename TO = T>
 __global__ void __launch_bounds__(kRowThreads, 3)
-    combine_rows_kernel(RowArgs a, const T *__restrict__ rows, T *__restrict__ y) {
+    combine_rows_kernel(RowArgs a, const T *__restrict__ rows, TO *__restrict__ y) {
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31;
@@ -348,9 +349,16 @@ __global__ void __launch_bounds__(kRowThreads, 3)
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] = fmaf(g, f[i], acc[i]);
       }
-      Piece<T, V> o;
-      o.pack(acc);
-      if (in) o.store(y + t * a.hidden + c);
+      if constexpr (std::is_same_v<T, TO>) {
+        Piece<T, V> o;
+        o.pack(acc);
+        if (in) o.store(y + t * a.hidden + c);
+      } else {
+        static_assert(V == 4 && std::is_same_v<TO, __nv_bfloat16>, "fp32 rows to bf16");
+        const uint2 o = make_uint2(bf16_bits(acc[0]) | (static_cast<uint32_t>(bf16_bits(acc[1])) << 16),
+                                   bf16_bits(acc[2]) | (static_cast<uint32_t>(bf16_bits(acc[3])) << 16));
+        if (in) *reinterpret_cast<uint2 *>(y + t * a.hidden + c) = o;
+      }
     }
   }
 }
@@ -486,10 +494,12 @@ static cudaError_t combine_rows(const RowArgs &a, si_dtype type, bool vec, const
   });
 }
 
-cudaError_t combine_launch(const void *rows, int64_t n_rows, int n_tokens, int top_k, int64_t hidden,
+cudaError_t combine_launch(const float *rows, int64_t n_rows, int n_tokens, int top_k, int64_t hidden,
                            const int32_t *position, const float *w, void *y, cudaStream_t s) {
   const RowArgs a{n_tokens, top_k, hidden, n_rows, position, w, nullptr};
-  return combine_rows(a, SI_BF16, true, rows, y, s);
+  const unsigned threads = row_threads(hidden / 4);
+  return launch_pdl(combine_rows_kernel<float, 4, __nv_bfloat16>, dim3(row_blocks(n_tokens, threads, 3 * kRowThreads)),
+                    dim3(threads), 0, s, a, rows, static_cast<__nv_bfloat16 *>(y));
 }
 
 }  // namespace si

@@ -30,9 +30,9 @@ struct SortArgs {
 size_t sort_workspace_bytes(int64_t pairs, int n_experts);
 cudaError_t sort_launch(SortArgs a, cudaStream_t s);
 
-// y[t] = sum_r w[t][r] rows[position[t][r]] over bf16 rows of `hidden` values
-// (a multiple of 8, 16-byte aligned), fp32 sums in rank order.
-cudaError_t combine_launch(const void *rows, int64_t n_rows, int n_tokens, int top_k, int64_t hidden,
+// y[t] = sum_r w[t][r] rows[position[t][r]] over fp32 rows of `hidden` values
+// (a multiple of 4, 16-byte aligned), fp32 sums in rank order, rounded to bf16.
+cudaError_t combine_launch(const float *rows, int64_t n_rows, int n_tokens, int top_k, int64_t hidden,
                            const int32_t *position, const float *w, void *y, cudaStream_t s);
 
 // Expert of a pair, E for a dropped one (negative ids are large unsigned ones).
