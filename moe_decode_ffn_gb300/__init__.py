@@ -591,12 +591,9 @@ def _ptr(t, dev: int, numel: int, dtype, name: str) -> int:
     raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
 
 
-def _pairs(T: int, k: int) -> int:
-    """T * k after checking that it is an int of the C ABI: ctypes would pass on
-    the low 32 bits of a larger one."""
-    if T * k >> 31 or T >> 31:
-        raise ValueError(f"{T} tokens x {k} ranks, expected fewer than 2^31 pairs")
-    return T * k
+def _too_many(T: int, k: int):
+    """T * k has to be an int of the C ABI: ctypes would pass on the low 32 bits of a larger one."""
+    raise ValueError(f"{T} tokens x {k} ranks, expected fewer than 2^31 pairs")
 
 
 def _bad_type(t, name: str):
@@ -621,12 +618,11 @@ def _scales(t, dev: int, n: int, rows: int, cols: int, many: bool, name: str) ->
     """Device pointer of the scale tiles of a matrix (or ``many``: n of them) after
     checking their shape; flat bytes are taken as tiles too. Scales that lie row by
     row can have the same number of bytes, so that alone does not do."""
-    r, c, b = mxfp4_scale_shape(rows, cols)
-    p = _ptr(t, dev, n * r * c * b, _u8, name)
-    shape = (n, r, c, b) if many else (r, c, b)
-    if t.shape != shape and t.dim() != 1:
-        raise ValueError(f"{name} have shape {tuple(t.shape)}, expected tiles {shape} or their bytes")
-    return p
+    r, c = (rows + 127) // 128, (cols + 127) // 128
+    if t.shape == ((n, r, c, 512) if many else (r, c, 512)) or t.dim() == 1:
+        return _ptr(t, dev, n * r * c * 512, _u8, name)
+    shape = (n, *mxfp4_scale_shape(rows, cols)) if many else mxfp4_scale_shape(rows, cols)
+    raise ValueError(f"{name} have shape {tuple(t.shape)}, expected tiles {shape} or their bytes")
 
 
 def _mxfp4(codes, scales, dev: int, name: str, dims: int):
@@ -754,7 +750,9 @@ def si_moe_sort(ids: torch.Tensor, n_experts: int, stream=None):
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(si_moe_sort, stream, ids, n_experts)
     (T, k), d, lib = ids.shape, ids.device, library()
-    n = _pairs(T, k)
+    n = T * k
+    if n >> 31:
+        _too_many(T, k)
     if n_experts >> 31:
         raise ValueError(f"{n_experts} experts, expected 1..1024")
     order = _empty((n,), dtype=_i32_t, device=d)
@@ -787,7 +785,9 @@ def si_moe_gather(x: torch.Tensor, position: torch.Tensor, offsets: torch.Tensor
     if x.requires_grad and torch.is_grad_enabled():
         return _Gather.apply(x, position, offsets)
     (T, H), k, dtype = x.shape, position.shape[-1], x.dtype
-    n = _pairs(T, k)
+    n = T * k
+    if n >> 31:
+        _too_many(T, k)
     if dtype not in _TYPES:
         _bad_type(x, "x")
     xs = _empty((n, H), dtype=dtype, device=x.device)
@@ -805,7 +805,9 @@ def si_moe_gather_backward(gxs: torch.Tensor, position: torch.Tensor, stream=Non
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(si_moe_gather_backward, stream, gxs, position)
     (T, k), H, dtype = position.shape, gxs.shape[-1], gxs.dtype
-    n = _pairs(T, k)
+    n = T * k
+    if n >> 31:
+        _too_many(T, k)
     if dtype not in _TYPES:
         _bad_type(gxs, "gxs")
     gx = _empty((T, H), dtype=dtype, device=gxs.device)
@@ -826,7 +828,9 @@ def si_moe_combine(ys: torch.Tensor, position: torch.Tensor, w: torch.Tensor, st
     if (ys.requires_grad or w.requires_grad) and torch.is_grad_enabled():
         return _Combine.apply(ys, position, w)
     (T, k), H, dtype = position.shape, ys.shape[-1], ys.dtype
-    n = _pairs(T, k)
+    n = T * k
+    if n >> 31:
+        _too_many(T, k)
     if dtype not in _TYPES:
         _bad_type(ys, "ys")
     y = _empty((T, H), dtype=dtype, device=ys.device)
@@ -849,7 +853,9 @@ def si_moe_combine_backward(gy: torch.Tensor, ys: torch.Tensor, position: torch.
 
 def _combine_backward(dev: int, gy, ys, position, offsets, w, gys=None):
     (T, k), H, dtype, d = position.shape, gy.shape[-1], gy.dtype, gy.device
-    n = _pairs(T, k)
+    n = T * k
+    if n >> 31:
+        _too_many(T, k)
     if dtype not in _TYPES:
         _bad_type(gy, "gy")
     if gys is None:
@@ -944,7 +950,9 @@ def si_moe_ffn_mxfp4(experts: Mxfp4Experts, x: torch.Tensor, ids: torch.Tensor, 
         return _elsewhere(lambda x, ids, w, ws, *_: si_moe_ffn_mxfp4(experts, x, ids, w, ws), stream, x, ids, w, ws,
                           *weights)
     (T, k), H = ids.shape, experts.hidden
-    pairs = _pairs(T, k)
+    pairs = T * k
+    if pairs >> 31:
+        _too_many(T, k)
     if experts.dev != dev:
         raise ValueError(f"tensors on cuda:{dev}, experts on cuda:{experts.dev}")
     if ws is None:
