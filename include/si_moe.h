@@ -435,8 +435,8 @@ si_status si_moe_stack_graph_create_batched(const si_moe_layer *layers, int n_la
  *   cols    a multiple of 32; codes and scales 16-byte aligned
  * The float matrix is fp32, fp16 or bf16 with contiguous columns, row_stride
  * values between rows and mat_stride between matrices (ignored for one row, one
- * matrix): matrices one behind the other, or their rows in turn, without overlap. n_mats = 0 or rows = 0 returns
- * SI_OK and enqueues nothing. si_dequantize_mxfp4 rounds to nearest even where
+ * matrix): matrices one behind the other, or their rows in turn, without overlap.
+ * n_mats = 0 or rows = 0 returns SI_OK and enqueues nothing. si_dequantize_mxfp4 rounds to nearest even where
  * its type cannot hold a value (fp16; bf16 and fp32 hold every one).
  */
 size_t si_mxfp4_scale_bytes(int64_t rows, int64_t cols);
@@ -455,7 +455,7 @@ si_status si_dequantize_mxfp4(const void *codes, const void *scales, int64_t n_m
  *         values apart; the values between them are left as they are. May not alias a or w
  *   workspace  si_mxfp4_matmul_workspace_bytes(m, n, k) bytes, zeroed once, or NULL:
  *         it holds the status word alone, and without it a wait that ran out on
- *         the device is not reported
+ *         the device, which leaves out incomplete, is not reported
  */
 size_t si_mxfp4_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k);
 si_status si_mxfp4_matmul(const void *a_codes, const void *a_scales, int64_t m, const void *w_codes,
@@ -522,7 +522,9 @@ typedef struct si_mxfp4_experts {
  *   x          device bf16 [n_tokens][H]
  *   topk_ids   device int32 [n_tokens][top_k]; ids outside [0, n_experts) are dropped
  *   topk_w     device fp32 [n_tokens][top_k]; routed_out device bf16 [n_tokens][H]
- *   workspace  si_moe_ffn_mxfp4_workspace_bytes(L, n_tokens, top_k) bytes, zeroed once
+ *   workspace  si_moe_ffn_mxfp4_workspace_bytes(L, n_tokens, top_k) bytes, zeroed once;
+ *              its status word tells whether a wait on the device ran out, after
+ *              which routed_out is incomplete
  * n_tokens >= 1, top_k 1..8, n_tokens * top_k <= 2^24.
  */
 size_t si_moe_ffn_mxfp4_workspace_bytes(const si_mxfp4_experts *L, int n_tokens, int top_k);

@@ -5,7 +5,8 @@ kernels of ``libsi_moe.so`` (built in-tree from ``csrc/``); PyTorch supplies
 device memory and streams. There is no CPU fallback: if the library is not
 built, or a tensor is not on a CUDA device, the calls raise.
 
-Names follow the C ABI in ``include/si_moe.h``.
+Names follow the C ABI in ``include/si_moe.h``. Results carry no gradient, but for
+those of ``si_moe_gather`` and ``si_moe_combine``.
 """
 from __future__ import annotations
 
@@ -715,8 +716,9 @@ def si_mxfp4_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torc
                     dtype=torch.bfloat16, out: torch.Tensor | None = None, ws: torch.Tensor | None = None,
                     stream=None) -> torch.Tensor:
     """a [m, k] and w [n, k] in MXFP4 -> a w^T [m, n] in ``dtype`` or into ``out``
-    (any row stride); without rows (m or n 0) nothing is launched. ``ws`` receives the device status; without it an error on
-    the device is not reported."""
+    (any row stride); without rows (m or n 0) nothing is launched. ``ws`` receives the
+    device status; without it a wait that ran out on the device, which leaves
+    the result incomplete, is not reported."""
     dev = a_codes.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(si_mxfp4_matmul, stream, a_codes, a_scales, w_codes, w_scales, dtype, out, ws)
@@ -943,7 +945,10 @@ def ffn_mxfp4_workspace_bytes(experts: Mxfp4Experts, n_tokens: int, top_k: int) 
 def si_moe_ffn_mxfp4(experts: Mxfp4Experts, x: torch.Tensor, ids: torch.Tensor, w: torch.Tensor,
                      ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """T tokens with per-token routing: x bf16 [T, H], ids int32 [T, k], w fp32
-    [T, k] -> routed bf16 [T, H]."""
+    [T, k] -> routed bf16 [T, H]. ``ws`` is kept by the caller and receives the
+    device status (``si_workspace_status``); without it each call takes one of its
+    own, and a wait that ran out on the device, which leaves the result
+    incomplete, is not reported."""
     dev = x.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
         weights = (*experts.gate, *experts.up, *experts.down)

@@ -21,18 +21,22 @@
 // thread of warp 1 moves the scales into tensor memory (tcgen05.cp) and issues the
 // MMAs, warps 2.. read the accumulators and write the outputs (4 of them cover the
 // 128 lanes of tensor memory; each group of 4 takes a part of the columns).
-// Blocks are persistent: tile i of block b is b + i * gridDim. The accumulators are
-// a ring too, so that the MMAs of a tile run beside the epilogue of the one before.
+// Blocks are persistent: tile i of block b is b + i * gridDim. With the weights on the
+// lanes the accumulators are a ring of two tiles, so that the MMAs of a tile run beside
+// the epilogue of the one before. With the tokens on the lanes tensor memory holds one
+// accumulator of 256 columns beside the scales: the next tile's MMAs wait until the
+// epilogue has read it and run beside its packing and stores only.
 //
 // What bounds it. Few tokens: the weights' way from HBM; 64 tokens over 128 experts
-// (H 2048, I 768) read 181.5 MB for gate and up in 34.5 us and 90.4 MB for down in
-// 20 us. Many tokens: shared memory, into which a stage brings 51 KB while its MMAs
+// (H 2048, I 768) read 181.5 MB for gate and up in 34 us and 90.4 MB for down in
+// 23 us. Many tokens: shared memory, into which a stage brings 51 KB while its MMAs
 // read 48 KB (690 cycles, 512 of them the MMAs'; a third less to load or a quarter of
-// the MMAs takes only 4 or 5 us off 53, both 11), and the stores, which hold up the
-// loads of the next tile (11 us): 8192 x 4096 x 4096 takes 53 us (5.2 PFLOP/s; tensor
-// pipe active 62 % of cycles), gate/up of 4096 x 8 pairs 64 us, down 46 us. A plain
-// bulk copy holds its thread for about 270 cycles, so the copies of a stage are
-// spread over threads.
+// the MMAs takes only 4 or 5 us off 53, both 11), the reads of the accumulator, which
+// hold up the MMAs, and the stores, which hold up the loads of the next tile (11 us):
+// 8192 x 4096 x 4096 takes 52 us (5.3 PFLOP/s; tensor pipe active 63 % of cycles; its
+// 65536 MMAs alone 27 us), gate/up of 4096 x 8 pairs 64 us, down 70 us, of it the
+// fp32 rows' 268 MB. A plain bulk copy holds its thread for about 270 cycles, so the
+// copies of a stage are spread over threads.
 #include <cuda.h>
 
 #include <algorithm>
@@ -75,8 +79,8 @@ template <int MODE, int MA, int NT, bool TOK> struct MmCfg {
   static constexpr int kEpiBytes = MODE == kMmStaged ? 1024 : MODE == kMmGateUp || TOK ? 0 : kGroups == 1 ? 1024 : 2048;
   static constexpr int kMaxSmem = 227 * 1024 - kEpiWarps * kEpiBytes - 1536;   // less alignment and barriers
   static constexpr int kStages = kMaxSmem / kStage < 8 ? kMaxSmem / kStage : 8;
-  // tensor memory: a ring of accumulators (a tile takes one of 256 columns, or MA
-  // of NT columns), then the scales of every stage (a column holds 4 blocks of 32
+  // tensor memory: accumulators (a tile takes one of 256 columns, of which one fits, or
+  // MA of NT columns, a ring of two tiles), then the scales of every stage (a column holds 4 blocks of 32
   // rows: 128 rows x 8 blocks take 8 columns)
   static constexpr int kAccCols = TOK ? 256 : NT;
   static constexpr int kTileAccs = TOK ? 1 : MA;
@@ -86,6 +90,7 @@ template <int MODE, int MA, int NT, bool TOK> struct MmCfg {
   static constexpr int kUsed = kAccs * kAccCols + kStages * kSfCols;
   static constexpr int kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
   static_assert(kAccs >= kTileAccs && kUsed <= 512, "tensor memory has 512 columns");
+  static_assert(TOK ? kAccs == 1 : kAccs == 2 * MA, "one tile with the tokens on the lanes, else two");
   static constexpr int kBars = 2 * kStages + 2 * kAccs + 1;
   static constexpr int kSmem = kStages * kStage + kEpiWarps * kEpiBytes + 1024 + 512;
   static_assert(8 * kBars + 4 <= 512, "barriers");
@@ -306,7 +311,7 @@ SI_DEV uint32_t transpose_nibbles(uint32_t w, int lane) {
 }
 
 // silu(g) u: ex2 and rcp of the hardware, each within 2 units in the last place.
-// g far below zero: the exponential overflows, the reciprocal is 0.
+// g below -87 (|silu(g)| < 2^-119): the reciprocal, below the normal range, is 0.
 SI_DEV float mm_silu_mul(float g, float u) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
@@ -838,8 +843,10 @@ __global__ void __launch_bounds__(256) quantize_scatter_kernel(ScatterArgs a) {
 // At most 32 pairs: the sort too, in the same launch, by one warp of every block
 // (a lane per pair); block 0 writes the tile list. The launch that this saves
 // counts more there than the weights that gate/up could request before its wait
-// with the sort two launches back (128 experts, H 2048, I 768, top-8: 1 token
-// 19.8 against 22.0 us, 4 tokens 26.6 against 26.8, 16 tokens 44.0 against 43.2).
+// with the sort two launches back. In a graph, 1 / 4 tokens: 128 experts, H 2048, I 768,
+// top-8 14.6 / 23.9 us against 16.3 / 24.4 with two launches; 256, 2048, 512, top-8 14.8 / 16.8
+// against 16.8 / 19.3; 8, 4096, 2048, top-2 19.8 / 26.4 against 20.8 / 27.5. With more pairs it
+// turns (128 pairs on the first layer 44.0 against 43.2), and a lane holds one pair.
 constexpr int kFewPairs = 32;
 __global__ void __launch_bounds__(256) sort_scatter_kernel(SortArgs so, ScatterArgs a) {
   __shared__ ScatterRows s_rows;
@@ -933,12 +940,13 @@ static cudaError_t mm_launch_gateup(int nt, const MmParams &p, int64_t max_tiles
   return nt == 16 ? mm_launch_as<kMmGateUp, 2, 16, false, 0>(p, max_tiles, s)
                   : mm_launch_as<kMmGateUp, 2, 128, true, 0>(p, max_tiles, s);
 }
+// 256 rows a tile for few tokens: fewer loads for the same bytes (128 tokens, with
+// rows of bf16, 66.2 -> 63.5 us).
 // y stays fp32 until the ranks are summed, so that a token's output is rounded once
 // (with bf16 rows its error against 64 bits is 0.0024 relative, not 0.0017). Twice
 // the bytes: 58.2 against 57.5 us at 64 tokens, 104 against 90 at 1024, 213 against
 // 161 at 4096 (128 experts, H 2048, I 768, top-8).
 static cudaError_t mm_launch_down(int nt, const MmParams &p, int64_t max_tiles, cudaStream_t s) {
-  // 256 rows a tile: fewer loads for the same bytes (128 tokens 66.2 -> 63.5 us)
   return nt == 16 ? mm_launch_as<kMmPlain, 2, 16, false, kMmF32>(p, max_tiles, s)
                   : mm_launch_tok<kMmF32Vec>(p, max_tiles, s);
 }
@@ -953,9 +961,13 @@ struct FfnMxGeom {
 static FfnMxGeom ffn_mx_geom(const si_mxfp4_experts &L, int n_tokens, int top_k) {
   FfnMxGeom g{};
   g.pairs = static_cast<int64_t>(n_tokens) * top_k;
-  // tiles of 16 tokens as long as they hold an expert's average (128 experts,
-  // H 2048, I 768, top-8: 128 tokens 66.7 us), else the tokens on the lanes (256
-  // tokens 72.1 us, in tiles of 16 79.4)
+  // tiles of 16 tokens while an expert has 8 pairs on average, so that few experts
+  // need a second tile; else the tokens on the lanes. In a graph at averages of
+  // 8 / 24, tiles of 16 against 128: E 128, H 2048, I 768, top-8 66.3 / 82.0 against 73.4 / 81.7
+  // us; 256, 2048, 512, top-8 91.5 / 119.3 against 94.2 / 114.4; 64, 1024, 4096, top-2
+  // 78.5 / 98.0 against 81.8 / 88.5; 32, 2880, 1440, top-4 48.6 / 64.0 against 56.7 / 60.0; 8, 4096,
+  // 2048, top-2 32.1 / 35.9 against 33.6 / 34.8. In between the layers differ (at 16 the
+  // first four still gain 1 to 7 % with tiles of 16, the last loses 6 %).
   const int64_t avg = (g.pairs + L.n_experts - 1) / L.n_experts;
   g.nt = avg <= 8 ? 16 : 128;
   const int64_t with = std::min<int64_t>(L.n_experts, g.pairs);   // experts that can hold pairs

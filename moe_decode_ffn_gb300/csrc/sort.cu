@@ -317,7 +317,8 @@ __global__ void __launch_bounds__(kRowThreads) gather_rows_kernel(RowArgs a, con
 // y[t] = sum_r w[t][r] rows[position[t][r]]. Three blocks an SM: 53.6 us for 8192
 // x 8 rows of 4 KB (5.6 TB/s); four 58.2, two with the next token's rows in
 // flight as well 63.5, rows asked into the L2 a token ahead 64.2.
-// TO: the sums' type; the MXFP4 experts' rows are fp32 and their sums bf16.
+// TO: the sums' type; the MXFP4 experts' rows are fp32 and their sums bf16 (4096 x 8
+// rows of 8 KB 49.2 us, 5.8 TB/s).
 template <typename T, int V, typename TO = T>
 __global__ void __launch_bounds__(kRowThreads, 3)
     combine_rows_kernel(RowArgs a, const T *__restrict__ rows, TO *__restrict__ y) {
