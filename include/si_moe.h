@@ -505,6 +505,89 @@ si_status si_moe_combine_backward(const void *gy, const void *ys, si_dtype type,
                                   int64_t hidden, const int32_t *position, const int32_t *n_kept,
                                   const float *topk_w, void *gys, float *gw, void *stream);
 
+/*
+ * Products of sorted rows with their experts' matrices, on the tensor cores: bf16 or
+ * fp16 operands, fp32 sums, rounded once. The rows are those of si_moe_gather: expert e
+ * has rows offsets[e] .. offsets[e + 1] (device int32 [n_experts + 1], as si_moe_sort
+ * writes them); a bound outside [0, rows] counts as the nearest inside, one below an
+ * earlier bound as that one.
+ *
+ * si_moe_matmul:        out[r][i] = sum_c x[r][c] * W[e][i][c] for the rows r of expert e
+ * si_moe_matmul_grad_w: gw[e][i][c] = sum over the rows r of expert e of gy[r][i] * x[r][c]
+ * si_moe_gateup:        h[r][i] = silu(g) * u with g, u = out[r][i], out[r][inter + i] of
+ *                       si_moe_matmul in fp32, and g and u in 8 bits for the backward pass
+ *
+ *   type     SI_BF16 or SI_F16, of x, w, gy and h; out_type, gw_type: type or SI_F32
+ *   rows     0 .. 2^31 - 257; 0: gw becomes zeros, the others do nothing. Rows of no expert
+ *            (before offsets[0], behind offsets[n_experts]) are not read, and their outputs
+ *            (codes and scales too) are zeros; an expert without rows has gw 0
+ *   n, k     width of out and of x (rows and columns of a matrix), inter and hidden:
+ *            multiples of 8, up to 2^20; n_experts 1..1024
+ *   w        W[e] at w + e * mat_stride values: by_columns 0: n rows of k values,
+ *            ld_w apart; 1: k rows of n values (column c of W[e] is row c). So the
+ *            gradient of x is si_moe_matmul of gy with by_columns turned round.
+ *            gate_up [n_experts][2 * inter][hidden] contiguous, gate rows first
+ *   ld_*     distances of rows in values; every row, and every matrix, starts on a
+ *            16-byte boundary. gw [n_experts][n][k], h [rows][inter] contiguous
+ *   codes, scales  int8 [rows][2 * inter], uint8 [rows][2 * ceil(inter / 32)] in MXINT8
+ *            (si_quantize_mxint8), g's and u's blocks starting anew; or both NULL.
+ *            codes on a 16-byte boundary
+ *   workspace  si_moe_matmul_workspace_bytes() bytes, zeroed once, or NULL: the
+ *            status word, without which a wait that ran out on the device, which
+ *            leaves the outputs incomplete, is not reported
+ * Outputs may not alias inputs. More than 2^30 output tiles: SI_ERR_UNSUPPORTED.
+ */
+size_t si_moe_matmul_workspace_bytes(void);
+si_status si_moe_matmul(const void *x, si_dtype type, int64_t rows, int64_t ld_x, const void *w, int n_experts,
+                        int64_t n, int64_t k, int64_t ld_w, int64_t mat_stride, int by_columns,
+                        const int32_t *offsets, void *out, si_dtype out_type, int64_t ld_out, void *workspace,
+                        size_t workspace_bytes, void *stream);
+si_status si_moe_matmul_grad_w(const void *gy, int64_t ld_gy, const void *x, int64_t ld_x, si_dtype type,
+                               int64_t rows, int n_experts, int64_t n, int64_t k, const int32_t *offsets, void *gw,
+                               si_dtype gw_type, void *workspace, size_t workspace_bytes, void *stream);
+si_status si_moe_gateup(const void *x, si_dtype type, int64_t rows, int64_t ld_x, const void *gate_up,
+                        int n_experts, int64_t inter, int64_t hidden, const int32_t *offsets, void *h, void *codes,
+                        void *scales, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Activations in 8 bits (OCP MXINT8). 32 consecutive values of a row (the last block
+ * of a row may be shorter) share X = 2^(s - 127), s the exponent field of their largest
+ * magnitude in fp32; code = x / X * 64 rounded to nearest even, within +-127, value =
+ * code * X / 64. A block that holds an infinity or a NaN has s = 255 and codes 0 and is
+ * read as NaN as a whole.
+ *   x, y    device, `rows` rows of `cols` values (SI_F32, SI_F16 or SI_BF16), row_stride
+ *           >= cols values apart; values between the rows are left as they are
+ *   codes   int8 [rows][cols], scales uint8 [rows][ceil(cols / 32)], contiguous
+ * rows 0: nothing is done. Rows of whole 16-byte words at aligned addresses move in such
+ * words, others value by value. An fp16 y becomes infinite where its type cannot hold a value.
+ */
+si_status si_quantize_mxint8(const void *x, si_dtype x_type, int64_t rows, int64_t cols, int64_t row_stride,
+                             void *codes, void *scales, void *stream);
+si_status si_dequantize_mxint8(const void *codes, const void *scales, int64_t rows, int64_t cols, void *y,
+                               si_dtype y_type, int64_t row_stride, void *stream);
+
+/*
+ * si_swiglu - h = silu(g) * u over rows gu of inter values of g and inter of u, row_stride
+ * values apart; silu(g) = g * s, s = 1 / (1 + exp(-g)). codes, scales (as si_moe_gateup's)
+ * keep g and u for the backward pass, or are both NULL.
+ * si_swiglu_backward - from the kept g and u and the gradient gh of h, for rows of weight
+ * c (a routed row enters its token's sum as c * h):
+ *     ggu = (c * gh * u * s * (1 + g * (1 - s)), c * gh * g * s),  wh = c * h,
+ *     gw = sum_i gh[i] * h[i], the gradient of c;  h = g * s * u
+ *   order   device int32 [rows]: row r has weight row_w[order[r]] and writes
+ *           gw[order[r]] (si_moe_sort's order with topk_w and its gradient); rows whose
+ *           order lies outside [0, rows) get ggu 0, wh 0 and write no gw. NULL: row r itself
+ *   row_w   device fp32 [rows], or NULL: 1; wh, gw (fp32 [rows]) may be NULL
+ * gu, h, gh, ggu [rows][2 * inter], wh of `type` (SI_F32, SI_F16 or SI_BF16), contiguous but
+ * for gu's rows; fp32 arithmetic, rounded once. rows 0: nothing is done. Outputs may
+ * not alias inputs.
+ */
+si_status si_swiglu(const void *gu, si_dtype type, int64_t rows, int64_t inter, int64_t row_stride, void *h,
+                    void *codes, void *scales, void *stream);
+si_status si_swiglu_backward(const void *gh, si_dtype type, int64_t rows, int64_t inter, const void *codes,
+                             const void *scales, const float *row_w, const int32_t *order, void *ggu, void *wh,
+                             float *gw, void *stream);
+
 /* The routed experts of one layer as MXFP4 matrices. */
 typedef struct si_mxfp4_experts {
   int hidden, inter;          /* H, I: multiples of 32, <= 65536 */

@@ -6,7 +6,8 @@ device memory and streams. There is no CPU fallback: if the library is not
 built, or a tensor is not on a CUDA device, the calls raise.
 
 Names follow the C ABI in ``include/si_moe.h``. Results carry no gradient, but for
-those of ``si_moe_gather`` and ``si_moe_combine``.
+those of ``si_moe_gather``, ``si_moe_combine``, ``si_moe_matmul``, ``si_swiglu`` and
+``si_moe_experts``.
 """
 from __future__ import annotations
 
@@ -106,6 +107,16 @@ SIGNATURES = {
     "si_moe_combine": (_i32, [_vp, _i32, _i32, _i32, _i64, _vp, _vp, _vp, _vp]),
     "si_moe_combine_backward": (_i32, [_vp, _vp, _i32, _i32, _i32, _i64, _vp, _vp, _vp, _vp, _vp,
                                        _vp]),
+    "si_moe_matmul_workspace_bytes": (_sz, []),
+    "si_moe_matmul": (_i32, [_vp, _i32, _i64, _i64, _vp, _i32, _i64, _i64, _i64, _i64, _i32, _vp, _vp, _i32, _i64,
+                             _vp, _sz, _vp]),
+    "si_moe_matmul_grad_w": (_i32, [_vp, _i64, _vp, _i64, _i32, _i64, _i32, _i64, _i64, _vp, _vp, _i32, _vp, _sz,
+                                    _vp]),
+    "si_moe_gateup": (_i32, [_vp, _i32, _i64, _i64, _vp, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "si_quantize_mxint8": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "si_dequantize_mxint8": (_i32, [_vp, _vp, _i64, _i64, _vp, _i32, _i64, _vp]),
+    "si_swiglu": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp]),
+    "si_swiglu_backward": (_i32, [_vp, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "si_moe_ffn_mxfp4_workspace_bytes": (_sz, [ctypes.POINTER(SiMxfp4Experts), _i32, _i32]),
     "si_moe_ffn_mxfp4": (_i32, [ctypes.POINTER(SiMxfp4Experts), _i32, _i32, _vp, _vp, _vp, _vp, _vp,
                                 _sz, _vp]),
@@ -904,6 +915,426 @@ class _Combine(torch.autograd.Function):
         kept = torch.full((1,), position.numel(), dtype=_i32_t, device=ys.device)
         gys, gw = _combine_backward(ys.get_device(), gy.contiguous(), ys, position, kept, w, torch.zeros_like(ys))
         return gys if ctx.needs_input_grad[0] else None, None, gw.view(w.shape) if ctx.needs_input_grad[2] else None
+
+
+# ----------------------------------------------------------------------------
+# Products of sorted rows in 16 bits, activations kept in 8, the experts' training
+# ----------------------------------------------------------------------------
+
+_HALVES = {torch.float16: SI_F16, torch.bfloat16: SI_BF16}
+_i8 = torch.int8
+
+
+def moe_matmul_workspace_bytes() -> int:
+    return int(library().si_moe_matmul_workspace_bytes())
+
+
+def _half(t, name: str) -> int:
+    """Type code of a 16-bit tensor."""
+    code = _HALVES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected bfloat16 or float16")
+    return code
+
+
+def _same(t, like, name: str, dims: int):
+    """Checks that ``t`` has the device, the type and ``dims`` dimensions beside ``like``."""
+    if not isinstance(t, _Tensor) or t.dim() != dims:
+        raise ValueError(f"{name} must be a tensor of {dims} dimensions")
+    if t.get_device() != like.get_device() or t.dtype is not like.dtype:
+        raise ValueError(f"{name} is {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
+
+
+def _width(n: int, name: str):
+    if n < 8 or n % 8 or n > 1 << 20:
+        raise ValueError(f"{name} is {n} wide, expected a multiple of 8 up to 2^20")
+
+
+def _rows(t, name: str):
+    """(row stride, pointer) of rows whose values are contiguous and which start on 16-byte boundaries."""
+    rows, cols = t.shape
+    ld = t.stride(0) if rows > 1 else cols
+    p = t.data_ptr()
+    if (t.stride(1) != 1 and cols > 1) or ld < cols or (ld * t.element_size() | p) & 15:
+        raise ValueError(f"{name} must have contiguous values in rows that start on 16-byte boundaries without overlap, "
+                         f"got strides {t.stride()}")
+    return ld, p
+
+
+def _matrices(w, name: str):
+    """(experts, rows, cols, row stride, matrix stride, by columns, pointer) of [E, n, k], or of a transposed view."""
+    E, n, k = w.shape
+    mat, row, col = w.stride()
+    by = 0
+    if col != 1 and row == 1:
+        by, row = 1, col
+    inner, outer = (n, k) if by else (k, n)
+    if E == 1:
+        mat = row * outer
+    p = w.data_ptr()
+    if (col != 1 and not by) or row < inner or mat < row * (outer - 1) + inner or (2 * row | 2 * mat | p) & 15:
+        raise ValueError(f"{name} must be [E, n, k] with contiguous rows or columns that start on 16-byte boundaries "
+                         f"without overlap, got strides {w.stride()}")
+    return E, n, k, row, mat, by, p
+
+
+def _offsets(offsets, dev: int, E: int) -> int:
+    if offsets.dim() != 1:
+        raise ValueError("offsets must be int32 [n_experts + 1]")
+    return _ptr(offsets, dev, E + 1, _i32_t, "offsets")
+
+
+def _status_word(ws, dev: int):
+    return (None, 0) if ws is None else (_ptr(ws, dev, ws.numel(), _u8, "ws"), ws.numel())
+
+
+def si_moe_matmul(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, dtype=None, out: torch.Tensor | None = None,
+                  ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Sorted rows through their experts' matrices: x [R, k] and w [E, n, k] (bf16 or
+    fp16; rows of x at any 16-byte aligned stride, matrices by rows or, as a
+    transposed view, by columns), offsets int32 [E + 1] of ``si_moe_sort`` -> [R, n] in
+    x's type, in ``dtype`` (that or fp32) or into ``out``; zero rows for rows of no expert.
+    Differentiable in x and w (once), without ``out``. ``ws`` (``moe_matmul_workspace_bytes``)
+    receives the device status; without it a wait that ran out on the device, which
+    leaves the result incomplete, is not reported."""
+    dev = x.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(si_moe_matmul, stream, x, w, offsets, dtype, out, ws)
+    if (x.requires_grad or w.requires_grad) and torch.is_grad_enabled():
+        if out is not None:
+            raise ValueError("out cannot be given where x or w requires a gradient")
+        return _Matmul.apply(x, w, offsets, dtype, ws)
+    t = _half(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [R, k]")
+    _same(w, x, "w", 3)
+    (R, k), (E, n, k2, ldw, mat, by, wp) = x.shape, _matrices(w, "w")
+    if k != k2:
+        raise ValueError(f"x is {k} wide, w takes {k2}")
+    _width(n, "out")
+    _width(k, "x")
+    ldx, xp = _rows(x, "x")
+    op = _offsets(offsets, dev, E)
+    if out is None:
+        out, ldo = _empty((R, n), dtype=dtype or x.dtype, device=x.device), n
+        yp = out.data_ptr()
+    else:
+        if out.shape != (R, n) or out.get_device() != dev:
+            raise ValueError(f"out has shape {tuple(out.shape)} on {out.device}, expected {(R, n)} on cuda:{dev}")
+        ldo, yp = _rows(out, "out")
+        if R and yp in (xp, wp):
+            raise ValueError("out is x or w itself")
+    if out.dtype is not x.dtype and out.dtype is not _f32_t:
+        raise ValueError(f"the result is {out.dtype}, expected {x.dtype} or float32")
+    st = library().si_moe_matmul(xp, t, R, ldx, wp, E, n, k, ldw, mat, by, op, yp, _TYPES[out.dtype], ldo,
+                                 *_status_word(ws, dev), _raw_stream(dev))
+    if st:
+        _check(st, "si_moe_matmul")
+    return out
+
+
+def si_moe_matmul_grad_w(gy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, dtype=None,
+                         ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The gradient of the matrices of ``si_moe_matmul``: gy [R, n] and x [R, k] -> gw [E, n, k],
+    gw[e] the sum of gy[r] x[r]^T over expert e's rows, zeros without rows, in gy's type or fp32."""
+    dev = gy.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(si_moe_matmul_grad_w, stream, gy, x, offsets, dtype, ws)
+    t = _half(gy, "gy")
+    if gy.dim() != 2:
+        raise ValueError("gy must be [R, n]")
+    _same(x, gy, "x", 2)
+    (R, n), (R2, k), E = gy.shape, x.shape, offsets.numel() - 1
+    if R != R2:
+        raise ValueError(f"gy has {R} rows, x has {R2}")
+    if E < 1:
+        raise ValueError("offsets must be int32 [n_experts + 1]")
+    _width(n, "gy")
+    _width(k, "x")
+    ldg, gp = _rows(gy, "gy")
+    ldx, xp = _rows(x, "x")
+    op = _offsets(offsets, dev, E)
+    dtype = dtype or gy.dtype
+    if dtype is not gy.dtype and dtype is not _f32_t:
+        raise ValueError(f"the result is {dtype}, expected {gy.dtype} or float32")
+    gw = _empty((E, n, k), dtype=dtype, device=gy.device)
+    st = library().si_moe_matmul_grad_w(gp, ldg, xp, ldx, t, R, E, n, k, op, gw.data_ptr(), _TYPES[dtype],
+                                        *_status_word(ws, dev), _raw_stream(dev))
+    if st:
+        _check(st, "si_moe_matmul_grad_w")
+    return gw
+
+
+def si_moe_matmul_backward(gy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
+                           ws: torch.Tensor | None = None, stream=None):
+    """gy [R, n], and x [R, k], w [E, n, k] of the product -> (gx [R, k], gw [E, n, k])."""
+    dev = gy.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(si_moe_matmul_backward, stream, gy, x, w, offsets, ws)
+    with torch.no_grad():
+        _same(w, gy, "w", 3)
+        if w.shape[1:] != (gy.shape[-1], x.shape[-1]) or w.shape[0] != offsets.numel() - 1:
+            raise ValueError(f"w has shape {tuple(w.shape)}, expected "
+                             f"{(offsets.numel() - 1, gy.shape[-1], x.shape[-1])}")
+        gw = si_moe_matmul_grad_w(gy, x, offsets, None, ws)
+        return si_moe_matmul(gy, w.transpose(1, 2), offsets, None, None, ws), gw
+
+
+class _Matmul(torch.autograd.Function):
+    """si_moe_matmul of an x or a w that requires a gradient."""
+
+    @staticmethod
+    def forward(ctx, x, w, offsets, dtype, ws):
+        ctx.save_for_backward(x, w, offsets)
+        ctx.ws = ws
+        return si_moe_matmul(x, w, offsets, dtype, None, ws)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, gy):
+        x, w, offsets = ctx.saved_tensors
+        gy = gy.to(x.dtype).contiguous()
+        gx = si_moe_matmul(gy, w.transpose(1, 2), offsets, None, None, ctx.ws) if ctx.needs_input_grad[0] else None
+        gw = si_moe_matmul_grad_w(gy, x, offsets, None, ctx.ws) if ctx.needs_input_grad[1] else None
+        return gx, gw, None, None, None
+
+
+def mxint8_scale_shape(rows: int, cols: int) -> tuple:
+    """Shape of the scales of [rows, cols] values: one for 32 of a row."""
+    return (rows, -(-cols // 32))
+
+
+def _act_rows(t, name: str):
+    """Row stride of [rows, cols] with contiguous values, rows without overlap."""
+    rows, cols = t.shape
+    ld = t.stride(0) if rows > 1 else cols
+    if (t.stride(1) != 1 and cols > 1) or ld < cols:
+        raise ValueError(f"{name} must have contiguous values in rows without overlap, got strides {t.stride()}")
+    return ld
+
+
+def si_quantize_mxint8(x: torch.Tensor, stream=None):
+    """x [rows, cols] (fp32, fp16, bf16; rows at any stride without overlap) in 8 bits ->
+    (codes int8 [rows, cols], scales uint8 [rows, ceil(cols / 32)])."""
+    dev = x.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(si_quantize_mxint8, stream, x)
+    if x.dim() != 2 or x.shape[1] == 0:
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected [rows, cols]")
+    if x.dtype not in _TYPES:
+        _bad_type(x, "x")
+    (rows, cols), d = x.shape, x.device
+    ld = _act_rows(x, "x")
+    codes = _empty((rows, cols), dtype=_i8, device=d)
+    scales = _empty((rows, (cols + 31) // 32), dtype=_u8, device=d)
+    st = library().si_quantize_mxint8(x.data_ptr(), _TYPES[x.dtype], rows, cols, ld, codes.data_ptr(),
+                                      scales.data_ptr(), _raw_stream(dev))
+    if st:
+        _check(st, "si_quantize_mxint8")
+    return codes, scales
+
+
+def si_dequantize_mxint8(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.bfloat16,
+                         out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The values of ``si_quantize_mxint8``'s codes as ``dtype`` or into ``out``."""
+    dev = codes.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(si_dequantize_mxint8, stream, codes, scales, dtype, out)
+    if codes.dim() != 2 or codes.shape[1] == 0:
+        raise ValueError(f"codes have shape {tuple(codes.shape)}, expected [rows, cols]")
+    rows, cols = codes.shape
+    c = _ptr(codes, dev, rows * cols, _i8, "codes")
+    if scales.shape != (rows, (cols + 31) // 32):
+        raise ValueError(f"scales have shape {tuple(scales.shape)}, expected {mxint8_scale_shape(rows, cols)}")
+    s = _ptr(scales, dev, scales.numel(), _u8, "scales")
+    if out is None:
+        out, ld = _empty((rows, cols), dtype=dtype, device=codes.device), cols
+    elif out.shape != (rows, cols) or out.get_device() != dev:
+        raise ValueError(f"out has shape {tuple(out.shape)} on {out.device}, expected {(rows, cols)} on cuda:{dev}")
+    else:
+        ld = _act_rows(out, "out")
+    if out.dtype not in _TYPES:
+        _bad_type(out, "out")
+    st = library().si_dequantize_mxint8(c, s, rows, cols, out.data_ptr(), _TYPES[out.dtype], ld, _raw_stream(dev))
+    if st:
+        _check(st, "si_dequantize_mxint8")
+    return out
+
+
+def _kept_empty(rows: int, inter: int, device):
+    """Room for g and u of ``rows`` rows in 8 bits, each with blocks of its own."""
+    return (_empty((rows, 2 * inter), dtype=_i8, device=device),
+            _empty((rows, 2 * ((inter + 31) // 32)), dtype=_u8, device=device))
+
+
+def si_swiglu(gu: torch.Tensor, keep: bool = False, stream=None):
+    """h = silu(g) * u: gu [R, 2 I] (g, then u; fp32, fp16, bf16, rows at any stride) -> h [R, I];
+    with ``keep`` (h, kept), kept = (codes int8 [R, 2 I], scales uint8 [R, 2 ceil(I / 32)]) for
+    ``si_swiglu_backward``. Differentiable (once): the history holds g and u in 8 bits."""
+    dev = gu.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(si_swiglu, stream, gu, keep)
+    if gu.dim() != 2 or gu.shape[1] == 0 or gu.shape[1] % 2:
+        raise ValueError(f"gu has shape {tuple(gu.shape)}, expected [R, 2 I]")
+    if gu.dtype not in _TYPES:
+        _bad_type(gu, "gu")
+    if gu.requires_grad and torch.is_grad_enabled():
+        h, codes, scales = _Swiglu.apply(gu)
+        return (h, (codes, scales)) if keep else h
+    rows, inter, d = gu.shape[0], gu.shape[1] // 2, gu.device
+    ld = _act_rows(gu, "gu")
+    h = _empty((rows, inter), dtype=gu.dtype, device=d)
+    kept = _kept_empty(rows, inter, d) if keep else None
+    cp, sp = (kept[0].data_ptr(), kept[1].data_ptr()) if keep else (None, None)
+    st = library().si_swiglu(gu.data_ptr(), _TYPES[gu.dtype], rows, inter, ld, h.data_ptr(), cp, sp, _raw_stream(dev))
+    if st:
+        _check(st, "si_swiglu")
+    return (h, kept) if keep else h
+
+
+def si_swiglu_backward(gh: torch.Tensor, kept, w: torch.Tensor | None = None, order: torch.Tensor | None = None,
+                       stream=None):
+    """The gradients of h = silu(g) u, from the kept g and u, in rows that enter a sum as
+    w * h: gh [R, I] -> (ggu [R, 2 I], wh [R, I], gw). Without ``w`` every weight is 1 and gw
+    None; w fp32 of R values is row r's, or with ``order`` int32 [R] (``si_moe_sort``'s, w the
+    [T, k] weights) w[order[r]]. gw has w's shape; rows of no pair (order -1) give zero rows, pairs
+    without a row gw 0."""
+    return _swiglu_backward(gh, kept, w, order, True, stream)
+
+
+def _swiglu_backward(gh, kept, w, order, want_wh, stream=None):
+    codes, scales = kept
+    dev = gh.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(lambda gh, c, s, w, o: _swiglu_backward(gh, (c, s), w, o, want_wh), stream, gh, codes, scales,
+                          w, order)
+    if gh.dim() != 2 or gh.shape[1] == 0:
+        raise ValueError(f"gh has shape {tuple(gh.shape)}, expected [R, I]")
+    (R, I), d, dtype = gh.shape, gh.device, gh.dtype
+    if dtype not in _TYPES:
+        _bad_type(gh, "gh")
+    if codes.shape != (R, 2 * I) or scales.shape != (R, 2 * ((I + 31) // 32)):
+        raise ValueError(f"kept codes and scales have shapes {tuple(codes.shape)} and {tuple(scales.shape)}, expected "
+                         f"{(R, 2 * I)} and {(R, 2 * ((I + 31) // 32))}")
+    if order is not None and w is None:
+        raise ValueError("order needs w")
+    gp, cp = _ptr(gh, dev, R * I, dtype, "gh"), _ptr(codes, dev, 2 * R * I, _i8, "codes")
+    sp = _ptr(scales, dev, scales.numel(), _u8, "scales")
+    wp = None if w is None else _ptr(w, dev, R, _f32_t, "w")
+    op = None if order is None else _ptr(order, dev, R, _i32_t, "order")
+    ggu = _empty((R, 2 * I), dtype=dtype, device=d)
+    wh = _empty((R, I), dtype=dtype, device=d) if want_wh else None
+    gw = None if w is None else (torch.zeros if order is not None else _empty)(w.shape, dtype=_f32_t, device=d)
+    st = library().si_swiglu_backward(gp, _TYPES[dtype], R, I, cp, sp, wp, op, ggu.data_ptr(),
+                                      wh.data_ptr() if want_wh else None, None if gw is None else gw.data_ptr(),
+                                      _raw_stream(dev))
+    if st:
+        _check(st, "si_swiglu_backward")
+    return ggu, wh, gw
+
+
+class _Swiglu(torch.autograd.Function):
+    """si_swiglu of a gu that requires a gradient."""
+
+    @staticmethod
+    def forward(ctx, gu):
+        h, kept = si_swiglu(gu, True)
+        ctx.save_for_backward(*kept)
+        ctx.mark_non_differentiable(*kept)
+        return h, *kept
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, gh, *_):
+        return _swiglu_backward(gh.contiguous(), ctx.saved_tensors, None, None, False)[0]
+
+
+def si_moe_gateup(x: torch.Tensor, gate_up: torch.Tensor, offsets: torch.Tensor, keep: bool = False,
+                  ws: torch.Tensor | None = None, stream=None):
+    """si_swiglu of si_moe_matmul's fp32 sums in one launch: sorted rows x [R, H] and gate_up
+    [E, 2 I, H] contiguous (bf16 or fp16) -> h [R, I], with ``keep`` (h, kept) as ``si_swiglu``."""
+    dev = x.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(si_moe_gateup, stream, x, gate_up, offsets, keep, ws)
+    t = _half(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [R, H]")
+    _same(gate_up, x, "gate_up", 3)
+    (R, H), (E, rows, cols), d = x.shape, gate_up.shape, x.device
+    if cols != H or rows % 2:
+        raise ValueError(f"gate_up has shape {tuple(gate_up.shape)}, expected [E, 2 I, {H}]")
+    I = rows // 2
+    _width(I, "h")
+    _width(H, "x")
+    ldx, xp = _rows(x, "x")
+    wp, op = _ptr(gate_up, dev, E * rows * H, x.dtype, "gate_up"), _offsets(offsets, dev, E)
+    h = _empty((R, I), dtype=x.dtype, device=d)
+    kept = _kept_empty(R, I, d) if keep else None
+    cp, sp = (kept[0].data_ptr(), kept[1].data_ptr()) if keep else (None, None)
+    st = library().si_moe_gateup(xp, t, R, ldx, wp, E, I, H, op, h.data_ptr(), cp, sp, *_status_word(ws, dev),
+                                 _raw_stream(dev))
+    if st:
+        _check(st, "si_moe_gateup")
+    return (h, kept) if keep else h
+
+
+def si_moe_experts(x: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor,
+                   ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The routed experts in 16 bits, differentiable: x [T, H], ids int32 [T, k], w fp32 [T, k],
+    gate_up [E, 2 I, H] (gate rows first) and down [E, H, I] contiguous, bf16 or fp16 as x -> [T, H]:
+    y[t] = sum_r w[t, r] down[e] (silu(g) u), (g, u) = gate_up[e] x[t], e = ids[t, r]; ids outside
+    [0, E) are dropped. The gradients (once) reach x, w, gate_up and down; their history
+    holds x and, of the experts' rows, g and u in 8 bits alone."""
+    dev = x.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(si_moe_experts, stream, x, ids, w, gate_up, down, ws)
+    if x.dim() != 2 or ids.dim() != 2 or ids.shape[0] != x.shape[0]:
+        raise ValueError(f"x has shape {tuple(x.shape)}, ids {tuple(ids.shape)}, expected [T, H] and [T, k]")
+    _half(x, "x")
+    _same(gate_up, x, "gate_up", 3)
+    _same(down, x, "down", 3)
+    H, (E, rows, _) = x.shape[1], gate_up.shape
+    if gate_up.shape[2] != H or rows % 2 or down.shape != (E, H, rows // 2):
+        raise ValueError(f"gate_up has shape {tuple(gate_up.shape)} and down {tuple(down.shape)}, expected [E, 2 I, {H}] "
+                         f"and [E, {H}, I]")
+    if w.shape != ids.shape:
+        raise ValueError(f"w has shape {tuple(w.shape)}, expected {tuple(ids.shape)}")
+    if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad or gate_up.requires_grad or down.requires_grad):
+        return _Experts.apply(x, ids, w, gate_up, down, ws)
+    return _experts_forward(x, ids, w, gate_up, down, ws, False)[0]
+
+
+def _experts_forward(x, ids, w, gate_up, down, ws, keep):
+    order, position, offsets = si_moe_sort(ids, gate_up.shape[0])
+    h = si_moe_gateup(si_moe_gather(x, position, offsets), gate_up, offsets, keep, ws)
+    h, kept = h if keep else (h, None)
+    return si_moe_combine(si_moe_matmul(h, down, offsets, None, None, ws), position, w), order, position, offsets, kept
+
+
+class _Experts(torch.autograd.Function):
+    """si_moe_experts with a gradient. Nothing of the experts' outputs is kept: with gh =
+    down^T gy, the gradient of a pair's weight is <gh, h>."""
+
+    @staticmethod
+    def forward(ctx, x, ids, w, gate_up, down, ws):
+        y, order, position, offsets, kept = _experts_forward(x, ids, w, gate_up, down, ws, True)
+        ctx.save_for_backward(x, w, gate_up, down, order, position, offsets, *kept)
+        ctx.ws = ws
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, gy):
+        x, w, gate_up, down, order, position, offsets, *kept = ctx.saved_tensors
+        ws, (need_x, _, need_w, need_gu, need_down, _) = ctx.ws, ctx.needs_input_grad
+        gys = si_moe_gather(gy.contiguous(), position, offsets)
+        gh = si_moe_matmul(gys, down.transpose(1, 2), offsets, None, None, ws)
+        ggu, wh, gw = _swiglu_backward(gh, kept, w, order, need_down)
+        gdown = si_moe_matmul_grad_w(gys, wh, offsets, None, ws) if need_down else None
+        ggate_up = si_moe_matmul_grad_w(ggu, si_moe_gather(x, position, offsets), offsets, None, ws) if need_gu else None
+        gx = (si_moe_gather_backward(si_moe_matmul(ggu, gate_up.transpose(1, 2), offsets, None, None, ws), position)
+              if need_x else None)
+        return gx, None, gw if need_w else None, ggate_up, gdown, None
 
 
 class Mxfp4Experts:

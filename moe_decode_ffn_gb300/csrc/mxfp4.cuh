@@ -141,11 +141,10 @@ template <typename T> struct Raw8 {
   }
 };
 
-// Quantise 8 values of a 32-value block held by 4 consecutive lanes (8 each):
-// the codes of this lane's values; s is the same on the four lanes. Every lane
-// of the warp takes part. Magnitudes order like their bits, so the largest of a
-// 16-bit type is found two values at a time.
-template <typename T> SI_DEV uint32_t mx_encode_4lanes(const Raw8<T> &x, uint32_t &s) {
+// Bits of the largest |x| of a 32-value block held by 4 consecutive lanes (8 values
+// each), on all four. Every lane of the warp takes part. Magnitudes order like their bits,
+// so the largest of a 16-bit type is found two values at a time.
+template <typename T> SI_DEV uint32_t mx_top_4lanes(const Raw8<T> &x) {
   uint32_t top;
   if constexpr (sizeof(T) == 4) {
     top = 0;
@@ -162,7 +161,12 @@ template <typename T> SI_DEV uint32_t mx_encode_4lanes(const Raw8<T> &x, uint32_
     if constexpr (std::is_same_v<T, __nv_bfloat16>) top = m << 16;
     else top = __float_as_uint(half_bits_to_float(static_cast<uint16_t>(m)));
   }
-  s = mx_scale_of(top);
+  return top;
+}
+// Quantise 8 values of such a block: the codes of this lane's values; s is the
+// same on the four lanes.
+template <typename T> SI_DEV uint32_t mx_encode_4lanes(const Raw8<T> &x, uint32_t &s) {
+  s = mx_scale_of(mx_top_4lanes(x));
   const float up = mx_inv_scale(s);
   float q[8];
   x.unpack(q);

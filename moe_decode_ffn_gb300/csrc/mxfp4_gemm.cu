@@ -37,14 +37,13 @@
 // 65536 MMAs alone 27 us), gate/up of 4096 x 8 pairs 64 us, down 70 us, of it the
 // fp32 rows' 268 MB. A plain bulk copy holds its thread for about 270 cycles, so the
 // copies of a stage are spread over threads.
-#include <cuda.h>
-
 #include <algorithm>
 
 #include "host.hpp"
 #include "mxfp4.cuh"
 #include "sort.cuh"
 #include "tc.cuh"
+#include "tma.cuh"
 
 namespace si {
 
@@ -139,17 +138,6 @@ SI_DEV MmTile mm_tile(const MmParams &p, int w, int nt) {
   return t;
 }
 
-SI_DEV void tma_load3(void *dst, const CUtensorMap *map, int c0, int c1, int c2, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-      "[%5];" ::"r"(smem_addr(dst)),
-      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar))
-      : "memory");
-}
-SI_DEV void mbar_arrive(uint64_t *bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
-
 // Shared-memory matrix descriptors (bits as in umma_desc_kmajor): low words,
 // with the address, and the high words, which are constants.
 //  - codes: K-major, 128-byte swizzle (layout 2), rows of 128 bytes, 8-row
@@ -159,15 +147,6 @@ constexpr uint32_t kMmCodesHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 constexpr uint32_t kMmScaleHi = (128u >> 4) | (1u << 14);
 SI_DEV uint32_t mm_codes_lo(uint32_t addr) { return (addr >> 4) | (1u << 16); }
 SI_DEV uint32_t mm_scale_lo(uint32_t addr) { return addr >> 4; }
-// One lane of a converged warp. The MMA warp runs its loops together and only
-// this lane issues: the operands then are uniform values, which the tensor
-// instructions take as they are (a single-lane loop converts each of them for
-// each instruction and cannot feed the tensor core).
-SI_DEV bool elect_lane() {
-  uint32_t is;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(is));
-  return is != 0;
-}
 // 512 bytes of scales to 4 columns of tensor memory, on all four 32-lane quarters.
 SI_DEV void mm_copy_sf(uint32_t taddr, uint32_t lo) {
   asm volatile("{\n .reg .b64 d;\n mov.b64 d, {%1, %2};\n"
@@ -190,19 +169,6 @@ SI_DEV void mm_mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uin
       "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc), "n"(kMmCodesHi)
       : "memory");
 }
-// 16 consecutive fp32 columns of this warp's 32 lanes; the wait is separate so
-// that two loads can be in flight.
-SI_DEV void tmem_ld16(uint32_t taddr, uint32_t r[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-SI_DEV void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-
 // ---- epilogues ---------------------------------------------------------------
 
 // Outputs whose rows start on 16-byte boundaries leave in 16-byte words (2-byte
@@ -365,26 +331,6 @@ SI_DEV void mm_write_h(const MmParams &p, const MmTile &t, uint32_t acc_g, uint3
 }
 
 // ---- epilogues, tokens on the lanes ---------------------------------------------
-
-SI_DEV void tmem_ld32(uint32_t taddr, uint32_t r[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-// 32 bytes of a row: one sector, one store (mm_launch_tok says when). Not kept in
-// the L1, which the ring of stages shares: 8192 x 4096 x 4096 with its quantisation
-// 73.0 -> 72.1 us.
-SI_DEV void st_global32(void *p, const uint32_t w[8]) {
-  asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
 
 // 64 features (from f0) of this lane's token `j`, 32 at a time; 2-byte
 // outputs wait, packed, until all are read.
@@ -881,33 +827,14 @@ __global__ void __launch_bounds__(256) sort_scatter_kernel(SortArgs so, ScatterA
 
 // ---- host ------------------------------------------------------------------
 
-typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-static EncodeTiled encode_tiled() {
-  static const EncodeTiled fn = [] {
-    void *f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<EncodeTiled>(f);
-  }();
-  return fn;
-}
-
 // Codes [mats][rows][cols / 2], boxes of box_rows rows x 128 bytes; what lies
 // outside reads as zero.
 static bool codes_map(CUtensorMap *m, const void *codes, int64_t mats, int64_t rows, int64_t cols, int box_rows) {
-  const EncodeTiled fn = encode_tiled();
-  if (!fn) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols / 2), static_cast<cuuint64_t>(rows),
                               static_cast<cuuint64_t>(mats)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols / 2), static_cast<cuuint64_t>(cols / 2 * rows)};
-  const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(box_rows), 1}, one[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(codes), dims, strides, box, one,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(box_rows), 1};
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, 3, dims, strides, box);
 }
 
 template <int MODE, int MA, int NT, bool TOK, int OUT>

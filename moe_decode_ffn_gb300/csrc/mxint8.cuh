@@ -1,0 +1,40 @@
+// MXINT8 (OCP microscaling, 8-bit integer elements, E8M0 scales) on the device.
+//
+// 32 consecutive values of a row share the power of two X = 2^(s - 127) with s the
+// exponent field of max |x| in fp32, so that the largest lies in [X, 2X); every
+// value is code * X / 64, code = x / X * 64 rounded to nearest even and kept within
+// +-127. A block that holds an infinity or a NaN gets s = 255 (the E8M0 NaN) and
+// codes 0.
+#pragma once
+
+#include "mxfp4.cuh"
+
+namespace si {
+
+// s from the largest |x| of the block, as bits.
+SI_DEV uint32_t mi_scale_of(uint32_t amax_bits) { return amax_bits >> 23; }
+// 2^(127 - s), exact; s = 255: 0.
+SI_DEV float mi_inv_scale(uint32_t s) {
+  return s >= 254u ? (s == 254u ? __uint_as_float(1u << 22) : 0.f) : __uint_as_float((254u - s) << 23);
+}
+// 2^(s - 133), the value of code 1 (exact, subnormal below s = 7); NaN for 255.
+SI_DEV float mi_step(uint32_t s) {
+  return __uint_as_float(s == 255u ? 0x7FC00000u : s > 6u ? (s - 6u) << 23 : 1u << (s + 16u));
+}
+// A value, times 2^(127 - s), to its code in the low byte: within +-127/64, then
+// rounded to a multiple of 1/64 by the addition to 1.5 * 2^23.
+SI_DEV uint32_t mi_code(float v) {
+  return __float_as_uint(fmaf(fminf(fmaxf(v, -127.f / 64.f), 127.f / 64.f), 64.f, 12582912.f));
+}
+SI_DEV uint32_t mi_pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+// Four codes to their integers as fp32.
+SI_DEV void mi_values4(uint32_t w, float v[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = static_cast<float>(static_cast<int8_t>(w >> (8 * i)));
+}
+// Scales of a row of `cols` values.
+__host__ __device__ constexpr int64_t mi_blocks(int64_t cols) { return (cols + 31) / 32; }
+
+}  // namespace si

@@ -1,0 +1,95 @@
+"""Arguments of the products of sorted rows, of the 8-bit activations and of SwiGLU
+are checked on the host (no device work; every call here is refused or has nothing
+to do)."""
+import pytest
+import torch
+
+import moe_decode_ffn_gb300 as m
+
+BAD, UNS, WS, OK = m.SI_ERR_INVALID_ARG, m.SI_ERR_UNSUPPORTED, m.SI_ERR_WORKSPACE, m.SI_OK
+
+
+@pytest.fixture(scope="module")
+def lib():
+    m.build()
+    return m.library()
+
+
+def refused(call, ok, cases, want):
+    for kw in cases:
+        assert set(kw) <= set(ok)
+        assert call(*{**ok, **kw}.values(), None) == want, kw
+
+
+def test_product_refusals(lib):
+    assert lib.si_moe_matmul_workspace_bytes() == 256
+    ok = dict(x=16, type=m.SI_BF16, rows=40, ldx=64, w=16, e=4, n=24, k=64, ldw=64, mat=24 * 64, cols=0, off=16, out=16,
+              to=m.SI_BF16, ldo=24, ws=256, nb=256)
+    refused(lib.si_moe_matmul, ok, [
+        {"x": None}, {"x": 8}, {"w": None}, {"w": 24}, {"off": None}, {"off": 18}, {"out": None}, {"out": 8},
+        {"rows": -1}, {"rows": 1 << 31}, {"ldx": 56}, {"ldx": 68}, {"ldx": -64}, {"e": 0}, {"e": 1025}, {"n": 0}, {"n": 12},
+        {"n": (1 << 20) + 8}, {"k": 0}, {"k": 60}, {"ldw": 56}, {"ldw": 66}, {"mat": 24 * 64 - 8}, {"mat": 24 * 64 + 4},
+        {"cols": 1, "ldw": 16}, {"cols": 1, "ldw": 24, "mat": 24 * 63}, {"ldo": 16}, {"ldo": 28}], BAD)
+    refused(lib.si_moe_matmul, ok, [{"type": m.SI_F32}, {"type": m.SI_Q8_0}, {"to": m.SI_F16}, {"to": m.SI_Q8_0},
+                                    {"rows": 1 << 30, "n": 1 << 20, "ldo": 1 << 20, "mat": 1 << 26}], UNS)
+    refused(lib.si_moe_matmul, ok, [{"ws": 16}, {"nb": 255}], WS)
+    refused(lib.si_moe_matmul, ok, [{"rows": 0}, {"rows": 0, "x": None, "out": None}], OK)
+
+
+def test_gradient_refusals(lib):
+    ok = dict(gy=16, ldg=24, x=16, ldx=64, type=m.SI_F16, rows=40, e=4, n=24, k=64, off=16, gw=16, to=m.SI_F32, ws=256,
+              nb=256)
+    refused(lib.si_moe_matmul_grad_w, ok, [
+        {"gy": None}, {"gy": 8}, {"ldg": 16}, {"ldg": 28}, {"x": None}, {"x": 8}, {"ldx": 56}, {"rows": -1},
+        {"rows": 1 << 31}, {"e": 0}, {"e": 1025}, {"n": 20}, {"k": 4}, {"off": None}, {"off": 17}, {"gw": None},
+        {"gw": 8}], BAD)
+    refused(lib.si_moe_matmul_grad_w, ok, [{"type": m.SI_F32}, {"to": m.SI_BF16}, {"e": 1024, "n": 1 << 20, "ldg": 1 << 20, "k": 1 << 20, "ldx": 1 << 20}], UNS)
+    refused(lib.si_moe_matmul_grad_w, ok, [{"ws": 16}, {"nb": 255}], WS)
+
+
+def test_gateup_refusals(lib):
+    ok = dict(x=16, type=m.SI_BF16, rows=40, ldx=64, w=16, e=4, inter=24, hidden=64, off=16, h=16, codes=16, scales=16,
+              ws=256, nb=256)
+    refused(lib.si_moe_gateup, ok, [
+        {"x": None}, {"w": 8}, {"off": None}, {"h": None}, {"h": 8}, {"codes": None}, {"codes": 8}, {"scales": None},
+        {"ldx": 56}, {"inter": 4}, {"hidden": 68}, {"e": 0}, {"rows": -1}], BAD)
+    refused(lib.si_moe_gateup, ok, [{"type": m.SI_F32}], UNS)
+    refused(lib.si_moe_gateup, ok, [{"ws": 128}, {"nb": 0}], WS)
+    refused(lib.si_moe_gateup, ok, [{"rows": 0, "x": None}], OK)
+
+
+def test_mxint8_refusals(lib):
+    ok = dict(x=16, type=m.SI_F32, rows=4, cols=40, ld=40, codes=16, scales=16)
+    refused(lib.si_quantize_mxint8, ok, [
+        {"x": None}, {"x": 18}, {"rows": -1}, {"cols": 0}, {"cols": -8}, {"ld": 39}, {"codes": None}, {"scales": None},
+        {"rows": 1 << 30, "cols": 1 << 30, "ld": 1 << 30}], BAD)
+    refused(lib.si_quantize_mxint8, ok, [{"type": m.SI_Q8_0}], UNS)
+    refused(lib.si_quantize_mxint8, ok, [{"rows": 0, "x": None}], OK)
+    ok = dict(codes=16, scales=16, rows=4, cols=40, y=16, type=m.SI_BF16, ld=40)
+    refused(lib.si_dequantize_mxint8, ok, [{"y": None}, {"y": 17}, {"ld": 32}, {"codes": None}, {"scales": None}], BAD)
+    refused(lib.si_dequantize_mxint8, ok, [{"type": m.SI_Q4_K}], UNS)
+
+
+def test_swiglu_refusals(lib):
+    ok = dict(gu=16, type=m.SI_BF16, rows=4, inter=40, ld=80, h=16, codes=16, scales=16)
+    refused(lib.si_swiglu, ok, [{"gu": None}, {"gu": 17}, {"h": None}, {"inter": 0}, {"ld": 79}, {"rows": -1},
+                                {"codes": None}, {"scales": None}], BAD)
+    refused(lib.si_swiglu, ok, [{"type": m.SI_Q8_1}], UNS)
+    ok = dict(gh=16, type=m.SI_F32, rows=4, inter=40, codes=16, scales=16, w=16, order=16, ggu=16, wh=16, gw=16)
+    refused(lib.si_swiglu_backward, ok, [
+        {"gh": None}, {"gh": 18}, {"codes": None}, {"scales": None}, {"w": 18}, {"order": 17}, {"ggu": None}, {"wh": 18},
+        {"gw": 18}, {"inter": 0}, {"rows": 1 << 31}], BAD)
+    refused(lib.si_swiglu_backward, ok, [{"type": m.SI_Q8_1}], UNS)
+    refused(lib.si_swiglu_backward, ok, [{"rows": 0}], OK)
+
+
+def test_binding_refuses_host_tensors(lib):
+    x, w, off = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(2, 8, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    ids, c = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    for call in (lambda: m.si_moe_matmul(x, w, off), lambda: m.si_moe_matmul_grad_w(x, x, off),
+                 lambda: m.si_moe_matmul_backward(x, x, w, off), lambda: m.si_moe_gateup(x, w, off),
+                 lambda: m.si_moe_experts(x, ids, c, w, w), lambda: m.si_quantize_mxint8(x),
+                 lambda: m.si_dequantize_mxint8(x, x), lambda: m.si_swiglu(x),
+                 lambda: m.si_swiglu_backward(x, (x, x))):
+        with pytest.raises(ValueError):
+            call()
