@@ -487,7 +487,9 @@ si_status si_mxfp4_matmul(const void *a_codes, const void *a_scales, int64_t m, 
  * rounded once. A dropped pair adds nothing and has gw 0; a token without kept
  * pairs gets a zero row; sorted rows at and behind *n_kept (device int32:
  * offsets + n_experts) are written as zeros. Places must be distinct; those
- * outside the sorted rows count as dropped. hidden 1..2^24; rows of whole 16-byte
+ * outside the sorted rows count as dropped. si_moe_combine_f32 sums fp32 rows (ys) into
+ * y_type, rounded once; topk_w NULL: weights of 1, as in si_moe_gather_backward.
+ * hidden 1..2^24; rows of whole 16-byte
  * words at 16-byte aligned addresses move in such words, others value by value.
  * Outputs may not alias inputs.
  */
@@ -501,6 +503,8 @@ si_status si_moe_gather_backward(const void *gxs, si_dtype type, int n_tokens, i
                                  const int32_t *position, void *gx, void *stream);
 si_status si_moe_combine(const void *ys, si_dtype type, int n_tokens, int top_k, int64_t hidden,
                          const int32_t *position, const float *topk_w, void *y, void *stream);
+si_status si_moe_combine_f32(const float *ys, int n_tokens, int top_k, int64_t hidden, const int32_t *position,
+                             const float *topk_w, void *y, si_dtype y_type, void *stream);
 si_status si_moe_combine_backward(const void *gy, const void *ys, si_dtype type, int n_tokens, int top_k,
                                   int64_t hidden, const int32_t *position, const int32_t *n_kept,
                                   const float *topk_w, void *gys, float *gw, void *stream);
@@ -516,8 +520,10 @@ si_status si_moe_combine_backward(const void *gy, const void *ys, si_dtype type,
  * si_moe_matmul_grad_w: gw[e][i][c] = sum over the rows r of expert e of gy[r][i] * x[r][c]
  * si_moe_gateup:        h[r][i] = silu(g) * u with g, u = out[r][i], out[r][inter + i] of
  *                       si_moe_matmul in fp32, and g and u in 8 bits for the backward pass
+ * si_moe_down_backward: what si_swiglu_backward (below) makes of gh = si_moe_matmul of gy
+ *                       [rows][hidden] with down by columns, gh in fp32 and not written
  *
- *   type     SI_BF16 or SI_F16, of x, w, gy and h; out_type, gw_type: type or SI_F32
+ *   type     SI_BF16 or SI_F16, of x, w, gy, h, ggu and wh; out_type, gw_type: type or SI_F32
  *   rows     0 .. 2^31 - 257; 0: gw becomes zeros, the others do nothing. Rows of no expert
  *            (before offsets[0], behind offsets[n_experts]) are not read, and their outputs
  *            (codes and scales too) are zeros; an expert without rows has gw 0
@@ -534,8 +540,12 @@ si_status si_moe_combine_backward(const void *gy, const void *ys, si_dtype type,
  *            codes on a 16-byte boundary
  *   workspace  si_moe_matmul_workspace_bytes() bytes, zeroed once, or NULL: the
  *            status word, without which a wait that ran out on the device, which
- *            leaves the outputs incomplete, is not reported
- * Outputs may not alias inputs. More than 2^30 output tiles: SI_ERR_UNSUPPORTED.
+ *            leaves the outputs incomplete, is not reported. si_moe_down_backward with
+ *            gw: si_moe_down_backward_workspace_bytes(rows, n_experts, inter) bytes, of
+ *            which the first 256 are zeroed once
+ * fp32 sums of 512 terms on the tensor cores (whose additions may truncate); with SI_F32
+ * outputs these are added to one another rounded to nearest. More sums than 512 terms'
+ * stay on the tensor cores otherwise. Outputs may not alias inputs. More than 2^30 output tiles: SI_ERR_UNSUPPORTED.
  */
 size_t si_moe_matmul_workspace_bytes(void);
 si_status si_moe_matmul(const void *x, si_dtype type, int64_t rows, int64_t ld_x, const void *w, int n_experts,
@@ -548,6 +558,13 @@ si_status si_moe_matmul_grad_w(const void *gy, int64_t ld_gy, const void *x, int
 si_status si_moe_gateup(const void *x, si_dtype type, int64_t rows, int64_t ld_x, const void *gate_up,
                         int n_experts, int64_t inter, int64_t hidden, const int32_t *offsets, void *h, void *codes,
                         void *scales, void *workspace, size_t workspace_bytes, void *stream);
+/* down [n_experts][hidden][inter] contiguous; codes, scales as si_moe_gateup left them;
+ * row_w, order, ggu, wh and gw as in si_swiglu_backward. */
+size_t si_moe_down_backward_workspace_bytes(int64_t rows, int n_experts, int64_t inter);
+si_status si_moe_down_backward(const void *gy, si_dtype type, int64_t rows, int64_t ld_gy, const void *down,
+                               int n_experts, int64_t hidden, int64_t inter, const int32_t *offsets,
+                               const void *codes, const void *scales, const float *row_w, const int32_t *order,
+                               void *ggu, void *wh, float *gw, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * Activations in 8 bits (OCP MXINT8). 32 consecutive values of a row (the last block

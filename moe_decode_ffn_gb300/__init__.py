@@ -105,6 +105,7 @@ SIGNATURES = {
     "si_moe_gather": (_i32, [_vp, _i32, _i32, _i32, _i64, _vp, _vp, _vp, _vp]),
     "si_moe_gather_backward": (_i32, [_vp, _i32, _i32, _i32, _i64, _vp, _vp, _vp]),
     "si_moe_combine": (_i32, [_vp, _i32, _i32, _i32, _i64, _vp, _vp, _vp, _vp]),
+    "si_moe_combine_f32": (_i32, [_vp, _i32, _i32, _i64, _vp, _vp, _vp, _i32, _vp]),
     "si_moe_combine_backward": (_i32, [_vp, _vp, _i32, _i32, _i32, _i64, _vp, _vp, _vp, _vp, _vp,
                                        _vp]),
     "si_moe_matmul_workspace_bytes": (_sz, []),
@@ -113,6 +114,9 @@ SIGNATURES = {
     "si_moe_matmul_grad_w": (_i32, [_vp, _i64, _vp, _i64, _i32, _i64, _i32, _i64, _i64, _vp, _vp, _i32, _vp, _sz,
                                     _vp]),
     "si_moe_gateup": (_i32, [_vp, _i32, _i64, _i64, _vp, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "si_moe_down_backward_workspace_bytes": (_sz, [_i64, _i32, _i64]),
+    "si_moe_down_backward": (_i32, [_vp, _i32, _i64, _i64, _vp, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                    _vp, _vp, _sz, _vp]),
     "si_quantize_mxint8": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp]),
     "si_dequantize_mxint8": (_i32, [_vp, _vp, _i64, _i64, _vp, _i32, _i64, _vp]),
     "si_swiglu": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp]),
@@ -812,11 +816,13 @@ def si_moe_gather(x: torch.Tensor, position: torch.Tensor, offsets: torch.Tensor
     return xs
 
 
-def si_moe_gather_backward(gxs: torch.Tensor, position: torch.Tensor, stream=None) -> torch.Tensor:
-    """gx[t] = sum_r gxs[position[t, r]]: gxs [T * k, H] -> [T, H]."""
+def si_moe_gather_backward(gxs: torch.Tensor, position: torch.Tensor, stream=None, dtype=None) -> torch.Tensor:
+    """gx[t] = sum_r gxs[position[t, r]]: gxs [T * k, H] -> [T, H] in gxs' type, or fp32 rows in ``dtype``."""
     dev = gxs.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
-        return _elsewhere(si_moe_gather_backward, stream, gxs, position)
+        return _elsewhere(si_moe_gather_backward, stream, gxs, position, None, dtype)
+    if dtype is not None and dtype is not gxs.dtype:
+        return _combine_f32(dev, gxs, position, None, dtype)
     (T, k), H, dtype = position.shape, gxs.shape[-1], gxs.dtype
     n = T * k
     if n >> 31:
@@ -832,14 +838,16 @@ def si_moe_gather_backward(gxs: torch.Tensor, position: torch.Tensor, stream=Non
     return gx
 
 
-def si_moe_combine(ys: torch.Tensor, position: torch.Tensor, w: torch.Tensor, stream=None) -> torch.Tensor:
-    """y[t] = sum_r w[t, r] ys[position[t, r]]: ys [T * k, H], w fp32 [T, k] -> [T, H].
-    Differentiable in ys and w (once)."""
+def si_moe_combine(ys: torch.Tensor, position: torch.Tensor, w: torch.Tensor, stream=None, dtype=None) -> torch.Tensor:
+    """y[t] = sum_r w[t, r] ys[position[t, r]]: ys [T * k, H], w fp32 [T, k] -> [T, H] in ys'
+    type, or fp32 rows in ``dtype``. Differentiable in ys and w (once)."""
     dev = ys.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
-        return _elsewhere(si_moe_combine, stream, ys, position, w)
+        return _elsewhere(si_moe_combine, stream, ys, position, w, None, dtype)
     if (ys.requires_grad or w.requires_grad) and torch.is_grad_enabled():
-        return _Combine.apply(ys, position, w)
+        return _Combine.apply(ys, position, w, dtype)
+    if dtype is not None and dtype is not ys.dtype:
+        return _combine_f32(dev, ys, position, w, dtype)
     (T, k), H, dtype = position.shape, ys.shape[-1], ys.dtype
     n = T * k
     if n >> 31:
@@ -852,6 +860,23 @@ def si_moe_combine(ys: torch.Tensor, position: torch.Tensor, w: torch.Tensor, st
                                   y.data_ptr(), _raw_stream(dev))
     if st:
         _check(st, "si_moe_combine")
+    return y
+
+
+def _combine_f32(dev: int, ys, position, w, dtype):
+    (T, k), H = position.shape, ys.shape[-1]
+    n = T * k
+    if n >> 31:
+        _too_many(T, k)
+    if dtype not in _TYPES:
+        raise ValueError(f"dtype is {dtype}, expected float32, float16 or bfloat16")
+    y = _empty((T, H), dtype=dtype, device=ys.device)
+    st = library().si_moe_combine_f32(_ptr(ys, dev, n * H, _f32_t, "rows summed in another type"), T, k, H,
+                                      _ptr(position, dev, n, _i32_t, "position"),
+                                      None if w is None else _ptr(w, dev, n, _f32_t, "w"), y.data_ptr(), _TYPES[dtype],
+                                      _raw_stream(dev))
+    if st:
+        _check(st, "si_moe_combine_f32")
     return y
 
 
@@ -904,17 +929,19 @@ class _Combine(torch.autograd.Function):
     and the kernel, told that every row is kept, clears none."""
 
     @staticmethod
-    def forward(ctx, ys, position, w):
+    def forward(ctx, ys, position, w, dtype):
         ctx.save_for_backward(ys, position, w)
-        return si_moe_combine(ys, position, w)
+        return si_moe_combine(ys, position, w, None, dtype)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, gy):
         ys, position, w = ctx.saved_tensors
         kept = torch.full((1,), position.numel(), dtype=_i32_t, device=ys.device)
-        gys, gw = _combine_backward(ys.get_device(), gy.contiguous(), ys, position, kept, w, torch.zeros_like(ys))
-        return gys if ctx.needs_input_grad[0] else None, None, gw.view(w.shape) if ctx.needs_input_grad[2] else None
+        gys, gw = _combine_backward(ys.get_device(), gy.to(ys.dtype).contiguous(), ys, position, kept, w,
+                                    torch.zeros_like(ys))
+        return (gys if ctx.needs_input_grad[0] else None, None, gw.view(w.shape) if ctx.needs_input_grad[2] else None,
+                None)
 
 
 # ----------------------------------------------------------------------------
@@ -1278,13 +1305,75 @@ def si_moe_gateup(x: torch.Tensor, gate_up: torch.Tensor, offsets: torch.Tensor,
     return (h, kept) if keep else h
 
 
+def moe_down_backward_workspace_bytes(rows: int, n_experts: int, inter: int) -> int:
+    return int(library().si_moe_down_backward_workspace_bytes(rows, n_experts, inter))
+
+
+def si_moe_down_backward(gy: torch.Tensor, down: torch.Tensor, kept, offsets: torch.Tensor,
+                         w: torch.Tensor | None = None, order: torch.Tensor | None = None,
+                         ws: torch.Tensor | None = None, stream=None):
+    """``si_swiglu_backward`` of gh = si_moe_matmul(gy, down^T) in one launch, gh in fp32 and not
+    written: sorted rows gy [R, H], down [E, H, I] contiguous (bf16 or fp16), kept of
+    ``si_moe_gateup`` -> (ggu [R, 2 I], wh [R, I], gw). ``ws``, if given, has at least
+    ``moe_down_backward_workspace_bytes(R, E, I)`` bytes with w."""
+    return _down_backward(gy, down, kept, offsets, w, order, ws, True, True, stream)
+
+
+def _down_backward(gy, down, kept, offsets, w, order, ws, want_wh, want_gw, stream=None):
+    codes, scales = kept
+    dev = gy.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(lambda gy, down, c, s, *a: _down_backward(gy, down, (c, s), *a, want_wh, want_gw), stream, gy,
+                          down, codes, scales, offsets, w, order, ws)
+    t = _half(gy, "gy")
+    if gy.dim() != 2:
+        raise ValueError("gy must be [R, H]")
+    _same(down, gy, "down", 3)
+    (R, H), (E, H2, I), d = gy.shape, down.shape, gy.device
+    if H != H2:
+        raise ValueError(f"gy is {H} wide, down has {H2} rows")
+    _width(I, "wh")
+    _width(H, "gy")
+    if codes.shape != (R, 2 * I) or scales.shape != (R, 2 * ((I + 31) // 32)):
+        raise ValueError(f"kept codes and scales have shapes {tuple(codes.shape)} and {tuple(scales.shape)}, expected "
+                         f"{(R, 2 * I)} and {(R, 2 * ((I + 31) // 32))}")
+    if order is not None and w is None:
+        raise ValueError("order needs w")
+    ldg, gp = _rows(gy, "gy")
+    dp, op = _ptr(down, dev, E * H * I, gy.dtype, "down"), _offsets(offsets, dev, E)
+    cp, sp = _ptr(codes, dev, 2 * R * I, _i8, "codes"), _ptr(scales, dev, scales.numel(), _u8, "scales")
+    wp = None if w is None else _ptr(w, dev, R, _f32_t, "w")
+    rp = None if order is None else _ptr(order, dev, R, _i32_t, "order")
+    ggu = _empty((R, 2 * I), dtype=gy.dtype, device=d)
+    wh = _empty((R, I), dtype=gy.dtype, device=d) if want_wh else None
+    gw = None
+    if w is not None and want_gw:
+        gw = (torch.zeros if order is not None else _empty)(w.shape, dtype=_f32_t, device=d)
+        if ws is None:
+            ws = _scratch(moe_down_backward_workspace_bytes(R, E, I), d)
+    st = library().si_moe_down_backward(gp, t, R, ldg, dp, E, H, I, op, cp, sp, wp, rp, ggu.data_ptr(),
+                                        wh.data_ptr() if want_wh else None, None if gw is None else gw.data_ptr(),
+                                        *_status_word(ws, dev), _raw_stream(dev))
+    if st:
+        _check(st, "si_moe_down_backward")
+    return ggu, wh, gw
+
+
+def moe_experts_workspace_bytes(n_tokens: int, top_k: int, gate_up: torch.Tensor) -> int:
+    """Of ``si_moe_experts`` and its gradients."""
+    E, rows, _ = gate_up.shape
+    return moe_down_backward_workspace_bytes(n_tokens * top_k, E, rows // 2)
+
+
 def si_moe_experts(x: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor,
                    ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The routed experts in 16 bits, differentiable: x [T, H], ids int32 [T, k], w fp32 [T, k],
     gate_up [E, 2 I, H] (gate rows first) and down [E, H, I] contiguous, bf16 or fp16 as x -> [T, H]:
     y[t] = sum_r w[t, r] down[e] (silu(g) u), (g, u) = gate_up[e] x[t], e = ids[t, r]; ids outside
     [0, E) are dropped. The gradients (once) reach x, w, gate_up and down; their history
-    holds x and, of the experts' rows, g and u in 8 bits alone."""
+    holds x and, of the experts' rows, g and u in 8 bits alone. ``ws`` is kept by the caller
+    (``moe_experts_workspace_bytes``) and receives the device status; without it a wait that
+    ran out on the device, which leaves the results incomplete, is not reported."""
     dev = x.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(si_moe_experts, stream, x, ids, w, gate_up, down, ws)
@@ -1308,12 +1397,16 @@ def _experts_forward(x, ids, w, gate_up, down, ws, keep):
     order, position, offsets = si_moe_sort(ids, gate_up.shape[0])
     h = si_moe_gateup(si_moe_gather(x, position, offsets), gate_up, offsets, keep, ws)
     h, kept = h if keep else (h, None)
-    return si_moe_combine(si_moe_matmul(h, down, offsets, None, None, ws), position, w), order, position, offsets, kept
+    # the experts' rows stay fp32 until the ranks are summed
+    ys = si_moe_matmul(h, down, offsets, _f32_t, None, ws)
+    return si_moe_combine(ys, position, w, None, x.dtype), order, position, offsets, kept
 
 
 class _Experts(torch.autograd.Function):
     """si_moe_experts with a gradient. Nothing of the experts' outputs is kept: with gh =
-    down^T gy, the gradient of a pair's weight is <gh, h>."""
+    down^T gy, the gradient of a pair's weight is <gh, h>. gh stays in the registers of
+    the launch that forms it, and x's gradient in fp32 rows until the ranks are summed: so
+    every gradient is rounded once as an operand of a product and once as a result."""
 
     @staticmethod
     def forward(ctx, x, ids, w, gate_up, down, ws):
@@ -1328,13 +1421,14 @@ class _Experts(torch.autograd.Function):
         x, w, gate_up, down, order, position, offsets, *kept = ctx.saved_tensors
         ws, (need_x, _, need_w, need_gu, need_down, _) = ctx.ws, ctx.needs_input_grad
         gys = si_moe_gather(gy.contiguous(), position, offsets)
-        gh = si_moe_matmul(gys, down.transpose(1, 2), offsets, None, None, ws)
-        ggu, wh, gw = _swiglu_backward(gh, kept, w, order, need_down)
+        ggu, wh, gw = _down_backward(gys, down, kept, offsets, w, order, ws, need_down, need_w)
         gdown = si_moe_matmul_grad_w(gys, wh, offsets, None, ws) if need_down else None
         ggate_up = si_moe_matmul_grad_w(ggu, si_moe_gather(x, position, offsets), offsets, None, ws) if need_gu else None
-        gx = (si_moe_gather_backward(si_moe_matmul(ggu, gate_up.transpose(1, 2), offsets, None, None, ws), position)
-              if need_x else None)
-        return gx, None, gw if need_w else None, ggate_up, gdown, None
+        gx = None
+        if need_x:
+            gxs = si_moe_matmul(ggu, gate_up.transpose(1, 2), offsets, _f32_t, None, ws)
+            gx = si_moe_gather_backward(gxs, position, None, x.dtype)
+        return gx, None, gw, ggate_up, gdown, None
 
 
 class Mxfp4Experts:

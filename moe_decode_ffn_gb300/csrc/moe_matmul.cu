@@ -8,24 +8,28 @@
 // bf16 or fp16 operands, fp32 sums in tensor memory (tcgen05.mma kind::f16), rounded
 // once. The experts' rows follow one another without padding: expert e has rows
 // offsets[e] .. offsets[e + 1]. Three forms of one kernel:
-//  - kGmTokens: 128 rows of an expert on the lanes of tensor memory, 256 of its
-//    features as the N operand;
-//  - kGmFew: 128 features on the lanes, NT rows as the N operand, where an expert has
-//    few rows: the matrices then pass through the tensor cores once;
-//  - kGmGrad: 128 x 256 of an expert's gradient, summed over its rows.
+//  - kGmWide: 256 features on the lanes of tensor memory, 128 in each of two neighbouring
+//    SMs (cta_group::2), up to 256 rows of an expert as the N operand, half of them in
+//    each SM: a tile's N is its own number of rows, to the next 32, so that ragged
+//    experts cost no more than they hold, and every SM brings in half of each operand;
+//  - kGmFew: the same in one SM with 16 rows, where an expert has few: a deep ring of
+//    its matrix' pieces and nothing else;
+//  - kGmGrad: 256 x 256 of an expert's gradient, summed over its rows, in two SMs.
 // An operand whose summed index is contiguous in memory lies in shared memory row
 // by row (K-major), the others as they are, 64 values of 64 summed indices a piece
 // (MN-major): nothing is transposed on the way.
 //
 // A tile of rows may reach behind its expert's: the rows of the next expert that it
-// then holds give rows of tensor memory that are not written. In kGmGrad they would
-// enter the sums, so the MMA warp clears them in shared memory.
+// then holds give columns of tensor memory that are not written. In kGmGrad they would
+// enter the sums, so a warp of each SM clears them in shared memory.
 //
 // A block: a thread of warp 0 keeps operand A of a ring of stages (64 summed
-// indices) coming by tensor TMA, one of the last warp operand B, warp 1 issues the
-// MMAs, the others read the accumulators and write. Blocks are persistent; two accumulators,
-// so that the MMAs of a tile run beside the epilogue of the one before.
+// indices) coming by tensor TMA, one of another warp operand B, warp 1 (of the first SM
+// of a pair) issues the MMAs, the others read the accumulators and write. Blocks are
+// persistent; two accumulators, so that the MMAs of a tile run beside the epilogue of
+// the one before.
 #include <algorithm>
+#include <atomic>
 
 #include "host.hpp"
 #include "mxint8.cuh"
@@ -38,38 +42,54 @@ constexpr int kGmK = 64;              // summed indices of a stage: 128 bytes
 constexpr int kGmPiece = 8192;        // 64 x 64 values of an MN-major operand
 constexpr int kGmGroups = kSortMaxExperts + 2;
 
-enum GmOp { kGmTokens, kGmFew, kGmGrad };
+enum GmOp { kGmWide, kGmFew, kGmGrad };
+// What becomes of the sums: written, SwiGLU of gate and up, the gradients of SwiGLU.
+enum GmMode { kGmPlain, kGmSwiglu, kGmSwigluBack };
 enum GmOut { kGmBf16, kGmF16, kGmF32 };
 template <int OUT> constexpr int kGmSize = OUT == kGmF32 ? 4 : 2;
 
-template <int OP, int NT, bool SWIGLU> struct GmCfg {
-  static constexpr int MA = OP == kGmFew && SWIGLU ? 2 : 1;   // 128-row A tiles: gate and up
-  static constexpr int kN = OP == kGmFew ? NT : 256;
-  static constexpr int kEpiWarps = OP == kGmFew ? 4 : 8;
-  static constexpr int kThreads = 32 * (3 + kEpiWarps);
-  static constexpr int kABytes = MA * 128 * 128, kBBytes = kN * 128, kStage = kABytes + kBBytes;
+template <int OP, int MODE, int OUT> struct GmCfg {
+  static constexpr int CG = OP == kGmFew ? 1 : 2;                    // SMs of a tile
+  static constexpr int MA = OP == kGmFew && MODE == kGmSwiglu ? 2 : 1;   // 128-row A tiles: gate and up
+  static constexpr int kN = OP == kGmFew ? 16 : 256;                 // columns of an accumulator
+  // fp32 outputs are summed up in registers: 64 columns a warp instead of 128
+  static constexpr int kEpiWarps = OP == kGmFew ? 4 : OUT == kGmF32 ? 16 : 8;
+  static constexpr int kBWarp = 2 + kEpiWarps, kTailWarp = OP == kGmGrad ? kBWarp + 1 : -1;
+  static constexpr int kThreads = 32 * (kBWarp + 1 + (OP == kGmGrad));
+  static constexpr int kABytes = MA * 128 * 128, kBBytes = kN / CG * 128, kStage = kABytes + kBBytes;
   static constexpr int kList = OP == kGmGrad ? 0 : (kGmGroups + 1) * 8;
-  static constexpr int kFit = (227 * 1024 - kList - 1536) / kStage;
+  // gate and up rows lie on different lanes: u on its way to g's warps, 16 rows of 32
+  // features, twice for each of 4 pairs of warps
+  static constexpr int kSwap = OP == kGmWide && MODE == kGmSwiglu ? 4 * 2 * 16 * 32 * 4 : 0;
+  static constexpr int kOut = OP == kGmGrad ? kEpiWarps * 4096 : 0;  // rows on their way out
+  static constexpr int kFit = (227 * 1024 - kList - kSwap - kOut - 1536) / kStage;
   static constexpr int kStages = kFit < 12 ? kFit : 12;
   static constexpr int kAccCols = MA * kN;       // of one accumulator; two of them
-  static constexpr int kCols = 2 * kAccCols <= 32 ? 32 : 2 * kAccCols <= 64 ? 64 : 2 * kAccCols <= 128 ? 128 : 2 * kAccCols <= 256 ? 256 : 512;
-  static_assert(2 * kAccCols <= 512, "tensor memory has 512 columns");
-  static constexpr int kBars = 2 * kStages + 5;
+  static constexpr int kCols = 2 * kAccCols <= 32 ? 32 : 2 * kAccCols <= 64 ? 64 : 512;
+  static_assert(2 * kAccCols <= kCols, "tensor memory has 512 columns");
+  static constexpr int kBars = 3 * kStages + 5;
   static_assert(8 * kBars + 4 <= 512, "barriers");
-  static constexpr int kSmem = kStages * kStage + 512 + kList + 1024;
+  static constexpr int kSmem = kStages * kStage + kOut + kSwap + 512 + kList + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
 struct GmParams {
-  CUtensorMap a, b;
+  CUtensorMap a, b, b32; // b, b32 (kGmWide): boxes of 128 and of 32 rows
+  CUtensorMap o;         // kGmGrad: the gradient, boxes of 32 rows x 128 bytes
   const int32_t *offsets;
   int n_experts;
   int rows;              // sorted rows
   int n, k;              // features (of y; rows of gW) and summed columns (of x; columns of gW)
   int n_rt, n_ct;        // tiles along n; kGmGrad: along k
-  void *out;
-  int64_t ld, mat;       // distances of rows; kGmGrad: of matrices, in values
-  int wide, codes_wide;  // rows of `out` and blocks of codes on 32-byte boundaries
-  uint8_t *codes, *scales;   // SWIGLU: [rows][2 n], [rows][2 mi_blocks(n)]
+  void *out;             // y; h; kGmSwigluBack: ggu
+  int64_t ld;            // distance of its rows in values
+  uint8_t *codes, *scales;   // kGmSwiglu[Back]: [rows][2 n], [rows][2 mi_blocks(n)]
+  // kGmSwigluBack: row weights by pair, the pair of a row, c h, partial sums of gw [rows][parts]
+  const float *c;
+  const int32_t *order;
+  void *wh;
+  float *part;
+  int parts;
   uint32_t fmt;          // input type in the instruction descriptor
   uint32_t *status;
 };
@@ -171,310 +191,309 @@ template <bool MN> SI_DEV uint32_t gm_desc_lo(uint32_t addr) {
   return (addr >> 4) | ((MN ? kGmPiece >> 4 : 1u) << 16);
 }
 template <bool MN> constexpr uint32_t kGmK16 = (MN ? 16 * 128 : 32) / 16;   // 16 summed indices on
-SI_DEV void gm_mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 da, db;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
-      " setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
-      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kGmDescHi)
-      : "memory");
+template <int CG> SI_DEV void gm_mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 da, db;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+        " setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kGmDescHi)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 da, db;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+        " setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kGmDescHi)
+        : "memory");
+}
+// Arrive on `bar` (of both blocks of a pair) once the MMAs issued so far are complete.
+template <int CG> SI_DEV void gm_commit(uint64_t *bar) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_addr(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    umma_commit(bar);
+}
+template <int CG> SI_DEV void gm_tmem_alloc(uint32_t *dst, uint32_t cols) {   // a whole warp (of each block)
+  if constexpr (CG == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tmem_alloc(dst, cols);
+    tmem_relinquish();
+  }
+}
+template <int CG> SI_DEV void gm_tmem_free(uint32_t addr, uint32_t cols) {
+  if constexpr (CG == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+  else
+    tmem_dealloc(addr, cols);
 }
 
 // ---- epilogues ---------------------------------------------------------------
 
-template <int OUT> SI_DEV uint32_t gm_pack(uint32_t lo, uint32_t hi) {
+template <int OUT> SI_DEV uint32_t gm_pack(float lo, float hi) {
   uint32_t w;
-  if constexpr (OUT == kGmBf16)
-    asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(w) : "f"(__uint_as_float(lo)), "f"(__uint_as_float(hi)));
-  else
-    asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(w) : "f"(__uint_as_float(lo)), "f"(__uint_as_float(hi)));
+  if constexpr (OUT == kGmBf16) asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(w) : "f"(lo), "f"(hi));
+  else asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(w) : "f"(lo), "f"(hi));
   return w;
 }
-// `bytes` (a multiple of 16, at most 4 N) of w to p, 32 at a time where rows allow it.
-template <int N> SI_DEV void gm_store(uint8_t *p, const uint32_t *w, int bytes, bool wide) {
-#pragma unroll
-  for (int i = 0; i < N; i += 8) {
-    if (4 * i >= bytes) break;
-    if (wide && 4 * i + 32 <= bytes) {
-      st_global32(p + 4 * i, w + i);
-    } else {
-      *reinterpret_cast<uint4 *>(p + 4 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-      if (4 * i + 32 <= bytes)
-        *reinterpret_cast<uint4 *>(p + 4 * i + 16) = make_uint4(w[i + 4], w[i + 5], w[i + 6], w[i + 7]);
-    }
-  }
-}
-
-// 128 columns of the accumulator to this lane's row: `cols` of them are inside it.
-template <int OUT, typename Release>
-SI_DEV void gm_write_row(uint8_t *out, int cols, bool wide, bool valid, bool zero, uint32_t acc, Release release) {
-  constexpr int kWords = 8 * kGmSize<OUT>;       // of 32 values
-#pragma unroll
-  for (int c = 0; c < 128; c += 32) {
-    uint32_t r[32], w[kWords];
-    if (zero) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) r[i] = 0;
-    } else {
-      if (c < cols) {
-        tmem_ld32(acc + c, r);
-        tmem_wait_ld();
-      }
-      if (c == 96) release();
-    }
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      if constexpr (OUT == kGmF32) w[i] = r[i];
-      else w[i] = gm_pack<OUT>(r[2 * i], r[2 * i + 1]);
-    }
-    if (valid && c < cols) gm_store<kWords>(out + c * kGmSize<OUT>, w, min(32, cols - c) * kGmSize<OUT>, wide);
-  }
-}
-
-// silu(g) u; g below -87 (|silu(g)| < 2^-119) gives 0: the reciprocal is below the
-// normal range. ex2 and rcp of the hardware, each within 2 units in the last place.
-SI_DEV float gm_silu_mul(float g, float u) {
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-  return g * r * u;
-}
-
-// 32 values to their MXINT8 block: 8 words of codes, the scale.
-SI_DEV uint32_t gm_encode32(const uint32_t *v, uint32_t w[8]) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) top = max(top, v[i] & 0x7FFFFFFFu);
-  const uint32_t s = mi_scale_of(top);
-  const float up = mi_inv_scale(s);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    uint32_t c[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) c[j] = mi_code(__uint_as_float(v[4 * i + j]) * up);
-    w[i] = s == 255u ? 0u : mi_pack4(c[0], c[1], c[2], c[3]);
-  }
-  return s;
-}
-// `bytes` (a multiple of 8, at most 32) of codes.
-SI_DEV void gm_store_codes(uint8_t *p, const uint32_t w[8], int bytes, bool wide) {
-  if (wide && bytes == 32) {
-    st_global32(p, w);
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (8 * i < bytes) *reinterpret_cast<uint2 *>(p + 8 * i) = make_uint2(w[2 * i], w[2 * i + 1]);
-}
-
-// 64 features (from f0) of this lane's row: h, and the blocks of g and u.
-template <int OUT, typename Release>
-SI_DEV void gm_write_swiglu_row(const GmParams &p, int f0, int64_t row, bool valid, bool zero, uint32_t acc_g,
-                                uint32_t acc_u, Release release) {
-  const int64_t blocks = mi_blocks(p.n);
-#pragma unroll
-  for (int c = 0; c < 64; c += 32) {
-    const int f = f0 + c, left = min(32, p.n - f);
-    uint32_t g[32], u[32], w[16];
-    if (left > 0 && !zero) {
-      tmem_ld32(acc_g + c, g);
-      tmem_ld32(acc_u + c, u);
-      tmem_wait_ld();
-    }
-    if (c == 32 && !zero) release();
-    if (left <= 0) continue;
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (zero || i >= left) g[i] = u[i] = 0;    // behind the last feature
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      w[i] = gm_pack<OUT>(__float_as_uint(gm_silu_mul(__uint_as_float(g[2 * i]), __uint_as_float(u[2 * i]))),
-                          __float_as_uint(gm_silu_mul(__uint_as_float(g[2 * i + 1]), __uint_as_float(u[2 * i + 1]))));
-    if (valid) gm_store<16>(static_cast<uint8_t *>(p.out) + (row * p.ld + f) * 2, w, 2 * left, p.wide);
-    if (!p.codes) continue;
-    uint32_t q[8];
-    uint8_t *codes = p.codes + row * 2 * p.n + f, *scales = p.scales + row * 2 * blocks + (f >> 5);
-    const uint32_t sg = gm_encode32(g, q);
-    if (valid) gm_store_codes(codes, q, left, p.codes_wide);
-    const uint32_t su = gm_encode32(u, q);
-    if (valid) {
-      gm_store_codes(codes + p.n, q, left, p.codes_wide);
-      scales[0] = static_cast<uint8_t>(sg);
-      scales[blocks] = static_cast<uint8_t>(su);
-    }
-  }
-}
-
 template <int OUT> SI_DEV void gm_store1(void *out, int64_t at, float v) {
   if constexpr (OUT == kGmBf16) static_cast<__nv_bfloat16 *>(out)[at] = __float2bfloat16_rn(v);
   else if constexpr (OUT == kGmF16) static_cast<__half *>(out)[at] = __float2half_rn(v);
   else static_cast<float *>(out)[at] = v;
 }
-// This lane's feature f of `count` rows from row0, the accumulator's columns.
-template <int OUT, int NT>
-SI_DEV void gm_write_few(const GmParams &p, int f, int64_t row0, int count, bool zero, uint32_t acc) {
-#pragma unroll
-  for (int j0 = 0; j0 < NT; j0 += 16) {
-    if (j0 >= count) break;
-    uint32_t r[16];
-    if (!zero) {
-      tmem_ld16(acc + j0, r);
-      tmem_wait_ld();
-    }
-    if (f < p.n) {
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (j0 + j < count) gm_store1<OUT>(p.out, (row0 + j0 + j) * p.ld + f, zero ? 0.f : __uint_as_float(r[j]));
-    }
-  }
+
+// The logistic function; g below -87 gives 0 where the reciprocal is below the normal
+// range (s < 2^-125). ex2 and rcp of the hardware, each within 2 units in the last place.
+SI_DEV float gm_logistic(float g) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
 }
-// The same of h, g and u: the warp's 32 lanes are one block of every row.
-template <int OUT, int NT>
-SI_DEV void gm_write_swiglu_few(const GmParams &p, int f, int64_t row0, int count, bool zero, uint32_t acc_g,
-                                uint32_t acc_u, int lane) {
-  const int64_t blocks = mi_blocks(p.n);
-  const bool in = f < p.n;
-  if (f - lane >= p.n) return;                   // the whole warp
-#pragma unroll 1
-  for (int j0 = 0; j0 < NT; j0 += 16) {
-    if (j0 >= count) break;
-    uint32_t g[16], u[16];
-    if (!zero) {
-      tmem_ld16(acc_g + j0, g);
-      tmem_ld16(acc_u + j0, u);
-      tmem_wait_ld();
-    }
+// The code of this lane's value of a block that the warp's 32 lanes hold.
+SI_DEV uint32_t gm_encode_lane(float v, uint32_t &s) {
+  s = mi_scale_of(__reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7FFFFFFFu));
+  return s == 255u ? 0u : mi_code(v * mi_inv_scale(s));
+}
+
+// The tokens of a tile, 16 columns of the accumulator at a time, dealt out to the
+// parts of the epilogue: piece i of a part.
+template <int PARTS> SI_DEV int gm_piece(int i, int part) { return (i * PARTS + part) * 16; }
+
+// This lane's feature f of 16 rows from row0, `left` of them in the tile.
+template <int OUT> SI_DEV void gm_write16(const GmParams &p, int f, int64_t row0, int left, const float v[16]) {
+  if (f >= p.n) return;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      if (j0 + j >= count) break;
-      if (zero || !in) g[j] = u[j] = 0;
-      const int64_t row = row0 + j0 + j;
-      if (in) gm_store1<OUT>(p.out, row * p.ld + f, gm_silu_mul(__uint_as_float(g[j]), __uint_as_float(u[j])));
-      if (!p.codes) continue;
-      const uint32_t sg = mi_scale_of(__reduce_max_sync(0xffffffffu, g[j] & 0x7FFFFFFFu));
-      const uint32_t su = mi_scale_of(__reduce_max_sync(0xffffffffu, u[j] & 0x7FFFFFFFu));
-      const uint32_t cg = sg == 255u ? 0u : mi_code(__uint_as_float(g[j]) * mi_inv_scale(sg));
-      const uint32_t cu = su == 255u ? 0u : mi_code(__uint_as_float(u[j]) * mi_inv_scale(su));
-      uint8_t *codes = p.codes + row * 2 * p.n + f, *scales = p.scales + row * 2 * blocks + (f >> 5);
-      if (in) {
-        codes[0] = static_cast<uint8_t>(cg);
-        codes[p.n] = static_cast<uint8_t>(cu);
-      }
-      if (lane == 0) {
-        scales[0] = static_cast<uint8_t>(sg);
-        scales[blocks] = static_cast<uint8_t>(su);
-      }
+  for (int j = 0; j < 16; ++j)
+    if (j < left) gm_store1<OUT>(p.out, (row0 + j) * p.ld + f, v[j]);
+}
+// The 8-bit block of 16 rows at this warp's 32 values (side 0: g, 1: u) from feature f - lane.
+SI_DEV void gm_keep16(const GmParams &p, int f, int lane, int64_t row0, int left, const float v[16], int side) {
+  const int64_t blocks = mi_blocks(p.n);
+  uint8_t *codes = p.codes + row0 * 2 * p.n + side * static_cast<int64_t>(p.n) + f;
+  uint32_t mine = 0;                             // lane j: the scale of row j
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    uint32_t s;
+    const uint32_t c = gm_encode_lane(v[j], s);
+    if (lane == j) mine = s;
+    if (j < left && f < p.n) codes[static_cast<int64_t>(j) * 2 * p.n] = static_cast<uint8_t>(c);
+  }
+  if (lane < 16 && lane < left && f - lane < p.n)
+    p.scales[(row0 + lane) * 2 * blocks + side * blocks + ((f - lane) >> 5)] = static_cast<uint8_t>(mine);
+}
+
+// Sums of 16 values over the warp: value (lane / 2) on even lanes, each lane handing
+// half of its values on at every step.
+SI_DEV float gm_reduce16(float v[16], int lane) {
+#pragma unroll
+  for (int n = 8, m = 16; n > 0; n >>= 1, m >>= 1) {
+    const bool up = (lane & m) != 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, m);
     }
   }
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
+
+// What 16 rows need beside gh: the codes of this lane's g and u, lane j's and 16 + j's
+// scales of row j's, and lane j's weight of row j.
+struct GmKept {
+  uint32_t q[16];        // g in the low byte, u in the next
+  uint32_t s, live;      // live: bit j, row j is a pair's
+  float c;
+};
+SI_DEV GmKept gm_load_kept(const GmParams &p, int f, int lane, int64_t row0, int left) {
+  GmKept k;
+  const int64_t blocks = mi_blocks(p.n);
+  const uint8_t *codes = p.codes + row0 * 2 * p.n + f;
+  const bool in = f < p.n;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    k.q[j] = 0;
+    if (in && j < left) {
+      const uint8_t *c = codes + static_cast<int64_t>(j) * 2 * p.n;
+      k.q[j] = __ldg(c) | (static_cast<uint32_t>(__ldg(c + p.n)) << 8);
+    }
+  }
+  const int j = lane & 15;
+  k.s = 0;
+  k.c = 0.f;
+  bool live = false;
+  if (j < left) {
+    if (f - lane < p.n) k.s = __ldg(p.scales + (row0 + j) * 2 * blocks + (lane >> 4) * blocks + ((f - lane) >> 5));
+    const int64_t pair = p.order ? __ldg(p.order + row0 + j) : row0 + j;
+    live = pair >= 0 && pair < p.rows;
+    if (live) k.c = p.c ? __ldg(p.c + pair) : 1.f;
+  }
+  k.live = __ballot_sync(0xffffffffu, live);
+  return k;
+}
+// The gradients of h = silu(g) u in 16 rows: gh comes from the accumulator.
+template <int OUT>
+SI_DEV void gm_swiglu_back16(const GmParams &p, int f, int lane, int64_t row0, int left, const GmKept &k, float gh[16],
+                             int slot) {
+  const bool in = f < p.n;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const float g = static_cast<float>(static_cast<int8_t>(k.q[j])) * mi_step(__shfl_sync(0xffffffffu, k.s, j));
+    const float u = static_cast<float>(static_cast<int8_t>(k.q[j] >> 8)) * mi_step(__shfl_sync(0xffffffffu, k.s, 16 + j));
+    const float c = __shfl_sync(0xffffffffu, k.c, j), l = gm_logistic(g), si = g * l, h = si * u, cd = c * gh[j];
+    const bool live = (k.live >> j) & 1u;        // a row of no pair: zeros
+    if (in && j < left) {
+      const int64_t at = (row0 + j) * 2 * p.n + f;
+      gm_store1<OUT>(p.out, at, live ? cd * u * (l * fmaf(g, 1.f - l, 1.f)) : 0.f);
+      gm_store1<OUT>(p.out, at + p.n, live ? cd * si : 0.f);
+      if (p.wh) gm_store1<OUT>(p.wh, (row0 + j) * p.n + f, live ? c * h : 0.f);
+    }
+    gh[j] = in && live ? gh[j] * h : 0.f;
+  }
+  const float sum = gm_reduce16(gh, lane);
+  const int j = lane >> 1;
+  if (p.part && !(lane & 1) && j < left) p.part[(row0 + j) * p.parts + slot] = sum;
 }
 
 // ---- the kernel ----------------------------------------------------------------
 
+// Stages that one accumulator takes up. The tensor cores' additions truncate: with
+// fp32 outputs the sums of 512 terms are added up in registers instead, rounded to
+// nearest (1448 terms off by 1.8e-6 relative otherwise, now TODO).
+template <int OUT> constexpr int kGmChunk = OUT == kGmF32 ? 8 : 1 << 30;
+
 // WMN: the matrices lie by columns (features contiguous).
-template <int OP, bool WMN, int NT, bool SWIGLU, int OUT>
-__global__ void __launch_bounds__(GmCfg<OP, NT, SWIGLU>::kThreads, 1)
-    moe_mm_kernel(const __grid_constant__ GmParams p) {
-  using C = GmCfg<OP, NT, SWIGLU>;
-  constexpr int S = C::kStages, M = OP == kGmFew ? NT : 128;
-  constexpr bool kAMn = OP == kGmGrad || (OP == kGmFew && WMN), kBMn = OP == kGmGrad || (OP == kGmTokens && WMN);
-  static_assert(!(SWIGLU && (WMN || OP == kGmGrad || OUT == kGmF32)), "gate and up lie row by row");
+template <int OP, int MODE, bool WMN, int OUT>
+__global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kernel(const __grid_constant__ GmParams p) {
+  using C = GmCfg<OP, MODE, OUT>;
+  constexpr int S = C::kStages, CG = C::CG, M = C::kN, PARTS = C::kEpiWarps / 4, PIECES = C::kN / 16 / PARTS;
+  constexpr bool kAMn = OP == kGmGrad || WMN, kBMn = OP == kGmGrad;
+  static_assert(MODE == kGmPlain || (OP != kGmGrad && OUT != kGmF32 && !(MODE == kGmSwiglu && WMN)), "forms");
   extern __shared__ uint8_t gm_smem[];
   uint8_t *base = gm_smem + ((1024u - (smem_addr(gm_smem) & 1023u)) & 1023u);
-  uint64_t *full = reinterpret_cast<uint64_t *>(base + S * C::kStage);
+  uint8_t *outs = base + S * C::kStage;
+  float *swap = reinterpret_cast<float *>(outs + C::kOut);
+  uint64_t *full = reinterpret_cast<uint64_t *>(outs + C::kOut + C::kSwap);
   uint64_t *empty = full + S, *acc_full = empty + S, *acc_empty = acc_full + 2, *drain = acc_empty + 2;
-  uint32_t *s_taddr = reinterpret_cast<uint32_t *>(drain + 1);
-  GmList &list = *reinterpret_cast<GmList *>(base + S * C::kStage + 512);
+  uint64_t *tail = drain + 1;                    // by stage
+  uint32_t *s_taddr = reinterpret_cast<uint32_t *>(tail + S);
+  GmList &list = *reinterpret_cast<GmList *>(outs + C::kOut + C::kSwap + 512);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(full + i, 2);
+      mbar_init(full + i, 2 * CG);       // of the first block: both producers of both
       mbar_init(empty + i, 1);
+      mbar_init(tail + i, 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full + i, 1);
-      mbar_init(acc_empty + i, C::kEpiWarps);
+      mbar_init(acc_empty + i, C::kEpiWarps * CG);   // of the first block
     }
     mbar_init(drain, 1);
     fence_mbar_init();
   }
   grid_dep_wait();
-  if (warp == 1) {
-    // before the next kernel may start: its blocks take tensor memory too
-    tmem_alloc(s_taddr, C::kCols);
-    tmem_relinquish();
-  }
+  // before the next kernel may start: its blocks take tensor memory too
+  if (warp == 1) gm_tmem_alloc<CG>(s_taddr, C::kCols);
   tc_fence_before();
   if constexpr (OP != kGmGrad) gm_list<M>(p, list);
-  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  else __syncthreads();
   tc_fence_after();
   grid_dep_launch();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *s_taddr, 0);
   const int total = OP == kGmGrad ? p.n_experts * p.n_rt * p.n_ct : list.tile[p.n_experts + 2];
-  const int step = gridDim.x;
+  const int first = blockIdx.x / CG, step = gridDim.x / CG;
   auto tile = [&](int w) {
     if constexpr (OP == kGmGrad) return gm_tile_grad(p, w);
     else return gm_tile<M>(p, list, w);
   };
+  // a tile's columns of the accumulator: its rows, to the next 32 (16 in one SM)
+  auto columns = [&](const GmTile &t) { return OP == kGmGrad ? 256 : (t.count + 16 * CG - 1) & -(16 * CG); };
+  // rows of the expert in the last stage if they need clearing behind them, else 0
+  auto tail_rows = [&](const GmTile &t, int ks, int nk) {
+    return OP == kGmGrad && ks == nk - 1 && (t.count & 15) ? t.count - ks * kGmK : 0;
+  };
+  const uint32_t full0 = CG == 2 ? cluster_addr(smem_addr(full), 0) : smem_addr(full);
 
-  if (warp == 0 || warp == 2 + C::kEpiWarps) {
+  if (warp == 0 || warp == C::kBWarp) {
     if (lane == 0) {
       uint32_t it = 0;
       bool ok = true;
-      for (int w = blockIdx.x; ok && w < total; w += step) {
+      for (int w = first; ok && w < total; w += step) {
         const GmTile t = tile(w);
-        const int nk = gm_steps<OP>(p, t);
+        const int nk = gm_steps<OP>(p, t), half = columns(t) / CG;
         for (int ks = 0; ks < nk; ++ks, ++it) {
           const int s = it % S;
           if (!mbar_wait_bounded(empty + s, ((it / S) & 1) ^ 1, p.status)) {
             ok = false;
             break;
           }
-          uint8_t *st = base + s * C::kStage;
+          uint8_t *st = base + s * C::kStage + (warp == 0 ? 0 : C::kABytes);
           const int c = ks * kGmK;
+          // this block's copies count at the pair's barrier of the stage, or at its own where
+          // it clears rows first
+          const bool cut = tail_rows(t, ks, nk) != 0;
+          const uint32_t bar = cut ? smem_addr(tail + s) : full0 + s * 8;
+          auto expect = [&](uint32_t bytes) {
+            if (CG == 2 && !cut) mbar_expect_tx_cluster(bar, bytes);
+            else mbar_arrive_expect_tx(cut ? tail + s : full + s, bytes);
+          };
+          auto load = [&](int to, const CUtensorMap *m, int c0, int c1, int c2) {
+            if constexpr (CG == 2) tma_load3_pair(st + to, m, c0, c1, c2, bar);
+            else tma_load3(st + to, m, c0, c1, c2, full + s);
+          };
           if (warp == 0) {
-            mbar_arrive_expect_tx(full + s, C::kABytes);
-            if constexpr (OP == kGmTokens) {
-              tma_load3(st, &p.a, c, t.row0, 0, full + s);
-            } else if constexpr (OP == kGmGrad) {
+            expect(C::kABytes);
+            if constexpr (OP == kGmGrad) {
 #pragma unroll
-              for (int i = 0; i < 2; ++i)
-                tma_load3(st + i * kGmPiece, &p.a, t.rt * 128 + i * 64, t.row0 + c, 0, full + s);
+              for (int i = 0; i < 2; ++i) load(i * kGmPiece, &p.a, t.rt * 256 + rank * 128 + i * 64, t.row0 + c, 0);
+            } else if constexpr (MODE == kGmSwiglu && OP == kGmWide) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) load(i * kGmPiece, &p.a, c, t.rt * 128 + rank * 64 + i * p.n, t.e);
+            } else if constexpr (MODE == kGmSwiglu) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) load(i * 128 * 128, &p.a, c, t.rt * 128 + i * p.n, t.e);
             } else if constexpr (WMN) {
 #pragma unroll
-              for (int i = 0; i < 2; ++i)
-                tma_load3(st + i * kGmPiece, &p.a, t.rt * 128 + i * 64, c, t.e, full + s);
+              for (int i = 0; i < 2; ++i) load(i * kGmPiece, &p.a, (t.rt * CG + rank) * 128 + i * 64, c, t.e);
             } else {
-#pragma unroll
-              for (int i = 0; i < C::MA; ++i)
-                tma_load3(st + i * 128 * 128, &p.a, c, t.rt * 128 + i * p.n, t.e, full + s);
+              load(0, &p.a, c, (t.rt * CG + rank) * 128, t.e);
             }
           } else {
-            st += C::kABytes;
-            mbar_arrive_expect_tx(full + s, C::kBBytes);
-            if constexpr (OP == kGmFew) {
-              tma_load3(st, &p.b, c, t.row0, 0, full + s);
-            } else if constexpr (OP == kGmGrad) {
+            if constexpr (OP == kGmGrad) {
+              expect(C::kBBytes);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                tma_load3(st + i * kGmPiece, &p.b, t.ct * 256 + i * 64, t.row0 + c, 0, full + s);
-            } else if constexpr (WMN) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                tma_load3(st + i * kGmPiece, &p.b, t.rt * 256 + i * 64, c, t.e, full + s);
-            } else if constexpr (SWIGLU) {
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-                tma_load3(st + i * 128 * 128, &p.b, c, t.rt * 128 + i * p.n, t.e, full + s);
+              for (int i = 0; i < 2; ++i) load(i * kGmPiece, &p.b, t.ct * 256 + rank * 128 + i * 64, t.row0 + c, 0);
+            } else if (OP == kGmFew || half > 96) {
+              expect(C::kBBytes);
+              load(0, &p.b, c, t.row0 + rank * half, 0);
             } else {
-              tma_load3(st, &p.b, c, t.rt * 256, t.e, full + s);
+              const int n = (half + 31) >> 5;
+              expect(n * 32 * 128);
+              for (int i = 0; i < n; ++i) load(i * 32 * 128, &p.b32, c, t.row0 + rank * half + i * 32, 0);
             }
           }
         }
       }
       if (!ok) {   // copies in flight land before the block's memory goes
-        const uint32_t n = it < static_cast<uint32_t>(S) ? it : S;
-        for (uint32_t i = it - n; i < it; ++i) mbar_wait_bounded(full + i % S, (i / S) & 1, p.status);
+        if constexpr (CG == 1) {
+          const uint32_t n = it < static_cast<uint32_t>(S) ? it : S;
+          for (uint32_t i = it - n; i < it; ++i) mbar_wait_bounded(full + i % S, (i / S) & 1, p.status);
+        } else {   // their barrier may be the other block's: 10 ms are a thousand times their way
+          const uint64_t t0 = now_ns();
+          while (now_ns() - t0 < 10000000u) {
+          }
+        }
       }
     }
   } else if (warp == 1) {
@@ -485,144 +504,377 @@ __global__ void __launch_bounds__(GmCfg<OP, NT, SWIGLU>::kThreads, 1)
     int s = 0;                       // stage and its parity
     uint32_t parity = 0;
     bool ok = true;
-    for (int w = blockIdx.x; w < total; w += step) {
+    for (int w = rank == 0 ? first : total; w < total; w += step) {
       const GmTile t = tile(w);
       const int nk = gm_steps<OP>(p, t);
-      if (nk == 0) continue;         // zeros: no accumulator
-      const uint32_t u = n & 1, d = tmem + u * C::kAccCols;
-      if (leader && ok) ok = mbar_wait_bounded(acc_empty + u, ((n >> 1) & 1) ^ 1, p.status);
-      const int cols = OP == kGmFew ? (t.count + 15) & ~15 : 256;
       const uint32_t idesc = (1u << 4) | p.fmt | (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u) |
-                             (static_cast<uint32_t>(cols >> 3) << 17) | ((128u >> 4) << 24);
+                             (static_cast<uint32_t>(columns(t) >> 3) << 17) | ((CG * 128u >> 4) << 24);
       const int last = OP == kGmGrad ? t.count : p.k;   // summed indices
-      for (int ks = 0; ks < nk; ++ks) {
-        const int left = min(kGmK, last - ks * kGmK), n16 = (left + 15) >> 4;
-        const uint32_t st = smem0 + s * C::kStage;
-        if constexpr (OP == kGmGrad) {
-          if (left & 15) {           // the rows behind the expert's in the last 16: cleared
-            ok = __all_sync(0xffffffffu, ok || !leader) != 0;
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(full + s, parity, p.status)) != 0;
-            uint8_t *q = base + s * C::kStage;
-            for (int r = left; ok && r < n16 * 16; ++r)
-              for (int i = lane; i < C::kStage / kGmPiece * 8; i += 32)
-                *reinterpret_cast<uint4 *>(q + (i >> 3) * kGmPiece + r * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-            fence_async_smem();
-            __syncwarp();
+      for (int k0 = 0; k0 < nk; k0 += kGmChunk<OUT>, ++n) {
+        const uint32_t u = n & 1, d = tmem + u * C::kAccCols;
+        if (leader && ok) ok = mbar_wait_bounded(acc_empty + u, ((n >> 1) & 1) ^ 1, p.status);
+        const int k1 = min(nk, kGmChunk<OUT> < nk ? k0 + kGmChunk<OUT> : nk);
+        for (int ks = k0; ks < k1; ++ks) {
+          const int n16 = (min(kGmK, last - ks * kGmK) + 15) >> 4;
+          const uint32_t st = smem0 + s * C::kStage;
+          if (leader && ok)
+            ok = CG == 2 ? mbar_wait_cluster(full + s, parity, p.status) : mbar_wait_bounded(full + s, parity, p.status);
+          if (leader && ok) {
+            tc_fence_after();
+            const uint32_t la = gm_desc_lo<kAMn>(st), lb = gm_desc_lo<kBMn>(st + C::kABytes);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (i >= n16) break;
+#pragma unroll
+              for (int a = 0; a < C::MA; ++a)
+                gm_mma<CG>(d + a * C::kN, la + a * (128 * 128 / 16) + i * kGmK16<kAMn>, lb + i * kGmK16<kBMn>, idesc,
+                           i > 0 || ks > k0);
+            }
+            gm_commit<CG>(empty + s);
+          }
+          if (++s == S) {
+            s = 0;
+            parity ^= 1;
           }
         }
-        if (leader && ok) ok = mbar_wait_bounded(full + s, parity, p.status);
-        if (leader && ok) {
-          tc_fence_after();
-          const uint32_t la = gm_desc_lo<kAMn>(st), lb = gm_desc_lo<kBMn>(st + C::kABytes);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (i >= n16) break;
-#pragma unroll
-            for (int a = 0; a < C::MA; ++a)
-              gm_mma(d + a * C::kN, la + a * (128 * 128 / 16) + i * kGmK16<kAMn>, lb + i * kGmK16<kBMn>, idesc,
-                     i > 0 || ks > 0);
-          }
-          umma_commit(empty + s);
-        }
-        if (++s == S) {
-          s = 0;
-          parity ^= 1;
-        }
+        if (leader && ok) gm_commit<CG>(acc_full + u);
       }
-      if (leader && ok) umma_commit(acc_full + u);
-      ++n;
     }
     if (leader && !ok) {   // MMAs in flight end before the tensor memory goes
-      umma_commit(drain);
+      gm_commit<CG>(drain);
       mbar_wait_bounded(drain, 0, p.status);
     }
     __syncwarp();
+  } else if (warp == C::kTailWarp) {
+    // rows behind the expert's in the last 16 of its sums: cleared, in both operands
+    uint32_t it = 0, cuts = 0;       // cuts: the parity of each stage's barrier
+    for (int w = first; w < total; w += step) {
+      const GmTile t = tile(w);
+      const int nk = gm_steps<OP>(p, t);
+      it += nk;
+      const int left = nk > 0 ? tail_rows(t, nk - 1, nk) : 0;
+      if (left == 0) continue;
+      const int s = (it - 1) % S;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(tail + s, (cuts >> s) & 1, p.status))) break;
+      cuts ^= 1u << s;
+      uint8_t *q = base + s * C::kStage;
+      for (int r = left; r < ((left + 15) & ~15); ++r)
+        *reinterpret_cast<uint4 *>(q + (lane >> 3) * kGmPiece + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(full0 + s * 8, 2);
+    }
   } else {
     const int q = warp & 3, part = (warp - 2) >> 2;   // the 32 lanes of tensor memory this warp may read
     const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const uint32_t free0 = CG == 2 ? cluster_addr(smem_addr(acc_empty), 0) : smem_addr(acc_empty);
     uint32_t n = 0;
-    for (int w = blockIdx.x; w < total; w += step) {
+    bool ok = true;
+    auto wait_acc = [&] {            // its address; n goes on with release()
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_full + (n & 1), (n >> 1) & 1, p.status));
+      tc_fence_after();
+      return lanes + (n & 1) * C::kAccCols;
+    };
+    auto release = [&] {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CG == 2) mbar_arrive_cluster_relaxed(free0 + (n & 1) * 8);   // what was read is in registers
+        else mbar_arrive(acc_empty + (n & 1));
+      }
+      ++n;
+    };
+    // after a wait that ran out nothing is waited for any more: zeros, so that warps that
+    // meet at a barrier all come there
+    for (int w = first; w < total; w += step) {
       const GmTile t = tile(w);
-      const bool zero = gm_steps<OP>(p, t) == 0;
-      uint32_t acc = 0;
-      if (!zero) {
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(acc_full + (n & 1), (n >> 1) & 1, p.status))) break;
-        tc_fence_after();
-        acc = lanes + (n & 1) * C::kAccCols;
-      }
-      auto release = [&] {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(acc_empty + (n & 1));
-      };
-      if constexpr (OP == kGmFew) {
-        const int f = t.rt * 128 + q * 32 + lane;
-        if constexpr (SWIGLU) gm_write_swiglu_few<OUT, NT>(p, f, t.row0, t.count, zero, acc, acc + NT, lane);
-        else gm_write_few<OUT, NT>(p, f, t.row0, t.count, zero, acc);
-        if (!zero) release();
-      } else if constexpr (SWIGLU) {
-        const int j = q * 32 + lane;
-        gm_write_swiglu_row<OUT>(p, t.rt * 128 + part * 64, static_cast<int64_t>(t.row0) + j, j < t.count, zero,
-                                 acc + part * 64, acc + 128 + part * 64, release);
-      } else {
-        const int j = q * 32 + lane;
-        int64_t row;
-        int col, cols;
-        bool valid;
-        if constexpr (OP == kGmGrad) {
-          row = t.rt * 128 + j;
-          valid = row < p.n;
-          col = t.ct * 256 + part * 128;
-          cols = p.k - col;
-        } else {
-          row = static_cast<int64_t>(t.row0) + j;
-          valid = j < t.count;
-          col = t.rt * 256 + part * 128;
-          cols = p.n - col;
+      const int nk = ok ? gm_steps<OP>(p, t) : 0;
+      bool zero = nk == 0;
+      if constexpr (OP == kGmGrad) {
+        // lane = row of the gradient; a part's columns, 128 bytes of them at a time through shared memory
+        constexpr int kPer = OUT == kGmF32 ? 32 : 64, kMine = 256 / PARTS;   // columns of a box, of a part
+        uint8_t *stage = outs + (warp - 2) * 4096;
+        const int row = t.rt * 256 + rank * 128 + q * 32, col = t.ct * 256 + part * kMine;
+        float sum[OUT == kGmF32 ? kMine : 1] = {};
+        uint32_t acc = 0;
+        if constexpr (OUT == kGmF32) {
+          for (int k0 = 0; ok && k0 < nk; k0 += kGmChunk<OUT>) {
+            acc = wait_acc();
+            if (!ok) break;
+#pragma unroll
+            for (int c = 0; c < kMine; c += 8) {
+              float r[8];
+              tmem_ld8(acc + part * kMine + c, r);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) sum[c + i] += r[i];
+            }
+            release();
+          }
+        } else if (!zero) {
+          acc = wait_acc();
         }
-        uint8_t *out = static_cast<uint8_t *>(p.out) +
-                       ((OP == kGmGrad ? t.e * p.mat : 0) + row * p.ld + col) * kGmSize<OUT>;
-        gm_write_row<OUT>(out, min(cols, 128), p.wide, valid, zero, acc + part * 128, release);
+        zero |= !ok;
+#pragma unroll
+        for (int c = 0; c < kMine; c += kPer) {
+          uint32_t v[32];            // 128 bytes of the row
+          if (OUT != kGmF32 && zero) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0;
+          } else if constexpr (OUT == kGmF32) {   // zeros where there was nothing to add
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(sum[c + i]);
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t r[32];
+              tmem_ld32(acc + part * kMine + c + 32 * h, r);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[16 * h + i] = gm_pack<OUT>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+            }
+            if (c + kPer == kMine) release();
+          }
+          if (lane == 0) tma_store_wait_read();        // the box before has been read
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4 *>(stage + lane * 128 + ((i ^ (lane & 7)) * 16)) =
+                make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0 && row < p.n && col + c < p.k) tma_store3(&p.o, stage, col + c, row, t.e);
+        }
+      } else {
+        // lane = feature; 16 rows at a time
+        const int tf = MODE == kGmSwiglu && OP == kGmWide ? t.rt * 128 + rank * 64 + (q & 1) * 32
+                                                          : (t.rt * CG + rank) * 128 + q * 32;
+        const int f = tf + lane;
+        auto read16 = [&](uint32_t addr, float v[16]) {
+          uint32_t r[16];
+          tmem_ld16(addr, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
+        };
+        auto zeros = [&](float v[16]) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = 0.f;
+        };
+        // the last piece of this part, behind which the accumulator is free
+        const int mine = t.count > part * 16 ? (t.count - part * 16 + 16 * PARTS - 1) / (16 * PARTS) : 0;
+        uint32_t acc = 0;
+        if constexpr (OUT == kGmF32) {
+          float sum[PIECES][16] = {};
+          for (int k0 = 0; ok && k0 < nk; k0 += kGmChunk<OUT>) {
+            acc = wait_acc();
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) {
+              if (i >= mine) break;
+#pragma unroll
+              for (int h = 0; h < 16; h += 8) {
+                float r[8];
+                tmem_ld8(acc + gm_piece<PARTS>(i, part) + h, r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[i][h + j] += r[j];
+              }
+            }
+            release();
+          }
+#pragma unroll
+          for (int i = 0; i < PIECES; ++i) {
+            if (i >= mine) break;
+            const int j0 = gm_piece<PARTS>(i, part);
+            gm_write16<OUT>(p, f, static_cast<int64_t>(t.row0) + j0, t.count - j0, sum[i]);
+          }
+        } else {
+          if constexpr (MODE != kGmSwigluBack) {
+            if (!zero) acc = wait_acc();
+            zero |= !ok;
+            if (!zero && mine == 0) release();
+          }
+          bool have = MODE != kGmSwigluBack;     // the accumulator has been waited for
+          for (int i = 0; i < mine; ++i) {
+            const int j0 = gm_piece<PARTS>(i, part), left = t.count - j0;
+            const int64_t row0 = static_cast<int64_t>(t.row0) + j0;
+            float v[16];
+            if constexpr (MODE == kGmPlain) {
+              if (zero) zeros(v);
+              else read16(acc + j0, v);
+              if (!zero && i == mine - 1) release();
+              gm_write16<OUT>(p, f, row0, left, v);
+            } else if constexpr (MODE == kGmSwigluBack) {
+              const GmKept kept = gm_load_kept(p, f, lane, row0, zero ? 0 : left);
+              if (!zero && !have) {
+                acc = wait_acc();
+                zero = !ok;
+                have = true;
+              }
+              if (zero) zeros(v);
+              else read16(acc + j0, v);
+              if (!zero && i == mine - 1) release();
+              gm_swiglu_back16<OUT>(p, f, lane, row0, left, kept, v, (t.rt * CG + rank) * 4 + q);
+            } else if constexpr (OP == kGmFew) {
+              float u[16];
+              if (zero) {
+                zeros(v);
+                zeros(u);
+              } else {
+                read16(acc + j0, v);
+                read16(acc + C::kN + j0, u);
+                if (i == mine - 1) release();
+              }
+              if (f >= p.n) {        // behind the last feature: the next rows of the matrix
+                zeros(v);
+                zeros(u);
+              }
+              if (tf < p.n && p.codes) {
+                gm_keep16(p, f, lane, row0, left, v, 0);
+                gm_keep16(p, f, lane, row0, left, u, 1);
+              }
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[j] = v[j] * gm_logistic(v[j]) * u[j];
+              gm_write16<OUT>(p, f, row0, left, v);
+            } else {
+              // lanes 0-63 hold g, 64-127 u: u goes to g's warps through shared memory
+              const int side = q >> 1;
+              float *box = swap + ((part * 2 + (q & 1)) * 2 + (i & 1)) * 512;
+              const int pair = 1 + part * 2 + (q & 1);
+              if (zero) zeros(v);
+              else read16(acc + j0, v);
+              if (!zero && i == mine - 1) release();
+              if (f >= p.n) zeros(v);
+              if (side == 1) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) box[j * 32 + lane] = v[j];
+              }
+              asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+              if (tf < p.n && p.codes) gm_keep16(p, f, lane, row0, left, v, side);
+              if (side == 0) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = v[j] * gm_logistic(v[j]) * box[j * 32 + lane];
+                gm_write16<OUT>(p, f, row0, left, v);
+              }
+            }
+          }
+          if constexpr (MODE == kGmSwigluBack) {
+            if (!zero && !have) {                // no rows of this part
+              wait_acc();
+              if (ok) release();
+            }
+          }
+        }
       }
-      if (!zero) ++n;
     }
+    if (OP == kGmGrad && lane == 0) tma_store_wait_read();
   }
+  __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();         // the other block's MMAs and arrivals are over too
+  else __syncthreads();
   tc_fence_after();
   if (warp == 1) {
     __syncwarp();
-    tmem_dealloc(tmem, C::kCols);
+    gm_tmem_free<CG>(tmem, C::kCols);
   }
+}
+
+// gw of a row's pair: the sum of its partial sums, in their order.
+__global__ void __launch_bounds__(256) gm_sum_kernel(const float *part, int n, int rows, const int32_t *order, float *gw) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int row = blockIdx.x * 256 + threadIdx.x;
+  if (row >= rows) return;
+  const int64_t pair = order ? __ldg(order + row) : row;
+  if (pair < 0 || pair >= rows) return;
+  float sum = 0.f;
+  for (int i = 0; i < n; i += 4) {               // n is a multiple of 4
+    const float4 v = __ldcg(reinterpret_cast<const float4 *>(part + static_cast<int64_t>(row) * n + i));
+    sum += v.x;
+    sum += v.y;
+    sum += v.z;
+    sum += v.w;
+  }
+  gw[pair] = sum;
 }
 
 // ---- host ------------------------------------------------------------------
 
-// 16-bit values [mats][rows][cols], boxes of box_rows rows x 64 values in the 128-byte
-// swizzle; what lies outside reads as zero.
-static bool gm_map(CUtensorMap *m, const void *v, bool bf16, int64_t mats, int64_t rows, int64_t cols, int64_t ld,
+// Values [mats][rows][cols] of 2 or 4 bytes, boxes of box_rows rows x 128 bytes in the
+// 128-byte swizzle; what lies outside reads as zero and is not written.
+static bool gm_map(CUtensorMap *m, const void *v, si_dtype type, int64_t mats, int64_t rows, int64_t cols, int64_t ld,
                    int64_t mat, int box_rows) {
+  const int size = type == SI_F32 ? 4 : 2;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                               static_cast<cuuint64_t>(mats)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * 2), static_cast<cuuint64_t>(mats > 1 ? mat * 2 : ld * 2)};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
-  return encode_map(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, v, 3, dims, strides,
-                    box);
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * size),
+                                 static_cast<cuuint64_t>((mats > 1 ? mat : ld) * size)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / size), static_cast<cuuint32_t>(box_rows), 1};
+  return encode_map(m, type == SI_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                       : type == SI_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                    v, 3, dims, strides, box);
 }
 
-template <int OP, bool WMN, int NT, bool SWIGLU, int OUT>
-static cudaError_t gm_launch(const GmParams &p, int64_t most, cudaStream_t s) {
-  using C = GmCfg<OP, NT, SWIGLU>;
-  const cudaError_t e = allow_smem(moe_mm_kernel<OP, WMN, NT, SWIGLU, OUT>, C::kSmem);
+// Pairs of blocks that are resident at once, on the current device: fewer than half of
+// the SMs where a part of the chip has an odd number of them.
+template <typename C, typename K> static cudaError_t gm_pairs(K kernel, int *pairs) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(most, sm_count()));
-  return launch_pdl(moe_mm_kernel<OP, WMN, NT, SWIGLU, OUT>, dim3(grid), dim3(C::kThreads), C::kSmem, s, p);
+  if (dev < 64 && (*pairs = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(sm_count() & ~1));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaOccupancyMaxActiveClusters(pairs, kernel, &cfg);
+  if (e == cudaSuccess && *pairs < 1) e = cudaErrorInvalidConfiguration;
+  if (e == cudaSuccess && dev < 64) known[dev].store(*pairs, std::memory_order_relaxed);
+  return e;
+}
+
+template <int OP, int MODE, bool WMN, int OUT>
+static cudaError_t gm_launch(const GmParams &p, int64_t most, cudaStream_t s) {
+  using C = GmCfg<OP, MODE, OUT>;
+  const auto kernel = moe_mm_kernel<OP, MODE, WMN, OUT>;
+  cudaError_t e = allow_smem(kernel, C::kSmem);
+  if (e != cudaSuccess) return e;
+  int units = sm_count();
+  if (C::CG == 2) {
+    e = gm_pairs<C>(kernel, &units);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(most, units)) * C::CG);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = C::CG;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = C::CG == 2 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 template <typename F> static cudaError_t gm_by_out(si_dtype t, F f) {
   using std::integral_constant;
   return t == SI_BF16  ? f(integral_constant<int, kGmBf16>{})
          : t == SI_F16 ? f(integral_constant<int, kGmF16>{})
                        : f(integral_constant<int, kGmF32>{});
+}
+template <typename F> static cudaError_t gm_by_half(si_dtype t, F f) {
+  using std::integral_constant;
+  return t == SI_BF16 ? f(integral_constant<int, kGmBf16>{}) : f(integral_constant<int, kGmF16>{});
 }
 
 static bool gm_type(si_dtype t) { return t == SI_BF16 || t == SI_F16; }
@@ -635,17 +887,30 @@ static bool gm_rows(int64_t rows, int n_experts) {
 static bool gm_ld(int64_t ld, int64_t cols, int size) {
   return ld >= cols && ld * size % 16 == 0 && ld <= (int64_t(1) << 36);
 }
-static bool gm_wide(const void *p, int64_t ld, int size) {
-  return ld * size % 32 == 0 && (reinterpret_cast<uintptr_t>(p) & 31u) == 0;
-}
+static bool gm_whole(const void *p, int size) { return p && reinterpret_cast<uintptr_t>(p) % size == 0; }
 
-// Rows of an expert on average up to which its features go on the lanes.
+// Rows of an expert on average up to which a tile is one SM's, with 16 rows.
 static bool gm_few(int64_t rows, int n_experts) { return rows <= 16 * static_cast<int64_t>(n_experts); }
 
-// Tiles of the sorted rows in M rows each, at most: 0 if they pass 2^30.
-static int64_t gm_tiles(int64_t rows, int n_experts, int m, int64_t n_rt) {
-  const int64_t t = (rows / m + std::min<int64_t>(n_experts + 2, rows)) * n_rt;
-  return t <= (int64_t(1) << 30) ? t : 0;
+// What the products of sorted rows share: the rows' operand and the list. `tile`: features
+// of a tile. Returns the number of tiles at most, 0 if they pass 2^30, -1 without a map.
+static int64_t gm_forward(GmParams &p, bool few, const void *x, si_dtype type, int64_t rows, int64_t k, int64_t ldx,
+                          int n_experts, int64_t n, int tile, const int32_t *offsets, void *workspace) {
+  p.n_rt = static_cast<int>((n + tile - 1) / tile);
+  const int m = few ? 16 : 256;
+  const int64_t most = (rows / m + std::min<int64_t>(n_experts + 2, rows)) * p.n_rt;
+  if (most > (int64_t(1) << 30)) return 0;
+  if (!gm_map(&p.b, x, type, 1, rows, k, ldx, 0, few ? 16 : 128) ||
+      (!few && !gm_map(&p.b32, x, type, 1, rows, k, ldx, 0, 32)))
+    return -1;
+  p.offsets = offsets;
+  p.n_experts = n_experts;
+  p.rows = static_cast<int>(rows);
+  p.n = static_cast<int>(n);
+  p.k = static_cast<int>(k);
+  p.fmt = gm_fmt(type);
+  p.status = static_cast<uint32_t *>(workspace);
+  return most;
 }
 
 }  // namespace si
@@ -660,39 +925,26 @@ extern "C" si_status si_moe_matmul(const void *x, si_dtype type, int64_t rows, i
                                    size_t workspace_bytes, void *stream) {
   if (!gm_rows(rows, n_experts) || !gm_width(n) || !gm_width(k)) return SI_ERR_INVALID_ARG;
   if (!gm_type(type) || (out_type != SI_F32 && out_type != type)) return SI_ERR_UNSUPPORTED;
-  const int size = out_type == SI_F32 ? 4 : 2;
   if (rows == 0) return SI_OK;
-  if (!x || !w || !offsets || !out || !aligned16(x) || !aligned16(w) || !aligned16(out) ||
-      (reinterpret_cast<uintptr_t>(offsets) & 3u) || !gm_ld(ldx, k, 2) || !gm_ld(ldo, n, size) ||
-      !gm_ld(ldw, by_columns ? n : k, 2) || (n_experts > 1 && !gm_ld(matw, ldw * (by_columns ? k : n) - (ldw - (by_columns ? n : k)), 2)))
+  const bool few = gm_few(rows, n_experts), cols = by_columns != 0;
+  const int64_t inner = cols ? n : k, outer = cols ? k : n;
+  if (!x || !w || !offsets || !out || !aligned16(x) || !aligned16(w) || !aligned16(out) || !gm_whole(offsets, 4) ||
+      !gm_ld(ldx, k, 2) || !gm_ld(ldo, n, out_type == SI_F32 ? 4 : 2) || !gm_ld(ldw, inner, 2) ||
+      (n_experts > 1 && !gm_ld(matw, ldw * (outer - 1) + inner, 2)))
     return SI_ERR_INVALID_ARG;
   if (workspace && (!aligned256(workspace) || workspace_bytes < sizeof(WsHeader))) return SI_ERR_WORKSPACE;
-  const bool few = gm_few(rows, n_experts), cols = by_columns != 0, bf16 = type == SI_BF16;
   GmParams p{};
-  p.n_rt = static_cast<int>(few ? (n + 127) / 128 : (n + 255) / 256);
-  const int64_t most = gm_tiles(rows, n_experts, few ? 16 : 128, p.n_rt);
-  if (!most) return SI_ERR_UNSUPPORTED;
-  CUtensorMap &mx = few ? p.b : p.a, &mw = few ? p.a : p.b;
-  if (!gm_map(&mx, x, bf16, 1, rows, k, ldx, 0, few ? 16 : 128) ||
-      !gm_map(&mw, w, bf16, n_experts, cols ? k : n, cols ? n : k, ldw, matw, cols ? 64 : few ? 128 : 256))
-    return SI_ERR_CUDA;
-  p.offsets = offsets;
-  p.n_experts = n_experts;
-  p.rows = static_cast<int>(rows);
-  p.n = static_cast<int>(n);
-  p.k = static_cast<int>(k);
+  const int64_t most = gm_forward(p, few, x, type, rows, k, ldx, n_experts, n, few ? 128 : 256, offsets, workspace);
+  if (most == 0) return SI_ERR_UNSUPPORTED;
+  if (most < 0 || !gm_map(&p.a, w, type, n_experts, outer, inner, ldw, matw, cols ? 64 : 128)) return SI_ERR_CUDA;
   p.out = out;
   p.ld = ldo;
-  p.wide = gm_wide(out, ldo, size);
-  p.fmt = gm_fmt(type);
-  p.status = static_cast<uint32_t *>(workspace);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   return cuda_status(gm_by_out(out_type, [&](auto o) {
     constexpr int O = decltype(o)::value;
     if (few)
-      return cols ? gm_launch<kGmFew, true, 16, false, O>(p, most, s) : gm_launch<kGmFew, false, 16, false, O>(p, most, s);
-    return cols ? gm_launch<kGmTokens, true, 0, false, O>(p, most, s)
-                : gm_launch<kGmTokens, false, 0, false, O>(p, most, s);
+      return cols ? gm_launch<kGmFew, kGmPlain, true, O>(p, most, s) : gm_launch<kGmFew, kGmPlain, false, O>(p, most, s);
+    return cols ? gm_launch<kGmWide, kGmPlain, true, O>(p, most, s) : gm_launch<kGmWide, kGmPlain, false, O>(p, most, s);
   }));
 }
 
@@ -704,33 +956,28 @@ extern "C" si_status si_moe_matmul_grad_w(const void *gy, int64_t ldg, const voi
   if (!gm_type(type) || (gw_type != SI_F32 && gw_type != type)) return SI_ERR_UNSUPPORTED;
   const int size = gw_type == SI_F32 ? 4 : 2;
   if (!gw || !aligned16(gw)) return SI_ERR_INVALID_ARG;
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (rows == 0) return cuda_status(cudaMemsetAsync(gw, 0, static_cast<size_t>(n_experts) * n * k * size, s));
-  if (!gy || !x || !offsets || !aligned16(gy) || !aligned16(x) || (reinterpret_cast<uintptr_t>(offsets) & 3u) ||
-      !gm_ld(ldg, n, 2) || !gm_ld(ldx, k, 2))
-    return SI_ERR_INVALID_ARG;
-  if (workspace && (!aligned256(workspace) || workspace_bytes < sizeof(WsHeader))) return SI_ERR_WORKSPACE;
   GmParams p{};
-  p.n_rt = static_cast<int>((n + 127) / 128);
+  p.n_rt = static_cast<int>((n + 255) / 256);
   p.n_ct = static_cast<int>((k + 255) / 256);
   const int64_t most = static_cast<int64_t>(n_experts) * p.n_rt * p.n_ct;
   if (most > (int64_t(1) << 30)) return SI_ERR_UNSUPPORTED;
-  const bool bf16 = type == SI_BF16;
-  if (!gm_map(&p.a, gy, bf16, 1, rows, n, ldg, 0, kGmK) || !gm_map(&p.b, x, bf16, 1, rows, k, ldx, 0, kGmK))
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rows == 0) return cuda_status(cudaMemsetAsync(gw, 0, static_cast<size_t>(n_experts) * n * k * size, s));
+  if (!gy || !x || !aligned16(gy) || !aligned16(x) || !gm_whole(offsets, 4) || !gm_ld(ldg, n, 2) || !gm_ld(ldx, k, 2))
+    return SI_ERR_INVALID_ARG;
+  if (workspace && (!aligned256(workspace) || workspace_bytes < sizeof(WsHeader))) return SI_ERR_WORKSPACE;
+  if (!gm_map(&p.a, gy, type, 1, rows, n, ldg, 0, kGmK) || !gm_map(&p.b, x, type, 1, rows, k, ldx, 0, kGmK) ||
+      !gm_map(&p.o, gw, gw_type, n_experts, n, k, k, n * k, 32))
     return SI_ERR_CUDA;
   p.offsets = offsets;
   p.n_experts = n_experts;
   p.rows = static_cast<int>(rows);
   p.n = static_cast<int>(n);
   p.k = static_cast<int>(k);
-  p.out = gw;
-  p.ld = k;
-  p.mat = n * k;
-  p.wide = gm_wide(gw, k, size);
   p.fmt = gm_fmt(type);
   p.status = static_cast<uint32_t *>(workspace);
-  return cuda_status(
-      gm_by_out(gw_type, [&](auto o) { return gm_launch<kGmGrad, false, 0, false, decltype(o)::value>(p, most, s); }));
+  return cuda_status(gm_by_out(
+      gw_type, [&](auto o) { return gm_launch<kGmGrad, kGmPlain, false, decltype(o)::value>(p, most, s); }));
 }
 
 extern "C" si_status si_moe_gateup(const void *x, si_dtype type, int64_t rows, int64_t ldx, const void *gate_up,
@@ -739,36 +986,73 @@ extern "C" si_status si_moe_gateup(const void *x, si_dtype type, int64_t rows, i
   if (!gm_rows(rows, n_experts) || !gm_width(inter) || !gm_width(hidden)) return SI_ERR_INVALID_ARG;
   if (!gm_type(type)) return SI_ERR_UNSUPPORTED;
   if (rows == 0) return SI_OK;
-  if (!x || !gate_up || !offsets || !h || !aligned16(x) || !aligned16(gate_up) || !aligned16(h) || !aligned16(codes) ||
-      (reinterpret_cast<uintptr_t>(offsets) & 3u) || !gm_ld(ldx, hidden, 2) || !codes != !scales)
+  if (!x || !gate_up || !h || !aligned16(x) || !aligned16(gate_up) || !aligned16(h) || !gm_whole(offsets, 4) ||
+      !gm_ld(ldx, hidden, 2) || !codes != !scales || !aligned16(codes))
     return SI_ERR_INVALID_ARG;
   if (workspace && (!aligned256(workspace) || workspace_bytes < sizeof(WsHeader))) return SI_ERR_WORKSPACE;
-  const bool few = gm_few(rows, n_experts), bf16 = type == SI_BF16;
+  const bool few = gm_few(rows, n_experts);
   GmParams p{};
-  p.n_rt = static_cast<int>((inter + 127) / 128);
-  const int64_t most = gm_tiles(rows, n_experts, few ? 16 : 128, p.n_rt);
-  if (!most) return SI_ERR_UNSUPPORTED;
-  CUtensorMap &mx = few ? p.b : p.a, &mw = few ? p.a : p.b;
-  if (!gm_map(&mx, x, bf16, 1, rows, hidden, ldx, 0, few ? 16 : 128) ||
-      !gm_map(&mw, gate_up, bf16, n_experts, 2 * inter, hidden, hidden, 2 * inter * hidden, 128))
+  const int64_t most = gm_forward(p, few, x, type, rows, hidden, ldx, n_experts, inter, 128, offsets, workspace);
+  if (most == 0) return SI_ERR_UNSUPPORTED;
+  if (most < 0 ||
+      !gm_map(&p.a, gate_up, type, n_experts, 2 * inter, hidden, hidden, 2 * inter * hidden, few ? 128 : 64))
     return SI_ERR_CUDA;
-  p.offsets = offsets;
-  p.n_experts = n_experts;
-  p.rows = static_cast<int>(rows);
-  p.n = static_cast<int>(inter);
-  p.k = static_cast<int>(hidden);
   p.out = h;
   p.ld = inter;
-  p.wide = gm_wide(h, inter, 2);
-  p.codes_wide = gm_wide(codes, inter, 1);
   p.codes = static_cast<uint8_t *>(codes);
   p.scales = static_cast<uint8_t *>(scales);
-  p.fmt = gm_fmt(type);
-  p.status = static_cast<uint32_t *>(workspace);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (type == SI_BF16)
-    return cuda_status(few ? gm_launch<kGmFew, false, 16, true, kGmBf16>(p, most, s)
-                           : gm_launch<kGmTokens, false, 0, true, kGmBf16>(p, most, s));
-  return cuda_status(few ? gm_launch<kGmFew, false, 16, true, kGmF16>(p, most, s)
-                         : gm_launch<kGmTokens, false, 0, true, kGmF16>(p, most, s));
+  return cuda_status(gm_by_half(type, [&](auto o) {
+    constexpr int O = decltype(o)::value;
+    return few ? gm_launch<kGmFew, kGmSwiglu, false, O>(p, most, s) : gm_launch<kGmWide, kGmSwiglu, false, O>(p, most, s);
+  }));
+}
+
+// Partial sums of a row's gw: one of 32 features each, in whole tiles.
+static int64_t gm_parts(int64_t rows, int n_experts, int64_t inter) {
+  return gm_few(rows, n_experts) ? (inter + 127) / 128 * 4 : (inter + 255) / 256 * 8;
+}
+
+extern "C" size_t si_moe_down_backward_workspace_bytes(int64_t rows, int n_experts, int64_t inter) {
+  if (!gm_rows(rows, n_experts) || !gm_width(inter)) return 0;
+  return round_up(sizeof(WsHeader) + static_cast<size_t>(rows) * gm_parts(rows, n_experts, inter) * 4, 256);
+}
+
+extern "C" si_status si_moe_down_backward(const void *gy, si_dtype type, int64_t rows, int64_t ldg, const void *down,
+                                          int n_experts, int64_t hidden, int64_t inter, const int32_t *offsets,
+                                          const void *codes, const void *scales, const float *row_w,
+                                          const int32_t *order, void *ggu, void *wh, float *gw, void *workspace,
+                                          size_t workspace_bytes, void *stream) {
+  if (!gm_rows(rows, n_experts) || !gm_width(inter) || !gm_width(hidden)) return SI_ERR_INVALID_ARG;
+  if (!gm_type(type)) return SI_ERR_UNSUPPORTED;
+  if (rows == 0) return SI_OK;
+  if (!gy || !down || !codes || !scales || !ggu || !aligned16(gy) || !aligned16(down) || !gm_whole(offsets, 4) ||
+      !gm_whole(ggu, 2) || (wh && !gm_whole(wh, 2)) || (row_w && !gm_whole(row_w, 4)) ||
+      (order && !gm_whole(order, 4)) || (gw && !gm_whole(gw, 4)) || !gm_ld(ldg, hidden, 2))
+    return SI_ERR_INVALID_ARG;
+  if ((gw && !workspace) ||
+      (workspace && (!aligned256(workspace) ||
+                     workspace_bytes < (gw ? si_moe_down_backward_workspace_bytes(rows, n_experts, inter) : sizeof(WsHeader)))))
+    return SI_ERR_WORKSPACE;
+  const bool few = gm_few(rows, n_experts);
+  GmParams p{};
+  const int64_t most = gm_forward(p, few, gy, type, rows, hidden, ldg, n_experts, inter, few ? 128 : 256, offsets, workspace);
+  if (most == 0) return SI_ERR_UNSUPPORTED;
+  if (most < 0 || !gm_map(&p.a, down, type, n_experts, hidden, inter, inter, hidden * inter, 64)) return SI_ERR_CUDA;
+  p.out = ggu;
+  p.codes = static_cast<uint8_t *>(const_cast<void *>(codes));
+  p.scales = static_cast<uint8_t *>(const_cast<void *>(scales));
+  p.c = row_w;
+  p.order = order;
+  p.wh = wh;
+  p.parts = static_cast<int>(gm_parts(rows, n_experts, inter));
+  p.part = gw ? reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + sizeof(WsHeader)) : nullptr;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = gm_by_half(type, [&](auto o) {
+    constexpr int O = decltype(o)::value;
+    return few ? gm_launch<kGmFew, kGmSwigluBack, true, O>(p, most, s) : gm_launch<kGmWide, kGmSwigluBack, true, O>(p, most, s);
+  });
+  if (e != cudaSuccess || !gw) return cuda_status(e);
+  return cuda_status(launch_pdl(gm_sum_kernel, dim3(static_cast<unsigned>((rows + 255) / 256)), dim3(256), 0, s,
+                                static_cast<const float *>(p.part), p.parts, p.rows, order, gw));
 }

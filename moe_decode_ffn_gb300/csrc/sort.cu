@@ -354,11 +354,14 @@ __global__ void __launch_bounds__(kRowThreads, 3)
         Piece<T, V> o;
         o.pack(acc);
         if (in) o.store(y + t * a.hidden + c);
-      } else {
-        static_assert(V == 4 && std::is_same_v<TO, __nv_bfloat16>, "fp32 rows to bf16");
-        const uint2 o = make_uint2(bf16_bits(acc[0]) | (static_cast<uint32_t>(bf16_bits(acc[1])) << 16),
-                                   bf16_bits(acc[2]) | (static_cast<uint32_t>(bf16_bits(acc[3])) << 16));
+      } else if constexpr (V == 4) {               // fp32 rows to 2-byte sums
+        const float pad[8] = {acc[0], acc[1], acc[2], acc[3]};
+        const uint4 b = pack16<TO>(pad);
+        const uint2 o = make_uint2(b.x, b.y);
         if (in) *reinterpret_cast<uint2 *>(y + t * a.hidden + c) = o;
+      } else {
+        static_assert(V == 1, "whole words of fp32 or single values");
+        if (in) y[t * a.hidden + c] = from_f32<TO>(acc[0]);
       }
     }
   }
@@ -573,6 +576,29 @@ extern "C" si_status si_moe_combine(const void *ys, si_dtype type, int n_tokens,
 extern "C" si_status si_moe_gather_backward(const void *gxs, si_dtype type, int n_tokens, int top_k, int64_t hidden,
                                             const int32_t *position, void *gx, void *stream) {
   return combine_enqueue(gxs, type, n_tokens, top_k, hidden, position, nullptr, gx, stream);
+}
+
+template <typename TO>
+static cudaError_t combine_f32(const RowArgs &a, bool vec, const float *rows, void *y, cudaStream_t s) {
+  const unsigned threads = row_threads(vec ? a.hidden / 4 : a.hidden);
+  const dim3 grid(row_blocks(a.tokens, threads, 3 * kRowThreads));
+  return vec ? launch_pdl(combine_rows_kernel<float, 4, TO>, grid, dim3(threads), 0, s, a, rows, static_cast<TO *>(y))
+             : launch_pdl(combine_rows_kernel<float, 1, TO>, grid, dim3(threads), 0, s, a, rows, static_cast<TO *>(y));
+}
+
+extern "C" si_status si_moe_combine_f32(const float *ys, int n_tokens, int top_k, int64_t hidden,
+                                        const int32_t *position, const float *topk_w, void *y, si_dtype y_type,
+                                        void *stream) {
+  const si_status st = rows_check(n_tokens, top_k, hidden, y_type, position);
+  if (st != SI_OK) return st;
+  const int size = y_type == SI_F32 ? 4 : 2;
+  if (!whole(ys, 4) || !whole(y, size) || (topk_w && !whole(topk_w, 4))) return SI_ERR_INVALID_ARG;
+  const bool vec = hidden % 4 == 0 && aligned16(ys) && aligned16(y);
+  const RowArgs a{n_tokens, top_k, hidden, static_cast<int64_t>(n_tokens) * top_k, position, topk_w, nullptr};
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cuda_status(y_type == SI_F32    ? combine_f32<float>(a, vec, ys, y, s)
+                     : y_type == SI_BF16 ? combine_f32<__nv_bfloat16>(a, vec, ys, y, s)
+                                         : combine_f32<__half>(a, vec, ys, y, s));
 }
 
 extern "C" si_status si_moe_combine_backward(const void *gy, const void *ys, si_dtype type, int n_tokens, int top_k,

@@ -80,10 +80,10 @@ def expected(x, ids, w, gate_up, down, gy):
         g, u = gu[:, :I], gu[:, I:]
         h = torch.nn.functional.silu(g) * u
         h = V(h, silu_off(g, h)).round(dtype)
-        ys = h.matmul(dn.T).round(dtype)
+        ys = h.matmul(dn.T)
         y.v.index_add_(0, t, c * ys.v), y.off.index_add_(0, t, c * ys.off), size_y.index_add_(0, t, c * (ys.v.abs() + ys.off))
         q = [torch.from_numpy(Q.dequantize(*Q.quantize(v.cpu().numpy()))).cuda() for v in (g, u)]
-        gh = GY.matmul(dn).round(dtype)
+        gh = GY.matmul(dn)
         s = torch.sigmoid(q[0])
         qh = q[0] * s * q[1]
         slope = q[1] * s * (1 + q[0] * (1 - s))
@@ -100,7 +100,7 @@ def expected(x, ids, w, gate_up, down, gy):
         for out, got in ((gdown, GY.T.matmul(ch)), (ggate_up, ggu.T.matmul(X))):
             got = got.round(dtype)
             out.v[e], out.off[e] = got.v, got.off
-        gxs = ggu.matmul(up).round(dtype)
+        gxs = ggu.matmul(up)
         gx.v.index_add_(0, t, gxs.v), gx.off.index_add_(0, t, gxs.off), size_x.index_add_(0, t, gxs.v.abs() + gxs.off)
     y.off += 2 * k * 2.0 ** -24 * size_y
     gx.off += k * 2.0 ** -24 * size_x
@@ -132,11 +132,12 @@ def test_equals_the_calls_that_it_is_made_of(case, kind):
     order, position, offsets = m.si_moe_sort(ids, E)
     xs = m.si_moe_gather(x, position, offsets)
     h, kept = m.si_moe_gateup(xs, gate_up, offsets, keep=True)
-    y = m.si_moe_combine(m.si_moe_matmul(h, down, offsets), position, w)
+    y = m.si_moe_combine(m.si_moe_matmul(h, down, offsets, dtype=torch.float32), position, w, dtype=x.dtype)
     gys = m.si_moe_gather(gy, position, offsets)
-    ggu, wh, gw = m.si_swiglu_backward(m.si_moe_matmul(gys, down.transpose(1, 2), offsets), kept, w, order)
-    gxs, ggate_up = m.si_moe_matmul_backward(ggu, xs, gate_up, offsets)
-    want = y, m.si_moe_gather_backward(gxs, position), gw, ggate_up, m.si_moe_matmul_grad_w(gys, wh, offsets)
+    ggu, wh, gw = m.si_moe_down_backward(gys, down, kept, offsets, w, order)
+    gxs = m.si_moe_matmul(ggu, gate_up.transpose(1, 2), offsets, dtype=torch.float32)
+    ggate_up, gdown = m.si_moe_matmul_grad_w(ggu, xs, offsets), m.si_moe_matmul_grad_w(gys, wh, offsets)
+    want = y, m.si_moe_gather_backward(gxs, position, dtype=x.dtype), gw, ggate_up, gdown
     leaves = [t.clone().requires_grad_() for t in (x, w, gate_up, down)]
     out = m.si_moe_experts(leaves[0], ids, *leaves[1:])
     got = out, *torch.autograd.grad(out, leaves, gy)
@@ -167,6 +168,47 @@ def test_gate_and_up_product(counts, H, I, kind):
     want = torch.nn.functional.silu(gd) * ud
     near(h, V(want, silu_off(gd, want)).round(dtype), "h")
     assert not bool(h[:head].any()) and not bool(h[R - tail:].any()) and not bool(codes[R - tail:].any())
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("counts,H,I", [([1], 8, 8), ([3, 0, 5], 72, 40), ([16, 17, 2], 64, 136), ([200, 0, 130], 136, 264),
+                                        ([100, 3], 72, 40), ([290], 64, 512)])
+def test_gradient_behind_the_down_product(counts, H, I, kind):
+    """Equal to the steps: gh = gy down in fp32 is exact here (whole numbers), so
+    si_swiglu_backward of fp32 rows differs by its logistic function alone: an error of
+    2 (16 (1 + |g|) + 4) 2^-24 of every term, and each result rounded to its type once."""
+    dtype, head, tail = TYPES[kind], 2, 3
+    R, E, g_ = head + sum(counts) + tail, len(counts), torch.Generator(device="cuda").manual_seed(I)
+    gy = torch.randint(-2, 3, (R, H), generator=g_, device="cuda").to(dtype)
+    down = torch.randint(-2, 3, (E, H, I), generator=g_, device="cuda").to(dtype)
+    gu = torch.randn(R, 2 * I, generator=g_, device="cuda") * 3
+    offsets = torch.tensor([head + sum(counts[:e]) for e in range(E + 1)], dtype=torch.int32, device="cuda")
+    _, kept = m.si_swiglu(gu, keep=True)
+    order = torch.randperm(R, generator=g_, device="cuda").to(torch.int32)
+    order[head + 1] = -1                         # a row without a pair
+    w = torch.randn(R, generator=g_, device="cuda")
+    gh = m.si_moe_matmul(gy, down.transpose(1, 2), offsets, dtype=torch.float32)
+    q = m.si_dequantize_mxint8(*(t.reshape(R * 2, -1) for t in kept), torch.float32).double()
+    qg, qu = q[0::2], q[1::2]
+    f = 2 * (16 * (1 + qg.abs()) + 4) * 2.0 ** -24
+    for args in ((None, None), (w, None), (w, order)):
+        want = list(m.si_swiglu_backward(gh, kept, *args))
+        for t in want[:2]:                       # rows of no expert: zeros
+            t[:head], t[R - tail:] = 0, 0
+        got = m.si_moe_down_backward(gy, down, kept, offsets, *args)
+        c = torch.ones_like(w) if args[0] is None else w if args[1] is None else torch.where(order >= 0, w[order.long().clamp(min=0)], 0 * w)
+        a, s = (c[:, None] * gh).abs().double(), torch.sigmoid(qg)
+        sizes = torch.cat([a * qu.abs() * s * (1 + qg.abs() * (1 - s)), a * qg.abs() * s], 1), (c[:, None] * qg * s * qu).abs()
+        for x, y, size, ff in zip(got, want, sizes, (torch.cat([f, f], 1), f)):
+            near(x, V(y.double(), ff * size).round(dtype), "ggu or wh")
+        if args[0] is None:
+            assert got[2] is None
+        else:
+            terms = (gh.double() * qg * s * qu).abs()
+            off = (((f + 2 * I * 2.0 ** -24) * terms).sum(1))
+            if args[1] is not None:
+                off = torch.zeros_like(off).index_copy_(0, order[order >= 0].long(), off[order >= 0])
+            near(got[2], V(want[2].double(), off), "gw")
 
 
 def test_gradients_against_differences():
@@ -203,7 +245,7 @@ def test_gradients_against_differences():
 def test_captured_and_replayed_beside_a_second_graph():
     case = (20, 2, 4, 64, 32, 0.1)
     x, ids, w, gate_up, down, gy = inputs(*case, "bf16", seed=4)
-    ws = m.workspace(m.moe_matmul_workspace_bytes())
+    ws = m.workspace(m.moe_experts_workspace_bytes(20, 2, gate_up))
     graphs = []
     for _ in range(2):
         leaves = [t.clone().requires_grad_() for t in (x, w, gate_up, down)]
@@ -269,3 +311,22 @@ def test_refusals():
                  lambda: m.si_quantize_mxint8(xs.int()), lambda: m.si_dequantize_mxint8(*m.si_quantize_mxint8(xs), dtype=torch.int32)):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("hidden", [1, 6, 8, 200])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_fp32_rows_combined_into_another_type(hidden, dtype):
+    """The same sums as in fp32, rounded once; gradients as through fp32."""
+    g = torch.Generator(device="cuda").manual_seed(hidden)
+    ids = torch.randint(0, 6, (33, 3), generator=g, device="cuda", dtype=torch.int32)
+    _, position, _ = m.si_moe_sort(ids, 5)
+    ys, w = torch.randn(99, hidden, generator=g, device="cuda"), torch.randn(33, 3, generator=g, device="cuda")
+    assert torch.equal(m.si_moe_combine(ys, position, w, dtype=dtype), m.si_moe_combine(ys, position, w).to(dtype))
+    assert torch.equal(m.si_moe_gather_backward(ys, position, dtype=dtype), m.si_moe_gather_backward(ys, position).to(dtype))
+    a, b = (t.clone().requires_grad_() for t in (ys, w))
+    gy = torch.randn(33, hidden, generator=g, device="cuda").to(dtype)
+    got = torch.autograd.grad(m.si_moe_combine(a, position, b, dtype=dtype), (a, b), gy)
+    want = torch.autograd.grad(m.si_moe_combine(a, position, b), (a, b), gy.float())
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    with pytest.raises(ValueError):
+        m.si_moe_combine(ys.to(dtype), position, w, dtype=torch.float32)

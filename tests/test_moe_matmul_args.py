@@ -58,6 +58,28 @@ def test_gateup_refusals(lib):
     refused(lib.si_moe_gateup, ok, [{"rows": 0, "x": None}], OK)
 
 
+def test_down_backward_refusals(lib):
+    need = lib.si_moe_down_backward_workspace_bytes(40, 4, 24)   # a header of 256 bytes and 40 rows of 4 sums, to the next 256
+    assert need == 1024 and lib.si_moe_down_backward_workspace_bytes(-1, 4, 24) == 0
+    assert lib.si_moe_down_backward_workspace_bytes(40, 0, 24) == 0 and lib.si_moe_down_backward_workspace_bytes(40, 4, 20) == 0
+    ok = dict(gy=16, type=m.SI_BF16, rows=40, ldg=64, down=16, e=4, hidden=64, inter=24, off=16, codes=16, scales=16, w=16,
+              order=16, ggu=16, wh=16, gw=16, ws=256, nb=need)
+    refused(lib.si_moe_down_backward, ok, [
+        {"gy": None}, {"gy": 8}, {"ldg": 56}, {"down": None}, {"down": 8}, {"off": None}, {"codes": None}, {"scales": None},
+        {"w": 18}, {"order": 18}, {"ggu": None}, {"ggu": 17}, {"wh": 17}, {"gw": 18}, {"hidden": 60}, {"inter": 20},
+        {"e": 1025}, {"rows": -1}], BAD)
+    refused(lib.si_moe_down_backward, ok, [{"type": m.SI_F32}], UNS)
+    refused(lib.si_moe_down_backward, ok, [{"ws": None}, {"ws": 128}, {"nb": need - 1}, {"gw": None, "nb": 255}], WS)
+    refused(lib.si_moe_down_backward, ok, [{"rows": 0, "gy": None}], OK)
+
+
+def test_combine_of_fp32_rows_refusals(lib):
+    ok = dict(ys=16, t=4, k=2, hidden=64, position=16, w=16, y=16, type=m.SI_BF16)
+    refused(lib.si_moe_combine_f32, ok, [{"ys": None}, {"ys": 18}, {"t": 0}, {"k": 9}, {"hidden": 0}, {"position": None},
+                                         {"w": 18}, {"y": None}, {"y": 17}], BAD)
+    refused(lib.si_moe_combine_f32, ok, [{"type": m.SI_Q8_0}], UNS)
+
+
 def test_mxint8_refusals(lib):
     ok = dict(x=16, type=m.SI_F32, rows=4, cols=40, ld=40, codes=16, scales=16)
     refused(lib.si_quantize_mxint8, ok, [
