@@ -514,7 +514,8 @@ si_status si_moe_combine_backward(const void *gy, const void *ys, si_dtype type,
  * fp16 operands, fp32 sums, rounded once. The rows are those of si_moe_gather: expert e
  * has rows offsets[e] .. offsets[e + 1] (device int32 [n_experts + 1], as si_moe_sort
  * writes them); a bound outside [0, rows] counts as the nearest inside, one below an
- * earlier bound as that one.
+ * earlier bound as that one (in si_moe_matmul_grad_w an expert's own two bounds count:
+ * none of its rows if they decrease).
  *
  * si_moe_matmul:        out[r][i] = sum_c x[r][c] * W[e][i][c] for the rows r of expert e
  * si_moe_matmul_grad_w: gw[e][i][c] = sum over the rows r of expert e of gy[r][i] * x[r][c]

@@ -40,6 +40,7 @@ namespace si {
 
 constexpr int kGmK = 64;              // summed indices of a stage: 128 bytes
 constexpr int kGmPiece = 8192;        // 64 x 64 values of an MN-major operand
+constexpr int kGmTail = 2 * 16 * 128;  // 128 values of 16 summed indices
 constexpr int kGmGroups = kSortMaxExperts + 2;
 
 enum GmOp { kGmWide, kGmFew, kGmGrad };
@@ -61,26 +62,30 @@ template <int OP, int MODE, int OUT> struct GmCfg {
   // gate and up rows lie on different lanes: u on its way to g's warps, 16 rows of 32
   // features, twice for each of 4 pairs of warps
   static constexpr int kSwap = OP == kGmWide && MODE == kGmSwiglu ? 4 * 2 * 16 * 32 * 4 : 0;
-  static constexpr int kOut = OP == kGmGrad ? kEpiWarps * 4096 : 0;  // rows on their way out
-  static constexpr int kFit = (227 * 1024 - kList - kSwap - kOut - 1536) / kStage;
+  static constexpr int kBox = OP == kGmGrad ? 2048 : 1024;           // a warp's rows on their way out
+  static constexpr int kOut = kEpiWarps * kBox;
+  // the last rows of an expert, of both operands, twice
+  static constexpr int kTail = OP == kGmGrad ? 2 * 2 * kGmTail : 0;
+  static constexpr int kFit = (227 * 1024 - kList - kSwap - kOut - kTail - 1536) / kStage;
   static constexpr int kStages = kFit < 12 ? kFit : 12;
   static constexpr int kAccCols = MA * kN;       // of one accumulator; two of them
   static constexpr int kCols = 2 * kAccCols <= 32 ? 32 : 2 * kAccCols <= 64 ? 64 : 512;
   static_assert(2 * kAccCols <= kCols, "tensor memory has 512 columns");
-  static constexpr int kBars = 3 * kStages + 5;
+  static constexpr int kBars = 2 * kStages + 11;
   static_assert(8 * kBars + 4 <= 512, "barriers");
-  static constexpr int kSmem = kStages * kStage + kOut + kSwap + 512 + kList + 1024;
+  static constexpr int kSmem = kStages * kStage + kTail + kOut + kSwap + 512 + kList + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
 struct GmParams {
-  CUtensorMap a, b, b32; // b, b32 (kGmWide): boxes of 128 and of 32 rows
-  CUtensorMap o;         // kGmGrad: the gradient, boxes of 32 rows x 128 bytes
+  CUtensorMap a, b[4];   // b, kGmWide: by boxes of 32, 64, 96 and 128 rows
+  CUtensorMap o, ta, tb; // kGmGrad: the gradient, boxes of 32 rows x 64 bytes; a and b by 16 rows
   const int32_t *offsets;
   int n_experts;
   int rows;              // sorted rows
   int n, k;              // features (of y; rows of gW) and summed columns (of x; columns of gW)
   int n_rt, n_ct;        // tiles along n; kGmGrad: along k
+  int whole_a, whole_b;  // MN-major operands: whole pieces of 64 values, two in a box
   void *out;             // y; h; kGmSwigluBack: ggu
   int64_t ld;            // distance of its rows in values
   uint8_t *codes, *scales;   // kGmSwiglu[Back]: [rows][2 n], [rows][2 mi_blocks(n)]
@@ -99,16 +104,33 @@ struct GmParams {
 // Sorted rows in groups: 0 the rows before offsets[0], 1 + e expert e's, n_experts + 1
 // the rows behind the last; the first and the last are written as zeros. Bounds
 // outside the rows are moved inside, and a bound below an earlier one to that one.
+// Tiles are dealt out to the pairs of SMs in turn. (Dealt out by their cost, the largest
+// first or large and small by turns, measured the same.)
 struct GmList {
-  int row[kGmGroups + 1], tile[kGmGroups + 1];
+  int row[kGmGroups + 1], tile[kGmGroups + 1];   // first row and first tile of a group
 };
 struct GmTile {
   int e, row0, count;    // expert (-1: zeros), first row, rows
   int rt, ct;
 };
 
+// Rows of a group's tiles: kGmWide as even parts of at most 256, to the next 32.
+template <int OP> SI_DEV int gm_per(int rows) {
+  if (OP == kGmFew) return 16;
+  const int n = (rows + 255) >> 8;
+  return n > 0 ? min(256, ((rows + n - 1) / n + 31) & ~31) : 256;
+}
+SI_DEV int gm_scan_add(int v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
 // The list, by all threads of the block.
-template <int M> SI_DEV void gm_list(const GmParams &p, GmList &l) {
+template <int OP> SI_DEV void gm_list(const GmParams &p, GmList &l) {
   const int E = p.n_experts;
   for (int i = threadIdx.x; i <= E; i += blockDim.x) l.tile[i] = min(max(__ldcg(p.offsets + i), 0), p.rows);
   __syncthreads();
@@ -134,13 +156,12 @@ template <int M> SI_DEV void gm_list(const GmParams &p, GmList &l) {
     int at = 0;
     for (int i0 = 0; i0 < E + 2; i0 += 32) {
       const int i = i0 + lane;
-      const int own = i < E + 2 ? (l.row[i + 1] - l.row[i] + M - 1) / M * p.n_rt : 0;
-      int v = own;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, v, d);
-        if (lane >= d) v += o;
+      int own = 0;
+      if (i < E + 2) {
+        const int rows = l.row[i + 1] - l.row[i], per = gm_per<OP>(rows);
+        own = (rows + per - 1) / per * p.n_rt;
       }
+      const int v = gm_scan_add(own, lane);
       if (i < E + 2) l.tile[i] = at + v - own;
       at += __shfl_sync(0xffffffffu, v, 31);
     }
@@ -149,36 +170,37 @@ template <int M> SI_DEV void gm_list(const GmParams &p, GmList &l) {
   __syncthreads();
 }
 // Tile w: the tiles of a group's rows lie side by side for the same features.
-template <int M> SI_DEV GmTile gm_tile(const GmParams &p, const GmList &l, int w) {
-  int lo = 0, hi = p.n_experts + 1;              // the last group whose first tile is at most w
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (l.tile[mid] <= w) lo = mid;
-    else hi = mid - 1;
+template <int OP> SI_DEV GmTile gm_tile(const GmParams &p, const GmList &l, int w) {
+  GmTile t;
+  if constexpr (OP == kGmGrad) {
+    t.ct = w % p.n_ct;
+    const int r = w / p.n_ct;
+    t.rt = r % p.n_rt;
+    t.e = r / p.n_rt;
+    t.row0 = min(max(__ldcg(p.offsets + t.e), 0), p.rows);
+    t.count = max(min(max(__ldcg(p.offsets + t.e + 1), 0), p.rows) - t.row0, 0);
+  } else {
+    int lo = 0, hi = p.n_experts + 1;            // the last group whose first tile is at most w
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (l.tile[mid] <= w) lo = mid;
+      else hi = mid - 1;
+    }
+    const int rows = l.row[lo + 1] - l.row[lo], i = w - l.tile[lo];
+    const int per = gm_per<OP>(rows), parts = (rows + per - 1) / per;
+    t.rt = i / parts;
+    t.ct = 0;
+    const int r = (i - t.rt * parts) * per;
+    t.row0 = l.row[lo] + r;
+    t.count = min(per, rows - r);
+    t.e = lo <= p.n_experts ? lo - 1 : -1;
   }
-  const int r0 = l.row[lo], r1 = l.row[lo + 1], mts = (r1 - r0 + M - 1) / M, i = w - l.tile[lo];
-  GmTile t;
-  t.rt = i / mts;
-  t.ct = 0;
-  t.row0 = r0 + (i - t.rt * mts) * M;
-  t.count = min(M, r1 - t.row0);
-  t.e = lo <= p.n_experts ? lo - 1 : -1;
-  return t;
-}
-SI_DEV GmTile gm_tile_grad(const GmParams &p, int w) {
-  GmTile t;
-  t.ct = w % p.n_ct;
-  const int r = w / p.n_ct;
-  t.rt = r % p.n_rt;
-  t.e = r / p.n_rt;
-  const int r0 = min(max(__ldcg(p.offsets + t.e), 0), p.rows), r1 = min(max(__ldcg(p.offsets + t.e + 1), 0), p.rows);
-  t.row0 = r0;
-  t.count = max(r1 - r0, 0);
   return t;
 }
 // Stages of a tile.
+// kGmGrad: of its whole 16 rows; up to 15 more are the tail.
 template <int OP> SI_DEV int gm_steps(const GmParams &p, const GmTile &t) {
-  return OP == kGmGrad ? (t.count + kGmK - 1) / kGmK : t.e < 0 ? 0 : (p.k + kGmK - 1) / kGmK;
+  return OP == kGmGrad ? ((t.count & ~15) + kGmK - 1) / kGmK : t.e < 0 ? 0 : (p.k + kGmK - 1) / kGmK;
 }
 
 // ---- tensor core -----------------------------------------------------------------
@@ -187,8 +209,8 @@ template <int OP> SI_DEV int gm_steps(const GmParams &p, const GmTile &t) {
 // groups (8 summed indices, MN-major) 1024 bytes apart, and MN-major the next 64
 // values kGmPiece bytes on. The high word is the same for both.
 constexpr uint32_t kGmDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-template <bool MN> SI_DEV uint32_t gm_desc_lo(uint32_t addr) {
-  return (addr >> 4) | ((MN ? kGmPiece >> 4 : 1u) << 16);
+template <bool MN> SI_DEV uint32_t gm_desc_lo(uint32_t addr, uint32_t piece = kGmPiece) {
+  return (addr >> 4) | ((MN ? piece >> 4 : 1u) << 16);
 }
 template <bool MN> constexpr uint32_t kGmK16 = (MN ? 16 * 128 : 32) / 16;   // 16 summed indices on
 template <int CG> SI_DEV void gm_mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
@@ -257,37 +279,88 @@ SI_DEV float gm_logistic(float g) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   return r;
 }
-// The code of this lane's value of a block that the warp's 32 lanes hold.
-SI_DEV uint32_t gm_encode_lane(float v, uint32_t &s) {
-  s = mi_scale_of(__reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7FFFFFFFu));
-  return s == 255u ? 0u : mi_code(v * mi_inv_scale(s));
+// The largest magnitude over the warp of each of 16 values, cut to 16 bits (which hold
+// its exponent): value 2 i in the low half of top[i]. A lane hands half of its words on
+// at every step, so 17 shuffles do; redux.sync for each value made gate and up of
+// 512 rows an expert, kept, 528 us instead of TODO.
+SI_DEV void gm_top16(const float v[16], int lane, uint32_t top[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    top[i] = __byte_perm(__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1]), 0x7632) & 0x7FFF7FFFu;
+#pragma unroll
+  for (int n = 4, m = 16; n > 0; n >>= 1, m >>= 1) {
+    const bool up = (lane & m) != 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const uint32_t give = up ? top[i] : top[i + n], keep = up ? top[i + n] : top[i];
+      top[i] = __vmaxu2(keep, __shfl_xor_sync(0xffffffffu, give, m));
+    }
+  }
+  uint32_t t = top[0];                           // word lane / 4
+  t = __vmaxu2(t, __shfl_xor_sync(0xffffffffu, t, 2));
+  t = __vmaxu2(t, __shfl_xor_sync(0xffffffffu, t, 1));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top[i] = __shfl_sync(0xffffffffu, t, 4 * i);
 }
 
 // The tokens of a tile, 16 columns of the accumulator at a time, dealt out to the
 // parts of the epilogue: piece i of a part.
 template <int PARTS> SI_DEV int gm_piece(int i, int part) { return (i * PARTS + part) * 16; }
 
-// This lane's feature f of 16 rows from row0, `left` of them in the tile.
-template <int OUT> SI_DEV void gm_write16(const GmParams &p, int f, int64_t row0, int left, const float v[16]) {
-  if (f >= p.n) return;
+// This lane's feature f of 16 rows from row0, `left` of them in the tile: fp32 rows
+// straight from the registers (128 bytes of a row a store), others in 16-byte words
+// through `box` (1024 bytes of the warp's own).
+template <int OUT>
+SI_DEV void gm_write16(const GmParams &p, void *out, int64_t ld, int f, int lane, int64_t row0, int left,
+                       const float v[16], uint8_t *box) {
+  if constexpr (OUT == kGmF32) {
+    if (f >= p.n) return;
+    float *o = static_cast<float *>(out) + row0 * ld + f;
 #pragma unroll
-  for (int j = 0; j < 16; ++j)
-    if (j < left) gm_store1<OUT>(p.out, (row0 + j) * p.ld + f, v[j]);
+    for (int j = 0; j < 16; ++j, o += ld)
+      if (j < left) *o = v[j];
+  } else {
+    __syncwarp();                                // the box has been read
+#pragma unroll
+    for (int j = 0; j < 16; ++j) gm_store1<OUT>(box + j * 64, lane, v[j]);
+    __syncwarp();
+    const int f0 = f - lane + (lane & 3) * 8;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int j = h * 8 + (lane >> 2);
+      const uint4 w = *reinterpret_cast<const uint4 *>(box + j * 64 + (lane & 3) * 16);
+      if (j < left && f0 < p.n) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + (row0 + j) * ld + f0) = w;
+    }
+  }
 }
-// The 8-bit block of 16 rows at this warp's 32 values (side 0: g, 1: u) from feature f - lane.
-SI_DEV void gm_keep16(const GmParams &p, int f, int lane, int64_t row0, int left, const float v[16], int side) {
-  const int64_t blocks = mi_blocks(p.n);
-  uint8_t *codes = p.codes + row0 * 2 * p.n + side * static_cast<int64_t>(p.n) + f;
+// The 8-bit blocks of 16 rows at this warp's 32 values (side 0: g, 1: u) from feature
+// f - lane, through `box` (512 bytes of the warp's own) so that rows leave in 16-byte words.
+SI_DEV void gm_keep16(const GmParams &p, int f, int lane, int64_t row0, int left, const float v[16], int side,
+                      uint8_t *box) {
+  uint32_t top[8];
+  gm_top16(v, lane, top);
   uint32_t mine = 0;                             // lane j: the scale of row j
+  __syncwarp();                                  // the box has been read
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    uint32_t s;
-    const uint32_t c = gm_encode_lane(v[j], s);
+    const uint32_t s = j & 1 ? top[j / 2] >> 23 : (top[j / 2] >> 7) & 0xFFu;
     if (lane == j) mine = s;
-    if (j < left && f < p.n) codes[static_cast<int64_t>(j) * 2 * p.n] = static_cast<uint8_t>(c);
+    box[j * 32 + lane] = static_cast<uint8_t>(s == 255u ? 0u : mi_code(v[j] * mi_inv_scale(s)));
   }
-  if (lane < 16 && lane < left && f - lane < p.n)
-    p.scales[(row0 + lane) * 2 * blocks + side * blocks + ((f - lane) >> 5)] = static_cast<uint8_t>(mine);
+  __syncwarp();
+  const int f0 = f - lane, j = lane >> 1, c = (lane & 1) * 16;
+  const int64_t blocks = mi_blocks(p.n);
+  if (j < left) {
+    uint8_t *to = p.codes + (row0 + j) * 2 * p.n + side * static_cast<int64_t>(p.n) + f0 + c;
+    const uint4 w = *reinterpret_cast<const uint4 *>(box + lane * 16);
+    if (f0 + c + 16 <= p.n && (p.n & 15) == 0) {
+      *reinterpret_cast<uint4 *>(to) = w;
+    } else {                                     // n is a multiple of 8
+      if (f0 + c < p.n) *reinterpret_cast<uint2 *>(to) = make_uint2(w.x, w.y);
+      if (f0 + c + 8 < p.n) *reinterpret_cast<uint2 *>(to + 8) = make_uint2(w.z, w.w);
+    }
+  }
+  if (lane < 16 && lane < left) p.scales[(row0 + lane) * 2 * blocks + side * blocks + (f0 >> 5)] = static_cast<uint8_t>(mine);
 }
 
 // Sums of 16 values over the warp: value (lane / 2) on even lanes, each lane handing
@@ -305,27 +378,36 @@ SI_DEV float gm_reduce16(float v[16], int lane) {
   return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
-// What 16 rows need beside gh: the codes of this lane's g and u, lane j's and 16 + j's
-// scales of row j's, and lane j's weight of row j.
+// What 16 rows need beside gh, as it comes from memory: 16 codes of g and of u of row
+// lane / 2, lane j's and 16 + j's scales of row j's, lane j's weight of row j, and which rows
+// are a pair's.
 struct GmKept {
-  uint32_t q[16];        // g in the low byte, u in the next
-  uint32_t s, live;      // live: bit j, row j is a pair's
+  uint4 g, u;
+  uint32_t s, live;
   float c;
 };
 SI_DEV GmKept gm_load_kept(const GmParams &p, int f, int lane, int64_t row0, int left) {
   GmKept k;
+  k.g = k.u = make_uint4(0, 0, 0, 0);
   const int64_t blocks = mi_blocks(p.n);
-  const uint8_t *codes = p.codes + row0 * 2 * p.n + f;
-  const bool in = f < p.n;
+  const int f0 = f - lane + (lane & 1) * 16, r = lane >> 1, j = lane & 15;
+  if (r < left) {
+    const uint8_t *at = p.codes + (row0 + r) * 2 * p.n + f0;
+    if (f0 + 16 <= p.n && (p.n & 15) == 0) {
+      k.g = __ldg(reinterpret_cast<const uint4 *>(at));
+      k.u = __ldg(reinterpret_cast<const uint4 *>(at + p.n));
+    } else {                                     // n is a multiple of 8
+      uint2 w[4] = {};
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    k.q[j] = 0;
-    if (in && j < left) {
-      const uint8_t *c = codes + static_cast<int64_t>(j) * 2 * p.n;
-      k.q[j] = __ldg(c) | (static_cast<uint32_t>(__ldg(c + p.n)) << 8);
+      for (int i = 0; i < 2; ++i)
+        if (f0 + 8 * i < p.n) {
+          w[i] = __ldg(reinterpret_cast<const uint2 *>(at + 8 * i));
+          w[2 + i] = __ldg(reinterpret_cast<const uint2 *>(at + p.n + 8 * i));
+        }
+      k.g = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
+      k.u = make_uint4(w[2].x, w[2].y, w[3].x, w[3].y);
     }
   }
-  const int j = lane & 15;
   k.s = 0;
   k.c = 0.f;
   bool live = false;
@@ -341,25 +423,33 @@ SI_DEV GmKept gm_load_kept(const GmParams &p, int f, int lane, int64_t row0, int
 // The gradients of h = silu(g) u in 16 rows: gh comes from the accumulator.
 template <int OUT>
 SI_DEV void gm_swiglu_back16(const GmParams &p, int f, int lane, int64_t row0, int left, const GmKept &k, float gh[16],
-                             int slot) {
+                             int slot, uint8_t *box) {
   const bool in = f < p.n;
+  __syncwarp();                                  // the box has been read
+  *reinterpret_cast<uint4 *>(box + lane * 16) = k.g;
+  *reinterpret_cast<uint4 *>(box + 512 + lane * 16) = k.u;
+  __syncwarp();
+  float gg[16], gu[16], ch[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    const float g = static_cast<float>(static_cast<int8_t>(k.q[j])) * mi_step(__shfl_sync(0xffffffffu, k.s, j));
-    const float u = static_cast<float>(static_cast<int8_t>(k.q[j] >> 8)) * mi_step(__shfl_sync(0xffffffffu, k.s, 16 + j));
+    const float g = static_cast<float>(static_cast<int8_t>(box[j * 32 + lane])) * mi_step(__shfl_sync(0xffffffffu, k.s, j));
+    const float u = static_cast<float>(static_cast<int8_t>(box[512 + j * 32 + lane])) *
+                    mi_step(__shfl_sync(0xffffffffu, k.s, 16 + j));
     const float c = __shfl_sync(0xffffffffu, k.c, j), l = gm_logistic(g), si = g * l, h = si * u, cd = c * gh[j];
     const bool live = (k.live >> j) & 1u;        // a row of no pair: zeros
-    if (in && j < left) {
-      const int64_t at = (row0 + j) * 2 * p.n + f;
-      gm_store1<OUT>(p.out, at, live ? cd * u * (l * fmaf(g, 1.f - l, 1.f)) : 0.f);
-      gm_store1<OUT>(p.out, at + p.n, live ? cd * si : 0.f);
-      if (p.wh) gm_store1<OUT>(p.wh, (row0 + j) * p.n + f, live ? c * h : 0.f);
-    }
+    gg[j] = live ? cd * u * (l * fmaf(g, 1.f - l, 1.f)) : 0.f;
+    gu[j] = live ? cd * si : 0.f;
+    ch[j] = live ? c * h : 0.f;
     gh[j] = in && live ? gh[j] * h : 0.f;
   }
+  const int64_t ld = 2 * static_cast<int64_t>(p.n);
+  gm_write16<OUT>(p, p.out, ld, f, lane, row0, left, gg, box);
+  gm_write16<OUT>(p, static_cast<uint16_t *>(p.out) + p.n, ld, f, lane, row0, left, gu, box);
+  if (p.wh) gm_write16<OUT>(p, p.wh, p.n, f, lane, row0, left, ch, box);
+  if (!p.part) return;
   const float sum = gm_reduce16(gh, lane);
   const int j = lane >> 1;
-  if (p.part && !(lane & 1) && j < left) p.part[(row0 + j) * p.parts + slot] = sum;
+  if (!(lane & 1) && j < left) p.part[(row0 + j) * p.parts + slot] = sum;
 }
 
 // ---- the kernel ----------------------------------------------------------------
@@ -373,39 +463,44 @@ template <int OUT> constexpr int kGmChunk = OUT == kGmF32 ? 8 : 1 << 30;
 template <int OP, int MODE, bool WMN, int OUT>
 __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kernel(const __grid_constant__ GmParams p) {
   using C = GmCfg<OP, MODE, OUT>;
-  constexpr int S = C::kStages, CG = C::CG, M = C::kN, PARTS = C::kEpiWarps / 4, PIECES = C::kN / 16 / PARTS;
+  constexpr int S = C::kStages, CG = C::CG, PARTS = C::kEpiWarps / 4, PIECES = C::kN / 16 / PARTS;
   constexpr bool kAMn = OP == kGmGrad || WMN, kBMn = OP == kGmGrad;
   static_assert(MODE == kGmPlain || (OP != kGmGrad && OUT != kGmF32 && !(MODE == kGmSwiglu && WMN)), "forms");
   extern __shared__ uint8_t gm_smem[];
   uint8_t *base = gm_smem + ((1024u - (smem_addr(gm_smem) & 1023u)) & 1023u);
-  uint8_t *outs = base + S * C::kStage;
+  uint8_t *tails = base + S * C::kStage, *outs = tails + C::kTail;
   float *swap = reinterpret_cast<float *>(outs + C::kOut);
   uint64_t *full = reinterpret_cast<uint64_t *>(outs + C::kOut + C::kSwap);
   uint64_t *empty = full + S, *acc_full = empty + S, *acc_empty = acc_full + 2, *drain = acc_empty + 2;
-  uint64_t *tail = drain + 1;                    // by stage
-  uint32_t *s_taddr = reinterpret_cast<uint32_t *>(tail + S);
+  // tails: landed in this block, cleared in both, read by their MMA
+  uint64_t *tail_full = drain + 1, *tail_ready = tail_full + 2, *tail_empty = tail_ready + 2;
+  uint32_t *s_taddr = reinterpret_cast<uint32_t *>(tail_empty + 2);
   GmList &list = *reinterpret_cast<GmList *>(outs + C::kOut + C::kSwap + 512);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(full + i, 2 * CG);       // of the first block: both producers of both
+      mbar_init(full + i, 2);            // the producers; of a pair, the first block's
       mbar_init(empty + i, 1);
-      mbar_init(tail + i, 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full + i, 1);
       mbar_init(acc_empty + i, C::kEpiWarps * CG);   // of the first block
     }
     mbar_init(drain, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(tail_full + i, 2);
+      mbar_init(tail_ready + i, CG);
+      mbar_init(tail_empty + i, 1);
+    }
     fence_mbar_init();
   }
   grid_dep_wait();
   // before the next kernel may start: its blocks take tensor memory too
   if (warp == 1) gm_tmem_alloc<CG>(s_taddr, C::kCols);
   tc_fence_before();
-  if constexpr (OP != kGmGrad) gm_list<M>(p, list);
+  if constexpr (OP != kGmGrad) gm_list<OP>(p, list);
   if constexpr (CG == 2) cluster_sync();
   else __syncthreads();
   tc_fence_after();
@@ -413,25 +508,50 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
   const uint32_t tmem = __shfl_sync(0xffffffffu, *s_taddr, 0);
   const int total = OP == kGmGrad ? p.n_experts * p.n_rt * p.n_ct : list.tile[p.n_experts + 2];
   const int first = blockIdx.x / CG, step = gridDim.x / CG;
-  auto tile = [&](int w) {
-    if constexpr (OP == kGmGrad) return gm_tile_grad(p, w);
-    else return gm_tile<M>(p, list, w);
-  };
+  auto tile = [&](int w) { return gm_tile<OP>(p, list, w); };
   // a tile's columns of the accumulator: its rows, to the next 32 (16 in one SM)
   auto columns = [&](const GmTile &t) { return OP == kGmGrad ? 256 : (t.count + 16 * CG - 1) & -(16 * CG); };
-  // rows of the expert in the last stage if they need clearing behind them, else 0
-  auto tail_rows = [&](const GmTile &t, int ks, int nk) {
-    return OP == kGmGrad && ks == nk - 1 && (t.count & 15) ? t.count - ks * kGmK : 0;
-  };
+  // rows of the tail, behind an expert's whole 16
+  auto tail_rows = [&](const GmTile &t) { return OP == kGmGrad ? t.count & 15 : 0; };
   const uint32_t full0 = CG == 2 ? cluster_addr(smem_addr(full), 0) : smem_addr(full);
 
   if (warp == 0 || warp == C::kBWarp) {
     if (lane == 0) {
-      uint32_t it = 0;
+      uint32_t it = 0, cuts = 0;
       bool ok = true;
+      auto load = [&](void *to, const CUtensorMap *m, int c0, int c1, int c2, int c3, uint32_t bar) {
+        tma_load4<CG == 2>(to, m, c0, c1, c2, c3, bar);
+      };
+      // 128 values, from v, of some summed indices of an MN-major operand: pieces of 64 values
+      auto load_mn = [&](uint8_t *to, int piece, const CUtensorMap *m, int whole, int v, int c1, int c3, uint32_t bar) {
+        if (whole) {
+          load(to, m, 0, c1, v >> 6, c3, bar);
+        } else {
+          load(to, m, v, c1, 0, c3, bar);
+          load(to + piece, m, v + 64, c1, 0, c3, bar);
+        }
+      };
       for (int w = first; ok && w < total; w += step) {
         const GmTile t = tile(w);
         const int nk = gm_steps<OP>(p, t), half = columns(t) / CG;
+        if constexpr (OP == kGmGrad) {
+          // the tail first: it is cleared while the stages are on their way
+          if (tail_rows(t)) {
+            const uint32_t u = cuts & 1;
+            if (!mbar_wait_bounded(tail_empty + u, ((cuts >> 1) & 1) ^ 1, p.status)) {
+              ok = false;
+              break;
+            }
+            uint8_t *to = tails + (u * 2 + (warp != 0)) * kGmTail;
+            const int r = t.row0 + (t.count & ~15);
+            mbar_arrive_expect_tx(tail_full + u, kGmTail);
+            if (warp == 0)
+              load_mn(to, kGmTail / 2, &p.ta, p.whole_a, t.rt * 256 + rank * 128, r, 0, smem_addr(tail_full + u));
+            else
+              load_mn(to, kGmTail / 2, &p.tb, p.whole_b, t.ct * 256 + rank * 128, r, 0, smem_addr(tail_full + u));
+            ++cuts;
+          }
+        }
         for (int ks = 0; ks < nk; ++ks, ++it) {
           const int s = it % S;
           if (!mbar_wait_bounded(empty + s, ((it / S) & 1) ^ 1, p.status)) {
@@ -440,48 +560,34 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
           }
           uint8_t *st = base + s * C::kStage + (warp == 0 ? 0 : C::kABytes);
           const int c = ks * kGmK;
-          // this block's copies count at the pair's barrier of the stage, or at its own where
-          // it clears rows first
-          const bool cut = tail_rows(t, ks, nk) != 0;
-          const uint32_t bar = cut ? smem_addr(tail + s) : full0 + s * 8;
+          // The copies of both blocks count at the first one's barrier of the stage, which its
+          // producers arrive at for both. One copy a stage and thread: two or three of them,
+          // at a few hundred cycles each, bound the stage (320 rows an expert in three boxes
+          // of 32 a stage 302 us, in one 231).
+          const uint32_t bar = full0 + s * 8;
           auto expect = [&](uint32_t bytes) {
-            if (CG == 2 && !cut) mbar_expect_tx_cluster(bar, bytes);
-            else mbar_arrive_expect_tx(cut ? tail + s : full + s, bytes);
-          };
-          auto load = [&](int to, const CUtensorMap *m, int c0, int c1, int c2) {
-            if constexpr (CG == 2) tma_load3_pair(st + to, m, c0, c1, c2, bar);
-            else tma_load3(st + to, m, c0, c1, c2, full + s);
+            if (rank == 0) mbar_arrive_expect_tx(full + s, bytes * CG);
           };
           if (warp == 0) {
             expect(C::kABytes);
-            if constexpr (OP == kGmGrad) {
-#pragma unroll
-              for (int i = 0; i < 2; ++i) load(i * kGmPiece, &p.a, t.rt * 256 + rank * 128 + i * 64, t.row0 + c, 0);
-            } else if constexpr (MODE == kGmSwiglu && OP == kGmWide) {
-#pragma unroll
-              for (int i = 0; i < 2; ++i) load(i * kGmPiece, &p.a, c, t.rt * 128 + rank * 64 + i * p.n, t.e);
-            } else if constexpr (MODE == kGmSwiglu) {
-#pragma unroll
-              for (int i = 0; i < 2; ++i) load(i * 128 * 128, &p.a, c, t.rt * 128 + i * p.n, t.e);
-            } else if constexpr (WMN) {
-#pragma unroll
-              for (int i = 0; i < 2; ++i) load(i * kGmPiece, &p.a, (t.rt * CG + rank) * 128 + i * 64, c, t.e);
-            } else {
-              load(0, &p.a, c, (t.rt * CG + rank) * 128, t.e);
-            }
-          } else {
-            if constexpr (OP == kGmGrad) {
-              expect(C::kBBytes);
-#pragma unroll
-              for (int i = 0; i < 2; ++i) load(i * kGmPiece, &p.b, t.ct * 256 + rank * 128 + i * 64, t.row0 + c, 0);
-            } else if (OP == kGmFew || half > 96) {
-              expect(C::kBBytes);
-              load(0, &p.b, c, t.row0 + rank * half, 0);
-            } else {
-              const int n = (half + 31) >> 5;
-              expect(n * 32 * 128);
-              for (int i = 0; i < n; ++i) load(i * 32 * 128, &p.b32, c, t.row0 + rank * half + i * 32, 0);
-            }
+            if constexpr (OP == kGmGrad)
+              load_mn(st, kGmPiece, &p.a, p.whole_a, t.rt * 256 + rank * 128, t.row0 + c, 0, bar);
+            else if constexpr (MODE == kGmSwiglu)    // gate and up
+              load(st, &p.a, c, t.rt * 128 + rank * 64, 0, t.e, bar);
+            else if constexpr (WMN)
+              load_mn(st, kGmPiece, &p.a, p.whole_a, (t.rt * CG + rank) * 128, c, t.e, bar);
+            else
+              load(st, &p.a, c, (t.rt * CG + rank) * 128, 0, t.e, bar);
+          } else if constexpr (OP == kGmGrad) {
+            expect(C::kBBytes);
+            load_mn(st, kGmPiece, p.b, p.whole_b, t.ct * 256 + rank * 128, t.row0 + c, 0, bar);
+          } else if constexpr (OP == kGmFew) {
+            expect(C::kBBytes);
+            load(st, p.b, c, t.row0, 0, 0, bar);
+          } else {                   // no more rows than the next 32: they come from the L2
+            const int n = (half - 1) >> 5;
+            expect((n + 1) * 32 * 128);
+            load(st, p.b + n, c, t.row0 + rank * half, 0, 0, bar);
           }
         }
       }
@@ -500,7 +606,7 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
     // the warp walks over the stages together, the leader alone waits and issues
     const bool leader = elect_lane();
     const uint32_t smem0 = smem_addr(base);
-    uint32_t n = 0;                  // accumulators taken so far
+    uint32_t n = 0, cuts = 0;        // accumulators and tails taken so far
     int s = 0;                       // stage and its parity
     uint32_t parity = 0;
     bool ok = true;
@@ -509,16 +615,15 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
       const int nk = gm_steps<OP>(p, t);
       const uint32_t idesc = (1u << 4) | p.fmt | (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u) |
                              (static_cast<uint32_t>(columns(t) >> 3) << 17) | ((CG * 128u >> 4) << 24);
-      const int last = OP == kGmGrad ? t.count : p.k;   // summed indices
-      for (int k0 = 0; k0 < nk; k0 += kGmChunk<OUT>, ++n) {
+      const int last = OP == kGmGrad ? t.count & ~15 : p.k, cut = tail_rows(t);   // summed indices
+      for (int k0 = 0; k0 < nk || (k0 == 0 && cut); k0 += kGmChunk<OUT>, ++n) {
         const uint32_t u = n & 1, d = tmem + u * C::kAccCols;
         if (leader && ok) ok = mbar_wait_bounded(acc_empty + u, ((n >> 1) & 1) ^ 1, p.status);
         const int k1 = min(nk, kGmChunk<OUT> < nk ? k0 + kGmChunk<OUT> : nk);
         for (int ks = k0; ks < k1; ++ks) {
           const int n16 = (min(kGmK, last - ks * kGmK) + 15) >> 4;
           const uint32_t st = smem0 + s * C::kStage;
-          if (leader && ok)
-            ok = CG == 2 ? mbar_wait_cluster(full + s, parity, p.status) : mbar_wait_bounded(full + s, parity, p.status);
+          if (leader && ok) ok = mbar_wait_bounded(full + s, parity, p.status);
           if (leader && ok) {
             tc_fence_after();
             const uint32_t la = gm_desc_lo<kAMn>(st), lb = gm_desc_lo<kBMn>(st + C::kABytes);
@@ -537,6 +642,18 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
             parity ^= 1;
           }
         }
+        if constexpr (OP == kGmGrad) {
+          if (cut && k1 == nk) {
+            const uint32_t v = cuts & 1, at = smem_addr(tails) + v * 2 * kGmTail;
+            if (leader && ok) ok = mbar_wait_cluster(tail_ready + v, (cuts >> 1) & 1, p.status);
+            if (leader && ok) {
+              tc_fence_after();
+              gm_mma<CG>(d, gm_desc_lo<true>(at, kGmTail / 2), gm_desc_lo<true>(at + kGmTail, kGmTail / 2), idesc, k1 > k0);
+              gm_commit<CG>(tail_empty + v);
+            }
+            ++cuts;
+          }
+        }
         if (leader && ok) gm_commit<CG>(acc_full + u);
       }
     }
@@ -546,28 +663,26 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
     }
     __syncwarp();
   } else if (warp == C::kTailWarp) {
-    // rows behind the expert's in the last 16 of its sums: cleared, in both operands
-    uint32_t it = 0, cuts = 0;       // cuts: the parity of each stage's barrier
+    // the rows behind the expert's in its tail: cleared, in both operands
+    const uint32_t ready0 = cluster_addr(smem_addr(tail_ready), 0);
+    uint32_t cuts = 0;
     for (int w = first; w < total; w += step) {
-      const GmTile t = tile(w);
-      const int nk = gm_steps<OP>(p, t);
-      it += nk;
-      const int left = nk > 0 ? tail_rows(t, nk - 1, nk) : 0;
+      const int left = tail_rows(tile(w));
       if (left == 0) continue;
-      const int s = (it - 1) % S;
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(tail + s, (cuts >> s) & 1, p.status))) break;
-      cuts ^= 1u << s;
-      uint8_t *q = base + s * C::kStage;
-      for (int r = left; r < ((left + 15) & ~15); ++r)
-        *reinterpret_cast<uint4 *>(q + (lane >> 3) * kGmPiece + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+      const uint32_t u = cuts & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(tail_full + u, (cuts >> 1) & 1, p.status))) break;
+      ++cuts;
+      uint8_t *to = tails + u * 2 * kGmTail + (lane >> 3) * (kGmTail / 2) + (lane & 7) * 16;
+      for (int r = left; r < 16; ++r) *reinterpret_cast<uint4 *>(to + r * 128) = make_uint4(0, 0, 0, 0);
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(full0 + s * 8, 2);
+      if (lane == 0) mbar_arrive_cluster(ready0 + u * 8, 1);
     }
   } else {
     const int q = warp & 3, part = (warp - 2) >> 2;   // the 32 lanes of tensor memory this warp may read
     const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const uint32_t free0 = CG == 2 ? cluster_addr(smem_addr(acc_empty), 0) : smem_addr(acc_empty);
+    uint8_t *stage = outs + (warp - 2) * C::kBox;
     uint32_t n = 0;
     bool ok = true;
     auto wait_acc = [&] {            // its address; n goes on with release()
@@ -588,12 +703,12 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
     // meet at a barrier all come there
     for (int w = first; w < total; w += step) {
       const GmTile t = tile(w);
-      const int nk = ok ? gm_steps<OP>(p, t) : 0;
+      const int steps = gm_steps<OP>(p, t), nk = !ok ? 0 : steps == 0 && tail_rows(t) ? 1 : steps;
       bool zero = nk == 0;
       if constexpr (OP == kGmGrad) {
-        // lane = row of the gradient; a part's columns, 128 bytes of them at a time through shared memory
-        constexpr int kPer = OUT == kGmF32 ? 32 : 64, kMine = 256 / PARTS;   // columns of a box, of a part
-        uint8_t *stage = outs + (warp - 2) * 4096;
+        // lane = row of the gradient; a part's columns, 64 bytes of them at a time through shared
+        // memory (boxes of 128 bytes would take the room of a stage)
+        constexpr int kPer = 64 / kGmSize<OUT>, kMine = 256 / PARTS;   // columns of a box, of a part
         const int row = t.rt * 256 + rank * 128 + q * 32, col = t.ct * 256 + part * kMine;
         float sum[OUT == kGmF32 ? kMine : 1] = {};
         uint32_t acc = 0;
@@ -616,33 +731,30 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
         zero |= !ok;
 #pragma unroll
         for (int c = 0; c < kMine; c += kPer) {
-          uint32_t v[32];            // 128 bytes of the row
+          uint32_t v[16];            // 64 bytes of the row
           if (OUT != kGmF32 && zero) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0;
+            for (int i = 0; i < 16; ++i) v[i] = 0;
           } else if constexpr (OUT == kGmF32) {   // zeros where there was nothing to add
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(sum[c + i]);
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(sum[c + i]);
           } else {
+            uint32_t r[32];
+            tmem_ld32(acc + part * kMine + c, r);
+            tmem_wait_ld();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t r[32];
-              tmem_ld32(acc + part * kMine + c + 32 * h, r);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[16 * h + i] = gm_pack<OUT>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-            }
+            for (int i = 0; i < 16; ++i) v[i] = gm_pack<OUT>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
             if (c + kPer == kMine) release();
           }
           if (lane == 0) tma_store_wait_read();        // the box before has been read
           __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<uint4 *>(stage + lane * 128 + ((i ^ (lane & 7)) * 16)) =
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4 *>(stage + lane * 64 + ((i ^ (lane >> 1 & 3)) * 16)) =
                 make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           fence_async_smem();
           __syncwarp();
-          if (lane == 0 && row < p.n && col + c < p.k) tma_store3(&p.o, stage, col + c, row, t.e);
+          if (lane == 0 && row < p.n && col + c < p.k) tma_store4(&p.o, stage, col + c, row, 0, t.e);
         }
       } else {
         // lane = feature; 16 rows at a time
@@ -685,7 +797,7 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
           for (int i = 0; i < PIECES; ++i) {
             if (i >= mine) break;
             const int j0 = gm_piece<PARTS>(i, part);
-            gm_write16<OUT>(p, f, static_cast<int64_t>(t.row0) + j0, t.count - j0, sum[i]);
+            gm_write16<OUT>(p, p.out, p.ld, f, lane, static_cast<int64_t>(t.row0) + j0, t.count - j0, sum[i], stage);
           }
         } else {
           if constexpr (MODE != kGmSwigluBack) {
@@ -694,6 +806,9 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
             if (!zero && mine == 0) release();
           }
           bool have = MODE != kGmSwigluBack;     // the accumulator has been waited for
+          GmKept next;                           // of the piece to come
+          if constexpr (MODE == kGmSwigluBack)
+            next = gm_load_kept(p, f, lane, static_cast<int64_t>(t.row0) + part * 16, zero ? 0 : t.count - part * 16);
           for (int i = 0; i < mine; ++i) {
             const int j0 = gm_piece<PARTS>(i, part), left = t.count - j0;
             const int64_t row0 = static_cast<int64_t>(t.row0) + j0;
@@ -702,9 +817,10 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
               if (zero) zeros(v);
               else read16(acc + j0, v);
               if (!zero && i == mine - 1) release();
-              gm_write16<OUT>(p, f, row0, left, v);
+              gm_write16<OUT>(p, p.out, p.ld, f, lane, row0, left, v, stage);
             } else if constexpr (MODE == kGmSwigluBack) {
-              const GmKept kept = gm_load_kept(p, f, lane, row0, zero ? 0 : left);
+              const GmKept kept = next;
+              next = gm_load_kept(p, f, lane, row0 + 16 * PARTS, zero || i == mine - 1 ? 0 : left - 16 * PARTS);
               if (!zero && !have) {
                 acc = wait_acc();
                 zero = !ok;
@@ -713,7 +829,7 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
               if (zero) zeros(v);
               else read16(acc + j0, v);
               if (!zero && i == mine - 1) release();
-              gm_swiglu_back16<OUT>(p, f, lane, row0, left, kept, v, (t.rt * CG + rank) * 4 + q);
+              gm_swiglu_back16<OUT>(p, f, lane, row0, left, kept, v, (t.rt * CG + rank) * 4 + q, stage);
             } else if constexpr (OP == kGmFew) {
               float u[16];
               if (zero) {
@@ -724,17 +840,13 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
                 read16(acc + C::kN + j0, u);
                 if (i == mine - 1) release();
               }
-              if (f >= p.n) {        // behind the last feature: the next rows of the matrix
-                zeros(v);
-                zeros(u);
-              }
               if (tf < p.n && p.codes) {
-                gm_keep16(p, f, lane, row0, left, v, 0);
-                gm_keep16(p, f, lane, row0, left, u, 1);
+                gm_keep16(p, f, lane, row0, left, v, 0, stage);
+                gm_keep16(p, f, lane, row0, left, u, 1, stage);
               }
 #pragma unroll
               for (int j = 0; j < 16; ++j) v[j] = v[j] * gm_logistic(v[j]) * u[j];
-              gm_write16<OUT>(p, f, row0, left, v);
+              gm_write16<OUT>(p, p.out, p.ld, f, lane, row0, left, v, stage);
             } else {
               // lanes 0-63 hold g, 64-127 u: u goes to g's warps through shared memory
               const int side = q >> 1;
@@ -743,17 +855,16 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
               if (zero) zeros(v);
               else read16(acc + j0, v);
               if (!zero && i == mine - 1) release();
-              if (f >= p.n) zeros(v);
               if (side == 1) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) box[j * 32 + lane] = v[j];
               }
               asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
-              if (tf < p.n && p.codes) gm_keep16(p, f, lane, row0, left, v, side);
+              if (tf < p.n && p.codes) gm_keep16(p, f, lane, row0, left, v, side, stage);
               if (side == 0) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] = v[j] * gm_logistic(v[j]) * box[j * 32 + lane];
-                gm_write16<OUT>(p, f, row0, left, v);
+                gm_write16<OUT>(p, p.out, p.ld, f, lane, row0, left, v, stage);
               }
             }
           }
@@ -800,20 +911,38 @@ __global__ void __launch_bounds__(256) gm_sum_kernel(const float *part, int n, i
 
 // ---- host ------------------------------------------------------------------
 
-// Values [mats][rows][cols] of 2 or 4 bytes, boxes of box_rows rows x 128 bytes in the
-// 128-byte swizzle; what lies outside reads as zero and is not written.
-static bool gm_map(CUtensorMap *m, const void *v, si_dtype type, int64_t mats, int64_t rows, int64_t cols, int64_t ld,
-                   int64_t mat, int box_rows) {
-  const int size = type == SI_F32 ? 4 : 2;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
-                              static_cast<cuuint64_t>(mats)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * size),
-                                 static_cast<cuuint64_t>((mats > 1 ? mat : ld) * size)};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / size), static_cast<cuuint32_t>(box_rows), 1};
+// Values of 2 or 4 bytes in four dimensions, the inner one contiguous, the others `stride`
+// values apart, boxes of `inner` (128 or 64) bytes x b1 x b2 in the swizzle of that size; what lies outside
+// reads as zero and is not written.
+struct GmDims {
+  int64_t d0, d1, s1, d2, s2, d3, s3;
+};
+static bool gm_map(CUtensorMap *m, const void *v, si_dtype type, const GmDims &g, int b1, int b2 = 1, int inner = 128) {
+  const int64_t size = type == SI_F32 ? 4 : 2;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(g.d0), static_cast<cuuint64_t>(g.d1),
+                              static_cast<cuuint64_t>(g.d2), static_cast<cuuint64_t>(g.d3)};
+  // a dimension of one has a stride all the same: any that is allowed
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(g.s1 * size),
+                                 static_cast<cuuint64_t>((g.d2 > 1 ? g.s2 : g.s1) * size),
+                                 static_cast<cuuint64_t>((g.d3 > 1 ? g.s3 : g.s1) * size)};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(inner / size), static_cast<cuuint32_t>(b1),
+                             static_cast<cuuint32_t>(b2), 1};
   return encode_map(m, type == SI_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                        : type == SI_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                    v, 3, dims, strides, box);
+                    v, 4, dims, strides, box, inner == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// Rows [rows][cols], ld apart, in boxes of `box` of them.
+static bool gm_map_rows(CUtensorMap *m, const void *v, si_dtype type, int64_t rows, int64_t cols, int64_t ld, int box) {
+  return gm_map(m, v, type, {cols, rows, ld, 1, 0, 1, 0}, box);
+}
+// The same (of each of `mats` matrices) as an MN-major operand: `box` rows x 64 columns, two such
+// pieces side by side where the columns are whole pieces.
+static bool gm_map_mn(CUtensorMap *m, int *whole, const void *v, si_dtype type, int64_t mats, int64_t rows,
+                      int64_t cols, int64_t ld, int64_t mat, int box = kGmK) {
+  *whole = cols % 64 == 0;
+  return *whole ? gm_map(m, v, type, {64, rows, ld, cols / 64, 64, mats, mat}, box, 2)
+                : gm_map(m, v, type, {cols, rows, ld, 1, 0, mats, mat}, box);
 }
 
 // Pairs of blocks that are resident at once, on the current device: fewer than half of
@@ -900,9 +1029,8 @@ static int64_t gm_forward(GmParams &p, bool few, const void *x, si_dtype type, i
   const int m = few ? 16 : 256;
   const int64_t most = (rows / m + std::min<int64_t>(n_experts + 2, rows)) * p.n_rt;
   if (most > (int64_t(1) << 30)) return 0;
-  if (!gm_map(&p.b, x, type, 1, rows, k, ldx, 0, few ? 16 : 128) ||
-      (!few && !gm_map(&p.b32, x, type, 1, rows, k, ldx, 0, 32)))
-    return -1;
+  for (int i = 0; i < (few ? 1 : 4); ++i)
+    if (!gm_map_rows(p.b + i, x, type, rows, k, ldx, few ? 16 : 32 * (i + 1))) return -1;
   p.offsets = offsets;
   p.n_experts = n_experts;
   p.rows = static_cast<int>(rows);
@@ -936,7 +1064,9 @@ extern "C" si_status si_moe_matmul(const void *x, si_dtype type, int64_t rows, i
   GmParams p{};
   const int64_t most = gm_forward(p, few, x, type, rows, k, ldx, n_experts, n, few ? 128 : 256, offsets, workspace);
   if (most == 0) return SI_ERR_UNSUPPORTED;
-  if (most < 0 || !gm_map(&p.a, w, type, n_experts, outer, inner, ldw, matw, cols ? 64 : 128)) return SI_ERR_CUDA;
+  if (most < 0 || !(cols ? gm_map_mn(&p.a, &p.whole_a, w, type, n_experts, k, n, ldw, matw)
+                         : gm_map(&p.a, w, type, {k, n, ldw, 1, 0, n_experts, matw}, 128)))
+    return SI_ERR_CUDA;
   p.out = out;
   p.ld = ldo;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -966,8 +1096,11 @@ extern "C" si_status si_moe_matmul_grad_w(const void *gy, int64_t ldg, const voi
   if (!gy || !x || !aligned16(gy) || !aligned16(x) || !gm_whole(offsets, 4) || !gm_ld(ldg, n, 2) || !gm_ld(ldx, k, 2))
     return SI_ERR_INVALID_ARG;
   if (workspace && (!aligned256(workspace) || workspace_bytes < sizeof(WsHeader))) return SI_ERR_WORKSPACE;
-  if (!gm_map(&p.a, gy, type, 1, rows, n, ldg, 0, kGmK) || !gm_map(&p.b, x, type, 1, rows, k, ldx, 0, kGmK) ||
-      !gm_map(&p.o, gw, gw_type, n_experts, n, k, k, n * k, 32))
+  if (!gm_map_mn(&p.a, &p.whole_a, gy, type, 1, rows, n, ldg, 0) ||
+      !gm_map_mn(p.b, &p.whole_b, x, type, 1, rows, k, ldx, 0) ||
+      !gm_map_mn(&p.ta, &p.whole_a, gy, type, 1, rows, n, ldg, 0, 16) ||
+      !gm_map_mn(&p.tb, &p.whole_b, x, type, 1, rows, k, ldx, 0, 16) ||
+      !gm_map(&p.o, gw, gw_type, {k, n, k, 1, 0, n_experts, n * k}, 32, 1, 64))
     return SI_ERR_CUDA;
   p.offsets = offsets;
   p.n_experts = n_experts;
@@ -995,7 +1128,8 @@ extern "C" si_status si_moe_gateup(const void *x, si_dtype type, int64_t rows, i
   const int64_t most = gm_forward(p, few, x, type, rows, hidden, ldx, n_experts, inter, 128, offsets, workspace);
   if (most == 0) return SI_ERR_UNSUPPORTED;
   if (most < 0 ||
-      !gm_map(&p.a, gate_up, type, n_experts, 2 * inter, hidden, hidden, 2 * inter * hidden, few ? 128 : 64))
+      !gm_map(&p.a, gate_up, type, {hidden, inter, hidden, 2, inter * hidden, n_experts, 2 * inter * hidden},
+              few ? 128 : 64, 2))
     return SI_ERR_CUDA;
   p.out = h;
   p.ld = inter;
@@ -1027,7 +1161,7 @@ extern "C" si_status si_moe_down_backward(const void *gy, si_dtype type, int64_t
   if (!gm_type(type)) return SI_ERR_UNSUPPORTED;
   if (rows == 0) return SI_OK;
   if (!gy || !down || !codes || !scales || !ggu || !aligned16(gy) || !aligned16(down) || !gm_whole(offsets, 4) ||
-      !gm_whole(ggu, 2) || (wh && !gm_whole(wh, 2)) || (row_w && !gm_whole(row_w, 4)) ||
+      !aligned16(codes) || !aligned16(ggu) || !aligned16(wh) || (row_w && !gm_whole(row_w, 4)) ||
       (order && !gm_whole(order, 4)) || (gw && !gm_whole(gw, 4)) || !gm_ld(ldg, hidden, 2))
     return SI_ERR_INVALID_ARG;
   if ((gw && !workspace) ||
@@ -1038,7 +1172,7 @@ extern "C" si_status si_moe_down_backward(const void *gy, si_dtype type, int64_t
   GmParams p{};
   const int64_t most = gm_forward(p, few, gy, type, rows, hidden, ldg, n_experts, inter, few ? 128 : 256, offsets, workspace);
   if (most == 0) return SI_ERR_UNSUPPORTED;
-  if (most < 0 || !gm_map(&p.a, down, type, n_experts, hidden, inter, inter, hidden * inter, 64)) return SI_ERR_CUDA;
+  if (most < 0 || !gm_map_mn(&p.a, &p.whole_a, down, type, n_experts, hidden, inter, inter, hidden * inter)) return SI_ERR_CUDA;
   p.out = ggu;
   p.codes = static_cast<uint8_t *>(const_cast<void *>(codes));
   p.scales = static_cast<uint8_t *>(const_cast<void *>(scales));

@@ -40,15 +40,11 @@ SI_DEV uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
 SI_DEV void mbar_arrive_cluster(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
-// The same by threads that have written nothing for the other block: a release of the
-// cluster waits for all of the thread's stores (by the producers, stage for stage, it made
-// a product of 8192 x 2 rows 816 us instead of 330).
+// The same by a thread that has written nothing for the other block: a release of the
+// cluster waits for all of the thread's stores (as the producers' arrival, stage for stage, it
+// made a product of 8192 x 2 rows 816 us instead of 353).
 SI_DEV void mbar_arrive_cluster_relaxed(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-SI_DEV void mbar_expect_tx_cluster(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-               : "memory");
 }
 // mbar_wait_bounded, for what threads and copies of both blocks did before they
 // arrived.
@@ -80,19 +76,27 @@ static __device__ __noinline__ bool mbar_wait_cluster_slow(uint64_t *bar, uint32
 SI_DEV bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, uint32_t *status) {
   return mbar_try_wait_cluster(bar, parity) || mbar_wait_cluster_slow(bar, parity, status);
 }
-// A box into this block's shared memory; its bytes count at a barrier of either block.
-SI_DEV void tma_load3_pair(void *dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
-      "%3, %4}], [%5];" ::"r"(smem_addr(dst)),
-      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
-      : "memory");
+// A box of four dimensions into this block's shared memory; PAIR: its bytes count at a
+// barrier of either block (an address in the cluster).
+template <bool PAIR> SI_DEV void tma_load4(void *dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+        "{%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
+        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+        "%5}], [%6];" ::"r"(smem_addr(dst)),
+        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
 }
 // A box of shared memory to a tensor, and the waits of the thread that asked for it:
 // until the boxes have been read.
-SI_DEV void tma_store3(const CUtensorMap *map, const void *src, int c0, int c1, int c2) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
-               "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(src))
+SI_DEV void tma_store4(const CUtensorMap *map, const void *src, int c0, int c1, int c2, int c3) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(map),
+               "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(src))
                : "memory");
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
@@ -157,16 +161,17 @@ inline EncodeTiled encode_tiled() {
   return fn;
 }
 
-// A tensor map of `rank` dimensions in the 128-byte swizzle; what lies outside reads
+// A tensor map of `rank` dimensions in a swizzle of shared memory; what lies outside reads
 // as zero. The call wants a current context, which a thread that has made no runtime
 // call yet (autograd's) lacks: choosing its device again gives it one.
 inline bool encode_map(CUtensorMap *m, CUtensorMapDataType type, const void *v, int rank, const cuuint64_t *dims,
-                       const cuuint64_t *strides, const cuuint32_t *box) {
+                       const cuuint64_t *strides, const cuuint32_t *box,
+                       CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   const EncodeTiled fn = encode_tiled();
   const cuuint32_t one[5] = {1, 1, 1, 1, 1};
   auto encode = [&] {
     return fn(m, type, static_cast<cuuint32_t>(rank), const_cast<void *>(v), dims, strides, box, one,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
   if (!fn) return false;

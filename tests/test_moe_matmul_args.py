@@ -66,7 +66,7 @@ def test_down_backward_refusals(lib):
               order=16, ggu=16, wh=16, gw=16, ws=256, nb=need)
     refused(lib.si_moe_down_backward, ok, [
         {"gy": None}, {"gy": 8}, {"ldg": 56}, {"down": None}, {"down": 8}, {"off": None}, {"codes": None}, {"scales": None},
-        {"w": 18}, {"order": 18}, {"ggu": None}, {"ggu": 17}, {"wh": 17}, {"gw": 18}, {"hidden": 60}, {"inter": 20},
+        {"w": 18}, {"order": 18}, {"ggu": None}, {"ggu": 17}, {"wh": 17}, {"codes": 8}, {"ggu": 8}, {"wh": 24}, {"gw": 18}, {"hidden": 60}, {"inter": 20},
         {"e": 1025}, {"rows": -1}], BAD)
     refused(lib.si_moe_down_backward, ok, [{"type": m.SI_F32}], UNS)
     refused(lib.si_moe_down_backward, ok, [{"ws": None}, {"ws": 128}, {"nb": need - 1}, {"gw": None, "nb": 255}], WS)
