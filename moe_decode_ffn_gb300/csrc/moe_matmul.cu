@@ -53,27 +53,25 @@ template <int OP, int MODE, int OUT> struct GmCfg {
   static constexpr int CG = OP == kGmFew ? 1 : 2;                    // SMs of a tile
   static constexpr int MA = OP == kGmFew && MODE == kGmSwiglu ? 2 : 1;   // 128-row A tiles: gate and up
   static constexpr int kN = OP == kGmFew ? 16 : 256;                 // columns of an accumulator
-  // fp32 outputs are summed up in registers: 64 columns a warp instead of 128
-  static constexpr int kEpiWarps = OP == kGmFew ? 4 : OUT == kGmF32 ? 16 : 8;
+  // fp32 outputs are summed up in registers: 64 columns a warp instead of 128; and what SwiGLU
+  // asks for goes faster with more warps to take turns
+  static constexpr int kEpiWarps = OP == kGmFew ? 4 : OUT == kGmF32 || MODE != kGmPlain ? 16 : 8;
   static constexpr int kBWarp = 2 + kEpiWarps, kTailWarp = OP == kGmGrad ? kBWarp + 1 : -1;
   static constexpr int kThreads = 32 * (kBWarp + 1 + (OP == kGmGrad));
   static constexpr int kABytes = MA * 128 * 128, kBBytes = kN / CG * 128, kStage = kABytes + kBBytes;
   static constexpr int kList = OP == kGmGrad ? 0 : (kGmGroups + 1) * 8;
-  // gate and up rows lie on different lanes: u on its way to g's warps, 16 rows of 32
-  // features, twice for each of 4 pairs of warps
-  static constexpr int kSwap = OP == kGmWide && MODE == kGmSwiglu ? 4 * 2 * 16 * 32 * 4 : 0;
   static constexpr int kBox = OP == kGmGrad ? 2048 : 1024;           // a warp's rows on their way out
   static constexpr int kOut = kEpiWarps * kBox;
   // the last rows of an expert, of both operands, twice
   static constexpr int kTail = OP == kGmGrad ? 2 * 2 * kGmTail : 0;
-  static constexpr int kFit = (227 * 1024 - kList - kSwap - kOut - kTail - 1536) / kStage;
+  static constexpr int kFit = (227 * 1024 - kList - kOut - kTail - 1536) / kStage;
   static constexpr int kStages = kFit < 12 ? kFit : 12;
   static constexpr int kAccCols = MA * kN;       // of one accumulator; two of them
   static constexpr int kCols = 2 * kAccCols <= 32 ? 32 : 2 * kAccCols <= 64 ? 64 : 512;
   static_assert(2 * kAccCols <= kCols, "tensor memory has 512 columns");
   static constexpr int kBars = 2 * kStages + 11;
   static_assert(8 * kBars + 4 <= 512, "barriers");
-  static constexpr int kSmem = kStages * kStage + kTail + kOut + kSwap + 512 + kList + 1024;
+  static constexpr int kSmem = kStages * kStage + kTail + kOut + 512 + kList + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -169,7 +167,9 @@ template <int OP> SI_DEV void gm_list(const GmParams &p, GmList &l) {
   }
   __syncthreads();
 }
-// Tile w: the tiles of a group's rows lie side by side for the same features.
+// Tile w: the tiles of a group's rows lie side by side for the same features. kGmGrad reads
+// its expert's bounds through the L1: from the L2, where all blocks' warps ask for the same
+// few lines, 128 rows an expert took 185 us instead of TODO.
 template <int OP> SI_DEV GmTile gm_tile(const GmParams &p, const GmList &l, int w) {
   GmTile t;
   if constexpr (OP == kGmGrad) {
@@ -177,8 +177,8 @@ template <int OP> SI_DEV GmTile gm_tile(const GmParams &p, const GmList &l, int 
     const int r = w / p.n_ct;
     t.rt = r % p.n_rt;
     t.e = r / p.n_rt;
-    t.row0 = min(max(__ldcg(p.offsets + t.e), 0), p.rows);
-    t.count = max(min(max(__ldcg(p.offsets + t.e + 1), 0), p.rows) - t.row0, 0);
+    t.row0 = min(max(__ldg(p.offsets + t.e), 0), p.rows);
+    t.count = max(min(max(__ldg(p.offsets + t.e + 1), 0), p.rows) - t.row0, 0);
   } else {
     int lo = 0, hi = p.n_experts + 1;            // the last group whose first tile is at most w
     while (lo < hi) {
@@ -280,10 +280,11 @@ SI_DEV float gm_logistic(float g) {
   return r;
 }
 // The largest magnitude over the warp of each of 16 values, cut to 16 bits (which hold
-// its exponent): value 2 i in the low half of top[i]. A lane hands half of its words on
-// at every step, so 17 shuffles do; redux.sync for each value made gate and up of
-// 512 rows an expert, kept, 528 us instead of TODO.
-SI_DEV void gm_top16(const float v[16], int lane, uint32_t top[8]) {
+// its exponent): lane j gets value (j & 15)'s, in the low half for even ones. A lane hands
+// half of its words on at every step, so 10 shuffles do (redux.sync for each value made gate
+// and up of 512 rows an expert, kept, 528 us instead of TODO).
+SI_DEV uint32_t gm_top16(const float v[16], int lane) {
+  uint32_t top[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     top[i] = __byte_perm(__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1]), 0x7632) & 0x7FFF7FFFu;
@@ -299,8 +300,7 @@ SI_DEV void gm_top16(const float v[16], int lane, uint32_t top[8]) {
   uint32_t t = top[0];                           // word lane / 4
   t = __vmaxu2(t, __shfl_xor_sync(0xffffffffu, t, 2));
   t = __vmaxu2(t, __shfl_xor_sync(0xffffffffu, t, 1));
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top[i] = __shfl_sync(0xffffffffu, t, 4 * i);
+  return __shfl_sync(0xffffffffu, t, (lane & 14) * 2) & 0x7FFF7FFFu;
 }
 
 // The tokens of a tile, 16 columns of the accumulator at a time, dealt out to the
@@ -310,9 +310,9 @@ template <int PARTS> SI_DEV int gm_piece(int i, int part) { return (i * PARTS + 
 // This lane's feature f of 16 rows from row0, `left` of them in the tile: fp32 rows
 // straight from the registers (128 bytes of a row a store), others in 16-byte words
 // through `box` (1024 bytes of the warp's own).
-template <int OUT>
+template <int OUT, int ROWS = 16>
 SI_DEV void gm_write16(const GmParams &p, void *out, int64_t ld, int f, int lane, int64_t row0, int left,
-                       const float v[16], uint8_t *box) {
+                       const float *v, uint8_t *box) {
   if constexpr (OUT == kGmF32) {
     if (f >= p.n) return;
     float *o = static_cast<float *>(out) + row0 * ld + f;
@@ -322,11 +322,11 @@ SI_DEV void gm_write16(const GmParams &p, void *out, int64_t ld, int f, int lane
   } else {
     __syncwarp();                                // the box has been read
 #pragma unroll
-    for (int j = 0; j < 16; ++j) gm_store1<OUT>(box + j * 64, lane, v[j]);
+    for (int j = 0; j < ROWS; ++j) gm_store1<OUT>(box + j * 64, lane, v[j]);
     __syncwarp();
     const int f0 = f - lane + (lane & 3) * 8;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < ROWS / 8; ++h) {
       const int j = h * 8 + (lane >> 2);
       const uint4 w = *reinterpret_cast<const uint4 *>(box + j * 64 + (lane & 3) * 16);
       if (j < left && f0 < p.n) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + (row0 + j) * ld + f0) = w;
@@ -334,18 +334,28 @@ SI_DEV void gm_write16(const GmParams &p, void *out, int64_t ld, int f, int lane
   }
 }
 // The 8-bit blocks of 16 rows at this warp's 32 values (side 0: g, 1: u) from feature
-// f - lane, through `box` (512 bytes of the warp's own) so that rows leave in 16-byte words.
+// f - lane, through `box` (512 bytes of the warp's own) so that rows leave in 16-byte
+// words. Lane j finds the scale of row j and its inverse, which the others fetch.
 SI_DEV void gm_keep16(const GmParams &p, int f, int lane, int64_t row0, int left, const float v[16], int side,
                       uint8_t *box) {
-  uint32_t top[8];
-  gm_top16(v, lane, top);
-  uint32_t mine = 0;                             // lane j: the scale of row j
+  const uint32_t top = gm_top16(v, lane), s = (lane & 1 ? top >> 23 : top >> 7) & 0xFFu;
+  // 64 / X, so that a value's code is one multiplication and addition away (1.5 * 2^23 leaves
+  // it in the low byte); X below 2^-121 or an infinity or a NaN take the long way
+  const float up = __uint_as_float((260u - s) << 23);
+  const bool far = s < 6u || s == 255u;
   __syncwarp();                                  // the box has been read
+  if (!__any_sync(0xffffffffu, far)) {
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const uint32_t s = j & 1 ? top[j / 2] >> 23 : (top[j / 2] >> 7) & 0xFFu;
-    if (lane == j) mine = s;
-    box[j * 32 + lane] = static_cast<uint8_t>(s == 255u ? 0u : mi_code(v[j] * mi_inv_scale(s)));
+    for (int j = 0; j < 16; ++j) {
+      const float c = fmaf(v[j], __shfl_sync(0xffffffffu, up, j), 12582912.f);
+      box[j * 32 + lane] = static_cast<uint8_t>(__float_as_uint(fminf(fmaxf(c, 12582912.f - 127.f), 12582912.f + 127.f)));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const uint32_t sj = __shfl_sync(0xffffffffu, s, j);
+      box[j * 32 + lane] = static_cast<uint8_t>(sj == 255u ? 0u : mi_code(v[j] * mi_inv_scale(sj)));
+    }
   }
   __syncwarp();
   const int f0 = f - lane, j = lane >> 1, c = (lane & 1) * 16;
@@ -360,7 +370,7 @@ SI_DEV void gm_keep16(const GmParams &p, int f, int lane, int64_t row0, int left
       if (f0 + c + 8 < p.n) *reinterpret_cast<uint2 *>(to + 8) = make_uint2(w.z, w.w);
     }
   }
-  if (lane < 16 && lane < left) p.scales[(row0 + lane) * 2 * blocks + side * blocks + (f0 >> 5)] = static_cast<uint8_t>(mine);
+  if (lane < 16 && lane < left) p.scales[(row0 + lane) * 2 * blocks + side * blocks + (f0 >> 5)] = static_cast<uint8_t>(s);
 }
 
 // Sums of 16 values over the warp: value (lane / 2) on even lanes, each lane handing
@@ -469,13 +479,12 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
   extern __shared__ uint8_t gm_smem[];
   uint8_t *base = gm_smem + ((1024u - (smem_addr(gm_smem) & 1023u)) & 1023u);
   uint8_t *tails = base + S * C::kStage, *outs = tails + C::kTail;
-  float *swap = reinterpret_cast<float *>(outs + C::kOut);
-  uint64_t *full = reinterpret_cast<uint64_t *>(outs + C::kOut + C::kSwap);
+  uint64_t *full = reinterpret_cast<uint64_t *>(outs + C::kOut);
   uint64_t *empty = full + S, *acc_full = empty + S, *acc_empty = acc_full + 2, *drain = acc_empty + 2;
   // tails: landed in this block, cleared in both, read by their MMA
   uint64_t *tail_full = drain + 1, *tail_ready = tail_full + 2, *tail_empty = tail_ready + 2;
   uint32_t *s_taddr = reinterpret_cast<uint32_t *>(tail_empty + 2);
-  GmList &list = *reinterpret_cast<GmList *>(outs + C::kOut + C::kSwap + 512);
+  GmList &list = *reinterpret_cast<GmList *>(outs + C::kOut + 512);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;
 
@@ -848,24 +857,28 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
               for (int j = 0; j < 16; ++j) v[j] = v[j] * gm_logistic(v[j]) * u[j];
               gm_write16<OUT>(p, p.out, p.ld, f, lane, row0, left, v, stage);
             } else {
-              // lanes 0-63 hold g, 64-127 u: u goes to g's warps through shared memory
-              const int side = q >> 1;
-              float *box = swap + ((part * 2 + (q & 1)) * 2 + (i & 1)) * 512;
-              const int pair = 1 + part * 2 + (q & 1);
+              // lanes 0-63 hold g, 64-127 u of the same features: a pair of warps exchanges
+              // halves of its rows through their boxes, g's takes the first 8, u's the last
+              const int side = q >> 1, pair = 1 + part * 2 + (q & 1);
               if (zero) zeros(v);
               else read16(acc + j0, v);
               if (!zero && i == mine - 1) release();
-              if (side == 1) {
+              float *own = reinterpret_cast<float *>(stage);
+              // (warps 2 and 3 of four read lanes 64-127)
+              const float *other = reinterpret_cast<const float *>(stage + (side ? 2 : -2) * C::kBox);
+              __syncwarp();          // the box has been read
 #pragma unroll
-                for (int j = 0; j < 16; ++j) box[j * 32 + lane] = v[j];
+              for (int j = 0; j < 8; ++j) own[j * 32 + lane] = side ? v[j] : v[8 + j];
+              asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+              float h[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const float o = other[j * 32 + lane], g = side ? o : v[j], u = side ? v[8 + j] : o;
+                h[j] = g * gm_logistic(g) * u;
               }
               asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+              gm_write16<OUT, 8>(p, p.out, p.ld, f, lane, row0 + side * 8, left - side * 8, h, stage);
               if (tf < p.n && p.codes) gm_keep16(p, f, lane, row0, left, v, side, stage);
-              if (side == 0) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = v[j] * gm_logistic(v[j]) * box[j * 32 + lane];
-                gm_write16<OUT>(p, p.out, p.ld, f, lane, row0, left, v, stage);
-              }
             }
           }
           if constexpr (MODE == kGmSwigluBack) {
