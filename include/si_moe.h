@@ -597,7 +597,7 @@ si_status si_dequantize_mxint8(const void *codes, const void *scales, int64_t ro
  *           order lies outside [0, rows) get ggu 0, wh 0 and write no gw. NULL: row r itself
  *   row_w   device fp32 [rows], or NULL: 1; wh, gw (fp32 [rows]) may be NULL
  * gu, h, gh, ggu [rows][2 * inter], wh of `type` (SI_F32, SI_F16 or SI_BF16), contiguous but
- * for gu's rows; fp32 arithmetic, rounded once. rows 0: nothing is done. Outputs may
+ * for gu's rows; inter 1..2^24; fp32 arithmetic, rounded once. rows 0: nothing is done. Outputs may
  * not alias inputs.
  */
 si_status si_swiglu(const void *gu, si_dtype type, int64_t rows, int64_t inter, int64_t row_stride, void *h,

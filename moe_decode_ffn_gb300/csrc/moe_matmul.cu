@@ -271,14 +271,6 @@ template <int OUT> SI_DEV void gm_store1(void *out, int64_t at, float v) {
   else static_cast<float *>(out)[at] = v;
 }
 
-// The logistic function; g below -87 gives 0 where the reciprocal is below the normal
-// range (s < 2^-125). ex2 and rcp of the hardware, each within 2 units in the last place.
-SI_DEV float gm_logistic(float g) {
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-  return r;
-}
 // The largest magnitude over the warp of each of 16 values, cut to 16 bits (which hold
 // its exponent): lane j gets value (j & 15)'s, in the low half for even ones. A lane hands
 // half of its words on at every step, so 10 shuffles do (redux.sync for each value made gate
@@ -338,18 +330,14 @@ SI_DEV void gm_write16(const GmParams &p, void *out, int64_t ld, int f, int lane
 // words. Lane j finds the scale of row j and its inverse, which the others fetch.
 SI_DEV void gm_keep16(const GmParams &p, int f, int lane, int64_t row0, int left, const float v[16], int side,
                       uint8_t *box) {
-  const uint32_t top = gm_top16(v, lane), s = (lane & 1 ? top >> 23 : top >> 7) & 0xFFu;
-  // 64 / X, so that a value's code is one multiplication and addition away (1.5 * 2^23 leaves
-  // it in the low byte); X below 2^-121 or an infinity or a NaN take the long way
-  const float up = __uint_as_float((260u - s) << 23);
-  const bool far = s < 6u || s == 255u;
+  const uint32_t pair = gm_top16(v, lane), top = lane & 1 ? pair & 0xFFFF0000u : pair << 16, s = mi_scale_of(top);
+  const bool far = mi_far(top);
+  const float up = far ? 0.f : mi_inv_step(s);
   __syncwarp();                                  // the box has been read
   if (!__any_sync(0xffffffffu, far)) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float c = fmaf(v[j], __shfl_sync(0xffffffffu, up, j), 12582912.f);
-      box[j * 32 + lane] = static_cast<uint8_t>(__float_as_uint(fminf(fmaxf(c, 12582912.f - 127.f), 12582912.f + 127.f)));
-    }
+    for (int j = 0; j < 16; ++j)
+      box[j * 32 + lane] = static_cast<uint8_t>(mi_code_near(v[j], __shfl_sync(0xffffffffu, up, j)));
   } else {
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
@@ -445,7 +433,7 @@ SI_DEV void gm_swiglu_back16(const GmParams &p, int f, int lane, int64_t row0, i
     const float g = static_cast<float>(static_cast<int8_t>(box[j * 32 + lane])) * mi_step(__shfl_sync(0xffffffffu, k.s, j));
     const float u = static_cast<float>(static_cast<int8_t>(box[512 + j * 32 + lane])) *
                     mi_step(__shfl_sync(0xffffffffu, k.s, 16 + j));
-    const float c = __shfl_sync(0xffffffffu, k.c, j), l = gm_logistic(g), si = g * l, h = si * u, cd = c * gh[j];
+    const float c = __shfl_sync(0xffffffffu, k.c, j), l = mi_logistic(g), si = g * l, h = si * u, cd = c * gh[j];
     const bool live = (k.live >> j) & 1u;        // a row of no pair: zeros
     gg[j] = live ? cd * u * (l * fmaf(g, 1.f - l, 1.f)) : 0.f;
     gu[j] = live ? cd * si : 0.f;
@@ -854,7 +842,7 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
                 gm_keep16(p, f, lane, row0, left, u, 1, stage);
               }
 #pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] = v[j] * gm_logistic(v[j]) * u[j];
+              for (int j = 0; j < 16; ++j) v[j] = v[j] * mi_logistic(v[j]) * u[j];
               gm_write16<OUT>(p, p.out, p.ld, f, lane, row0, left, v, stage);
             } else {
               // lanes 0-63 hold g, 64-127 u of the same features: a pair of warps exchanges
@@ -874,7 +862,7 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
                 const float o = other[j * 32 + lane], g = side ? o : v[j], u = side ? v[8 + j] : o;
-                h[j] = g * gm_logistic(g) * u;
+                h[j] = g * mi_logistic(g) * u;
               }
               asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
               gm_write16<OUT, 8>(p, p.out, p.ld, f, lane, row0 + side * 8, left - side * 8, h, stage);

@@ -100,10 +100,10 @@ template <typename T> SI_DEV uint4 pack16(const float *v) {
   for (int i = 0; i < 4; ++i) {
     if constexpr (sizeof(T) == 4) {
       w[i] = __float_as_uint(v[i]);
-    } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
-      w[i] = bf16_bits(v[2 * i]) | (static_cast<uint32_t>(bf16_bits(v[2 * i + 1])) << 16);
+    } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {   // both at once
+      asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(w[i]) : "f"(v[2 * i]), "f"(v[2 * i + 1]));
     } else {
-      w[i] = float_to_half_bits(v[2 * i]) | (static_cast<uint32_t>(float_to_half_bits(v[2 * i + 1])) << 16);
+      asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(w[i]) : "f"(v[2 * i]), "f"(v[2 * i + 1]));
     }
   }
   return make_uint4(w[0], w[1], w[2], w[3]);

@@ -26,13 +26,29 @@ SI_DEV float mi_step(uint32_t s) {
 SI_DEV uint32_t mi_code(float v) {
   return __float_as_uint(fmaf(fminf(fmaxf(v, -127.f / 64.f), 127.f / 64.f), 64.f, 12582912.f));
 }
+// Nearly every block needs less: one multiplication and addition by 64 / X. Not the ones that
+// mi_far() names: X below 2^-121, where 64 / X passes fp32; an infinity or a NaN; and a
+// largest magnitude from 127.5 / 64 X on (all seven leading bits of the mantissa), which
+// has to be kept within 127. `top`: at least its upper 16 bits.
+SI_DEV bool mi_far(uint32_t top) { return top < (6u << 23) || top >= (255u << 23) || (~top & 0x7F0000u) == 0; }
+SI_DEV float mi_inv_step(uint32_t s) { return __uint_as_float((260u - s) << 23); }
+SI_DEV uint32_t mi_code_near(float v, float inv_step) { return __float_as_uint(fmaf(v, inv_step, 12582912.f)); }
 SI_DEV uint32_t mi_pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
-// Four codes to their integers as fp32.
+// Four codes to their integers as fp32: code + 128 becomes the low byte of 2^23 + (code + 128).
 SI_DEV void mi_values4(uint32_t w, float v[4]) {
+  w ^= 0x80808080u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = static_cast<float>(static_cast<int8_t>(w >> (8 * i)));
+  for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 + i)) - 8388736.f;
+}
+// The logistic function; g below -87 gives 0 where the reciprocal is below the normal
+// range (s < 2^-125). ex2 and rcp of the hardware, each within 2 units in the last place.
+SI_DEV float mi_logistic(float g) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
 }
 // Scales of a row of `cols` values.
 __host__ __device__ constexpr int64_t mi_blocks(int64_t cols) { return (cols + 31) / 32; }
