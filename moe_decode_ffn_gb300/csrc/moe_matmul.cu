@@ -418,33 +418,61 @@ SI_DEV GmKept gm_load_kept(const GmParams &p, int f, int lane, int64_t row0, int
   k.live = __ballot_sync(0xffffffffu, live);
   return k;
 }
-// The gradients of h = silu(g) u in 16 rows: gh comes from the accumulator.
+// The gradients of h = silu(g) u in 16 rows: gh comes from the accumulator. The codes go
+// to the lanes of their features through `box` (1024 bytes of the warp's own), g's and u's
+// side by side; the results leave through it 8 rows at a time.
 template <int OUT>
 SI_DEV void gm_swiglu_back16(const GmParams &p, int f, int lane, int64_t row0, int left, const GmKept &k, float gh[16],
                              int slot, uint8_t *box) {
-  const bool in = f < p.n;
   __syncwarp();                                  // the box has been read
-  *reinterpret_cast<uint4 *>(box + lane * 16) = k.g;
-  *reinterpret_cast<uint4 *>(box + 512 + lane * 16) = k.u;
-  __syncwarp();
-  float gg[16], gu[16], ch[16];
+  const uint32_t g4[4] = {k.g.x, k.g.y, k.g.z, k.g.w}, u4[4] = {k.u.x, k.u.y, k.u.z, k.u.w};
+  uint32_t w[8];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const float g = static_cast<float>(static_cast<int8_t>(box[j * 32 + lane])) * mi_step(__shfl_sync(0xffffffffu, k.s, j));
-    const float u = static_cast<float>(static_cast<int8_t>(box[512 + j * 32 + lane])) *
-                    mi_step(__shfl_sync(0xffffffffu, k.s, 16 + j));
-    const float c = __shfl_sync(0xffffffffu, k.c, j), l = mi_logistic(g), si = g * l, h = si * u, cd = c * gh[j];
-    const bool live = (k.live >> j) & 1u;        // a row of no pair: zeros
-    gg[j] = live ? cd * u * (l * fmaf(g, 1.f - l, 1.f)) : 0.f;
-    gu[j] = live ? cd * si : 0.f;
-    ch[j] = live ? c * h : 0.f;
-    gh[j] = in && live ? gh[j] * h : 0.f;
+  for (int i = 0; i < 4; ++i) {                  // code + 128, as mi_values4 has it
+    w[2 * i] = __byte_perm(g4[i], u4[i], 0x5140) ^ 0x80808080u;
+    w[2 * i + 1] = __byte_perm(g4[i], u4[i], 0x7362) ^ 0x80808080u;
   }
+  *reinterpret_cast<uint4 *>(box + lane * 32) = make_uint4(w[0], w[1], w[2], w[3]);
+  *reinterpret_cast<uint4 *>(box + lane * 32 + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+  __syncwarp();
+  uint32_t q[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) q[j] = *reinterpret_cast<const uint16_t *>(box + (j * 32 + lane) * 2);
+  const float step = mi_step(k.s);               // lane j: of row j's g, lane 16 + j: of its u
   const int64_t ld = 2 * static_cast<int64_t>(p.n);
-  gm_write16<OUT>(p, p.out, ld, f, lane, row0, left, gg, box);
-  gm_write16<OUT>(p, static_cast<uint16_t *>(p.out) + p.n, ld, f, lane, row0, left, gu, box);
-  if (p.wh) gm_write16<OUT>(p, p.wh, p.n, f, lane, row0, left, ch, box);
+#pragma unroll
+  for (int h = 0; h < 16; h += 8) {
+    float ch[8];
+    __syncwarp();                                // the box has been read
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int j = h + i;
+      const float g = (__uint_as_float(__byte_perm(q[j], 0x4B000000u, 0x7540)) - 8388736.f) * __shfl_sync(0xffffffffu, step, j);
+      const float u = (__uint_as_float(__byte_perm(q[j], 0x4B000000u, 0x7541)) - 8388736.f) * __shfl_sync(0xffffffffu, step, 16 + j);
+      const float c = __shfl_sync(0xffffffffu, k.c, j), l = mi_logistic(g), si = g * l, hv = si * u, cd = c * gh[j];
+      float gg = cd * u * fmaf(si, 1.f - l, l), gu = cd * si;   // s (1 + g (1 - s))
+      ch[i] = c * hv;
+      gh[j] *= hv;
+      if (!((k.live >> j) & 1u)) gg = gu = ch[i] = gh[j] = 0.f;   // a row of no pair, the same for the warp
+      gm_store1<OUT>(box + i * 64, lane, gg);
+      gm_store1<OUT>(box + 512 + i * 64, lane, gu);
+    }
+    __syncwarp();
+    const int r = lane >> 2, f0 = f - lane + (lane & 3) * 8;
+    const bool out = h + r < left && f0 < p.n;
+    const uint4 a = *reinterpret_cast<const uint4 *>(box + lane * 16), b = *reinterpret_cast<const uint4 *>(box + 512 + lane * 16);
+    if (out) {
+      uint16_t *to = static_cast<uint16_t *>(p.out) + (row0 + h + r) * ld + f0;
+      *reinterpret_cast<uint4 *>(to) = a;
+      *reinterpret_cast<uint4 *>(to + p.n) = b;
+    }
+    if (p.wh) gm_write16<OUT, 8>(p, p.wh, p.n, f, lane, row0 + h, left - h, ch, box);
+  }
   if (!p.part) return;
+  if (f >= p.n) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) gh[j] = 0.f;
+  }
   const float sum = gm_reduce16(gh, lane);
   const int j = lane >> 1;
   if (!(lane & 1) && j < left) p.part[(row0 + j) * p.parts + slot] = sum;
