@@ -594,7 +594,8 @@ si_status si_dequantize_mxint8(const void *codes, const void *scales, int64_t ro
  *     gw = sum_i gh[i] * h[i], the gradient of c;  h = g * s * u
  *   order   device int32 [rows]: row r has weight row_w[order[r]] and writes
  *           gw[order[r]] (si_moe_sort's order with topk_w and its gradient); rows whose
- *           order lies outside [0, rows) get ggu 0, wh 0 and write no gw. NULL: row r itself
+ *           order lies outside [0, rows) get ggu 0 and wh 0, pairs without a row gw 0.
+ *           No pair may have two rows. NULL: row r itself
  *   row_w   device fp32 [rows], or NULL: 1; wh, gw (fp32 [rows]) may be NULL
  * gu, h, gh, ggu [rows][2 * inter], wh of `type` (SI_F32, SI_F16 or SI_BF16), contiguous but
  * for gu's rows; inter 1..2^24; fp32 arithmetic, rounded once. rows 0: nothing is done. Outputs may
@@ -605,6 +606,41 @@ si_status si_swiglu(const void *gu, si_dtype type, int64_t rows, int64_t inter, 
 si_status si_swiglu_backward(const void *gh, si_dtype type, int64_t rows, int64_t inter, const void *codes,
                              const void *scales, const float *row_w, const int32_t *order, void *ggu, void *wh,
                              float *gw, void *stream);
+
+/* The routed experts of one layer in 16 bits. */
+typedef struct si_experts {
+  si_dtype type;              /* SI_BF16 or SI_F16 */
+  int hidden, inter;          /* H, I: multiples of 8, <= 2^20 */
+  int n_experts;              /* 1..1024 */
+  const void *gate_up;        /* n_experts matrices [2 I][H], the gate's rows first */
+  const void *down;           /* n_experts matrices [H][I] */
+} si_experts;
+
+/*
+ * si_moe_experts - the routed experts of n_tokens tokens on the tensor cores, with
+ * what their gradients need: si_moe_sort, si_moe_gather, si_moe_gateup, si_moe_matmul
+ * with fp32 rows and si_moe_combine_f32 in one call:
+ *     y[t] = sum_r topk_w[t][r] * down_e (silu(g) * u), (g, u) = gate_up_e x[t], e = topk_ids[t][r]
+ * si_moe_experts_backward - the gradients of x, topk_w, gate_up and down from gy, each left
+ * out where its pointer is NULL (x may be NULL without ggate_up).
+ *   x, gy, y, gx  device [n_tokens][H] of L->type; topk_ids device int32 [n_tokens][top_k], ids
+ *                 outside [0, n_experts) are dropped; topk_w, gw device fp32 [n_tokens][top_k]
+ *   ggate_up, gdown  as gate_up and down; an expert without tokens gets zeros
+ *   kept       si_moe_experts_kept_bytes(L, n_tokens, top_k) bytes that the forward call fills
+ *              for the backward call (the order of the pairs; g and u in 8 bits), or NULL
+ *   workspace  si_moe_experts_workspace_bytes(L, n_tokens, top_k) bytes for either call,
+ *              its first 256 zeroed once; holds nothing between calls but the status word
+ * kept and workspace on 256-byte, the others on 16-byte boundaries (lists and weights on 4).
+ * n_tokens >= 1, top_k 1..8.
+ */
+size_t si_moe_experts_workspace_bytes(const si_experts *L, int n_tokens, int top_k);
+size_t si_moe_experts_kept_bytes(const si_experts *L, int n_tokens, int top_k);
+si_status si_moe_experts(const si_experts *L, int n_tokens, int top_k, const void *x, const int32_t *topk_ids,
+                         const float *topk_w, void *y, void *kept, void *workspace, size_t workspace_bytes,
+                         void *stream);
+si_status si_moe_experts_backward(const si_experts *L, int n_tokens, int top_k, const void *gy, const void *x,
+                                  const float *topk_w, const void *kept, void *gx, float *gw, void *ggate_up,
+                                  void *gdown, void *workspace, size_t workspace_bytes, void *stream);
 
 /* The routed experts of one layer as MXFP4 matrices. */
 typedef struct si_mxfp4_experts {

@@ -56,6 +56,13 @@ class SiMxfp4Experts(ctypes.Structure):
     ]
 
 
+class SiExperts(ctypes.Structure):
+    """Mirror of ``si_experts``."""
+    _fields_ = [
+        ("type", _i32), ("hidden", _i32), ("inter", _i32), ("n_experts", _i32), ("gate_up", _vp), ("down", _vp),
+    ]
+
+
 # name -> (restype, argtypes), exactly the exports of include/si_moe.h
 SIGNATURES = {
     "si_status_string": (ctypes.c_char_p, [_i32]),
@@ -117,6 +124,11 @@ SIGNATURES = {
     "si_moe_down_backward_workspace_bytes": (_sz, [_i64, _i32, _i64]),
     "si_moe_down_backward": (_i32, [_vp, _i32, _i64, _i64, _vp, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                     _vp, _vp, _sz, _vp]),
+    "si_moe_experts_workspace_bytes": (_sz, [ctypes.POINTER(SiExperts), _i32, _i32]),
+    "si_moe_experts_kept_bytes": (_sz, [ctypes.POINTER(SiExperts), _i32, _i32]),
+    "si_moe_experts": (_i32, [ctypes.POINTER(SiExperts), _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "si_moe_experts_backward": (_i32, [ctypes.POINTER(SiExperts), _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                       _vp, _sz, _vp]),
     "si_quantize_mxint8": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp]),
     "si_dequantize_mxint8": (_i32, [_vp, _vp, _i64, _i64, _vp, _i32, _i64, _vp]),
     "si_swiglu": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp]),
@@ -1031,11 +1043,18 @@ def si_moe_matmul(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, dtype
         if out is not None:
             raise ValueError("out cannot be given where x or w requires a gradient")
         return _Matmul.apply(x, w, offsets, dtype, ws)
+    return _matmul(dev, x, w, offsets, dtype, out, ws)
+
+
+def _matmul(dev: int, x, w, offsets, dtype=None, out=None, ws=None, turned=False):
+    """si_moe_matmul without a history; ``turned``: through w transposed."""
     t = _half(x, "x")
     if x.dim() != 2:
         raise ValueError("x must be [R, k]")
     _same(w, x, "w", 3)
     (R, k), (E, n, k2, ldw, mat, by, wp) = x.shape, _matrices(w, "w")
+    if turned:
+        n, k2, by = k2, n, 1 - by
     if k != k2:
         raise ValueError(f"x is {k} wide, w takes {k2}")
     _width(n, "out")
@@ -1067,6 +1086,10 @@ def si_moe_matmul_grad_w(gy: torch.Tensor, x: torch.Tensor, offsets: torch.Tenso
     dev = gy.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(si_moe_matmul_grad_w, stream, gy, x, offsets, dtype, ws)
+    return _grad_w(dev, gy, x, offsets, dtype, ws)
+
+
+def _grad_w(dev: int, gy, x, offsets, dtype=None, ws=None):
     t = _half(gy, "gy")
     if gy.dim() != 2:
         raise ValueError("gy must be [R, n]")
@@ -1098,13 +1121,10 @@ def si_moe_matmul_backward(gy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, o
     dev = gy.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(si_moe_matmul_backward, stream, gy, x, w, offsets, ws)
-    with torch.no_grad():
-        _same(w, gy, "w", 3)
-        if w.shape[1:] != (gy.shape[-1], x.shape[-1]) or w.shape[0] != offsets.numel() - 1:
-            raise ValueError(f"w has shape {tuple(w.shape)}, expected "
-                             f"{(offsets.numel() - 1, gy.shape[-1], x.shape[-1])}")
-        gw = si_moe_matmul_grad_w(gy, x, offsets, None, ws)
-        return si_moe_matmul(gy, w.transpose(1, 2), offsets, None, None, ws), gw
+    gw = _grad_w(dev, gy, x, offsets, None, ws)
+    if w.shape != gw.shape:
+        raise ValueError(f"w has shape {tuple(w.shape)}, expected {tuple(gw.shape)}")
+    return _matmul(dev, gy, w, offsets, None, None, ws, True), gw
 
 
 class _Matmul(torch.autograd.Function):
@@ -1120,9 +1140,9 @@ class _Matmul(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, gy):
         x, w, offsets = ctx.saved_tensors
-        gy = gy.to(x.dtype).contiguous()
-        gx = si_moe_matmul(gy, w.transpose(1, 2), offsets, None, None, ctx.ws) if ctx.needs_input_grad[0] else None
-        gw = si_moe_matmul_grad_w(gy, x, offsets, None, ctx.ws) if ctx.needs_input_grad[1] else None
+        gy, dev, need = gy.to(x.dtype).contiguous(), x.get_device(), ctx.needs_input_grad
+        gx = _matmul(dev, gy, w, offsets, None, None, ctx.ws, True) if need[0] else None
+        gw = _grad_w(dev, gy, x, offsets, None, ctx.ws) if need[1] else None
         return gx, gw, None, None, None
 
 
@@ -1251,7 +1271,7 @@ def _swiglu_backward(gh, kept, w, order, want_wh, stream=None):
     op = None if order is None else _ptr(order, dev, R, _i32_t, "order")
     ggu = _empty((R, 2 * I), dtype=dtype, device=d)
     wh = _empty((R, I), dtype=dtype, device=d) if want_wh else None
-    gw = None if w is None else (torch.zeros if order is not None else _empty)(w.shape, dtype=_f32_t, device=d)
+    gw = None if w is None else _empty(w.shape, dtype=_f32_t, device=d)
     st = library().si_swiglu_backward(gp, _TYPES[dtype], R, I, cp, sp, wp, op, ggu.data_ptr(),
                                       wh.data_ptr() if want_wh else None, None if gw is None else gw.data_ptr(),
                                       _raw_stream(dev))
@@ -1348,9 +1368,9 @@ def _down_backward(gy, down, kept, offsets, w, order, ws, want_wh, want_gw, stre
     wh = _empty((R, I), dtype=gy.dtype, device=d) if want_wh else None
     gw = None
     if w is not None and want_gw:
-        gw = (torch.zeros if order is not None else _empty)(w.shape, dtype=_f32_t, device=d)
-        if ws is None:
-            ws = _scratch(moe_down_backward_workspace_bytes(R, E, I), d)
+        gw = _empty(w.shape, dtype=_f32_t, device=d)
+        if ws is None and R:                     # for the partial sums alone: nobody reads its status word
+            ws = _empty((moe_down_backward_workspace_bytes(R, E, I),), dtype=_u8, device=d)
     st = library().si_moe_down_backward(gp, t, R, ldg, dp, E, H, I, op, cp, sp, wp, rp, ggu.data_ptr(),
                                         wh.data_ptr() if want_wh else None, None if gw is None else gw.data_ptr(),
                                         *_status_word(ws, dev), _raw_stream(dev))
@@ -1359,10 +1379,18 @@ def _down_backward(gy, down, kept, offsets, w, order, ws, want_wh, want_gw, stre
     return ggu, wh, gw
 
 
+def _experts_of(gate_up, down=None):
+    """The ``si_experts`` of gate_up [E, 2 I, H] and down (without it the sizes alone)."""
+    E, rows, H = gate_up.shape
+    return SiExperts(_half(gate_up, "gate_up"), H, rows // 2, E, None if down is None else gate_up.data_ptr(),
+                     None if down is None else down.data_ptr())
+
+
 def moe_experts_workspace_bytes(n_tokens: int, top_k: int, gate_up: torch.Tensor) -> int:
     """Of ``si_moe_experts`` and its gradients."""
-    E, rows, _ = gate_up.shape
-    return moe_down_backward_workspace_bytes(n_tokens * top_k, E, rows // 2)
+    if n_tokens * top_k >> 31:
+        return 0
+    return int(library().si_moe_experts_workspace_bytes(_experts_of(gate_up), n_tokens, top_k))
 
 
 def si_moe_experts(x: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor,
@@ -1372,62 +1400,79 @@ def si_moe_experts(x: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, gate_up:
     y[t] = sum_r w[t, r] down[e] (silu(g) u), (g, u) = gate_up[e] x[t], e = ids[t, r]; ids outside
     [0, E) are dropped. The gradients (once) reach x, w, gate_up and down; their history
     holds x and, of the experts' rows, g and u in 8 bits alone. ``ws`` is kept by the caller
-    (``moe_experts_workspace_bytes``) and receives the device status; without it a wait that
-    ran out on the device, which leaves the results incomplete, is not reported."""
+    (``moe_experts_workspace_bytes``) and receives the device status; without it each call takes
+    one of its own, and a wait that ran out on the device, which leaves the results incomplete,
+    is not reported."""
     dev = x.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(si_moe_experts, stream, x, ids, w, gate_up, down, ws)
     if x.dim() != 2 or ids.dim() != 2 or ids.shape[0] != x.shape[0]:
         raise ValueError(f"x has shape {tuple(x.shape)}, ids {tuple(ids.shape)}, expected [T, H] and [T, k]")
-    _half(x, "x")
-    _same(gate_up, x, "gate_up", 3)
-    _same(down, x, "down", 3)
-    H, (E, rows, _) = x.shape[1], gate_up.shape
-    if gate_up.shape[2] != H or rows % 2 or down.shape != (E, H, rows // 2):
-        raise ValueError(f"gate_up has shape {tuple(gate_up.shape)} and down {tuple(down.shape)}, expected [E, 2 I, {H}] "
-                         f"and [E, {H}, I]")
-    if w.shape != ids.shape:
-        raise ValueError(f"w has shape {tuple(w.shape)}, expected {tuple(ids.shape)}")
     if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad or gate_up.requires_grad or down.requires_grad):
         return _Experts.apply(x, ids, w, gate_up, down, ws)
-    return _experts_forward(x, ids, w, gate_up, down, ws, False)[0]
+    return _experts_forward(dev, x, ids, w, gate_up, down, ws, False)[0]
 
 
-def _experts_forward(x, ids, w, gate_up, down, ws, keep):
-    order, position, offsets = si_moe_sort(ids, gate_up.shape[0])
-    h = si_moe_gateup(si_moe_gather(x, position, offsets), gate_up, offsets, keep, ws)
-    h, kept = h if keep else (h, None)
-    # the experts' rows stay fp32 until the ranks are summed
-    ys = si_moe_matmul(h, down, offsets, _f32_t, None, ws)
-    return si_moe_combine(ys, position, w, None, x.dtype), order, position, offsets, kept
+def _experts_forward(dev: int, x, ids, w, gate_up, down, ws, keep: bool):
+    _half(x, "x")
+    _same(gate_up, x, "gate_up", 3)
+    (T, H), k, (E, rows, cols), d, lib = x.shape, ids.shape[1], gate_up.shape, x.device, library()
+    n, I = T * k, rows // 2
+    if cols != H or rows % 2 or down.shape != (E, H, I):
+        raise ValueError(f"gate_up has shape {tuple(gate_up.shape)} and down {tuple(down.shape)}, expected [E, 2 I, {H}] "
+                         f"and [E, {H}, I]")
+    _width(H, "x")
+    _width(I, "down")
+    if n >> 31:
+        _too_many(T, k)
+    if w.shape != ids.shape:
+        raise ValueError(f"w has shape {tuple(w.shape)}, expected {tuple(ids.shape)}")
+    _ptr(gate_up, dev, E * rows * H, x.dtype, "gate_up"), _ptr(down, dev, E * H * I, x.dtype, "down")
+    L = _experts_of(gate_up, down)
+    y, kept = _empty((T, H), dtype=x.dtype, device=d), None
+    if keep:
+        kept = _empty((lib.si_moe_experts_kept_bytes(L, T, k),), dtype=_u8, device=d)
+    if ws is None:                               # nobody reads its status word
+        ws = _empty((lib.si_moe_experts_workspace_bytes(L, T, k),), dtype=_u8, device=d)
+    m = ws.numel()
+    st = lib.si_moe_experts(L, T, k, _ptr(x, dev, T * H, x.dtype, "x"), _ptr(ids, dev, n, _i32_t, "ids"),
+                            _ptr(w, dev, n, _f32_t, "w"), y.data_ptr(), kept.data_ptr() if keep else None,
+                            _ptr(ws, dev, m, _u8, "ws"), m, _raw_stream(dev))
+    if st:
+        _check(st, "si_moe_experts")
+    return y, kept
 
 
 class _Experts(torch.autograd.Function):
-    """si_moe_experts with a gradient. Nothing of the experts' outputs is kept: with gh =
-    down^T gy, the gradient of a pair's weight is <gh, h>. gh stays in the registers of
-    the launch that forms it, and x's gradient in fp32 rows until the ranks are summed: so
-    every gradient is rounded once as an operand of a product and once as a result."""
+    """si_moe_experts with a gradient. gh = down^T gy stays in the registers of the launch
+    that forms it, and x's gradient in fp32 rows until the ranks are summed: so every
+    gradient is rounded once as an operand of a product and once as a result."""
 
     @staticmethod
     def forward(ctx, x, ids, w, gate_up, down, ws):
-        y, order, position, offsets, kept = _experts_forward(x, ids, w, gate_up, down, ws, True)
-        ctx.save_for_backward(x, w, gate_up, down, order, position, offsets, *kept)
-        ctx.ws = ws
+        y, kept = _experts_forward(x.get_device(), x, ids, w, gate_up, down, ws, True)
+        ctx.save_for_backward(x, w, gate_up, down, kept)
+        ctx.ws, ctx.k = ws, ids.shape[1]
         return y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, gy):
-        x, w, gate_up, down, order, position, offsets, *kept = ctx.saved_tensors
-        ws, (need_x, _, need_w, need_gu, need_down, _) = ctx.ws, ctx.needs_input_grad
-        gys = si_moe_gather(gy.contiguous(), position, offsets)
-        ggu, wh, gw = _down_backward(gys, down, kept, offsets, w, order, ws, need_down, need_w)
-        gdown = si_moe_matmul_grad_w(gys, wh, offsets, None, ws) if need_down else None
-        ggate_up = si_moe_matmul_grad_w(ggu, si_moe_gather(x, position, offsets), offsets, None, ws) if need_gu else None
-        gx = None
-        if need_x:
-            gxs = si_moe_matmul(ggu, gate_up.transpose(1, 2), offsets, _f32_t, None, ws)
-            gx = si_moe_gather_backward(gxs, position, None, x.dtype)
+        x, w, gate_up, down, kept = ctx.saved_tensors
+        ws, k, need, lib, dev = ctx.ws, ctx.k, ctx.needs_input_grad, library(), x.get_device()
+        T, H = x.shape
+        L, gy = _experts_of(gate_up, down), gy if gy.is_contiguous() else gy.contiguous()
+        gx, gw, ggate_up, gdown = (_empty(t.shape, dtype=t.dtype, device=t.device) if need[i] else None
+                                   for i, t in ((0, x), (2, w), (3, gate_up), (4, down)))
+        if ws is None:
+            ws = _empty((lib.si_moe_experts_workspace_bytes(L, T, k),), dtype=_u8, device=x.device)
+        p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        m = ws.numel()
+        st = lib.si_moe_experts_backward(L, T, k, _ptr(gy, dev, T * H, x.dtype, "gy"), x.data_ptr(), w.data_ptr(),
+                                         kept.data_ptr(), p(gx), p(gw), p(ggate_up), p(gdown),
+                                         _ptr(ws, dev, m, _u8, "ws"), m, _raw_stream(dev))
+        if st:
+            _check(st, "si_moe_experts_backward")
         return gx, None, gw, ggate_up, gdown, None
 
 

@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsi_moe.so")
 SOURCES = ["quant_norm.cu", "router.cu", "ffn.cu", "batched.cu", "stack.cu", "requant.cu", "mxfp4.cu",
-           "mxfp4_gemm.cu", "sort.cu", "moe_matmul.cu", "swiglu.cu", "api.cu"]
+           "mxfp4_gemm.cu", "sort.cu", "moe_matmul.cu", "swiglu.cu", "experts.cu", "api.cu"]
 HEADERS = [os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "host.hpp"),
            os.path.join(CSRC, "topk.cuh"), os.path.join(CSRC, "tc.cuh"), os.path.join(CSRC, "norm.cuh"),
            os.path.join(CSRC, "mxfp4.cuh"), os.path.join(CSRC, "sort.cuh"),

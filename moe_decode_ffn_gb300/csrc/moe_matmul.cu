@@ -1216,6 +1216,7 @@ extern "C" si_status si_moe_down_backward(const void *gy, si_dtype type, int64_t
     return few ? gm_launch<kGmFew, kGmSwigluBack, true, O>(p, most, s) : gm_launch<kGmWide, kGmSwigluBack, true, O>(p, most, s);
   });
   if (e != cudaSuccess || !gw) return cuda_status(e);
+  if (order && cudaMemsetAsync(gw, 0, static_cast<size_t>(rows) * sizeof(float), s) != cudaSuccess) return SI_ERR_CUDA;
   return cuda_status(launch_pdl(gm_sum_kernel, dim3(static_cast<unsigned>((rows + 255) / 256)), dim3(256), 0, s,
                                 static_cast<const float *>(p.part), p.parts, p.rows, order, gw));
 }

@@ -493,6 +493,10 @@ extern "C" si_status si_swiglu_backward(const void *gh, si_dtype type, int64_t r
   const SwigluBack p{rows, static_cast<int>(inter), static_cast<const uint8_t *>(codes), static_cast<const uint8_t *>(scales), row_w,
                      order, gw};
   const dim3 block = act_block(inter), grid = act_walk(rows, block, kActBackward);
+  if (gw && order) {                 // of the pairs without a row too
+    const cudaError_t e = cudaMemsetAsync(gw, 0, static_cast<size_t>(rows) * sizeof(float), static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return SI_ERR_CUDA;
+  }
   const bool one = inter <= kActThreads / 32 * kActCols;
   return cuda_status(act_by_type(type, vec, [&](auto t, auto v) {
     using T = decltype(t);

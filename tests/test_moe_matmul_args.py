@@ -1,6 +1,8 @@
 """Arguments of the products of sorted rows, of the 8-bit activations and of SwiGLU
 are checked on the host (no device work; every call here is refused or has nothing
 to do)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -71,6 +73,35 @@ def test_down_backward_refusals(lib):
     refused(lib.si_moe_down_backward, ok, [{"type": m.SI_F32}], UNS)
     refused(lib.si_moe_down_backward, ok, [{"ws": None}, {"ws": 128}, {"nb": need - 1}, {"gw": None, "nb": 255}], WS)
     refused(lib.si_moe_down_backward, ok, [{"rows": 0, "gy": None}], OK)
+
+
+def test_experts_refusals(lib):
+    def experts(**kw):
+        c = m.SiExperts(m.SI_BF16, 64, 24, 4, 16, 16)
+        for name, v in kw.items():
+            setattr(c, name, v)
+        return ctypes.byref(c)
+    size, kept = lib.si_moe_experts_workspace_bytes, lib.si_moe_experts_kept_bytes
+    need = size(experts(), 10, 2)
+    assert need > 0 and need % 256 == 0 and size(experts(), 1000, 2) > need
+    # order and position of 20 pairs, 5 offsets, 48 codes and 2 scales a pair, each to the next 256
+    assert kept(experts(), 10, 2) == 3 * 256 + 1024 + 256
+    for c, t, k in ((experts(hidden=60), 10, 2), (experts(inter=0), 10, 2), (experts(n_experts=0), 10, 2),
+                    (experts(n_experts=1025), 10, 2), (experts(), 0, 2), (experts(), 10, 0), (experts(), 10, 9),
+                    (experts(), 1 << 28, 8), (None, 10, 2)):
+        assert size(c, t, k) == 0 and kept(c, t, k) == 0
+        assert lib.si_moe_experts(c, t, k, 16, 16, 16, 16, None, 256, 1 << 40, None) == BAD
+        assert lib.si_moe_experts_backward(c, t, k, 16, 16, 16, 256, 16, 16, 16, 16, 256, 1 << 40, None) == BAD
+    ok = dict(L=experts(), t=10, k=2, x=16, ids=16, w=16, y=16, kept=256, ws=256, nb=need)
+    refused(lib.si_moe_experts, ok, [{"x": None}, {"x": 8}, {"ids": None}, {"w": None}, {"y": None}, {"y": 8}, {"kept": 128},
+                                     {"L": experts(gate_up=None)}, {"L": experts(down=8)}], BAD)
+    refused(lib.si_moe_experts, ok, [{"L": experts(type=m.SI_F32)}], UNS)
+    refused(lib.si_moe_experts, ok, [{"ws": None}, {"ws": 128}, {"nb": need - 1}], WS)
+    ok = dict(L=experts(), t=10, k=2, gy=16, x=16, w=16, kept=256, gx=16, gw=16, ggate_up=16, gdown=16, ws=256, nb=need)
+    refused(lib.si_moe_experts_backward, ok, [
+        {"gy": None}, {"gy": 8}, {"x": None}, {"x": 24}, {"w": None}, {"kept": None}, {"kept": 128}, {"gx": 8}, {"gw": 18},
+        {"ggate_up": 8}, {"gdown": 24}], BAD)
+    refused(lib.si_moe_experts_backward, ok, [{"ws": None}, {"nb": need - 1}], WS)
 
 
 def test_combine_of_fp32_rows_refusals(lib):
