@@ -112,11 +112,11 @@ struct GmTile {
   int rt, ct;
 };
 
-// Rows of a group's tiles: kGmWide as even parts of at most 256, to the next 32.
-template <int OP> SI_DEV int gm_per(int rows) {
-  if (OP == kGmFew) return 16;
-  const int n = (rows + 255) >> 8;
-  return n > 0 ? min(256, ((rows + n - 1) / n + 31) & ~31) : 256;
+// A group's rows in tiles: of 16, or kGmWide in as many even parts as parts of 256 would be,
+// each to the next 32 rows.
+template <int OP> SI_DEV int gm_parts(int rows) { return OP == kGmFew ? (rows + 15) >> 4 : (rows + 255) >> 8; }
+template <int OP> SI_DEV int gm_per(int rows, int parts) {
+  return OP == kGmFew ? 16 : min(256, ((rows + parts - 1) / parts + 31) & ~31);
 }
 SI_DEV int gm_scan_add(int v, int lane) {
 #pragma unroll
@@ -127,43 +127,41 @@ SI_DEV int gm_scan_add(int v, int lane) {
   return v;
 }
 
-// The list, by all threads of the block.
+// The list, by all threads of the block; of its first warp a lane has some neighbouring
+// bounds and groups, so that one scan over the lanes does for each.
 template <int OP> SI_DEV void gm_list(const GmParams &p, GmList &l) {
   const int E = p.n_experts;
-  for (int i = threadIdx.x; i <= E; i += blockDim.x) l.tile[i] = min(max(__ldcg(p.offsets + i), 0), p.rows);
+  for (int i = threadIdx.x; i <= E; i += blockDim.x) l.row[i + 1] = min(max(__ldcg(p.offsets + i), 0), p.rows);
+  if (threadIdx.x == 0) {
+    l.row[0] = 0;
+    l.row[E + 2] = p.rows;
+  }
   __syncthreads();
   if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
+    const int lane = threadIdx.x, n = (E + 32) >> 5;   // of E + 1 bounds, then of E + 2 groups
+    const int b0 = 1 + min(lane * n, E + 1), b1 = 1 + min((lane + 1) * n, E + 1);
     int most = 0;
-    for (int i0 = 0; i0 <= E; i0 += 32) {        // running maximum of the bounds
-      int v = i0 + lane <= E ? l.tile[i0 + lane] : 0;
+    for (int i = b0; i < b1; ++i) most = max(most, l.row[i]);
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, v, d);
-        if (lane >= d) v = max(v, o);
-      }
-      v = max(v, most);
-      most = __shfl_sync(0xffffffffu, v, 31);
-      if (i0 + lane <= E) l.row[i0 + lane + 1] = v;
+    for (int d = 1; d < 32; d <<= 1) {           // running maximum
+      const int o = __shfl_up_sync(0xffffffffu, most, d);
+      if (lane >= d) most = max(most, o);
     }
-    if (lane == 0) {
-      l.row[0] = 0;
-      l.row[E + 2] = p.rows;
-    }
+    most = __shfl_up_sync(0xffffffffu, most, 1);
+    if (lane == 0) most = 0;
+    for (int i = b0; i < b1; ++i) l.row[i] = most = max(most, l.row[i]);
     __syncwarp();
-    int at = 0;
-    for (int i0 = 0; i0 < E + 2; i0 += 32) {
-      const int i = i0 + lane;
-      int own = 0;
-      if (i < E + 2) {
-        const int rows = l.row[i + 1] - l.row[i], per = gm_per<OP>(rows);
-        own = (rows + per - 1) / per * p.n_rt;
-      }
-      const int v = gm_scan_add(own, lane);
-      if (i < E + 2) l.tile[i] = at + v - own;
-      at += __shfl_sync(0xffffffffu, v, 31);
+    const int m = (E + 33) >> 5, g0 = min(lane * m, E + 2), g1 = min((lane + 1) * m, E + 2);
+    auto tiles = [&](int i) { return gm_parts<OP>(l.row[i + 1] - l.row[i]) * p.n_rt; };
+    int sum = 0;
+    for (int i = g0; i < g1; ++i) sum += tiles(i);
+    const int upto = gm_scan_add(sum, lane);
+    int at = upto - sum;
+    for (int i = g0; i < g1; ++i) {
+      l.tile[i] = at;
+      at += tiles(i);
     }
-    if (lane == 0) l.tile[E + 2] = at;
+    if (lane == 31) l.tile[E + 2] = upto;
   }
   __syncthreads();
 }
@@ -187,7 +185,7 @@ template <int OP> SI_DEV GmTile gm_tile(const GmParams &p, const GmList &l, int 
       else hi = mid - 1;
     }
     const int rows = l.row[lo + 1] - l.row[lo], i = w - l.tile[lo];
-    const int per = gm_per<OP>(rows), parts = (rows + per - 1) / per;
+    const int parts = gm_parts<OP>(rows), per = gm_per<OP>(rows, parts);
     t.rt = i / parts;
     t.ct = 0;
     const int r = (i - t.rt * parts) * per;
@@ -521,9 +519,13 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
     }
     fence_mbar_init();
   }
+  if (threadIdx.x == 32) {           // the maps on their way
+    prefetch_map(&p.a);
+    prefetch_map(p.b);
+  }
   grid_dep_wait();
   // before the next kernel may start: its blocks take tensor memory too
-  if (warp == 1) gm_tmem_alloc<CG>(s_taddr, C::kCols);
+  if (warp == C::kBWarp) gm_tmem_alloc<CG>(s_taddr, C::kCols);
   tc_fence_before();
   if constexpr (OP != kGmGrad) gm_list<OP>(p, list);
   if constexpr (CG == 2) cluster_sync();
@@ -913,7 +915,7 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
   if constexpr (CG == 2) cluster_sync();         // the other block's MMAs and arrivals are over too
   else __syncthreads();
   tc_fence_after();
-  if (warp == 1) {
+  if (warp == C::kBWarp) {
     __syncwarp();
     gm_tmem_free<CG>(tmem, C::kCols);
   }
@@ -1047,8 +1049,12 @@ static bool gm_ld(int64_t ld, int64_t cols, int size) {
 }
 static bool gm_whole(const void *p, int size) { return p && reinterpret_cast<uintptr_t>(p) % size == 0; }
 
-// Rows of an expert on average up to which a tile is one SM's, with 16 rows.
-static bool gm_few(int64_t rows, int n_experts) { return rows <= 16 * static_cast<int64_t>(n_experts); }
+// Rows of an expert on average up to which a tile is one SM's, with 16 rows. Measured, in
+// one SM against two, rows dealt out at random: 128 experts 1536 x 2048, 8 / 12 / 16 / 20 rows 125 /
+// 126 / 128 / 150 us against 136 / 137 / 138 / 138; 2048 x 768 67 / 67 / 80 / 93 against 71 / 71 / 72 / 72;
+// 256 of 512 x 2048 88 / 88 / 90 / 106 against 93 / 94 / 95 / 96; 16 of 4096 x 1024, 8 / 12 / 16 rows
+// 27.4 / 26.1 / 32.0 against 28.9 / 29.4 / 29.5. Behind 16 rows an expert's second tile reads its matrix again.
+static bool gm_few(int64_t rows, int n_experts) { return rows <= 12 * static_cast<int64_t>(n_experts); }
 
 // What the products of sorted rows share: the rows' operand and the list. `tile`: features
 // of a tile. Returns the number of tiles at most, 0 if they pass 2^30, -1 without a map.
@@ -1172,13 +1178,13 @@ extern "C" si_status si_moe_gateup(const void *x, si_dtype type, int64_t rows, i
 }
 
 // Partial sums of a row's gw: one of 32 features each, in whole tiles.
-static int64_t gm_parts(int64_t rows, int n_experts, int64_t inter) {
+static int64_t gm_sums(int64_t rows, int n_experts, int64_t inter) {
   return gm_few(rows, n_experts) ? (inter + 127) / 128 * 4 : (inter + 255) / 256 * 8;
 }
 
 extern "C" size_t si_moe_down_backward_workspace_bytes(int64_t rows, int n_experts, int64_t inter) {
   if (!gm_rows(rows, n_experts) || !gm_width(inter)) return 0;
-  return round_up(sizeof(WsHeader) + static_cast<size_t>(rows) * gm_parts(rows, n_experts, inter) * 4, 256);
+  return round_up(sizeof(WsHeader) + static_cast<size_t>(rows) * gm_sums(rows, n_experts, inter) * 4, 256);
 }
 
 extern "C" si_status si_moe_down_backward(const void *gy, si_dtype type, int64_t rows, int64_t ldg, const void *down,
@@ -1208,7 +1214,7 @@ extern "C" si_status si_moe_down_backward(const void *gy, si_dtype type, int64_t
   p.c = row_w;
   p.order = order;
   p.wh = wh;
-  p.parts = static_cast<int>(gm_parts(rows, n_experts, inter));
+  p.parts = static_cast<int>(gm_sums(rows, n_experts, inter));
   p.part = gw ? reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + sizeof(WsHeader)) : nullptr;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = gm_by_half(type, [&](auto o) {

@@ -76,6 +76,9 @@ static __device__ __noinline__ bool mbar_wait_cluster_slow(uint64_t *bar, uint32
 SI_DEV bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, uint32_t *status) {
   return mbar_try_wait_cluster(bar, parity) || mbar_wait_cluster_slow(bar, parity, status);
 }
+SI_DEV void prefetch_map(const CUtensorMap *map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 // A box of four dimensions into this block's shared memory; PAIR: its bytes count at a
 // barrier of either block (an address in the cluster).
 template <bool PAIR> SI_DEV void tma_load4(void *dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, uint32_t bar) {
