@@ -976,6 +976,14 @@ def _half(t, name: str) -> int:
     return code
 
 
+def _rows_of_gradient(gy, dtype):
+    """A gradient that autograd hands on, as contiguous rows that start on 16-byte boundaries."""
+    if gy.dtype is not dtype:
+        gy = gy.to(dtype)
+    gy = gy.contiguous()
+    return gy.clone() if gy.data_ptr() & 15 else gy
+
+
 def _same(t, like, name: str, dims: int):
     """Checks that ``t`` has the device, the type and ``dims`` dimensions beside ``like``."""
     if not isinstance(t, _Tensor) or t.dim() != dims:
@@ -1140,7 +1148,7 @@ class _Matmul(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, gy):
         x, w, offsets = ctx.saved_tensors
-        gy, dev, need = gy.to(x.dtype).contiguous(), x.get_device(), ctx.needs_input_grad
+        gy, dev, need = _rows_of_gradient(gy, x.dtype), x.get_device(), ctx.needs_input_grad
         gx = _matmul(dev, gy, w, offsets, None, None, ctx.ws, True) if need[0] else None
         gw = _grad_w(dev, gy, x, offsets, None, ctx.ws) if need[1] else None
         return gx, gw, None, None, None
@@ -1461,7 +1469,7 @@ class _Experts(torch.autograd.Function):
         x, w, gate_up, down, kept = ctx.saved_tensors
         ws, k, need, lib, dev = ctx.ws, ctx.k, ctx.needs_input_grad, library(), x.get_device()
         T, H = x.shape
-        L, gy = _experts_of(gate_up, down), gy if gy.is_contiguous() else gy.contiguous()
+        L, gy = _experts_of(gate_up, down), _rows_of_gradient(gy, x.dtype)
         gx, gw, ggate_up, gdown = (_empty(t.shape, dtype=t.dtype, device=t.device) if need[i] else None
                                    for i, t in ((0, x), (2, w), (3, gate_up), (4, down)))
         if ws is None:
