@@ -16,7 +16,7 @@ struct ExpertsGeom {
   int64_t rows;
   size_t order, position, offsets, codes, scales, kept;       // of the kept block, its size
   size_t f_kept, f_sort, f_xs, f_h, f_ys, forward;            // f_kept: where nothing is kept
-  size_t b_part, part_bytes, b_rows, b_ggu, b_wh, b_gx, backward;
+  size_t part_bytes, b_rows, b_ggu, b_wh, b_gx, backward;
 };
 static bool experts_ok(const si_experts *L, int n_tokens, int top_k) {
   auto width = [](int n) { return n >= 8 && n % 8 == 0 && n <= (1 << 20); };

@@ -207,8 +207,7 @@ template <int OP> SI_DEV GmTile gm_tile(const GmParams &p, const GmList &l, int 
   }
   return t;
 }
-// Stages of a tile.
-// kGmGrad: of its whole 16 rows; up to 15 more are the tail.
+// Stages of a tile; for kGmGrad of its expert's whole 16 rows, up to 15 more are the tail.
 template <int OP> SI_DEV int gm_steps(const GmParams &p, const GmTile &t) {
   return OP == kGmGrad ? ((t.count & ~15) + kGmK - 1) / kGmK : t.e < 0 ? 0 : (p.k + kGmK - 1) / kGmK;
 }
