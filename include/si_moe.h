@@ -545,8 +545,9 @@ si_status si_moe_combine_backward(const void *gy, const void *ys, si_dtype type,
  *            gw: si_moe_down_backward_workspace_bytes(rows, n_experts, inter) bytes, of
  *            which the first 256 are zeroed once
  * fp32 sums of 512 terms on the tensor cores (whose additions may truncate); with SI_F32
- * outputs these are added to one another rounded to nearest. More sums than 512 terms'
- * stay on the tensor cores otherwise. Outputs may not alias inputs. More than 2^30 output tiles: SI_ERR_UNSUPPORTED.
+ * outputs, and in si_moe_gateup with SI_F16 (the first 1024 terms in one where experts have
+ * more than 12 rows on average), these are added to one another rounded to nearest. Otherwise
+ * sums of more than 512 terms stay on the tensor cores. Outputs may not alias inputs. More than 2^30 output tiles: SI_ERR_UNSUPPORTED.
  */
 size_t si_moe_matmul_workspace_bytes(void);
 si_status si_moe_matmul(const void *x, si_dtype type, int64_t rows, int64_t ld_x, const void *w, int n_experts,

@@ -56,14 +56,16 @@ constexpr int kGmTail = 2 * 16 * 128;  // 128 values of 16 summed indices
 constexpr int kGmGroups = kSortMaxExperts + 2;
 
 enum GmOp { kGmWide, kGmFew, kGmGrad };
-// What becomes of the sums: written, SwiGLU of gate and up, the gradients of SwiGLU.
-enum GmMode { kGmPlain, kGmSwiglu, kGmSwigluBack };
+// What becomes of the sums: written, SwiGLU of gate and up (kGmSwigluParts: summed in parts, see
+// kGmChunk), the gradients of SwiGLU.
+enum GmMode { kGmPlain, kGmSwiglu, kGmSwigluParts, kGmSwigluBack };
+template <int MODE> constexpr bool kGmForward = MODE == kGmSwiglu || MODE == kGmSwigluParts;
 enum GmOut { kGmBf16, kGmF16, kGmF32 };
 template <int OUT> constexpr int kGmSize = OUT == kGmF32 ? 4 : 2;
 
 template <int OP, int MODE, int OUT> struct GmCfg {
   static constexpr int CG = OP == kGmFew ? 1 : 2;                    // SMs of a tile
-  static constexpr int MA = OP == kGmFew && MODE == kGmSwiglu ? 2 : 1;   // 128-row A tiles: gate and up
+  static constexpr int MA = OP == kGmFew && kGmForward<MODE> ? 2 : 1;   // 128-row A tiles: gate and up
   static constexpr int kN = OP == kGmFew ? 16 : 256;                 // columns of an accumulator
   // fp32 outputs are summed up in registers: 64 columns a warp instead of 128; and what SwiGLU
   // asks for goes faster with more warps to take turns
@@ -264,6 +266,15 @@ template <int CG> SI_DEV void gm_tmem_free(uint32_t addr, uint32_t cols) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
   else
     tmem_dealloc(addr, cols);
+}
+
+// 8 columns of this warp's lanes; tcgen05.wait::st before they are read.
+SI_DEV void gm_tmem_st8(uint32_t addr, const float v[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
+               "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+               "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+               "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+               : "memory");
 }
 
 // ---- epilogues ---------------------------------------------------------------
@@ -493,7 +504,18 @@ SI_DEV void gm_swiglu_back16(const GmParams &p, int f, int lane, int64_t row0, i
 // Stages that one accumulator takes up. The tensor cores' additions truncate: with
 // fp32 outputs the sums of 512 terms are added up in registers instead, rounded to
 // nearest (1448 terms were off by 1.8e-6 relative, now 6e-7; fp32 sums in turn 7e-7).
-template <int OUT> constexpr int kGmChunk = OUT == kGmF32 ? 8 : 1 << 30;
+// kGmSwigluParts: so are fp16's gate and up, whose errors turn 8-bit codes (of 4096 terms
+// 1.5e-4 of them, in parts 2.7e-5, as fp32 products do; beside bf16's own rounding they do not
+// show). A pair of SMs adds the first 1024 terms up in one: its accumulator is held while the
+// 8-bit blocks before are made, and the MMAs get one part ahead (256 rows an expert, 2048
+// terms, kept 200 us, 217 in parts so, 237 in parts of 512; in one SM, 4 rows an expert, 122
+// and in parts of 512 124).
+template <int MODE, int OUT> constexpr int kGmChunk = OUT == kGmF32 || MODE == kGmSwigluParts ? 8 : 1 << 30;
+template <int OP, int MODE, int OUT>
+constexpr int kGmFirst = MODE == kGmSwigluParts && OP == kGmWide ? 16 : kGmChunk<MODE, OUT>;
+template <int OP, int MODE, int OUT> SI_DEV int gm_next(int k0) {
+  return k0 == 0 ? kGmFirst<OP, MODE, OUT> : k0 + kGmChunk<MODE, OUT>;
+}
 
 // WMN: the matrices lie by columns (features contiguous).
 template <int OP, int MODE, bool WMN, int OUT>
@@ -501,7 +523,7 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
   using C = GmCfg<OP, MODE, OUT>;
   constexpr int S = C::kStages, CG = C::CG, PARTS = C::kEpiWarps / 4, PIECES = C::kN / 16 / PARTS;
   constexpr bool kAMn = OP == kGmGrad || WMN, kBMn = OP == kGmGrad;
-  static_assert(MODE == kGmPlain || (OP != kGmGrad && OUT != kGmF32 && !(MODE == kGmSwiglu && WMN)), "forms");
+  static_assert(MODE == kGmPlain || (OP != kGmGrad && OUT != kGmF32 && !(kGmForward<MODE> && WMN)), "forms");
   extern __shared__ uint8_t gm_smem[];
   uint8_t *base = gm_smem + ((1024u - (smem_addr(gm_smem) & 1023u)) & 1023u);
   uint8_t *tails = base + S * C::kStage, *outs = tails + C::kTail;
@@ -611,7 +633,7 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
             expect(C::kABytes);
             if constexpr (OP == kGmGrad)
               load_mn(st, kGmPiece, &p.a, p.whole_a, t.rt * 256 + rank * 128, t.row0 + c, 0, bar);
-            else if constexpr (MODE == kGmSwiglu)    // gate and up
+            else if constexpr (kGmForward<MODE>)    // gate and up
               load(st, &p.a, c, t.rt * 128 + rank * 64, 0, t.e, bar);
             else if constexpr (WMN)
               load_mn(st, kGmPiece, &p.a, p.whole_a, (t.rt * CG + rank) * 128, c, t.e, bar);
@@ -655,10 +677,10 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
       const uint32_t idesc = (1u << 4) | p.fmt | (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u) |
                              (static_cast<uint32_t>(columns(t) >> 3) << 17) | ((CG * 128u >> 4) << 24);
       const int last = OP == kGmGrad ? t.count & ~15 : p.k, cut = tail_rows(t);   // summed indices
-      for (int k0 = 0; k0 < nk || (k0 == 0 && cut); k0 += kGmChunk<OUT>, ++n) {
+      for (int k0 = 0; k0 < nk || (k0 == 0 && cut); k0 = gm_next<OP, MODE, OUT>(k0), ++n) {
         const uint32_t u = n & 1, d = tmem + u * C::kAccCols;
         if (leader && ok) ok = mbar_wait_bounded(acc_empty + u, ((n >> 1) & 1) ^ 1, p.status);
-        const int k1 = min(nk, kGmChunk<OUT> < nk ? k0 + kGmChunk<OUT> : nk);
+        const int k1 = min(nk, gm_next<OP, MODE, OUT>(k0));
         for (int ks = k0; ks < k1; ++ks) {
           const int n16 = (min(kGmK, last - ks * kGmK) + 15) >> 4;
           const uint32_t st = smem0 + s * C::kStage;
@@ -753,7 +775,7 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
         float sum[OUT == kGmF32 ? kMine : 1] = {};
         uint32_t acc = 0;
         if constexpr (OUT == kGmF32) {
-          for (int k0 = 0; ok && k0 < nk; k0 += kGmChunk<OUT>) {
+          for (int k0 = 0; ok && k0 < nk; k0 += kGmChunk<MODE, OUT>) {
             acc = wait_acc();
             if (!ok) break;
 #pragma unroll
@@ -798,7 +820,7 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
         }
       } else {
         // lane = feature; 16 rows at a time
-        const int tf = MODE == kGmSwiglu && OP == kGmWide ? t.rt * 128 + rank * 64 + (q & 1) * 32
+        const int tf = kGmForward<MODE> && OP == kGmWide ? t.rt * 128 + rank * 64 + (q & 1) * 32
                                                           : (t.rt * CG + rank) * 128 + q * 32;
         const int f = tf + lane;
         auto read16 = [&](uint32_t addr, float v[16]) {
@@ -817,7 +839,7 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
         uint32_t acc = 0;
         if constexpr (OUT == kGmF32) {
           float sum[PIECES][16] = {};
-          for (int k0 = 0; ok && k0 < nk; k0 += kGmChunk<OUT>) {
+          for (int k0 = 0; ok && k0 < nk; k0 += kGmChunk<MODE, OUT>) {
             acc = wait_acc();
             if (!ok) break;
 #pragma unroll
@@ -841,8 +863,44 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
           }
         } else {
           if constexpr (MODE != kGmSwigluBack) {
-            if (!zero) acc = wait_acc();
+            constexpr bool kParts = MODE == kGmSwigluParts;
+            constexpr int HALVES = kParts && OP == kGmFew ? 2 : 1;
+            float sum[kParts ? HALVES * PIECES : 1][16] = {};
+            auto each = [&](auto f) {            // 8 columns of each piece
+#pragma unroll
+              for (int i = 0; i < HALVES * PIECES; ++i) {
+                if (i % PIECES >= mine) continue;
+#pragma unroll
+                for (int h = 0; h < 16; h += 8) f(acc + i / PIECES * C::kN + gm_piece<PARTS>(i % PIECES, part) + h, sum[i] + h);
+              }
+            };
+            if constexpr (kParts) {
+              for (int k0 = 0; ok && gm_next<OP, MODE, OUT>(k0) < nk; k0 = gm_next<OP, MODE, OUT>(k0)) {   // but the last
+                acc = wait_acc();
+                if (!ok) break;
+                each([&](uint32_t at, float *to) {
+                  float r[8];
+                  tmem_ld8(at, r);
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) to[j] += r[j];
+                });
+                release();
+              }
+            }
+            if (!zero && ok) acc = wait_acc();
             zero |= !ok;
+            if constexpr (kParts) {
+              if (!zero && nk > kGmFirst<OP, MODE, OUT>) {   // into the last one's place
+                each([&](uint32_t at, float *to) {
+                  float r[8];
+                  tmem_ld8(at, r);
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) r[j] += to[j];
+                  gm_tmem_st8(at, r);
+                });
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+              }
+            }
             if (!zero && mine == 0) release();
           }
           bool have = MODE != kGmSwigluBack;     // the accumulator has been waited for
@@ -1186,6 +1244,12 @@ extern "C" si_status si_moe_gateup(const void *x, si_dtype type, int64_t rows, i
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   return cuda_status(gm_by_half(type, [&](auto o) {
     constexpr int O = decltype(o)::value;
+    // more terms than the first part's (512 rows an expert, 512 terms, kept, took 43 us with the parts' code, 37 without)
+    if constexpr (O == kGmF16) {
+      if (hidden > (few ? kGmFirst<kGmFew, kGmSwigluParts, O> : kGmFirst<kGmWide, kGmSwigluParts, O>) * kGmK)
+        return few ? gm_launch<kGmFew, kGmSwigluParts, false, O>(p, most, s)
+                   : gm_launch<kGmWide, kGmSwigluParts, false, O>(p, most, s);
+    }
     return few ? gm_launch<kGmFew, kGmSwiglu, false, O>(p, most, s) : gm_launch<kGmWide, kGmSwiglu, false, O>(p, most, s);
   }));
 }

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import moe_decode_ffn_gb300 as m
-from tests.test_gpu_moe_experts import TYPES, expected, inputs, near
+from tests.test_gpu_moe_experts import TYPES, V, expected, inputs, near, silu_off
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +80,25 @@ def test_kept_blocks_that_are_not_finite(form, kind, bad):
     rows = torch.arange(xs.shape[0], device="cuda") != 3
     assert bool((scales2[3] == 255).all()) and int(torch.count_nonzero(codes2[3])) == 0
     assert same_bits(h2[rows], h[rows]) and torch.equal(codes2[rows], codes[rows]) and torch.equal(scales2[rows], scales[rows])
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("H", [520, 1024, 1032, 1536, 2056])
+@pytest.mark.parametrize("counts", [[3, 0, 9], [70, 0, 300]])
+def test_gate_and_up_over_long_sums(counts, H, kind):
+    """Whole numbers, exact in any order of the sums and in however many parts: every part once."""
+    g = torch.Generator(device="cuda").manual_seed(H)
+    dtype, R, I = TYPES[kind], sum(counts) + 2, 72
+    xs = torch.randint(-2, 3, (R, H), generator=g, device="cuda").to(dtype)
+    gate_up = torch.randint(-2, 3, (3, 2 * I, H), generator=g, device="cuda").to(dtype) / 64
+    offsets = torch.tensor([0] + torch.tensor(counts).cumsum(0).tolist(), dtype=torch.int32, device="cuda")
+    gu = torch.zeros(R, 2 * I, dtype=torch.float64, device="cuda")
+    for e in range(3):
+        rows = slice(int(offsets[e]), int(offsets[e + 1]))
+        gu[rows] = xs[rows].double() @ gate_up[e].double().T
+    h, (codes, scales) = m.si_moe_gateup(xs, gate_up, offsets, keep=True)
+    assert torch.equal(h, m.si_moe_gateup(xs, gate_up, offsets))
+    parts = [m.si_quantize_mxint8(v.float().contiguous()) for v in (gu[:, :I], gu[:, I:])]   # |sums| < 2^18 / 64: exact
+    assert torch.equal(codes, torch.cat([p[0] for p in parts], 1)) and torch.equal(scales, torch.cat([p[1] for p in parts], 1))
+    want = torch.nn.functional.silu(gu[:, :I]) * gu[:, I:]
+    near(h, V(want, silu_off(gu[:, :I], want)).round(dtype), "h")
