@@ -38,8 +38,8 @@
 // (16384 rows over 8 experts of 4096 x 4096 308 to 340 us, 1.6 to 1.8 PFLOP/s, by the clock that
 // the power limit leaves). Between them, 256 ragged rows an expert over 128 experts: the
 // loads, 187 us for 1536 x 2048 (5.0 TB/s from HBM, 10.8 TB/s from the L2; the MMA warp waits for
-// a stage for 44 % of the time, tensor pipe active 43 %); the gradients 208 us (805 MB
-// written, 5.0 TB/s with what is read).
+// a stage for 44 % of the time, tensor pipe active 43 %); the gradients 221 us (805 MB
+// written, 4.7 TB/s with what is read).
 #include <algorithm>
 #include <atomic>
 
@@ -679,7 +679,10 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
       const int last = OP == kGmGrad ? t.count & ~15 : p.k, cut = tail_rows(t);   // summed indices
       for (int k0 = 0; k0 < nk || (k0 == 0 && cut); k0 = gm_next<OP, MODE, OUT>(k0), ++n) {
         const uint32_t u = n & 1, d = tmem + u * C::kAccCols;
-        if (leader && ok) ok = mbar_wait_bounded(acc_empty + u, ((n >> 1) & 1) ^ 1, p.status);
+        if (leader && ok) {          // (the fence behind it is the stages' and the tail's)
+          const uint32_t free = ((n >> 1) & 1) ^ 1;
+          ok = CG == 2 ? mbar_wait_cluster(acc_empty + u, free, p.status) : mbar_wait_bounded(acc_empty + u, free, p.status);
+        }
         const int k1 = min(nk, gm_next<OP, MODE, OUT>(k0));
         for (int ks = k0; ks < k1; ++ks) {
           const int n16 = (min(kGmK, last - ks * kGmK) + 15) >> 4;
@@ -737,7 +740,7 @@ __global__ void __launch_bounds__(GmCfg<OP, MODE, OUT>::kThreads, 1) moe_mm_kern
       for (int r = left; r < 16; ++r) *reinterpret_cast<uint4 *>(to + r * 128) = make_uint4(0, 0, 0, 0);
       fence_async_smem();
       __syncwarp();
-      // what was written is this block's own, and its tensor core's to read
+      // written here, read by the MMA that a thread of the first block issues for both
       if (lane == 0) mbar_arrive_cluster(ready0 + u * 8);
     }
   } else {

@@ -37,15 +37,17 @@ SI_DEV uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-// At a barrier of either block, by a thread whose block's own shared memory is all that the
-// arrival is about: it releases within the block. (A release of the cluster waits for memory
-// as a whole, about 2400 cycles in a busy SM.)
+// At a barrier of either block, for a thread of that block to see what was written before:
+// the release has to reach the other block, though the memory written is this block's
+// own. (It waits for the thread's memory as a whole, about 2400 cycles in a busy SM.)
 SI_DEV void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// The same by a thread that has written nothing for the other block: a release of the
-// cluster waits for all of the thread's stores (as the producers' arrival, stage for stage, it
-// made a product of 8192 x 2 rows 816 us instead of 353).
+// The same by a thread that has written nothing for the other block, which needs no
+// release (as the producers' arrival, stage for stage, one made a product of 8192 x 2 rows 816 us
+// instead of 353): to hand tensor memory back, whose reads are complete (tcgen05.wait::ld) and
+// ordered before the arrival by tcgen05.fence::before_thread_sync, as the MMAs of the thread
+// that waits are behind its wait by tcgen05.fence::after_thread_sync.
 SI_DEV void mbar_arrive_cluster_relaxed(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
