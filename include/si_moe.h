@@ -529,7 +529,8 @@ si_status si_moe_combine_backward(const void *gy, const void *ys, si_dtype type,
  *            (before offsets[0], behind offsets[n_experts]) are not read, and their outputs
  *            (codes and scales too) are zeros; an expert without rows has gw 0
  *   n, k     width of out and of x (rows and columns of a matrix), inter and hidden:
- *            multiples of 8, up to 2^20; n_experts 1..1024
+ *            multiples of 8, up to 2^20 (k of si_moe_matmul and n of si_moe_matmul_grad_w up to
+ *            2^21: the gradients of a fused gate and up); n_experts 1..1024
  *   w        W[e] at w + e * mat_stride values: by_columns 0: n rows of k values,
  *            ld_w apart; 1: k rows of n values (column c of W[e] is row c). So the
  *            gradient of x is si_moe_matmul of gy with by_columns turned round.

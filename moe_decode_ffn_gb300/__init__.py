@@ -992,9 +992,9 @@ def _same(t, like, name: str, dims: int):
         raise ValueError(f"{name} is {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
 
 
-def _width(n: int, name: str):
-    if n < 8 or n % 8 or n > 1 << 20:
-        raise ValueError(f"{name} is {n} wide, expected a multiple of 8 up to 2^20")
+def _width(n: int, name: str, log: int = 20):
+    if n < 8 or n % 8 or n > 1 << log:
+        raise ValueError(f"{name} is {n} wide, expected a multiple of 8 up to 2^{log}")
 
 
 def _rows(t, name: str):
@@ -1066,7 +1066,7 @@ def _matmul(dev: int, x, w, offsets, dtype=None, out=None, ws=None, turned=False
     if k != k2:
         raise ValueError(f"x is {k} wide, w takes {k2}")
     _width(n, "out")
-    _width(k, "x")
+    _width(k, "x", 21)
     ldx, xp = _rows(x, "x")
     op = _offsets(offsets, dev, E)
     if out is None:
@@ -1107,7 +1107,7 @@ def _grad_w(dev: int, gy, x, offsets, dtype=None, ws=None):
         raise ValueError(f"gy has {R} rows, x has {R2}")
     if E < 1:
         raise ValueError("offsets must be int32 [n_experts + 1]")
-    _width(n, "gy")
+    _width(n, "gy", 21)
     _width(k, "x")
     ldg, gp = _rows(gy, "gy")
     ldx, xp = _rows(x, "x")

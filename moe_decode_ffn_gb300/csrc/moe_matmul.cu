@@ -1113,7 +1113,8 @@ template <typename F> static cudaError_t gm_by_half(si_dtype t, F f) {
 
 static bool gm_type(si_dtype t) { return t == SI_BF16 || t == SI_F16; }
 static uint32_t gm_fmt(si_dtype t) { return t == SI_BF16 ? (1u << 7) | (1u << 10) : 0u; }
-static bool gm_width(int64_t n) { return n >= 8 && n % 8 == 0 && n <= (int64_t(1) << 20); }
+static bool gm_width(int64_t n, int64_t most = int64_t(1) << 20) { return n >= 8 && n % 8 == 0 && n <= most; }
+constexpr int64_t kGmBoth = int64_t(1) << 21;    // g's and u's features side by side, where a gradient needs them
 static bool gm_rows(int64_t rows, int n_experts) {
   return rows >= 0 && rows <= 0x7FFFFFFF - 256 && n_experts >= 1 && n_experts <= kSortMaxExperts;
 }
@@ -1160,7 +1161,7 @@ extern "C" si_status si_moe_matmul(const void *x, si_dtype type, int64_t rows, i
                                    int n_experts, int64_t n, int64_t k, int64_t ldw, int64_t matw, int by_columns,
                                    const int32_t *offsets, void *out, si_dtype out_type, int64_t ldo, void *workspace,
                                    size_t workspace_bytes, void *stream) {
-  if (!gm_rows(rows, n_experts) || !gm_width(n) || !gm_width(k)) return SI_ERR_INVALID_ARG;
+  if (!gm_rows(rows, n_experts) || !gm_width(n) || !gm_width(k, kGmBoth)) return SI_ERR_INVALID_ARG;
   if (!gm_type(type) || (out_type != SI_F32 && out_type != type)) return SI_ERR_UNSUPPORTED;
   if (rows == 0) return SI_OK;
   const bool few = gm_few(rows, n_experts), cols = by_columns != 0;
@@ -1191,7 +1192,7 @@ extern "C" si_status si_moe_matmul_grad_w(const void *gy, int64_t ldg, const voi
                                           int64_t rows, int n_experts, int64_t n, int64_t k, const int32_t *offsets,
                                           void *gw, si_dtype gw_type, void *workspace, size_t workspace_bytes,
                                           void *stream) {
-  if (!gm_rows(rows, n_experts) || !gm_width(n) || !gm_width(k)) return SI_ERR_INVALID_ARG;
+  if (!gm_rows(rows, n_experts) || !gm_width(n, kGmBoth) || !gm_width(k)) return SI_ERR_INVALID_ARG;
   if (!gm_type(type) || (gw_type != SI_F32 && gw_type != type)) return SI_ERR_UNSUPPORTED;
   const int size = gw_type == SI_F32 ? 4 : 2;
   if (!gw || !aligned16(gw)) return SI_ERR_INVALID_ARG;
