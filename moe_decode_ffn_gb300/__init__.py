@@ -6,8 +6,8 @@ device memory and streams. There is no CPU fallback: if the library is not
 built, or a tensor is not on a CUDA device, the calls raise.
 
 Names follow the C ABI in ``include/si_moe.h``. Results carry no gradient, but for
-those of ``si_moe_gather``, ``si_moe_combine``, ``si_moe_matmul``, ``si_swiglu`` and
-``si_moe_experts``.
+those of ``si_moe_gather``, ``si_moe_combine``, ``si_moe_matmul``, ``si_swiglu``,
+``si_moe_gateup`` and ``si_moe_experts``.
 """
 from __future__ import annotations
 
@@ -1307,10 +1307,19 @@ class _Swiglu(torch.autograd.Function):
 def si_moe_gateup(x: torch.Tensor, gate_up: torch.Tensor, offsets: torch.Tensor, keep: bool = False,
                   ws: torch.Tensor | None = None, stream=None):
     """si_swiglu of si_moe_matmul's fp32 sums in one launch: sorted rows x [R, H] and gate_up
-    [E, 2 I, H] contiguous (bf16 or fp16) -> h [R, I], with ``keep`` (h, kept) as ``si_swiglu``."""
+    [E, 2 I, H] contiguous (bf16 or fp16) -> h [R, I], with ``keep`` (h, kept) as ``si_swiglu``.
+    Differentiable in x and gate_up (once): the history holds both, and g and u in 8 bits."""
     dev = x.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(si_moe_gateup, stream, x, gate_up, offsets, keep, ws)
+    if (x.requires_grad or gate_up.requires_grad) and torch.is_grad_enabled():
+        h, codes, scales = _Gateup.apply(x, gate_up, offsets, ws)
+        return (h, (codes, scales)) if keep else h
+    return _gateup(dev, x, gate_up, offsets, keep, ws)
+
+
+def _gateup(dev: int, x, gate_up, offsets, keep, ws):
+    """si_moe_gateup without a history."""
     t = _half(x, "x")
     if x.dim() != 2:
         raise ValueError("x must be [R, H]")
@@ -1331,6 +1340,28 @@ def si_moe_gateup(x: torch.Tensor, gate_up: torch.Tensor, offsets: torch.Tensor,
     if st:
         _check(st, "si_moe_gateup")
     return (h, kept) if keep else h
+
+
+class _Gateup(torch.autograd.Function):
+    """si_moe_gateup of an x or a gate_up that requires a gradient."""
+
+    @staticmethod
+    def forward(ctx, x, gate_up, offsets, ws):
+        h, kept = _gateup(x.get_device(), x, gate_up, offsets, True, ws)
+        ctx.save_for_backward(x, gate_up, offsets, *kept)
+        ctx.mark_non_differentiable(*kept)
+        ctx.ws = ws
+        return h, *kept
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, gh, *_):
+        x, gate_up, offsets, codes, scales = ctx.saved_tensors
+        dev, need = x.get_device(), ctx.needs_input_grad
+        ggu = _swiglu_backward(gh.contiguous(), (codes, scales), None, None, False)[0]
+        gx = _matmul(dev, ggu, gate_up, offsets, None, None, ctx.ws, True) if need[0] else None
+        ggate_up = _grad_w(dev, ggu, x, offsets, None, ctx.ws) if need[1] else None
+        return gx, ggate_up, None, None
 
 
 def moe_down_backward_workspace_bytes(rows: int, n_experts: int, inter: int) -> int:
