@@ -15,6 +15,7 @@ import ctypes
 import os
 
 import torch
+import torch.autograd.forward_ad as _forward_ad
 from torch.autograd.function import once_differentiable
 
 from ._build import LIB, build  # noqa: F401
@@ -611,6 +612,18 @@ def _elsewhere(call, stream, first, *args, **kw):
         return call(first, *args, **kw)
 
 
+def _dual() -> bool:
+    """Whether forward-mode differentiation is under way (one look at a number: the usual calls pay for no more)."""
+    return getattr(_forward_ad, "_current_level", 0) >= 0
+
+
+def _no_tangents(call: str, *tensors):
+    """Refuses dual tensors: the gradients are reverse mode's, and a tangent would be lost without a word."""
+    for t in tensors:
+        if isinstance(t, _Tensor) and _forward_ad.unpack_dual(t).tangent is not None:
+            raise ValueError(f"{call} hands no forward-mode tangent on: its gradients are reverse mode's")
+
+
 def _ptr(t, dev: int, numel: int, dtype, name: str) -> int:
     """Device pointer of ``t`` after checking its device, size, dtype and that it is contiguous."""
     if t.get_device() == dev and t.dtype is dtype and t.numel() == numel and t.is_contiguous():
@@ -811,6 +824,8 @@ def si_moe_gather(x: torch.Tensor, position: torch.Tensor, offsets: torch.Tensor
     dev = x.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(si_moe_gather, stream, x, position, offsets)
+    if _dual():
+        _no_tangents("si_moe_gather", x)
     if x.requires_grad and torch.is_grad_enabled():
         return _Gather.apply(x, position, offsets)
     (T, H), k, dtype = x.shape, position.shape[-1], x.dtype
@@ -856,6 +871,8 @@ def si_moe_combine(ys: torch.Tensor, position: torch.Tensor, w: torch.Tensor, st
     dev = ys.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(si_moe_combine, stream, ys, position, w, None, dtype)
+    if _dual():
+        _no_tangents("si_moe_combine", ys, w)
     if (ys.requires_grad or w.requires_grad) and torch.is_grad_enabled():
         return _Combine.apply(ys, position, w, dtype)
     if dtype is not None and dtype is not ys.dtype:
@@ -1047,6 +1064,8 @@ def si_moe_matmul(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, dtype
     dev = x.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(si_moe_matmul, stream, x, w, offsets, dtype, out, ws)
+    if _dual():
+        _no_tangents("si_moe_matmul", x, w)
     if (x.requires_grad or w.requires_grad) and torch.is_grad_enabled():
         if out is not None:
             raise ValueError("out cannot be given where x or w requires a gradient")
@@ -1233,6 +1252,8 @@ def si_swiglu(gu: torch.Tensor, keep: bool = False, stream=None):
         raise ValueError(f"gu has shape {tuple(gu.shape)}, expected [R, 2 I]")
     if gu.dtype not in _TYPES:
         _bad_type(gu, "gu")
+    if _dual():
+        _no_tangents("si_swiglu", gu)
     if gu.requires_grad and torch.is_grad_enabled():
         h, codes, scales = _Swiglu.apply(gu)
         return (h, (codes, scales)) if keep else h
@@ -1312,6 +1333,8 @@ def si_moe_gateup(x: torch.Tensor, gate_up: torch.Tensor, offsets: torch.Tensor,
     dev = x.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(si_moe_gateup, stream, x, gate_up, offsets, keep, ws)
+    if _dual():
+        _no_tangents("si_moe_gateup", x, gate_up)
     if (x.requires_grad or gate_up.requires_grad) and torch.is_grad_enabled():
         h, codes, scales = _Gateup.apply(x, gate_up, offsets, ws)
         return (h, (codes, scales)) if keep else h
@@ -1447,6 +1470,8 @@ def si_moe_experts(x: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, gate_up:
         return _elsewhere(si_moe_experts, stream, x, ids, w, gate_up, down, ws)
     if x.dim() != 2 or ids.dim() != 2 or ids.shape[0] != x.shape[0]:
         raise ValueError(f"x has shape {tuple(x.shape)}, ids {tuple(ids.shape)}, expected [T, H] and [T, k]")
+    if _dual():
+        _no_tangents("si_moe_experts", x, w, gate_up, down)
     if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad or gate_up.requires_grad or down.requires_grad):
         return _Experts.apply(x, ids, w, gate_up, down, ws)
     return _experts_forward(dev, x, ids, w, gate_up, down, ws, False)[0]
