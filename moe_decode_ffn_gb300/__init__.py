@@ -1460,7 +1460,8 @@ def si_moe_experts(x: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, gate_up:
     """The routed experts in 16 bits, differentiable: x [T, H], ids int32 [T, k], w fp32 [T, k],
     gate_up [E, 2 I, H] (gate rows first) and down [E, H, I] contiguous, bf16 or fp16 as x -> [T, H]:
     y[t] = sum_r w[t, r] down[e] (silu(g) u), (g, u) = gate_up[e] x[t], e = ids[t, r]; ids outside
-    [0, E) are dropped. The gradients (once) reach x, w, gate_up and down; their history
+    [0, E) are dropped; without tokens nothing is launched, and the matrices' gradients are
+    zeros. The gradients (once) reach x, w, gate_up and down; their history
     holds x and, of the experts' rows, g and u in 8 bits alone. ``ws`` is kept by the caller
     (``moe_experts_workspace_bytes``) and receives the device status; without it each call takes
     one of its own, and a wait that ran out on the device, which leaves the results incomplete,
@@ -1494,6 +1495,9 @@ def _experts_forward(dev: int, x, ids, w, gate_up, down, ws, keep: bool):
     _ptr(gate_up, dev, E * rows * H, x.dtype, "gate_up"), _ptr(down, dev, E * H * I, x.dtype, "down")
     L = _experts_of(gate_up, down)
     y, kept = _empty((T, H), dtype=x.dtype, device=d), None
+    if T == 0 and lib.si_moe_experts_kept_bytes(L, 1, k):   # sizes that a token could have
+        _ptr(x, dev, 0, x.dtype, "x"), _ptr(ids, dev, 0, _i32_t, "ids"), _ptr(w, dev, 0, _f32_t, "w")
+        return y, None
     if keep:
         kept = _empty((lib.si_moe_experts_kept_bytes(L, T, k),), dtype=_u8, device=d)
     if ws is None:                               # nobody reads its status word
@@ -1525,6 +1529,9 @@ class _Experts(torch.autograd.Function):
         x, w, gate_up, down, kept = ctx.saved_tensors
         ws, k, need, lib, dev = ctx.ws, ctx.k, ctx.needs_input_grad, library(), x.get_device()
         T, H = x.shape
+        if T == 0:
+            return tuple(torch.zeros_like(t) if need[i] else None
+                         for i, t in enumerate((x, None, w, gate_up, down, None)))
         L, gy = _experts_of(gate_up, down), _rows_of_gradient(gy, x.dtype)
         gx, gw, ggate_up, gdown = (_empty(t.shape, dtype=t.dtype, device=t.device) if need[i] else None
                                    for i, t in ((0, x), (2, w), (3, gate_up), (4, down)))
