@@ -994,7 +994,8 @@ def _half(t, name: str) -> int:
 
 
 def _rows_of_gradient(gy, dtype):
-    """A gradient that autograd hands on, as contiguous rows that start on 16-byte boundaries."""
+    """A gradient that autograd hands on, as contiguous rows of ``dtype`` (an operand of the tensor cores)
+    that start on 16-byte boundaries."""
     if gy.dtype is not dtype:
         gy = gy.to(dtype)
     gy = gy.contiguous()
@@ -1058,7 +1059,9 @@ def si_moe_matmul(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, dtype
     fp16; rows of x at any 16-byte aligned stride, matrices by rows or, as a
     transposed view, by columns), offsets int32 [E + 1] of ``si_moe_sort`` -> [R, n] in
     x's type, in ``dtype`` (that or fp32) or into ``out``; zero rows for rows of no expert.
-    Differentiable in x and w (once), without ``out``. ``ws`` (``moe_matmul_workspace_bytes``)
+    Differentiable in x and w (once), without ``out``: the gradient of the result enters the products
+    as an operand and is rounded to x's type first, an fp32 result's too (in fp16 beyond 65504 to
+    infinity, below 6e-8 to zero). ``ws`` (``moe_matmul_workspace_bytes``)
     receives the device status; without it a wait that ran out on the device, which
     leaves the result incomplete, is not reported."""
     dev = x.get_device()

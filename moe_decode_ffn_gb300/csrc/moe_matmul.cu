@@ -32,14 +32,17 @@
 // persistent; two accumulators, so that the MMAs of a tile run beside the epilogue of
 // the one before.
 //
-// What bounds it, on a GB300. Few rows: HBM (128 experts of 2048 x 768, 4 rows each,
-// 56.7 us, 98 % of a copy's rate; a matrix' piece of 16 KB takes an SM 0.23 us, the MMAs' own
-// time, which shows where fewer tiles than SMs are at work). Many rows: the tensor cores
+// What bounds it, on a GB300. Few rows: HBM (64 tokens, top-8 of 128 experts of 2048 x 768, of
+// which about 108 have rows, 56.7 us, 6.0 TB/s; all 128 with 4 rows each 66 us, 6.1 TB/s). Where there are
+// fewer tiles than SMs (one token, 96 tiles, 13.7 us) the way of a stage: of its 709 cycles (502 with
+// matrices that lie in the L2) the MMA warp waits 54 % (37 %) for the copies, the rest goes to issuing four
+// MMAs and their commit; the tensor pipe is active for 4.5 %. Many rows: the tensor cores
 // (16384 rows over 8 experts of 4096 x 4096 308 to 340 us, 1.6 to 1.8 PFLOP/s, by the clock that
 // the power limit leaves). Between them, 256 ragged rows an expert over 128 experts: the
-// loads, 187 us for 1536 x 2048 (5.0 TB/s from HBM, 10.8 TB/s from the L2; the MMA warp waits for
-// a stage for 44 % of the time, tensor pipe active 43 %); the gradients 221 us (805 MB
-// written, 4.7 TB/s with what is read).
+// loads, 188 us for 1536 x 2048 (5.0 TB/s from HBM, 10.8 TB/s from the L2; the MMA warp waits for
+// a stage for 47 % of the time, tensor pipe active 54 %); the gradients 221 us (805 MB
+// written, 4.7 TB/s with what is read; waits for stages 18 %, for last rows 11 %, for accumulators 8 %), in fp32
+// 314 us (1.61 GB written, 5.9 TB/s).
 #include <algorithm>
 #include <atomic>
 
@@ -1124,7 +1127,8 @@ static bool gm_ld(int64_t ld, int64_t cols, int size) {
 }
 static bool gm_whole(const void *p, int size) { return p && reinterpret_cast<uintptr_t>(p) % size == 0; }
 
-// Rows of an expert on average up to which a tile is one SM's, with 16 rows. Measured, in
+// Rows of an expert on average up to which a tile is one SM's, with 16 rows. The host does not know
+// how many of the rows are an expert's: those of none count too. Measured with every row an expert's, in
 // one SM against two, rows dealt out at random: 128 experts 1536 x 2048, 8 / 12 / 16 / 20 rows 125 /
 // 126 / 128 / 150 us against 136 / 137 / 138 / 138; 2048 x 768 67 / 67 / 80 / 93 against 71 / 71 / 72 / 72;
 // 256 of 512 x 2048 88 / 88 / 90 / 106 against 93 / 94 / 95 / 96; 16 of 4096 x 1024, 8 / 12 / 16 rows

@@ -43,7 +43,8 @@ SI_DEV void mi_values4(uint32_t w, float v[4]) {
   for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 + i)) - 8388736.f;
 }
 // The logistic function; g below -87 gives 0 where the reciprocal is below the normal
-// range (s < 2^-125). ex2 and rcp of the hardware, each within 2 units in the last place.
+// range (s < 2^-125). ex2 and rcp of the hardware, each within 2 units in the last place; the
+// argument's rounding adds about |g| units to exp(-g), which counts where g is well below 0.
 SI_DEV float mi_logistic(float g) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
