@@ -1162,6 +1162,8 @@ class _Matmul(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, w, offsets, dtype, ws):
+        if x.dim() == 2:
+            _width(x.shape[1], "x, whose width is that of its gradient,")
         ctx.save_for_backward(x, w, offsets)
         ctx.ws = ws
         return si_moe_matmul(x, w, offsets, dtype, None, ws)

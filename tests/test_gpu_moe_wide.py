@@ -63,3 +63,16 @@ def test_gradients_of_wide_experts():
     h = torch.nn.functional.silu(kept[0]) * kept[1]
     assert near(gdown[0], gy.T @ h, gy.abs().T @ h.abs(), T)
     assert near(gw[:, 0], (gh * h[:, at]).sum(1), (gh * h[:, at]).abs().sum(1), 32, 0.0)
+
+
+def test_a_product_whose_gradient_would_be_too_wide():
+    """Refused before the forward pass, not half way through the backward pass."""
+    k = (1 << 20) + 8
+    x, w = torch.ones(2, k, dtype=torch.bfloat16, device="cuda"), torch.ones(1, 8, k, dtype=torch.bfloat16, device="cuda")
+    offsets = torch.tensor([0, 2], dtype=torch.int32, device="cuda")
+    assert bool((m.si_moe_matmul(x, w, offsets, dtype=torch.float32) == k).all())
+    for a, b in ((x.clone().requires_grad_(), w), (x, w.clone().requires_grad_())):
+        with pytest.raises(ValueError, match="wide"):
+            m.si_moe_matmul(a, b, offsets)
+        with torch.no_grad():
+            assert bool((m.si_moe_matmul(a, b, offsets, dtype=torch.float32) == k).all())
