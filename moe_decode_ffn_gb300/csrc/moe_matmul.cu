@@ -40,8 +40,8 @@
 // (16384 rows over 8 experts of 4096 x 4096 308 to 340 us, 1.6 to 1.8 PFLOP/s, by the clock that
 // the power limit leaves). Between them, 256 ragged rows an expert over 128 experts: the
 // loads, 188 us for 1536 x 2048 (5.0 TB/s from HBM, 10.8 TB/s from the L2; the MMA warp waits for
-// a stage for 47 % of the time, tensor pipe active 54 %); the gradients 221 us (805 MB
-// written, 4.7 TB/s with what is read; waits for stages 18 %, for last rows 11 %, for accumulators 8 %), in fp32
+// a stage for 47 % of the time, tensor pipe active 54 %); the gradients 216 to 221 us (805 MB
+// written, 4.8 TB/s with what is read; waits for stages 18 %, for last rows 11 %, for accumulators 8 %), in fp32
 // 314 us (1.61 GB written, 5.9 TB/s).
 #include <algorithm>
 #include <atomic>

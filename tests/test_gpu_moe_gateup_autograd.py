@@ -103,3 +103,28 @@ def test_up_to_the_experts():
     for a, b in zip(grads, torch.autograd.grad(once, (x, w, gate_up, down), torch.ones_like(y))):
         # 16-bit rows between the steps: some roundings of 2^-8 more
         assert float((a.double() - b.double()).norm()) <= 0.02 * float(b.double().norm())
+
+
+def test_captured_and_replayed():
+    args = [40, 0, 17, 129], 2, 7, 136, 136, torch.bfloat16
+    x, gate_up, offsets, gh = inputs(*args)
+    ws, graph = m.workspace(m.moe_matmul_workspace_bytes()), torch.cuda.CUDAGraph()
+    a, b = x.clone().requires_grad_(), gate_up.clone().requires_grad_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):                # autograd's own first pass outside the capture
+        torch.autograd.grad(m.si_moe_gateup(a, b, offsets, ws=ws), (a, b), gh)
+    torch.cuda.current_stream().wait_stream(side)
+    with torch.cuda.graph(graph):
+        h = m.si_moe_gateup(a, b, offsets, ws=ws)
+        out = h, *torch.autograd.grad(h, (a, b), gh)
+    for cut in (1, 2):
+        with torch.no_grad():
+            a.copy_(x.flip(0)), b.copy_(gate_up.flip(1))
+        offsets.copy_(torch.tensor([cut, 100, 100, 130, 150 + cut], device="cuda"))
+        gh.copy_(torch.randn(gh.shape, device="cuda"))
+        graph.replay()
+        c, d = a.detach().clone().requires_grad_(), b.detach().clone().requires_grad_()
+        fresh = m.si_moe_gateup(c, d, offsets)
+        assert all(torch.equal(p, q) for p, q in zip(out, (fresh, *torch.autograd.grad(fresh, (c, d), gh))))
+    assert m.si_workspace_status(ws) == m.SI_OK
